@@ -370,6 +370,128 @@ int poetx_linear_bwd(const poetx_linear_desc* desc, const void* g_y, const void*
                      void* g_x, float* g_theta_R, float* g_theta_P,
                      void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Dense linear with bias, activation and residual in its epilogue ----
+ *
+ * The linear layer that carries no R and P: a POET-X weight merged after
+ * training (W = R W0 P), or one that was never reparameterised. Conventions
+ * as above; tokens may be any number >= 1.
+ *   forward   u = x W^T + bias,   y = act(u) + residual
+ *   backward  g_u = g_y act'(u),  g_x = g_u W,  g_W = g_u^T x,
+ *             g_bias = the column sums of g_u;  the residual's gradient is g_y
+ * u, act(u) and their sum are formed in float32 and y and the kept u each
+ * rounded once. In the backward g_u is rounded to the act type once, as the
+ * products' operand (the matrix cores take bf16); g_bias sums the unrounded
+ * values. */
+typedef enum poetx_activation {
+  POETX_ACT_NONE = 0,
+  POETX_ACT_RELU = 1,      /* max(u, 0); its slope at 0 is 0 */
+  POETX_ACT_GELU = 2,      /* u Phi(u), Phi the normal distribution function */
+  POETX_ACT_GELU_TANH = 3, /* u (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))) / 2 */
+  POETX_ACT_SILU = 4       /* u / (1 + exp(-u)) */
+} poetx_activation;
+
+typedef struct poetx_dense_desc {
+  int64_t tokens;     /* rows of x, y, u, residual, g_y, g_x; >= 1 */
+  int64_t d_in;       /* columns of W; at most 2^22 */
+  int64_t d_out;      /* rows of W; at most 2^22 */
+  int32_t act;        /* poetx_dtype of x, W, residual, y, u and their gradients */
+  int32_t activation; /* poetx_activation */
+  int32_t flags;      /* must be 0 */
+  int32_t reserved;   /* must be 0 */
+  /* NULL: W is in the act type. Otherwise W holds int8 codes q [d_out, d_in]
+   * and w_scale [d_out] float32 row scales (poetx_quantize_weight; 16-byte
+   * aligned), the weight being diag(w_scale) q exactly; d_in must be a
+   * multiple of 8. The scales are applied to the float32 products. */
+  const float* w_scale;
+} poetx_dense_desc;
+
+/* Workspace bytes (0 if the descriptor is invalid, and where none is needed:
+ * ws may then be NULL). The backward's covers every choice of outputs. */
+size_t poetx_dense_fwd_workspace_size(const poetx_dense_desc* desc);
+size_t poetx_dense_bwd_workspace_size(const poetx_dense_desc* desc);
+
+/*
+ * poetx_dense_fwd - y = act(x W^T + bias) + residual.
+ *
+ *   x        [tokens, d_in]   act
+ *   W        [d_out, d_in]    act, or int8 codes with desc->w_scale
+ *   bias     [d_out] float32, or NULL
+ *   residual [tokens, d_out]  act, or NULL; must not overlap y
+ *   y        out [tokens, d_out] act
+ *   u_save   out [tokens, d_out] act: the pre-activation u, for the backward;
+ *            or NULL
+ */
+int poetx_dense_fwd(const poetx_dense_desc* desc, const void* x, const void* W, const float* bias,
+                    const void* residual, void* y, void* u_save, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * poetx_dense_bwd - the gradients that are asked for (a NULL output is not
+ * formed; all three NULL is POETX_ERR_NULL).
+ *
+ *   g_y      [tokens, d_out] act
+ *   x        [tokens, d_in]  act; needed for g_W only
+ *   W        [d_out, d_in]   as in the forward; needed for g_x only
+ *   u_saved  [tokens, d_out] act: the forward's u_save; ignored (may be NULL)
+ *            with POETX_ACT_NONE
+ *   g_x      out [tokens, d_in]  act, or NULL
+ *   g_W      out [d_out, d_in]   act, or NULL (a frozen weight); with INT8
+ *            codes it must be NULL (POETX_ERR_DTYPE)
+ *   g_bias   out [d_out] float32, or NULL
+ * Sums are split over workgroups and joined in a fixed order: results are
+ * bitwise reproducible.
+ */
+int poetx_dense_bwd(const poetx_dense_desc* desc, const void* g_y, const void* x, const void* W,
+                    const void* u_saved, void* g_x, void* g_W, float* g_bias, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* ---- Gradient norm over many tensors, and clipping ----
+ *
+ *   norm = sqrt(sum over every value of every tensor of grad^2),
+ *   out  = grad min(1, max_norm / norm)
+ * for the gradients of a training step: generator gradients of all layers
+ * (float32), bias and weight gradients. Squares and sums are float64, so the
+ * norm of any finite gradients is right wherever float32 can hold it; out is
+ * rounded once. A norm that is not finite (a NaN or infinity among the
+ * gradients) leaves the values as they are: out = grad, and the caller reads
+ * it from the norm. Sums are joined in a fixed order: bitwise reproducible. */
+typedef struct poetx_grad_tensor {
+  const void* grad; /* n values of `dtype`, contiguous, aligned to one value */
+  void* out;        /* the clipped values: grad itself (in place) or memory that
+                       overlaps nothing else of the list; unused by
+                       poetx_grad_norm */
+  int64_t n;        /* >= 0; an empty tensor's pointers may be NULL */
+  int32_t dtype;    /* poetx_dtype */
+  int32_t reserved; /* must be 0 */
+} poetx_grad_tensor;
+
+/* Workspace bytes for lists of up to `count` tensors (0 for count < 0). */
+size_t poetx_grad_workspace_size(int32_t count);
+
+/*
+ * The list is host memory and is read before the call returns. Errors:
+ * POETX_ERR_SHAPE (count or an n below 0, more than 2^44 bytes in all,
+ * max_norm negative or NaN), POETX_ERR_DTYPE, POETX_ERR_NULL,
+ * POETX_ERR_ALIGN, POETX_ERR_WORKSPACE, POETX_ERR_ALIAS (an output that
+ * overlaps anything but its own tensor's gradient exactly), POETX_ERR_HIP.
+ *
+ *   norm     float32 on the device: an output of _norm and _clip, an input
+ *            of _scale
+ *   max_norm >= 0 (infinity: nothing is clipped)
+ *   ws       poetx_grad_workspace_size(count) bytes
+ *
+ * poetx_grad_norm measures only (a tensor may be listed twice).
+ * poetx_grad_clip measures and clips. poetx_grad_scale clips by a norm that
+ * the caller has, for example joined over the ranks of a sharded job from
+ * their poetx_grad_norm values.
+ */
+int poetx_grad_norm(const poetx_grad_tensor* tensors, int32_t count, float* norm, void* ws,
+                    size_t ws_bytes, void* stream);
+int poetx_grad_clip(const poetx_grad_tensor* tensors, int32_t count, float max_norm, float* norm,
+                    void* ws, size_t ws_bytes, void* stream);
+int poetx_grad_scale(const poetx_grad_tensor* tensors, int32_t count, float max_norm,
+                     const float* norm, void* stream);
+
 /* Thin hipEvent helpers so a caller without HIP headers can time stages.
  * Each returns a poetx_status. The events are for timing only: they are
  * created with hipEventDisableSystemFence, so recording one between two

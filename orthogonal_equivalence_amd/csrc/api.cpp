@@ -11,31 +11,17 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "api_util.h"
 #include "kernels.h"
 
 using poetx::DType;
 using poetx::GemmParams;
+using namespace poetx::api;
 
 namespace {
 
 constexpr int kMaxBlock = 4096;
 constexpr int64_t kMaxBatch = 65535;  // grid.y limit of the batched launches
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t act_size(int act) { return act == POETX_BF16 ? 2 : 4; }
-int act_vec(int act) { return act == POETX_BF16 ? 8 : 4; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-Range range_of(const void* p, size_t bytes) {
-  uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // Checks shape, dtype and alignment fields of a descriptor.
 int check_desc(const poetx_linear_desc* d) {
@@ -655,8 +641,6 @@ hipError_t cnp_vjp_bf16(const CnpVjpBf16Set& a, const CnpVjpBf16Set* b2, int b, 
   const poetx::PackSet p2{c.w1, Tb2, nb2, (int)(c.d - (nb2 - 1) * b), c.g_theta};
   return poetx::launch_pack_skew_grad(p1, &p2, 1.0f, b, 1.0f, s);
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? POETX_OK : POETX_ERR_HIP; }
 
 // The forward's host-detectable argument faults other than the workspace.
 int check_fwd_args(const poetx_linear_desc* d, const void* x, const void* W0, const void* R_act,

@@ -216,6 +216,82 @@ hipError_t launch_widen_codes(DType t, const int8_t* q, int64_t rows, int64_t ld
 hipError_t launch_scale_block_columns(DType t, const void* M, const float* scale, int64_t nblocks,
                                       int b, int64_t d, void* out, hipStream_t s);
 
+// ---- dense linear with its epilogue ----
+enum class Activation : int { None = 0, Relu = 1, Gelu = 2, GeluTanh = 3, Silu = 4 };
+
+// What happens to a product's float32 accumulators (epilogue.h):
+//   u = acc scale[n] + bias[n],  y = act(u) + residual;
+// scale, bias, residual and u may be null. residual, u and y are [M][ld].
+struct Epilogue {
+  const float* scale = nullptr;
+  const float* bias = nullptr;
+  const void* residual = nullptr;
+  void* y = nullptr;
+  void* u = nullptr;
+  int64_t ld = 0;
+  int act = 0;  // Activation
+};
+
+// C(m, n) = sum_k A(m, k) B(n, k) (layouts as GemmParams) through an
+// epilogue, any M >= 1; N, and every extent that is contiguous in memory, a
+// multiple of 16 bytes. part: plan.part_floats floats when the plan splits K.
+struct TileProduct {
+  const void* A = nullptr;
+  const void* B = nullptr;
+  int64_t lda = 0, ldb = 0;
+  int M = 0, N = 0, K = 0;
+  int kchunk = 0;  // set by the launcher
+  float* part = nullptr;
+  Epilogue ep;
+};
+struct TilePlan {
+  bool big;  // 128 x 128 tiles (else 64 x 64)
+  int nsplit, kchunk;
+  size_t part_floats;
+};
+TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K);
+hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
+                               bool b_kmajor, hipStream_t s);
+
+// g_u = g_y act'(u) (times scale[n] where g_u is stored) and g_bias = its
+// column sums over the rows; g_u and g_bias may be null, u with no
+// activation. d a multiple of 16 bytes. part: act_grad_splits(rows) * d
+// floats unless that is one range.
+struct ActGrad {
+  const void* g_y = nullptr;
+  const void* u = nullptr;
+  const float* scale = nullptr;
+  void* g_u = nullptr;
+  float* g_bias = nullptr;
+  float* part = nullptr;
+  int64_t rows = 0;
+  int d = 0;
+  Activation act = Activation::None;
+};
+int act_grad_splits(int64_t rows);
+hipError_t launch_act_grad(DType t, const ActGrad& a, hipStream_t s);
+
+// ---- gradient norm and clipping over many tensors ----
+// One contiguous run of gradient values; out may equal grad.
+struct GradRun {
+  const void* grad;
+  void* out;
+  int64_t n;
+  DType dtype;
+};
+// Most partial sums (float64) that a list of up to `count` runs leaves.
+int64_t grad_partials_max(int count);
+// The partial sums of squares, *nparts of them.
+hipError_t launch_grad_sumsq(const GradRun* runs, int count, double* part, int* nparts,
+                             hipStream_t s);
+// norm = sqrt(sum of part[0 .. nparts)) as float32.
+hipError_t launch_grad_norm(const double* part, int nparts, float* norm, hipStream_t s);
+// out = grad min(1, max_norm / norm) for every run, the norm from `part`
+// (then also stored to norm_out) or, with part null, from *norm_in; a norm
+// that is not finite leaves the values as they are.
+hipError_t launch_grad_scale(const GradRun* runs, int count, const double* part, int nparts,
+                             const float* norm_in, float max_norm, float* norm_out, hipStream_t s);
+
 // ---- backward helpers ----
 // G[blk] = sum_s part[s][blk] in split order (float32), stored as `out`;
 // entries of the last block at rows or columns >= last_valid are zero. With

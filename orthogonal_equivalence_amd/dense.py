@@ -1,0 +1,163 @@
+"""The dense linear with bias, activation and residual in its epilogue, on
+libpoetx's kernels: the layer that carries no R and P (a POET-X weight merged
+after training, or a weight that was never reparameterised).
+
+    u = x W^T + bias,   y = act(u) + residual
+
+dense_forward and dense_backward take contiguous device tensors x [tokens,
+d_in], W [d_out, d_in], residual and u [tokens, d_out] of one type (float32 or
+bfloat16) and a float32 bias [d_out]; W may be the int8 codes of
+poetx_quantize_weight with their float32 row scales w_scale [d_out].
+DenseLinear keeps a weight and its bias. Outputs and workspaces come from
+torch's allocator on the stream that the call runs on, so calls on different
+streams, and calls captured into different graphs, share no memory.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import poetx as P
+
+ACTIVATIONS = {"none": P.POETX_ACT_NONE, "relu": P.POETX_ACT_RELU, "gelu": P.POETX_ACT_GELU,
+               "gelu_tanh": P.POETX_ACT_GELU_TANH, "silu": P.POETX_ACT_SILU}
+_ACT = {torch.float32: P.POETX_F32, torch.bfloat16: P.POETX_BF16}
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device, and `stream` (a torch stream, or a hipStream_t
+    address) as the current one."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _check(name, t, shape, dtype, device):
+    if t is None:
+        return
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _desc(name, t, W, activation, w_scale, width):
+    """Checks the weight against the activations t (their columns are W's
+    dimension `width`) and makes the descriptor."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if t.dim() != 2 or W.dim() != 2:
+        raise ValueError(f"{name} and W must have two dimensions")
+    if t.dtype not in _ACT:
+        raise ValueError(f"{name} is {t.dtype}, expected float32 or bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    d_out, d_in = W.shape
+    _check(name, t, (t.shape[0], W.shape[width]), t.dtype, t.device)
+    _check("W", W, (d_out, d_in), torch.int8 if w_scale is not None else t.dtype, t.device)
+    _check("w_scale", w_scale, (d_out,), torch.float32, t.device)
+    return P.make_dense_desc(t.shape[0], d_in, d_out, _ACT[t.dtype], ACTIVATIONS[activation],
+                             w_scale)
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, device=device, dtype=torch.uint8) if nbytes else None
+
+
+def dense_forward(x, W, bias=None, residual=None, activation="none", w_scale=None, save_u=False,
+                  stream=None):
+    """Returns (y, u): u, the pre-activation that dense_backward takes, with
+    save_u, else None."""
+    desc = _desc("x", x, W, activation, w_scale, 1)
+    out = (x.shape[0], W.shape[0])
+    _check("bias", bias, out[1:], torch.float32, x.device)
+    _check("residual", residual, out, x.dtype, x.device)
+    if stream is None and x.device.index == torch.cuda.current_device():
+        return _forward(desc, x, W, bias, residual, out, save_u)
+    with _on(x.device, stream):
+        return _forward(desc, x, W, bias, residual, out, save_u)
+
+
+def _forward(desc, x, W, bias, residual, out, save_u):
+    y = torch.empty(out, device=x.device, dtype=x.dtype)
+    u = torch.empty_like(y) if save_u else None
+    ws = _workspace(P.poetx_dense_fwd_workspace_size(desc), x.device)
+    P.poetx_dense_fwd(desc, x, W, bias, residual, y, u, ws)
+    return y, u
+
+
+def dense_backward(g_y, W, x=None, u=None, activation="none", w_scale=None, need_g_x=True,
+                   need_g_W=False, need_g_bias=False, stream=None):
+    """Returns (g_x, g_W, g_bias), None in the place of one not asked for. x is
+    needed for g_W, u (dense_forward's, with save_u) for an activation. The
+    gradient of the residual is g_y itself. int8 codes have no g_W."""
+    desc = _desc("g_y", g_y, W, activation, w_scale, 0)
+    d_out, d_in = W.shape
+    _check("x", x, (g_y.shape[0], d_in), g_y.dtype, g_y.device)
+    _check("u", u, tuple(g_y.shape), g_y.dtype, g_y.device)
+    if need_g_W and x is None:
+        raise ValueError("g_W needs x")
+    if need_g_W and w_scale is not None:
+        raise ValueError("int8 codes have no gradient")
+    if activation != "none" and u is None:
+        raise ValueError("the backward of an activation needs u")
+    if not (need_g_x or need_g_W or need_g_bias):
+        raise ValueError("no gradient asked for")
+    if stream is None and g_y.device.index == torch.cuda.current_device():
+        return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias)
+    with _on(g_y.device, stream):
+        return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias)
+
+
+def _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias):
+    new = dict(device=g_y.device, dtype=g_y.dtype)
+    g_x = torch.empty(g_y.shape[0], W.shape[1], **new) if need_g_x else None
+    g_W = torch.empty(W.shape, **new) if need_g_W else None
+    g_b = torch.empty(W.shape[0], device=g_y.device, dtype=torch.float32) if need_g_bias else None
+    ws = _workspace(P.poetx_dense_bwd_workspace_size(desc), g_y.device)
+    P.poetx_dense_bwd(desc, g_y, x, W, u, g_x, g_W, g_b, ws)
+    return g_x, g_W, g_b
+
+
+class DenseLinear:
+    """y = act(x W^T + bias) + residual with W [d_out, d_in] kept on the device
+    in the activation type `act` ("f32", "bf16"), or with int8=True as INT8
+    codes with per-row scales (poetx_quantize_weight)."""
+
+    def __init__(self, W: torch.Tensor, act: str, bias=None, activation="none", device="cuda",
+                 int8: bool = False):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {activation!r}")
+        self.torch_dtype = {"f32": torch.float32, "bf16": torch.bfloat16}[act]
+        self.device = torch.device(device)
+        self.activation = activation
+        self.W = W.to(self.device, self.torch_dtype).contiguous()
+        self.d_out, self.d_in = self.W.shape
+        self.bias = None
+        if bias is not None:
+            self.bias = torch.as_tensor(bias).to(self.device, torch.float32).contiguous()
+        self.w_scale = None
+        if int8:
+            with torch.cuda.device(self.W.device):
+                q = torch.empty(self.W.shape, device=self.device, dtype=torch.int8)
+                self.w_scale = torch.empty(self.d_out, device=self.device, dtype=torch.float32)
+                P.poetx_quantize_weight(self.W, self.d_out, self.d_in, _ACT[self.torch_dtype], q,
+                                        self.w_scale)
+            self.W = q
+
+    def forward(self, x, residual=None, save_u=False, stream=None):
+        return dense_forward(x, self.W, self.bias, residual, self.activation, self.w_scale, save_u,
+                             stream)
+
+    def backward(self, g_y, x=None, u=None, need_g_x=True, need_g_W=False, need_g_bias=None,
+                 stream=None):
+        """(g_x, g_W, g_bias); g_bias by default where the layer has a bias."""
+        if need_g_bias is None:
+            need_g_bias = self.bias is not None
+        return dense_backward(g_y, self.W, x, u, self.activation, self.w_scale, need_g_x, need_g_W,
+                              need_g_bias, stream)

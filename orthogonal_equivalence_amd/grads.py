@@ -1,0 +1,68 @@
+"""Global gradient norm over many tensors, and clipping by it, on libpoetx's
+kernels: what a training step does with the generator gradients of every
+layer (PoetxLinear.backward) and the bias and weight gradients beside them.
+
+Gradients are contiguous float32 or bfloat16 tensors of any sizes on one GPU,
+the two types mixed freely; lists of views of one flat buffer, in order, are
+taken as one range.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import poetx as P
+from .dense import _on
+
+
+def _device_of(grads, outs, norm):
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError("one output per gradient")
+    tensors = grads if norm is None else [*grads, norm]
+    if not tensors:
+        return grads, outs, torch.device("cuda", torch.cuda.current_device())
+    device = tensors[0].device
+    if device.type != "cuda":
+        raise ValueError("gradients must be on a GPU")
+    for g, o in zip(grads, outs):
+        if g.dtype not in P._GRAD_DTYPE:
+            raise ValueError(f"a gradient is {g.dtype}, expected float32 or bfloat16")
+        if g.device != device:
+            raise ValueError(f"gradients on {device} and {g.device}")
+        if o is not g and (o.shape != g.shape or o.dtype != g.dtype or o.device != device):
+            raise ValueError("an output must have its gradient's shape, type and device")
+    return grads, outs, device
+
+
+def grad_norm(grads, stream=None):
+    """sqrt of the sum of squares of every value of every tensor: a float32
+    scalar tensor on their device."""
+    grads, outs, device = _device_of(grads, None, None)
+    tensors = P.make_grad_list(grads)
+    with _on(device, stream):
+        norm = torch.empty((), device=device, dtype=torch.float32)
+        ws = torch.empty(P.poetx_grad_workspace_size(len(grads)), device=device, dtype=torch.uint8)
+        P.poetx_grad_norm(tensors, norm, ws)
+    return norm
+
+
+def clip_grads(grads, max_norm, outs=None, norm=None, stream=None):
+    """grad min(1, max_norm / norm) for every tensor, in place or into `outs`,
+    and returns the norm before clipping (a float32 scalar tensor). A norm
+    that is not finite leaves the values as they are. norm: a float32 scalar
+    tensor to clip by, where the caller has the norm already (joined over the
+    ranks of a sharded job, say)."""
+    grads, outs, device = _device_of(grads, outs, norm)
+    if norm is not None and (norm.numel() != 1 or norm.dtype != torch.float32 or
+                             norm.device != device):
+        raise ValueError(f"norm must be one float32 value on {device}")
+    tensors = P.make_grad_list(grads, outs)
+    with _on(device, stream):
+        if norm is not None:
+            P.poetx_grad_scale(tensors, max_norm, norm)
+            return norm
+        norm = torch.empty((), device=device, dtype=torch.float32)
+        ws = torch.empty(P.poetx_grad_workspace_size(len(grads)), device=device, dtype=torch.uint8)
+        P.poetx_grad_clip(tensors, max_norm, norm, ws)
+    return norm

@@ -7,6 +7,7 @@ fallback. Importing this module fails loudly if libpoetx.so is missing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -34,11 +35,20 @@ POETX_RECOMPUTE_Z = 1
 POETX_CAYLEY_NEUMANN = 2
 POETX_SAVED_Y = 4
 
+POETX_ACT_NONE = 0
+POETX_ACT_RELU = 1
+POETX_ACT_GELU = 2
+POETX_ACT_GELU_TANH = 3
+POETX_ACT_SILU = 4
+
 EXPORTS = (
     "poetx_abi_version", "poetx_status_string", "poetx_num_blocks", "poetx_theta_count",
     "poetx_build_workspace_size", "poetx_build_orthogonal", "poetx_build_cnp_workspace_size",
     "poetx_build_cnp", "poetx_fold_weight", "poetx_quantize_weight", "poetx_fwd_workspace_size",
     "poetx_bwd_workspace_size", "poetx_linear_fwd", "poetx_linear_fwd_noalloc", "poetx_linear_bwd",
+    "poetx_dense_fwd_workspace_size", "poetx_dense_bwd_workspace_size", "poetx_dense_fwd",
+    "poetx_dense_bwd", "poetx_grad_workspace_size", "poetx_grad_norm", "poetx_grad_clip",
+    "poetx_grad_scale",
     "poetx_event_create", "poetx_event_destroy", "poetx_event_record",
     "poetx_event_synchronize", "poetx_event_elapsed_ms",
 )
@@ -68,6 +78,29 @@ class LinearDesc(ctypes.Structure):
     ]
 
 
+class DenseDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("d_in", ctypes.c_int64),
+        ("d_out", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("w_scale", ctypes.c_void_p),
+    ]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -76,6 +109,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     dp = ctypes.POINTER(LinearDesc)
+    dd, f32 = ctypes.POINTER(DenseDesc), ctypes.c_float
     sig = {
         "poetx_abi_version": (ctypes.c_int, []),
         "poetx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -92,6 +126,15 @@ def _load() -> ctypes.CDLL:
         "poetx_linear_fwd": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "poetx_linear_fwd_noalloc": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, vp]),
         "poetx_linear_bwd": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "poetx_dense_fwd_workspace_size": (sz, [dd]),
+        "poetx_dense_bwd_workspace_size": (sz, [dd]),
+        "poetx_dense_fwd": (ctypes.c_int, [dd, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "poetx_dense_bwd": (ctypes.c_int, [dd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        # (the list of tensors: the address of GradTensor records)
+        "poetx_grad_workspace_size": (sz, [i32]),
+        "poetx_grad_norm": (ctypes.c_int, [vp, i32, vp, vp, sz, vp]),
+        "poetx_grad_clip": (ctypes.c_int, [vp, i32, f32, vp, vp, sz, vp]),
+        "poetx_grad_scale": (ctypes.c_int, [vp, i32, f32, vp, vp]),
         "poetx_event_create": (ctypes.c_int, [ctypes.POINTER(vp)]),
         "poetx_event_destroy": (ctypes.c_int, [vp]),
         "poetx_event_record": (ctypes.c_int, [vp, vp]),
@@ -240,6 +283,79 @@ def poetx_linear_bwd(desc, g_y, x, W0, R_f32, P_f32, R_act, P_act, z_saved, g_x,
     if raw:
         return st
     _check(st, "poetx_linear_bwd")
+
+
+def make_dense_desc(tokens, d_in, d_out, act, activation=POETX_ACT_NONE,
+                    w_scale=None) -> DenseDesc:
+    return DenseDesc(tokens, d_in, d_out, act, activation, 0, 0, _ptr(w_scale))
+
+
+def poetx_dense_fwd_workspace_size(desc: DenseDesc) -> int:
+    return _lib.poetx_dense_fwd_workspace_size(desc)
+
+
+def poetx_dense_bwd_workspace_size(desc: DenseDesc) -> int:
+    return _lib.poetx_dense_bwd_workspace_size(desc)
+
+
+def poetx_dense_fwd(desc, x, W, bias, residual, y, u_save, ws, stream=None, raw=False):
+    st = _lib.poetx_dense_fwd(desc, _ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(y),
+                              _ptr(u_save), _ptr(ws), _nbytes(ws), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_dense_fwd")
+
+
+def poetx_dense_bwd(desc, g_y, x, W, u_saved, g_x, g_W, g_bias, ws, stream=None, raw=False):
+    st = _lib.poetx_dense_bwd(desc, _ptr(g_y), _ptr(x), _ptr(W), _ptr(u_saved), _ptr(g_x),
+                              _ptr(g_W), _ptr(g_bias), _ptr(ws), _nbytes(ws), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_dense_bwd")
+
+
+_GRAD_DTYPE = {torch.float32: POETX_F32, torch.bfloat16: POETX_BF16}
+
+
+def make_grad_list(grads, outs=None) -> array.array:
+    """The GradTensor records (four 64-bit words each: dtype fills the low
+    half of the last) of contiguous float32 and bfloat16 tensors; outs: where
+    the clipped values go (default: in place)."""
+    words = []
+    for g, o in zip(grads, grads if outs is None else outs):
+        if not (g.is_contiguous() and o.is_contiguous()):
+            raise ValueError("libpoetx takes contiguous tensors")
+        words += (g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_DTYPE[g.dtype])
+    return array.array("Q", words)
+
+
+def poetx_grad_workspace_size(count: int) -> int:
+    return _lib.poetx_grad_workspace_size(count)
+
+
+def poetx_grad_norm(tensors, norm, ws, stream=None, raw=False):
+    at, words = tensors.buffer_info()
+    st = _lib.poetx_grad_norm(at, words // 4, _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_grad_norm")
+
+
+def poetx_grad_clip(tensors, max_norm, norm, ws, stream=None, raw=False):
+    at, words = tensors.buffer_info()
+    st = _lib.poetx_grad_clip(at, words // 4, max_norm, _ptr(norm), _ptr(ws), _nbytes(ws),
+                              _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_grad_clip")
+
+
+def poetx_grad_scale(tensors, max_norm, norm, stream=None, raw=False):
+    at, words = tensors.buffer_info()
+    st = _lib.poetx_grad_scale(at, words // 4, max_norm, _ptr(norm), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_grad_scale")
 
 
 class Event:
