@@ -58,7 +58,7 @@ template <typename T, Activation ACT>
 __global__ void __launch_bounds__(NT)
 act_grad_kernel(const T* __restrict__ g_y, const T* __restrict__ u, const float* __restrict__ scale,
                 T* __restrict__ g_u, float* __restrict__ part, int64_t rows, int d,
-                int rows_per_split) {
+                int rows_per_split, int gu_tiled) {
   constexpr int E = Vec<T>::E;
   const int vec = threadIdx.x & (kVecs - 1), lane = threadIdx.x / kVecs;
   const int n = (blockIdx.x * kVecs + vec) * E;
@@ -86,7 +86,7 @@ act_grad_kernel(const T* __restrict__ g_y, const T* __restrict__ u, const float*
       if (g_u) {
 #pragma unroll
         for (int e = 0; e < E; ++e) g[e] *= sc[e];
-        Vec<T>::store(g_u + at, g);
+        Vec<T>::store(g_u + (gu_tiled ? tiled_offset(r, n, d) : at), g);
       }
     }
   }
@@ -120,7 +120,8 @@ hipError_t launch_typed(const ActGrad& a, float* part, hipStream_t s) {
   case Activation::A:                                                                         \
     hipLaunchKernelGGL((act_grad_kernel<T, Activation::A>), grid, dim3(NT), 0, s,             \
                        static_cast<const T*>(a.g_y), static_cast<const T*>(a.u), a.scale,     \
-                       static_cast<T*>(a.g_u), part, a.rows, a.d, rows_per_split(a.rows));    \
+                       static_cast<T*>(a.g_u), part, a.rows, a.d, rows_per_split(a.rows),     \
+                       (int)a.gu_tiled);                                                     \
     break;
   switch (a.act) {
     POETX_ACT_GRAD(None)
@@ -141,6 +142,8 @@ int act_grad_splits(int64_t rows) {
 }
 
 hipError_t launch_act_grad(DType t, const ActGrad& a, hipStream_t s) {
+  if (a.gu_tiled && (t != DType::BF16 || a.rows % kTileRows != 0 || a.d % kTileCols != 0))
+    return hipErrorInvalidValue;
   const int nsplit = act_grad_splits(a.rows);
   float* part = !a.g_bias ? nullptr : nsplit == 1 ? a.g_bias : a.part;
   hipError_t e = t == DType::BF16 ? launch_typed<bf16_t>(a, part, s) : launch_typed<float>(a, part, s);

@@ -51,21 +51,32 @@ size_t widened_bytes(const poetx_dense_desc* d) {
   return int8_weight(d) ? align_up((size_t)d->d_out * d->d_in * act_size(d->act)) : 0;
 }
 
+// Whether an M x N product of K-major A takes the dense kernel's 256 x 256
+// tiles rather than the tile kernel's.
+bool use_dense(DType t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc) {
+  return t == DType::BF16 && poetx::dense_supported(M, N, K, lda, ldb, ldc) &&
+         ceil_div(M, 256) * ceil_div(N, 256) >= 128;
+}
+
 struct FwdPlan {
   TilePlan tile;
+  bool dense, w_tiled;
   size_t wq, part, total;
 };
 FwdPlan plan_fwd(const poetx_dense_desc* d) {
   FwdPlan p;
+  p.dense = use_dense(dtype_of(d), d->tokens, d->d_out, d->d_in, d->d_in, d->d_in, d->d_out);
+  p.w_tiled = p.dense && int8_weight(d) && d->d_out % poetx::kTileRows == 0;
   p.tile = poetx::plan_tile_product(dtype_of(d), d->tokens, d->d_out, d->d_in);
   p.wq = 0;
   p.part = widened_bytes(d);
-  p.total = p.part + align_up(p.tile.part_floats * sizeof(float));
+  p.total = p.part + (p.dense ? 0 : align_up(p.tile.part_floats * sizeof(float)));
   return p;
 }
 
 struct BwdPlan {
   TilePlan gx, gw;
+  bool dense;  // g_x on the dense kernel
   size_t gu, bias, wq, part, total;
 };
 // whether the products take g_u from the workspace (else g_y is g_u)
@@ -75,7 +86,9 @@ bool forms_gu(const poetx_dense_desc* d) {
 BwdPlan plan_bwd(const poetx_dense_desc* d) {
   BwdPlan p;
   const DType t = dtype_of(d);
+  p.dense = use_dense(t, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in, d->d_in);
   p.gx = poetx::plan_tile_product(t, d->tokens, d->d_in, d->d_out);
+  if (p.dense) p.gx.part_floats = 0;
   p.gw = poetx::plan_tile_product(t, d->d_out, d->d_in, d->tokens);
   size_t off = 0;
   p.gu = off;
@@ -142,21 +155,33 @@ int poetx_dense_fwd(const poetx_dense_desc* d, const void* x, const void* W, con
   const void* B = W;
   if (int8_weight(d)) {
     POETX_TRY(poetx::launch_widen_codes(t, static_cast<const int8_t*>(W), d->d_out, d->d_in,
-                                        d->d_in, w + plan.wq, false, s));
+                                        d->d_in, w + plan.wq, plan.w_tiled, s));
     B = w + plan.wq;
+  }
+  poetx::Epilogue ep;
+  ep.scale = d->w_scale;
+  ep.bias = bias;
+  ep.residual = residual;
+  ep.y = y;
+  ep.u = u_save;
+  ep.ld = d->d_out;
+  ep.act = d->activation;
+  if (plan.dense) {
+    poetx::DenseProduct p;
+    p.A = x; p.lda = d->d_in;
+    p.B = B; p.ldb = d->d_in;
+    p.M = (int)d->tokens; p.N = (int)d->d_out; p.K = (int)d->d_in;
+    p.b_tiled = plan.w_tiled;
+    p.ep = ep;
+    POETX_TRY(poetx::launch_dense_epilogue(p, s));
+    return POETX_OK;
   }
   TileProduct p;
   p.A = x; p.lda = d->d_in;
   p.B = B; p.ldb = d->d_in;
   p.M = (int)d->tokens; p.N = (int)d->d_out; p.K = (int)d->d_in;
   p.part = reinterpret_cast<float*>(w + plan.part);
-  p.ep.scale = d->w_scale;
-  p.ep.bias = bias;
-  p.ep.residual = residual;
-  p.ep.y = y;
-  p.ep.u = u_save;
-  p.ep.ld = d->d_out;
-  p.ep.act = d->activation;
+  p.ep = ep;
   POETX_TRY(poetx::launch_tile_product(t, plan.tile, p, true, true, s));
   return POETX_OK;
 }
@@ -188,6 +213,8 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
   const bool products = g_x || g_W;
+  const bool gu_tiled = plan.dense && forms_gu(d) && g_x && !g_W &&
+                        d->tokens % poetx::kTileRows == 0;
   const void* gu = g_y;
   if ((forms_gu(d) && products) || g_bias) {
     poetx::ActGrad a;
@@ -200,6 +227,9 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
     a.rows = d->tokens;
     a.d = (int)d->d_out;
     a.act = static_cast<Activation>(d->activation);
+    // (the tiled layout is the dense kernel's fastest; g_W's product does not
+    // read it, nor does K % 32 != 0 reach the dense kernel)
+    a.gu_tiled = gu_tiled;
     POETX_TRY(poetx::launch_act_grad(t, a, s));
     if (a.g_u) gu = a.g_u;
   }
@@ -210,14 +240,19 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
                                           d->d_in, w + plan.wq, false, s));
       B = w + plan.wq;
     }
-    TileProduct p;
-    p.A = gu; p.lda = d->d_out;
-    p.B = B; p.ldb = d->d_in;
-    p.M = (int)d->tokens; p.N = (int)d->d_in; p.K = (int)d->d_out;
-    p.part = reinterpret_cast<float*>(w + plan.part);
-    p.ep.y = g_x;
-    p.ep.ld = d->d_in;
-    POETX_TRY(poetx::launch_tile_product(t, plan.gx, p, true, false, s));
+    if (plan.dense) {
+      POETX_TRY(poetx::launch_dense(gu, B, g_x, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in,
+                                    d->d_in, false, gu_tiled, false, s));
+    } else {
+      TileProduct p;
+      p.A = gu; p.lda = d->d_out;
+      p.B = B; p.ldb = d->d_in;
+      p.M = (int)d->tokens; p.N = (int)d->d_in; p.K = (int)d->d_out;
+      p.part = reinterpret_cast<float*>(w + plan.part);
+      p.ep.y = g_x;
+      p.ep.ld = d->d_in;
+      POETX_TRY(poetx::launch_tile_product(t, plan.gx, p, true, false, s));
+    }
   }
   if (g_W) {  // g_W = g_u^T x: A(m, k) = g_u[k][m], B(n, k) = x[k][n]
     TileProduct p;

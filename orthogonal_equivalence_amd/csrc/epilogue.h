@@ -101,11 +101,14 @@ template <> struct Quad<bf16_t> {
     v[2] = __uint_as_float(w.y << 16);
     v[3] = __uint_as_float(w.y & 0xffff0000u);
   }
-  static __device__ __forceinline__ void store(bf16_t* p, const float v[4]) {
+  static __device__ __forceinline__ uint2 pack(const float v[4]) {
     union { bf16_t h[4]; uint2 w; } o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o.h[e] = f32_to_bf16(v[e]);
-    *reinterpret_cast<uint2*>(p) = o.w;
+    return o.w;
+  }
+  static __device__ __forceinline__ void store(bf16_t* p, const float v[4]) {
+    *reinterpret_cast<uint2*>(p) = pack(v);
   }
 };
 template <> struct Quad<float> {

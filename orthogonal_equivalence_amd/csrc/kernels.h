@@ -87,6 +87,8 @@ static_assert(kTileRows == 256 && kTileCols == 32, "tiled_offset's shifts");
 // the tiled layout (M % 256 == 0 and lda == K, else hipErrorInvalidValue);
 // with b_tiled, a K-major B is (an N x K matrix: N % 256 == 0, ldb == K).
 bool dense_supported(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc);
+// Workgroups of the persistent kernel for an M x N output on this device.
+hipError_t dense_grid(int64_t M, int64_t N, int* grid_out);
 hipError_t launch_dense(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
                         int64_t lda, int64_t ldb, int64_t ldc, bool b_kmajor, bool a_tiled,
                         bool b_tiled, hipStream_t s);
@@ -253,6 +255,19 @@ TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K);
 hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
                                bool b_kmajor, hipStream_t s);
 
+// The same with A and B K-major bf16 on the dense kernel's 256 x 256 tile
+// loop, where dense_supported(M, N, K, lda, ldb, ep.ld) holds; B tiled as in
+// launch_dense.
+struct DenseProduct {
+  const void* A = nullptr;
+  const void* B = nullptr;
+  int64_t lda = 0, ldb = 0;
+  int M = 0, N = 0, K = 0;
+  bool b_tiled = false;
+  Epilogue ep;
+};
+hipError_t launch_dense_epilogue(const DenseProduct& p, hipStream_t s);
+
 // g_u = g_y act'(u) (times scale[n] where g_u is stored) and g_bias = its
 // column sums over the rows; g_u and g_bias may be null, u with no
 // activation. d a multiple of 16 bytes. part: act_grad_splits(rows) * d
@@ -267,6 +282,7 @@ struct ActGrad {
   int64_t rows = 0;
   int d = 0;
   Activation act = Activation::None;
+  bool gu_tiled = false;  // g_u in the tiled layout (bf16, rows % 256 == 0, d % 32 == 0)
 };
 int act_grad_splits(int64_t rows);
 hipError_t launch_act_grad(DType t, const ActGrad& a, hipStream_t s);
