@@ -20,9 +20,9 @@ namespace poetx {
 namespace {
 
 constexpr int NT = 256, kVecs = 32, kLanes = NT / kVecs;
-// rows of one range: short sums and many workgroups; more only where the
-// ranges would pass the grid's limit
-constexpr int kRows = 64, kMaxSplits = 32768;
+// rows of one range: four a thread, all of whose loads are in flight at once,
+// and many workgroups; more only where the ranges would pass the grid's limit
+constexpr int kRows = 4 * kLanes, kMaxSplits = 32768;
 int rows_per_split(int64_t rows) {
   return (int)(kRows * ((rows + (int64_t)kRows * kMaxSplits - 1) / ((int64_t)kRows * kMaxSplits)));
 }
@@ -71,22 +71,26 @@ act_grad_kernel(const T* __restrict__ g_y, const T* __restrict__ u, const float*
     float sc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) sc[e] = scale ? scale[n + e] : 1.0f;
-#pragma unroll 4
-    for (int64_t r = r0 + lane; r < r1; r += kLanes) {
-      const int64_t at = r * d + n;
-      float g[E], w[E];
-      Vec<T>::load(g_y + at, g);
-      if constexpr (ACT != Activation::None) {
-        Vec<T>::load(u + at, w);
+    for (int64_t r = r0 + lane; r < r1; r += 4 * kLanes) {
+      float g[4][E], w[4][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] *= activation_slope<ACT>(w[e]);
+      for (int q = 0; q < 4; ++q) {
+        // (rows past the end are read as the last one and left out below)
+        const int64_t at = min(r + q * kLanes, rows - 1) * d + n;
+        Vec<T>::load(g_y + at, g[q]);
+        if constexpr (ACT != Activation::None) Vec<T>::load(u + at, w[q]);
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum[e] += g[e];
-      if (g_u) {
+      for (int q = 0; q < 4; ++q) {
+        const int64_t rq = r + q * kLanes;
+        if (rq >= r1) break;
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] *= sc[e];
-        Vec<T>::store(g_u + (gu_tiled ? tiled_offset(r, n, d) : at), g);
+        for (int e = 0; e < E; ++e) {
+          if constexpr (ACT != Activation::None) g[q][e] *= activation_slope<ACT>(w[q][e]);
+          sum[e] += g[q][e];
+          g[q][e] *= sc[e];
+        }
+        if (g_u) Vec<T>::store(g_u + (gu_tiled ? tiled_offset(rq, n, d) : rq * d + n), g[q]);
       }
     }
   }
@@ -104,13 +108,28 @@ act_grad_kernel(const T* __restrict__ g_y, const T* __restrict__ u, const float*
   }
 }
 
+// 64 columns a workgroup; its four waves take every fourth range, eight loads
+// in flight each, and are joined in wave order
 __global__ void __launch_bounds__(NT)
 bias_reduce_kernel(const float* __restrict__ part, int nsplit, int d, float* __restrict__ g_bias) {
-  const int n = blockIdx.x * NT + threadIdx.x;
-  if (n >= d) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = blockIdx.x * 64 + lane;
   double t = 0.0;
-  for (int s = 0; s < nsplit; ++s) t += (double)part[(int64_t)s * d + n];
-  g_bias[n] = (float)t;
+  if (n < d) {
+    const float* p = part + n;
+    for (int s = wave; s < nsplit; s += 32) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = p[(int64_t)min(s + 4 * q, nsplit - 1) * d];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t += s + 4 * q < nsplit ? (double)v[q] : 0.0;
+    }
+  }
+  __shared__ double sums[NT / 64][64];
+  sums[wave][lane] = t;
+  __syncthreads();
+  if (wave == 0 && n < d)
+    g_bias[n] = (float)(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane]);
 }
 
 template <typename T>
@@ -148,7 +167,7 @@ hipError_t launch_act_grad(DType t, const ActGrad& a, hipStream_t s) {
   float* part = !a.g_bias ? nullptr : nsplit == 1 ? a.g_bias : a.part;
   hipError_t e = t == DType::BF16 ? launch_typed<bf16_t>(a, part, s) : launch_typed<float>(a, part, s);
   if (e != hipSuccess || !a.g_bias || nsplit == 1) return e;
-  hipLaunchKernelGGL(bias_reduce_kernel, dim3((a.d + NT - 1) / NT), dim3(NT), 0, s, part, nsplit,
+  hipLaunchKernelGGL(bias_reduce_kernel, dim3((a.d + 63) / 64), dim3(NT), 0, s, part, nsplit,
                      a.d, a.g_bias);
   return hipGetLastError();
 }

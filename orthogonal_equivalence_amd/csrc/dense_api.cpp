@@ -52,10 +52,14 @@ size_t widened_bytes(const poetx_dense_desc* d) {
 }
 
 // Whether an M x N product of K-major A takes the dense kernel's 256 x 256
-// tiles rather than the tile kernel's.
-bool use_dense(DType t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc) {
-  return t == DType::BF16 && poetx::dense_supported(M, N, K, lda, ldb, ldc) &&
-         ceil_div(M, 256) * ceil_div(N, 256) >= 128;
+// tiles rather than the tile kernel's: by the same estimate of rounds times
+// steps (1.38 us a round and 64 k, 6 us for a round's epilogue, measured at
+// 4096 x 4096 x 4096).
+bool use_dense(DType t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
+               const TilePlan& tile) {
+  if (t != DType::BF16 || !poetx::dense_supported(M, N, K, lda, ldb, ldc)) return false;
+  const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), 256);
+  return (float)rounds * (1.38f * (float)K / 64 + 6.0f) < tile.cost;
 }
 
 struct FwdPlan {
@@ -65,9 +69,9 @@ struct FwdPlan {
 };
 FwdPlan plan_fwd(const poetx_dense_desc* d) {
   FwdPlan p;
-  p.dense = use_dense(dtype_of(d), d->tokens, d->d_out, d->d_in, d->d_in, d->d_in, d->d_out);
-  p.w_tiled = p.dense && int8_weight(d) && d->d_out % poetx::kTileRows == 0;
   p.tile = poetx::plan_tile_product(dtype_of(d), d->tokens, d->d_out, d->d_in);
+  p.dense = use_dense(dtype_of(d), d->tokens, d->d_out, d->d_in, d->d_in, d->d_in, d->d_out, p.tile);
+  p.w_tiled = p.dense && int8_weight(d) && d->d_out % poetx::kTileRows == 0;
   p.wq = 0;
   p.part = widened_bytes(d);
   p.total = p.part + (p.dense ? 0 : align_up(p.tile.part_floats * sizeof(float)));
@@ -86,8 +90,8 @@ bool forms_gu(const poetx_dense_desc* d) {
 BwdPlan plan_bwd(const poetx_dense_desc* d) {
   BwdPlan p;
   const DType t = dtype_of(d);
-  p.dense = use_dense(t, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in, d->d_in);
   p.gx = poetx::plan_tile_product(t, d->tokens, d->d_in, d->d_out);
+  p.dense = use_dense(t, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in, d->d_in, p.gx);
   if (p.dense) p.gx.part_floats = 0;
   p.gw = poetx::plan_tile_product(t, d->d_out, d->d_in, d->tokens);
   size_t off = 0;

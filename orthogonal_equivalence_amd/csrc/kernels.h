@@ -247,9 +247,10 @@ struct TileProduct {
   Epilogue ep;
 };
 struct TilePlan {
-  bool big;  // 128 x 128 tiles (else 64 x 64)
+  int shape;  // of the type's tile shapes
   int nsplit, kchunk;
   size_t part_floats;
+  float cost;  // estimate in us, for comparison with another kernel's
 };
 TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K);
 hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,

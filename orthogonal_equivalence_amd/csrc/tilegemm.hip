@@ -1,5 +1,5 @@
 // Matrix products of the dense linear with its epilogue, for any number of
-// rows: one workgroup of four waves computes a BM x BN tile of
+// rows: one workgroup of four or eight waves computes a BM x BN tile of
 //   C(m, n) = sum_k A(m, k) B(n, k),
 //   A(m, k) = A[m lda + k] (K-major) or A[k lda + m] (M-major), B likewise,
 // and ends with the float32 accumulators in registers, so that scale, bias,
@@ -9,9 +9,11 @@
 // epilogue.
 //
 // The reduction runs in steps of 128 bytes (64 bf16, 32 float32) through a
-// ring of kStages LDS slots filled by global_load_lds_dwordx4, kStages - 1
-// steps ahead: at the mid sizes this kernel serves (a few tiles per CU, often
-// one) nothing else hides the latency of the loads. Rows past the end are
+// ring of NS LDS slots filled by global_load_lds_dwordx4, NS - 1 steps ahead: at
+// the mid sizes this kernel serves (a few tiles per CU, often one) nothing
+// else hides the latency of the loads. The fragments of one half step are
+// read while the products of the other run (read, then multiply, in turn took
+// 1400 cycles a step of 128 x 128 tiles whose products take 512). Rows past the end are
 // read as the last row and never stored; a last step that is not full is
 // zeroed in LDS past its end, in both operands.
 //
@@ -28,6 +30,8 @@
 // chunks, so the order of k inside a step of 16 differs from memory order in
 // the same way for both.
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "common.h"
 #include "epilogue.h"
@@ -59,45 +63,72 @@ template <typename T, int ROWS> __device__ __forceinline__ int mn_swz(int k) {
   return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;  // (k & 1 picks the half of the banks)
 }
 
-// One operand's tile: ROWS rows (m or n), one step of k.
-template <typename T, int ROWS, bool KMAJ>
+// (wave-uniform by construction; said so for the scalar registers)
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// One global_load_lds_dwordx4 in the scalar-base form: lane l copies the 16
+// bytes at sbase + voff into LDS at m0 + 16 l.
+__device__ __forceinline__ void dma16_at(const char* sbase, uint32_t voff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(m0)), "v"(voff), "s"(uniform(sbase))
+               : "memory", "m0");
+}
+
+// One operand's tile: ROWS rows (m or n), one step of k; NW waves share its
+// copies. The lanes' byte offsets within a step's panel are formed once; a
+// step moves the scalar base only.
+template <typename T, int ROWS, bool KMAJ, int NW>
 struct Operand {
   static constexpr int E = Elem<T>::E, BK = Elem<T>::BK;
   static constexpr int BYTES = ROWS * kRowBytes;
-  static constexpr int PIECES = BYTES / 1024 / 4;  // 1 KB copies per wave and step
-  static constexpr int CPR = ROWS / E;             // chunks per k row (MN-major)
-  static_assert(PIECES >= 1, "a tile is at least 4 KB");
+  static constexpr int PIECES = BYTES / 1024 / NW;  // 1 KB copies per wave and step
+  static constexpr int CPR = ROWS / E;              // chunks per k row (MN-major)
+  static_assert(PIECES >= 1, "every wave copies");
 
-  const T* base;  // K-major: row r0; MN-major: column r0
-  int64_t ld;
-  int rows, K;  // rows of the operand from r0 on; whole reduction length
+  const char* base;  // K-major: row r0, k = 0; MN-major: column r0, k = 0
+  int64_t step;      // bytes between steps
+  int64_t ld;        // elements
+  int rows, K;       // rows of the operand from r0 on; whole reduction length
+  uint32_t off[PIECES];
 
-  __device__ __forceinline__ void init(const T* p, int64_t ld_, int r0, int total, int K_) {
+  // 16-byte chunk c16 of the tile (LDS order) in the step at k0: its byte
+  // offset from the step's panel, rows and k clamped into the operand
+  __device__ __forceinline__ uint32_t offset(int c16, int k0) const {
+    if (KMAJ) {
+      const int r = c16 >> 3, c = (c16 & 7) ^ k_swz(r);
+      return (uint32_t)(min(r, rows - 1) * (int)ld + min(c * E, K - E - k0)) * (uint32_t)sizeof(T);
+    }
+    const int k = c16 / CPR, c = (c16 % CPR) ^ mn_swz<T, ROWS>(k);
+    return (uint32_t)(min(k, K - 1 - k0) * (int)ld + min(c * E, rows - E)) * (uint32_t)sizeof(T);
+  }
+  __device__ __forceinline__ void init(const T* p, int64_t ld_, int r0, int total, int K_, int wave,
+                                       int lane) {
     ld = ld_;
     K = K_;
     rows = total - r0;
-    base = KMAJ ? p + (int64_t)r0 * ld : p + r0;
-  }
-  // this wave's copies of step k0 into `slot`
-  __device__ __forceinline__ void issue(char* slot, int k0, int wave, int lane) const {
+    base = reinterpret_cast<const char*>(KMAJ ? p + (int64_t)r0 * ld : p + r0);
+    step = (KMAJ ? (int64_t)BK : (int64_t)BK * ld) * sizeof(T);
+    // (of a full step: issue() forms a cut one itself)
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j) {
-      const int q = wave + 4 * j;
-      const int c16 = q * 64 + lane;  // 16-byte chunk of the tile, in LDS order
-      const T* src;
-      if (KMAJ) {
-        const int r = c16 >> 3, c = (c16 & 7) ^ k_swz(r);
-        src = base + (int64_t)min(r, rows - 1) * ld + min(k0 + c * E, K - E);
-      } else {
-        const int k = c16 / CPR, c = (c16 % CPR) ^ mn_swz<T, ROWS>(k);
-        src = base + (int64_t)min(k0 + k, K - 1) * ld + min(c * E, rows - E);
-      }
-      dma16(src, reinterpret_cast<const bf16_t*>(slot + q * 1024));
-    }
+    for (int j = 0; j < PIECES; ++j) off[j] = offset((wave + NW * j) * 64 + lane, min(0, K - BK));
+  }
+  // copy J of this wave for step t (k0 = t BK) into the slot at LDS byte
+  // `lds`; FULL: the step is known to be
+  template <bool FULL, int J>
+  __device__ __forceinline__ void issue(uint32_t lds, int t, int wave, int lane) const {
+    const int q = wave + NW * J;
+    const bool cut = !FULL && (t + 1) * BK > K;  // the operand's last step, not full
+    dma16_at(base + t * step, cut ? offset(q * 64 + lane, t * BK) : off[J], lds + q * 1024);
   }
   // zeros from k = kleft on (the whole workgroup)
   __device__ __forceinline__ void zero_tail(char* slot, int kleft, int tid) const {
-    for (int c16 = tid; c16 < BYTES / 16; c16 += NT) {
+    for (int c16 = tid; c16 < BYTES / 16; c16 += 64 * NW) {
       bool out;
       if (KMAJ) {
         const int r = c16 >> 3, c = (c16 & 7) ^ k_swz(r);
@@ -140,29 +171,52 @@ struct Operand {
   }
 };
 
-__device__ __forceinline__ floatx4 mma(bf16x8_t a, bf16x8_t b, floatx4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+// c += a b in VGPRs. Inline asm because with one workgroup per CU the compiler
+// otherwise keeps the accumulators in AGPRs and copies them between the half
+// steps. It does not see these as matrix instructions: settle() stands
+// between them and any other use of their registers.
+// mma<J>: product J of a fragment pair (bf16 has one, float32 four).
+template <int J> __device__ __forceinline__ void mma(const bf16x8_t& a, const bf16x8_t& b, floatx4& c) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ floatx4 mma(floatx4 a, floatx4 b, floatx4 c) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
-  return c;
+template <int J> __device__ __forceinline__ void mma(const floatx4& a, const floatx4& b, floatx4& c) {
+  asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+v"(c) : "v"(a[J]), "v"(b[J]));
+}
+// wait states between VALU writes (of operands, accumulators or EXEC) and the
+// products that read them, and between products and VALU reads of their
+// results: more than any 16 x 16 product needs
+__device__ __forceinline__ void settle_before() { asm volatile("s_nop 4" ::: "memory"); }
+__device__ __forceinline__ void settle_after() {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 }
 
-// at most `n` steps of LPW copies still in flight
+// (lambdas of the unrolled loop: a call would put the fragments into scratch)
+#define POETX_INLINE __attribute__((always_inline))
+
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>)
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_of(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F> __device__ __forceinline__ void for_each(F&& f) {
+  for_each_of(std::make_integer_sequence<int, N>{}, f);
+}
+
+// until at most `n` steps of LPW copies are in flight
 template <int LPW, int NS> __device__ __forceinline__ void wait_steps(int n) {
-  static_assert(NS >= 2 && NS <= 4, "ring depth");
+  static_assert(NS >= 3 && NS <= 4, "ring depth");
   if (NS > 3 && n >= 2) wait_vm<2 * LPW>();
-  else if (NS > 2 && n >= 1) wait_vm<LPW>();
+  else if (n >= 1) wait_vm<LPW>();
   else wait_vm<0>();
 }
 
-template <typename T, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int NS>
-__global__ void __launch_bounds__(NT) tile_kernel(const TileProduct p) {
-  typedef Operand<T, BM, A_KMAJ> OpA;
-  typedef Operand<T, BN, B_KMAJ> OpB;
+template <typename T, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS>
+__global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct p) {
+  constexpr int NW = WM * WN;
+  typedef Operand<T, BM, A_KMAJ, NW> OpA;
+  typedef Operand<T, BN, B_KMAJ, NW> OpB;
   constexpr int BK = Elem<T>::BK;
-  constexpr int TM = BM / 2, TN = BN / 2;  // 2 x 2 waves
+  constexpr int TM = BM / WM, TN = BN / WN;
   constexpr int FM = TM / 16, FN = TN / 16;
   constexpr int SLOT = OpA::BYTES + OpB::BYTES;
   constexpr int LPW = OpA::PIECES + OpB::PIECES;
@@ -170,17 +224,20 @@ __global__ void __launch_bounds__(NT) tile_kernel(const TileProduct p) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % WM, wn = wave / WM;
   int mt, nt;
   xcd_grouped_tile((p.M + BM - 1) / BM, (p.N + BN - 1) / BN, mt, nt);
-  const int m0 = mt * BM, n0 = nt * BN;
-  const int kbeg = blockIdx.y * p.kchunk, kend = min(p.K, kbeg + p.kchunk);
-  const int steps = (kend - kbeg + BK - 1) / BK;
+  const int m0 = __builtin_amdgcn_readfirstlane(mt * BM);
+  const int n0 = __builtin_amdgcn_readfirstlane(nt * BN);
+  const int t0 = blockIdx.y * (p.kchunk / BK);
+  const int steps = (min(p.K, (int)(blockIdx.y + 1) * p.kchunk) + BK - 1) / BK - t0;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)ring)));
 
   OpA oa;
   OpB ob;
-  oa.init(static_cast<const T*>(p.A), p.lda, m0, p.M, p.K);
-  ob.init(static_cast<const T*>(p.B), p.ldb, n0, p.N, p.K);
+  oa.init(static_cast<const T*>(p.A), p.lda, m0, p.M, p.K, wave, lane);
+  ob.init(static_cast<const T*>(p.B), p.ldb, n0, p.N, p.K, wave, lane);
 
   floatx4 acc[FM][FN];
 #pragma unroll
@@ -188,47 +245,115 @@ __global__ void __launch_bounds__(NT) tile_kernel(const TileProduct p) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-#pragma unroll
-  for (int t = 0; t < NS - 1; ++t)
-    if (t < steps) {
-      oa.issue(ring + t * SLOT, kbeg + t * BK, wave, lane);
-      ob.issue(ring + t * SLOT + OpA::BYTES, kbeg + t * BK, wave, lane);
-    }
-  int slot = 0;
-  for (int t = 0; t < steps; ++t) {
-    char* sa = ring + slot * SLOT;
-    char* sb = sa + OpA::BYTES;
-    // this wave's copies of step t have landed and its reads of step t - 1
-    // are done; after the barrier that holds for every wave
-    wait_steps<LPW, NS>(steps - 1 - t);
-    wait_lds();
-    barrier_nofence();
-    const int kleft = kend - kbeg - t * BK;
+  // zeros past the reduction's end where step t is not full
+  auto clear_tail = [&](int slot, int t) POETX_INLINE {
+    const int kleft = p.K - (t0 + t) * BK;
     if (kleft < BK) {
-      oa.zero_tail(sa, kleft, tid);
-      ob.zero_tail(sb, kleft, tid);
+      oa.zero_tail(ring + slot * SLOT, kleft, tid);
+      ob.zero_tail(ring + slot * SLOT + OpA::BYTES, kleft, tid);
       wait_lds();
       barrier_nofence();
     }
-    if (t + NS - 1 < steps) {  // into the slot of step t - 1
-      char* nx = ring + (slot == 0 ? NS - 1 : slot - 1) * SLOT;
-      oa.issue(nx, kbeg + (t + NS - 1) * BK, wave, lane);
-      ob.issue(nx + OpA::BYTES, kbeg + (t + NS - 1) * BK, wave, lane);
+  };
+
+  typename Elem<T>::Frag fa[2][FM], fb[2][FN];
+  // copy J (of LPW) of step t into `slot`
+  auto issue = [&](int slot, int t, auto piece, auto full) POETX_INLINE {
+    constexpr int J = decltype(piece)::value;
+    constexpr bool kFull = decltype(full)::value;
+    if constexpr (J < OpA::PIECES)
+      oa.template issue<kFull, J>(lds0 + slot * SLOT, t0 + t, wave, lane);
+    else if constexpr (J < LPW)
+      ob.template issue<kFull, J - OpA::PIECES>(lds0 + slot * SLOT + OpA::BYTES, t0 + t, wave,
+                                                lane);
+  };
+  auto issue_all = [&](int slot, int t) POETX_INLINE {
+    for_each<LPW>([&](auto j) POETX_INLINE { issue(slot, t, j, std::false_type{}); });
+  };
+  auto read = [&](int slot, auto half) POETX_INLINE {
+    constexpr int H = decltype(half)::value;
+    const char* sa = ring + slot * SLOT;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[H][i] = oa.read(sa, wm * TM + 16 * i, H, lane);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[H][j] = ob.read(sa + OpA::BYTES, wn * TN + 16 * j, H, lane);
+  };
+  // the products of one half step, after(r) behind fragment row r (float32:
+  // product by product over all pairs, so that no two in a row take the same
+  // accumulator)
+  auto products = [&](auto half, auto after) POETX_INLINE {
+    constexpr int H = decltype(half)::value;
+    settle_before();
+    for_each<FM>([&](auto r) POETX_INLINE {
+      constexpr int i = decltype(r)::value;
+      for_each<FN>([&](auto j) POETX_INLINE { mma<0>(fb[H][j], fa[H][i], acc[i][j]); });
+      after(r);
+    });
+    if constexpr (sizeof(T) == 4)
+      for_each<3 * FM * FN>([&](auto q) POETX_INLINE {
+        constexpr int e = decltype(q)::value / (FM * FN), ij = decltype(q)::value % (FM * FN);
+        mma<1 + e>(fb[H][ij % FN], fa[H][ij / FN], acc[ij / FN][ij % FN]);
+      });
+  };
+  constexpr std::integral_constant<int, 0> kFirst{};
+  constexpr std::integral_constant<int, 1> kSecond{};
+  constexpr int PER_ROW = (LPW + 2 * FM - 1) / (2 * FM);  // copies behind a row of products
+  constexpr int FIRST_HALF = PER_ROW * FM < LPW ? PER_ROW * FM : LPW;
+  // Step t, whose first half is in registers. Its slot's predecessor is free:
+  // step t + NS - 1 is copied into it, spread over the products, since a burst
+  // of copies would hold back the products behind it (in-order issue; the
+  // address unit takes 16 cycles a copy, for four waves at once). Half way
+  // the second half's fragments are in registers too; once this wave's copies
+  // of step t + 1 have landed, the barrier makes that hold for every wave.
+  // Steady: steps t + 1 .. t + NS - 1 exist and are full; nothing is tested.
+  auto step = [&](int slot, int t, auto steady) POETX_INLINE {
+    constexpr bool kSteady = decltype(steady)::value;
+    const int prev = slot == 0 ? NS - 1 : slot - 1;
+    const int next = slot + 1 == NS ? 0 : slot + 1;
+    auto behind = [&](auto half) POETX_INLINE {
+      return [&](auto r) POETX_INLINE {
+        if constexpr (kSteady) {
+          constexpr int row = decltype(half)::value * FM + decltype(r)::value;
+          for_each<PER_ROW>([&](auto c) POETX_INLINE {
+            issue(prev, t + NS - 1,
+                  std::integral_constant<int, row * PER_ROW + decltype(c)::value>{},
+                  std::true_type{});
+          });
+        }
+      };
+    };
+    read(slot, kSecond);
+    if (!kSteady && t + NS - 1 < steps) issue_all(prev, t + NS - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    products(kFirst, behind(kFirst));
+    __builtin_amdgcn_sched_barrier(0);
+    if (kSteady || t + 1 < steps) {
+      if constexpr (kSteady) wait_vm<(NS - 3) * LPW + FIRST_HALF>();
+      else wait_steps<LPW, NS>(min(NS - 2, steps - 2 - t));
+      wait_lds();
+      barrier_nofence();
+      if constexpr (!kSteady) clear_tail(next, t + 1);
+      read(next, kFirst);
     }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      typename Elem<T>::Frag fa[FM], fb[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = oa.read(sa, wm * TM + 16 * i, s, lane);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = ob.read(sb, wn * TN + 16 * j, s, lane);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mma(fb[j], fa[i], acc[i][j]);
-    }
-    slot = slot + 1 == NS ? 0 : slot + 1;
-  }
+    __builtin_amdgcn_sched_barrier(0);
+    products(kSecond, behind(kSecond));
+  };
+
+  for_each<NS - 1>([&](auto t) POETX_INLINE {
+    if (decltype(t)::value < steps) issue_all(decltype(t)::value, decltype(t)::value);
+  });
+  wait_steps<LPW, NS>(min(NS - 1, steps) - 1);
+  barrier_nofence();
+  clear_tail(0, 0);
+  read(0, kFirst);
+  int t = 0;
+  for (; t + 2 * NS - 1 < steps; t += NS)
+    for_each<NS>([&](auto q) POETX_INLINE { step(decltype(q)::value, t + decltype(q)::value, std::true_type{}); });
+  for (int slot = 0; t < steps; ++t, slot = slot + 1 == NS ? 0 : slot + 1)
+    step(slot, t, std::false_type{});
+  __builtin_amdgcn_sched_barrier(0);
+  settle_after();
+  __builtin_amdgcn_sched_barrier(0);
 
   // (operand roles swapped: lane l holds row 16 i + l % 16, columns
   // 16 j + 4 (l / 16) .. + 3 of its wave's tile)
@@ -259,9 +384,20 @@ finish_kernel(const float* __restrict__ part, int nsplit, int64_t rows, int N, E
     const int64_t m = i / quads;
     const int n = (int)(i - m * quads) * 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < nsplit; ++s) {
+    const float* p = part + m * N + n;
+    int s = 0;
+    for (; s + 4 <= nsplit; s += 4) {  // four loads in flight
+      float w[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) Quad<float>::load(p + (s + q) * stride, w[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += w[q][e];
+    }
+    for (; s < nsplit; ++s) {
       float w[4];
-      Quad<float>::load(part + s * stride + m * N + n, w);
+      Quad<float>::load(p + s * stride, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += w[e];
     }
@@ -269,42 +405,72 @@ finish_kernel(const float* __restrict__ part, int nsplit, int64_t rows, int N, E
   }
 }
 
-template <typename T, int BM, int BN, int NS>
+template <typename T, int BM, int BN, int WM, int WN, int NS>
 hipError_t launch_cfg(bool ak, bool bk, const TileProduct& p, int nsplit, hipStream_t s) {
   const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, nsplit);
+  const dim3 grid((unsigned)tiles, nsplit), block(64 * WM * WN);
   if (ak && bk)
-    hipLaunchKernelGGL((tile_kernel<T, BM, BN, true, true, NS>), grid, dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((tile_kernel<T, BM, BN, WM, WN, true, true, NS>), grid, block, 0, s, p);
   else if (ak)
-    hipLaunchKernelGGL((tile_kernel<T, BM, BN, true, false, NS>), grid, dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((tile_kernel<T, BM, BN, WM, WN, true, false, NS>), grid, block, 0, s, p);
   else if (!bk)
-    hipLaunchKernelGGL((tile_kernel<T, BM, BN, false, false, NS>), grid, dim3(NT), 0, s, p);
+    hipLaunchKernelGGL((tile_kernel<T, BM, BN, WM, WN, false, false, NS>), grid, block, 0, s, p);
   else
     return hipErrorInvalidValue;  // no caller has an M-major A with a K-major B
   return hipGetLastError();
 }
 
-int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) {
-  return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-}
+// The tile shapes, with what one step of 128 bytes of k costs on a CU (us,
+// measured on an MI355X over 512 .. 4096 x 4096 x 4096 products with every CU
+// busy; `alone`: with one workgroup on a CU that holds two).
+struct Shape {
+  int bm, bn, per_cu;
+  float step, alone;
+};
+constexpr Shape kBf16Shapes[] = {
+    {256, 128, 1, 1.03f, 1.03f}, {128, 128, 1, 0.59f, 0.59f}, {128, 64, 1, 0.41f, 0.41f},
+    {64, 64, 2, 0.47f, 0.28f}};
+// float32 is bound by its matrix rate (a 64 x 64 step is 1024 cycles of it),
+// so the smallest shape, which fills the chip most evenly, serves all sizes
+constexpr Shape kF32Shapes[] = {{64, 64, 2, 0.90f, 0.47f}};
+constexpr int kCus = 256;
+constexpr float kPartBytesPerUs = 4.0e6f;  // partial tiles, written and read
+constexpr float kFinishLaunch = 3.0f;      // us of the pass that joins them
 
 }  // namespace
 
+// Every shape and a few splits of the reduction, by rounds of workgroups
+// times steps times the step's cost, plus the partial tiles' traffic. What it
+// decides, measured: 777 x 2048 x 2048 128 x 64 tiles 15.1 us, 64 x 64 16.8,
+// 128 x 128 21.0; 1024 x 4096 x 4096 39 us on 128 x 128, 53 on 128 x 64, 56
+// on 256 x 128; 2048 x 4096 x 4096 69 us on 256 x 128, 75 on 128 x 128.
 TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K) {
-  const int bk = t == DType::BF16 ? 64 : 32;
-  TilePlan r;
-  r.big = tiles_of(M, N, 128, 128) >= 192;
-  const int64_t tiles = r.big ? tiles_of(M, N, 128, 128) : tiles_of(M, N, 64, 64);
-  int64_t split = 1;
-  if (tiles < 192) split = std::min<int64_t>((256 + tiles - 1) / tiles, K / (8 * bk));
-  split = std::max<int64_t>(1, split);
+  const bool bf16 = t == DType::BF16;
+  const Shape* shapes = bf16 ? kBf16Shapes : kF32Shapes;
+  const int nshapes = bf16 ? (int)(sizeof(kBf16Shapes) / sizeof(Shape)) : 1;
+  const int bk = bf16 ? 64 : 32;
   const int64_t steps = (K + bk - 1) / bk;
-  const int64_t per = (steps + split - 1) / split;
-  r.kchunk = (int)(per * bk);
-  r.nsplit = (int)((steps + per - 1) / per);
-  r.part_floats = r.nsplit > 1 ? (size_t)r.nsplit * M * N : 0;
-  return r;
+  TilePlan best = {};
+  best.cost = 1e30f;
+  for (int i = 0; i < nshapes; ++i) {
+    const Shape& h = shapes[i];
+    const int64_t tiles = ((M + h.bm - 1) / h.bm) * ((N + h.bn - 1) / h.bn);
+    for (int64_t want = 1; want <= 16; ++want) {
+      const int64_t per = (steps + want - 1) / want, split = (steps + per - 1) / per;
+      // (a split leaves at least eight steps to each part)
+      if (split != want || (split > 1 && per < 8)) continue;
+      const int64_t wgs = tiles * split, slots = (int64_t)kCus * h.per_cu;
+      const int64_t whole = wgs / slots, rest = wgs % slots;
+      float cost = (float)whole * per * h.step;
+      if (rest) cost += (float)per * (rest <= kCus ? h.alone : h.step);
+      if (split > 1) cost += kFinishLaunch + (float)(2 * split * M * N * 4) / kPartBytesPerUs;
+      if (cost < best.cost)
+        best = TilePlan{i, (int)split, (int)(per * bk),
+                        split > 1 ? (size_t)split * M * N : 0, cost};
+    }
+  }
+  return best;
 }
 
 hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
@@ -312,13 +478,17 @@ hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, boo
   p.kchunk = plan.kchunk;
   if (plan.nsplit == 1) p.part = nullptr;
   else if (!p.part) return hipErrorInvalidValue;
-  hipError_t e;
-  if (t == DType::BF16)
-    e = plan.big ? launch_cfg<bf16_t, 128, 128, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s)
-                 : launch_cfg<bf16_t, 64, 64, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s);
-  else
-    e = plan.big ? launch_cfg<float, 128, 128, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s)
-                 : launch_cfg<float, 64, 64, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s);
+  hipError_t e = hipErrorInvalidValue;
+  if (t == DType::F32) {
+    e = launch_cfg<float, 64, 64, 2, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s);
+  } else {
+    switch (plan.shape) {  // kBf16Shapes
+      case 0: e = launch_cfg<bf16_t, 256, 128, 4, 2, 3>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+      case 1: e = launch_cfg<bf16_t, 128, 128, 2, 4, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+      case 2: e = launch_cfg<bf16_t, 128, 64, 4, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+      case 3: e = launch_cfg<bf16_t, 64, 64, 2, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+    }
+  }
   if (e != hipSuccess || plan.nsplit == 1) return e;
   const int64_t groups = (int64_t)p.M * (p.N / 4);
   const int grid = (int)std::min<int64_t>((groups + NT - 1) / NT, 4096);
