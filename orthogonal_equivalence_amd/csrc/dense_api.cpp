@@ -51,29 +51,50 @@ size_t widened_bytes(const poetx_dense_desc* d) {
   return int8_weight(d) ? align_up((size_t)d->d_out * d->d_in * act_size(d->act)) : 0;
 }
 
-// Whether an M x N product of K-major A takes the dense kernel's 256 x 256
-// tiles rather than the tile kernel's: by the same estimate of rounds times
-// steps (1.38 us a round and 64 k, 6 us for a round's epilogue, measured at
-// 4096 x 4096 x 4096).
+// The dense kernel's time for an M x N x K product, as the tile kernel's plan
+// estimates its own: rounds of 256 x 256 tiles over the CUs (1.38 us a round
+// and 64 of k, 6 us for a round's epilogue, measured at 4096 x 4096 x 4096).
+float dense_cost(int64_t M, int64_t N, int64_t K) {
+  const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), 256);
+  return 3.0f + (float)rounds * (1.38f * (float)K / 64 + 6.0f);
+}
+// Whether an M x N product of K-major A takes that kernel.
 bool use_dense(DType t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                const TilePlan& tile) {
-  if (t != DType::BF16 || !poetx::dense_supported(M, N, K, lda, ldb, ldc)) return false;
-  const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), 256);
-  return (float)rounds * (1.38f * (float)K / 64 + 6.0f) < tile.cost;
+  return t == DType::BF16 && poetx::dense_supported(M, N, K, lda, ldb, ldc) &&
+         dense_cost(M, N, K) < tile.cost;
 }
+constexpr float kWidenLaunch = 3.0f, kWidenBytesPerUs = 4.5e6f;
 
 struct FwdPlan {
   TilePlan tile;
-  bool dense, w_tiled;
+  bool stream, dense;
+  bool widen, w_tiled;  // INT8 codes widened into the workspace (in the tiled layout)
   size_t wq, part, total;
 };
 FwdPlan plan_fwd(const poetx_dense_desc* d) {
-  FwdPlan p;
-  p.tile = poetx::plan_tile_product(dtype_of(d), d->tokens, d->d_out, d->d_in);
-  p.dense = use_dense(dtype_of(d), d->tokens, d->d_out, d->d_in, d->d_in, d->d_in, d->d_out, p.tile);
-  p.w_tiled = p.dense && int8_weight(d) && d->d_out % poetx::kTileRows == 0;
-  p.wq = 0;
-  p.part = widened_bytes(d);
+  FwdPlan p = {};
+  // few tokens: the weight read once, straight into the products
+  p.stream = d->tokens <= poetx::kStreamRows && !(int8_weight(d) && d->act == POETX_F32);
+  if (p.stream) return p;
+  const DType t = dtype_of(d);
+  const int64_t M = d->tokens, N = d->d_out, K = d->d_in;
+  p.tile = poetx::plan_tile_product(t, M, N, K, false);
+  p.dense = use_dense(t, M, N, K, K, K, N, p.tile);
+  p.widen = int8_weight(d);
+  if (int8_weight(d) && t == DType::BF16 && K % 16 == 0) {
+    // the tile kernel can take the codes themselves: worth it while widening
+    // them (a byte read, two written) costs more than the products gain
+    const TilePlan direct = poetx::plan_tile_product(t, M, N, K, true);
+    const float widened = (p.dense ? dense_cost(M, N, K) : p.tile.cost) + kWidenLaunch +
+                          (float)(3 * N * K) / kWidenBytesPerUs;
+    if (direct.cost < widened) {
+      p.tile = direct;
+      p.dense = p.widen = false;
+    }
+  }
+  p.w_tiled = p.dense && p.widen && N % poetx::kTileRows == 0;
+  p.part = p.widen ? widened_bytes(d) : 0;
   p.total = p.part + (p.dense ? 0 : align_up(p.tile.part_floats * sizeof(float)));
   return p;
 }
@@ -90,10 +111,10 @@ bool forms_gu(const poetx_dense_desc* d) {
 BwdPlan plan_bwd(const poetx_dense_desc* d) {
   BwdPlan p;
   const DType t = dtype_of(d);
-  p.gx = poetx::plan_tile_product(t, d->tokens, d->d_in, d->d_out);
+  p.gx = poetx::plan_tile_product(t, d->tokens, d->d_in, d->d_out, false);
   p.dense = use_dense(t, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in, d->d_in, p.gx);
   if (p.dense) p.gx.part_floats = 0;
-  p.gw = poetx::plan_tile_product(t, d->d_out, d->d_in, d->tokens);
+  p.gw = poetx::plan_tile_product(t, d->d_out, d->d_in, d->tokens, false);
   size_t off = 0;
   p.gu = off;
   if (forms_gu(d)) off += align_up((size_t)d->tokens * d->d_out * act_size(d->act));
@@ -156,12 +177,6 @@ int poetx_dense_fwd(const poetx_dense_desc* d, const void* x, const void* W, con
   const DType t = dtype_of(d);
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
-  const void* B = W;
-  if (int8_weight(d)) {
-    POETX_TRY(poetx::launch_widen_codes(t, static_cast<const int8_t*>(W), d->d_out, d->d_in,
-                                        d->d_in, w + plan.wq, plan.w_tiled, s));
-    B = w + plan.wq;
-  }
   poetx::Epilogue ep;
   ep.scale = d->w_scale;
   ep.bias = bias;
@@ -170,6 +185,21 @@ int poetx_dense_fwd(const poetx_dense_desc* d, const void* x, const void* W, con
   ep.u = u_save;
   ep.ld = d->d_out;
   ep.act = d->activation;
+  if (plan.stream) {
+    poetx::StreamProduct p;
+    p.x = x;
+    p.W = W;
+    p.M = (int)d->tokens; p.N = (int)d->d_out; p.K = (int)d->d_in;
+    p.ep = ep;
+    POETX_TRY(poetx::launch_stream_product(t, int8_weight(d), p, s));
+    return POETX_OK;
+  }
+  const void* B = W;
+  if (plan.widen) {
+    POETX_TRY(poetx::launch_widen_codes(t, static_cast<const int8_t*>(W), d->d_out, d->d_in,
+                                        d->d_in, w + plan.wq, plan.w_tiled, s));
+    B = w + plan.wq;
+  }
   if (plan.dense) {
     poetx::DenseProduct p;
     p.A = x; p.lda = d->d_in;
@@ -184,6 +214,7 @@ int poetx_dense_fwd(const poetx_dense_desc* d, const void* x, const void* W, con
   p.A = x; p.lda = d->d_in;
   p.B = B; p.ldb = d->d_in;
   p.M = (int)d->tokens; p.N = (int)d->d_out; p.K = (int)d->d_in;
+  p.b_int8 = int8_weight(d) && !plan.widen;
   p.part = reinterpret_cast<float*>(w + plan.part);
   p.ep = ep;
   POETX_TRY(poetx::launch_tile_product(t, plan.tile, p, true, true, s));

@@ -58,9 +58,12 @@ __device__ __forceinline__ int k_swz(int row) { return (row >> 1) & 7; }
 
 // chunk XOR of row k of an MN-major tile of ROWS elements per k
 template <typename T, int ROWS> __device__ __forceinline__ int mn_swz(int k) {
-  if constexpr (sizeof(T) == 4) return ((k >> 2) & 3) << 2;  // 64-byte pieces
+  static_assert(ROWS >= 32, "the XOR stays inside a row's chunks");
+  if constexpr (sizeof(T) == 4) return ((k >> 2) & (ROWS >= 64 ? 3 : 1)) << 2;  // 64-byte pieces
   if constexpr (ROWS >= 128) return ((k & 3) | (((k >> 3) & 1) << 2)) << 1;  // 32-byte pieces
-  return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;  // (k & 1 picks the half of the banks)
+  if constexpr (ROWS == 64)  // (k & 1 picks the half of the banks)
+    return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
+  return ((k >> 3) & 1) << 1;  // (k & 3 picks the quarter)
 }
 
 // (wave-uniform by construction; said so for the scalar registers)
@@ -90,6 +93,8 @@ struct Operand {
   static constexpr int PIECES = BYTES / 1024 / NW;  // 1 KB copies per wave and step
   static constexpr int CPR = ROWS / E;              // chunks per k row (MN-major)
   static_assert(PIECES >= 1, "every wave copies");
+  typedef typename Elem<T>::Frag Raw;  // a fragment as it is read
+  static __device__ __forceinline__ const Raw& widen(const Raw& r) { return r; }
 
   const char* base;  // K-major: row r0, k = 0; MN-major: column r0, k = 0
   int64_t step;      // bytes between steps
@@ -171,6 +176,64 @@ struct Operand {
   }
 };
 
+// The INT8 codes of a bf16 product's B, K-major, K a multiple of 16: a step's
+// 64 codes of a row are 64 bytes, 16-byte chunk c of row r at
+// c ^ ((r >> 1) & 3); widened in registers (code + 128 as an unsigned byte to
+// float32, less 128, to bf16, all exact).
+template <int ROWS, int NW>
+struct Operand<int8_t, ROWS, true, NW> {
+  static constexpr int BK = Elem<bf16_t>::BK;
+  static constexpr int BYTES = ROWS * 64;
+  static constexpr int PIECES = BYTES / 1024 / NW;
+  static_assert(PIECES >= 1, "every wave copies");
+  typedef uint2 Raw;
+  static __device__ __forceinline__ bf16x8_t widen(const Raw& r) {
+    union { bf16_t h[8]; bf16x8_t v; } o;
+    const uint32_t w[2] = {r.x ^ 0x80808080u, r.y ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o.h[i] = f32_to_bf16((float)((w[i >> 2] >> (8 * (i & 3))) & 0xffu) - 128.0f);
+    return o.v;
+  }
+
+  const char* base;
+  int64_t ld;
+  int rows, K;
+  uint32_t off[PIECES];
+
+  static __device__ __forceinline__ int swz(int row) { return (row >> 1) & 3; }
+  __device__ __forceinline__ uint32_t offset(int c16, int k0) const {
+    const int r = c16 >> 2, c = (c16 & 3) ^ swz(r);
+    return (uint32_t)(min(r, rows - 1) * (int)ld + min(c * 16, K - 16 - k0));
+  }
+  __device__ __forceinline__ void init(const int8_t* p, int64_t ld_, int r0, int total, int K_,
+                                       int wave, int lane) {
+    ld = ld_;
+    K = K_;
+    rows = total - r0;
+    base = reinterpret_cast<const char*>(p + (int64_t)r0 * ld);
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) off[j] = offset((wave + NW * j) * 64 + lane, min(0, K - BK));
+  }
+  template <bool FULL, int J>
+  __device__ __forceinline__ void issue(uint32_t lds, int t, int wave, int lane) const {
+    const int q = wave + NW * J;
+    const bool cut = !FULL && (t + 1) * BK > K;
+    dma16_at(base + t * BK, cut ? offset(q * 64 + lane, t * BK) : off[J], lds + q * 1024);
+  }
+  __device__ __forceinline__ void zero_tail(char* slot, int kleft, int tid) const {
+    for (int c16 = tid; c16 < BYTES / 16; c16 += 64 * NW) {
+      const int r = c16 >> 2, c = (c16 & 3) ^ swz(r);
+      if (c * 16 >= kleft) *reinterpret_cast<uint4*>(slot + 16 * c16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ Raw read(const char* slot, int r0, int s, int lane) const {
+    const int r = r0 + (lane & 15), g = lane >> 4;
+    return *reinterpret_cast<const Raw*>(slot + r * 64 + (((2 * s + (g >> 1)) ^ swz(r)) << 4) +
+                                         8 * (g & 1));
+  }
+};
+
 // c += a b in VGPRs. Inline asm because with one workgroup per CU the compiler
 // otherwise keeps the accumulators in AGPRs and copies them between the half
 // steps. It does not see these as matrix instructions: settle() stands
@@ -210,11 +273,11 @@ template <int LPW, int NS> __device__ __forceinline__ void wait_steps(int n) {
   else wait_vm<0>();
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS>
+template <typename T, typename TB, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS>
 __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct p) {
   constexpr int NW = WM * WN;
   typedef Operand<T, BM, A_KMAJ, NW> OpA;
-  typedef Operand<T, BN, B_KMAJ, NW> OpB;
+  typedef Operand<TB, BN, B_KMAJ, NW> OpB;
   constexpr int BK = Elem<T>::BK;
   constexpr int TM = BM / WM, TN = BN / WN;
   constexpr int FM = TM / 16, FN = TN / 16;
@@ -237,7 +300,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
   OpA oa;
   OpB ob;
   oa.init(static_cast<const T*>(p.A), p.lda, m0, p.M, p.K, wave, lane);
-  ob.init(static_cast<const T*>(p.B), p.ldb, n0, p.N, p.K, wave, lane);
+  ob.init(static_cast<const TB*>(p.B), p.ldb, n0, p.N, p.K, wave, lane);
 
   floatx4 acc[FM][FN];
 #pragma unroll
@@ -256,7 +319,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
     }
   };
 
-  typename Elem<T>::Frag fa[2][FM], fb[2][FN];
+  typename Elem<T>::Frag fa[2][FM];
+  typename OpB::Raw fb[2][FN];
   // copy J (of LPW) of step t into `slot`
   auto issue = [&](int slot, int t, auto piece, auto full) POETX_INLINE {
     constexpr int J = decltype(piece)::value;
@@ -283,16 +347,22 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
   // accumulator)
   auto products = [&](auto half, auto after) POETX_INLINE {
     constexpr int H = decltype(half)::value;
+    typename Elem<T>::Frag b[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      b[j] = OpB::widen(fb[H][j]);
+      if constexpr (sizeof(TB) == 1) asm volatile("" : "+v"(b[j]));  // widened before settle_before
+    }
     settle_before();
     for_each<FM>([&](auto r) POETX_INLINE {
       constexpr int i = decltype(r)::value;
-      for_each<FN>([&](auto j) POETX_INLINE { mma<0>(fb[H][j], fa[H][i], acc[i][j]); });
+      for_each<FN>([&](auto j) POETX_INLINE { mma<0>(b[j], fa[H][i], acc[i][j]); });
       after(r);
     });
     if constexpr (sizeof(T) == 4)
       for_each<3 * FM * FN>([&](auto q) POETX_INLINE {
         constexpr int e = decltype(q)::value / (FM * FN), ij = decltype(q)::value % (FM * FN);
-        mma<1 + e>(fb[H][ij % FN], fa[H][ij / FN], acc[ij / FN][ij % FN]);
+        mma<1 + e>(b[ij % FN], fa[H][ij / FN], acc[ij / FN][ij % FN]);
       });
   };
   constexpr std::integral_constant<int, 0> kFirst{};
@@ -410,64 +480,92 @@ hipError_t launch_cfg(bool ak, bool bk, const TileProduct& p, int nsplit, hipStr
   const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, nsplit), block(64 * WM * WN);
+  if (p.b_int8) {
+    // (64 bytes a row and step: a shape whose waves each copy some of them)
+    if constexpr (sizeof(T) == 2 && BN * 64 >= 1024 * WM * WN) {
+      if (ak && bk && p.K % 16 == 0) {
+        hipLaunchKernelGGL((tile_kernel<T, int8_t, BM, BN, WM, WN, true, true, NS>), grid, block, 0,
+                           s, p);
+        return hipGetLastError();
+      }
+    }
+    return hipErrorInvalidValue;
+  }
   if (ak && bk)
-    hipLaunchKernelGGL((tile_kernel<T, BM, BN, WM, WN, true, true, NS>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((tile_kernel<T, T, BM, BN, WM, WN, true, true, NS>), grid, block, 0, s, p);
   else if (ak)
-    hipLaunchKernelGGL((tile_kernel<T, BM, BN, WM, WN, true, false, NS>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((tile_kernel<T, T, BM, BN, WM, WN, true, false, NS>), grid, block, 0, s, p);
   else if (!bk)
-    hipLaunchKernelGGL((tile_kernel<T, BM, BN, WM, WN, false, false, NS>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((tile_kernel<T, T, BM, BN, WM, WN, false, false, NS>), grid, block, 0, s, p);
   else
     return hipErrorInvalidValue;  // no caller has an M-major A with a K-major B
   return hipGetLastError();
 }
 
-// The tile shapes, with what one step of 128 bytes of k costs on a CU (us,
-// measured on an MI355X over 512 .. 4096 x 4096 x 4096 products with every CU
-// busy; `alone`: with one workgroup on a CU that holds two).
+// The tile shapes: workgroups that fit a CU, and what one step of 128 bytes
+// of k costs there (us) with one of them on it and with all, measured on an
+// MI355X with operands in the caches.
 struct Shape {
   int bm, bn, per_cu;
-  float step, alone;
+  float alone, full;
+  bool int8;  // B may be INT8 codes
 };
-constexpr Shape kBf16Shapes[] = {
-    {256, 128, 1, 1.03f, 1.03f}, {128, 128, 1, 0.59f, 0.59f}, {128, 64, 1, 0.41f, 0.41f},
-    {64, 64, 2, 0.47f, 0.28f}};
+constexpr Shape kBf16Shapes[] = {{256, 128, 1, 1.03f, 1.03f, true},
+                                 {128, 128, 1, 0.59f, 0.59f, true},
+                                 {128, 64, 1, 0.41f, 0.41f, false},
+                                 {64, 64, 2, 0.28f, 0.47f, true},
+                                 {32, 64, 3, 0.20f, 0.40f, true}};
 // float32 is bound by its matrix rate (a 64 x 64 step is 1024 cycles of it),
-// so the smallest shape, which fills the chip most evenly, serves all sizes
-constexpr Shape kF32Shapes[] = {{64, 64, 2, 0.90f, 0.47f}};
+// so small shapes, which fill the chip most evenly, serve all sizes
+constexpr Shape kF32Shapes[] = {{64, 64, 2, 0.56f, 0.90f, false}, {32, 64, 3, 0.26f, 0.76f, false}};
 constexpr int kCus = 256;
-constexpr float kPartBytesPerUs = 4.0e6f;  // partial tiles, written and read
-constexpr float kFinishLaunch = 3.0f;      // us of the pass that joins them
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+constexpr float kLaunch = 3.0f;            // us of a launch and its first loads
+constexpr float kFinish = 2.5f;            // and of the pass that joins the partial tiles
+constexpr float kPartBytesPerUs = 8.0e6f;  // which are written and read near the cores
+constexpr float kHbmBytesPerUs = 6.2e6f;
+// operands that come from HBM rather than a cache lengthen the steps by about
+// this share of their transfer time
+constexpr float kCold = 0.45f;
 
 }  // namespace
 
 // Every shape and a few splits of the reduction, by rounds of workgroups
-// times steps times the step's cost, plus the partial tiles' traffic. What it
-// decides, measured: 777 x 2048 x 2048 128 x 64 tiles 15.1 us, 64 x 64 16.8,
-// 128 x 128 21.0; 1024 x 4096 x 4096 39 us on 128 x 128, 53 on 128 x 64, 56
-// on 256 x 128; 2048 x 4096 x 4096 69 us on 256 x 128, 75 on 128 x 128.
-TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K) {
+// times steps times the step's cost, the operands' transfer and the partial
+// tiles'. What it decides, measured: 777 x 2048 x 2048 128 x 64 tiles 15.1 us,
+// 64 x 64 16.8, 128 x 128 21.0; 1024 x 4096 x 4096 39 us on 128 x 128, 53 on
+// 128 x 64, 56 on 256 x 128; 2048 x 4096 x 4096 69 us on 256 x 128, 75 on 128
+// x 128; 16 x 4096 x 14336 26.7 us on 32 x 64, 28.7 on 64 x 64; 16 x 14336 x
+// 4096 25.3 us on 32 x 64 in 8 splits, 27.0 in 4, 32.0 in 3.
+TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8) {
   const bool bf16 = t == DType::BF16;
   const Shape* shapes = bf16 ? kBf16Shapes : kF32Shapes;
-  const int nshapes = bf16 ? (int)(sizeof(kBf16Shapes) / sizeof(Shape)) : 1;
-  const int bk = bf16 ? 64 : 32;
-  const int64_t steps = (K + bk - 1) / bk;
+  const int nshapes = (int)((bf16 ? sizeof(kBf16Shapes) : sizeof(kF32Shapes)) / sizeof(Shape));
+  const int bk = bf16 ? 64 : 32, es = bf16 ? 2 : 4;
+  const int steps = (int)((K + bk - 1) / bk);
+  const float hbm = (float)(M * K * es + N * K * (b_int8 ? 1 : es)) / kHbmBytesPerUs;
   TilePlan best = {};
   best.cost = 1e30f;
   for (int i = 0; i < nshapes; ++i) {
     const Shape& h = shapes[i];
+    if (b_int8 && !h.int8) continue;
     const int64_t tiles = ((M + h.bm - 1) / h.bm) * ((N + h.bn - 1) / h.bn);
-    for (int64_t want = 1; want <= 16; ++want) {
-      const int64_t per = (steps + want - 1) / want, split = (steps + per - 1) / per;
-      // (a split leaves at least eight steps to each part)
-      if (split != want || (split > 1 && per < 8)) continue;
-      const int64_t wgs = tiles * split, slots = (int64_t)kCus * h.per_cu;
-      const int64_t whole = wgs / slots, rest = wgs % slots;
-      float cost = (float)whole * per * h.step;
-      if (rest) cost += (float)per * (rest <= kCus ? h.alone : h.step);
-      if (split > 1) cost += kFinishLaunch + (float)(2 * split * M * N * 4) / kPartBytesPerUs;
+    const int64_t slots = (int64_t)kCus * h.per_cu;
+    for (int want : kSplits) {
+      const int per = (steps + want - 1) / want, split = (steps + per - 1) / per;
+      // (a split leaves at least eight steps to each part, and none is made
+      // of tiles that fill the chip anyway)
+      if (split != want || (split > 1 && (per < 8 || tiles >= slots))) continue;
+      const int64_t wgs = tiles * split, rest = wgs % slots;
+      float rounds = (float)(wgs / slots) * h.full;
+      if (rest)
+        rounds += h.per_cu == 1 ? h.full
+                                : h.alone + (h.full - h.alone) * (float)((rest - 1) / kCus) /
+                                                (float)(h.per_cu - 1);
+      float cost = kLaunch + std::max(rounds * (float)per + kCold * hbm, hbm);
+      if (split > 1) cost += kFinish + (float)(2 * split * M * N * 4) / kPartBytesPerUs;
       if (cost < best.cost)
-        best = TilePlan{i, (int)split, (int)(per * bk),
-                        split > 1 ? (size_t)split * M * N : 0, cost};
+        best = TilePlan{i, split, per * bk, split > 1 ? (size_t)split * M * N : 0, cost};
     }
   }
   return best;
@@ -480,13 +578,17 @@ hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, boo
   else if (!p.part) return hipErrorInvalidValue;
   hipError_t e = hipErrorInvalidValue;
   if (t == DType::F32) {
-    e = launch_cfg<float, 64, 64, 2, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s);
+    switch (plan.shape) {  // kF32Shapes
+      case 0: e = launch_cfg<float, 64, 64, 2, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+      case 1: e = launch_cfg<float, 32, 64, 1, 4, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+    }
   } else {
     switch (plan.shape) {  // kBf16Shapes
       case 0: e = launch_cfg<bf16_t, 256, 128, 4, 2, 3>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
       case 1: e = launch_cfg<bf16_t, 128, 128, 2, 4, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
       case 2: e = launch_cfg<bf16_t, 128, 64, 4, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
       case 3: e = launch_cfg<bf16_t, 64, 64, 2, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+      case 4: e = launch_cfg<bf16_t, 32, 64, 1, 4, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
     }
   }
   if (e != hipSuccess || plan.nsplit == 1) return e;

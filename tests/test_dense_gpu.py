@@ -135,7 +135,9 @@ SIZES = [(1, 8, 8), (1, 128, 128), (1, 4096, 256), (2, 136, 264), (3, 2056, 72),
          (16, 1000, 520), (17, 64, 4096), (31, 4096, 512), (33, 8192, 128), (63, 256, 256),
          (64, 72, 8), (65, 320, 192), (100, 1024, 1536), (127, 256, 640), (128, 512, 128),
          (129, 2048, 256), (200, 1000, 136), (255, 512, 520), (256, 256, 256), (257, 512, 768),
-         (300, 2056, 1288), (513, 1024, 2048), (777, 2048, 1024), (1100, 768, 2816)]
+         (300, 2056, 1288), (513, 1024, 2048), (777, 2048, 1024), (1100, 768, 2816),
+         # INT8 rows of whole 16 bytes that end inside a step; a long split
+         (5, 144, 136), (20, 14336, 96), (40, 144, 136), (90, 1040, 264), (150, 4112, 512)]
 
 
 @pytest.mark.parametrize("i", range(len(SIZES)), ids=lambda i: "x".join(map(str, SIZES[i])))

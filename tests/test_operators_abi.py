@@ -84,8 +84,9 @@ def test_alignment_of_pointers():
 
 
 def test_workspace():
-    # a long reduction of few tiles, and INT8 codes, need one in the forward
-    for d in (desc(tokens=200, d_in=4096), desc(tokens=200, w_scale=A * 16)):
+    # a long reduction of few tiles, and INT8 codes whose rows are not whole 16
+    # bytes (widened into it), need one in the forward
+    for d in (desc(tokens=200, d_in=4096), desc(tokens=200, d_in=72, w_scale=A * 16)):
         need = P.poetx_dense_fwd_workspace_size(d)
         assert need > 0
         assert fwd(d, ws=None) == P.POETX_ERR_WORKSPACE
