@@ -23,7 +23,11 @@ constexpr int NT = 256, kVecs = 32, kLanes = NT / kVecs;
 // rows of one range: four a thread, all of whose loads are in flight at once,
 // and many workgroups; more only where the ranges would pass the grid's limit
 constexpr int kRows = 4 * kLanes, kMaxSplits = 32768;
+// so few rows are one range, whose sums are the bias gradient itself: one
+// launch less where launches are what costs
+constexpr int kOneRange = 64;
 int rows_per_split(int64_t rows) {
+  if (rows <= kOneRange) return (int)rows;
   return (int)(kRows * ((rows + (int64_t)kRows * kMaxSplits - 1) / ((int64_t)kRows * kMaxSplits)));
 }
 

@@ -52,7 +52,13 @@ __device__ __forceinline__ const bf16_t* uniform_ptr(const bf16_t* p) {
   return reinterpret_cast<const bf16_t*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-template <bool B_KMAJ>
+// PAIR (both operands K-major and row-major in memory): a K tile is 64 bytes
+// of each row, half a 128-byte line, and by the next tile's copies the lines
+// have left the 32 KB L1, so every line crossed from the L2 twice. Paired, the
+// copies of an even tile and of the odd one behind it are issued together,
+// piece by piece, during every second tile; a line's second half then finds it
+// in the L1.
+template <bool B_KMAJ, bool PAIR = false>
 struct Dense {
   const bf16_t* baseA;  // wave-uniform bases of the current tile's A and B panels
   const bf16_t* baseB;
@@ -133,6 +139,15 @@ struct Dense {
     dma<S, 1, 0>(t); dma<S, 1, 1>(t); dma<S, 1, 2>(t); dma<S, 1, 3>(t);
   }
 
+  // the copies of tiles t (slot S) and t + 1 (slot S + 1), piece by piece
+  template <int S>
+  __device__ __forceinline__ void issue_pair(int t) {
+    dma<S, 0, 0>(t); dma<S + 1, 0, 0>(t + 1); dma<S, 0, 1>(t); dma<S + 1, 0, 1>(t + 1);
+    dma<S, 0, 2>(t); dma<S + 1, 0, 2>(t + 1); dma<S, 0, 3>(t); dma<S + 1, 0, 3>(t + 1);
+    dma<S, 1, 0>(t); dma<S + 1, 1, 0>(t + 1); dma<S, 1, 1>(t); dma<S + 1, 1, 1>(t + 1);
+    dma<S, 1, 2>(t); dma<S + 1, 1, 2>(t + 1); dma<S, 1, 3>(t); dma<S + 1, 1, 3>(t + 1);
+  }
+
   // A fragment I (rows 16 I .. of this wave's 128; lane l holds row l % 16,
   // k = 8 (l / 16) .. +7) from ring slot S into set P
   template <int S, int P, int I>
@@ -179,23 +194,35 @@ struct Dense {
   __device__ __forceinline__ void tile(int t, int ntiles) {
     constexpr int S1 = (S + 1) & 3;
     const bool more = STEADY || t + 1 < ntiles;
-    const bool iss = STEADY || t + 4 < ntiles;
+    // paired: an odd tile issues the copies of tiles t + 3 and t + 4
+    constexpr bool ODD = (S & 1) != 0;
+    const bool iss = (!PAIR || ODD) && (STEADY || t + 4 < ntiles);
+    const bool iss3 = PAIR && ODD && (STEADY || t + 3 < ntiles);
+    constexpr int S3 = (S + 3) & 3;
     mma_row<P, 0, FIRST>();
     __builtin_amdgcn_sched_barrier(0);
     if (more) {
       // this wave's part of tile t+1 landed (tiles t+2, t+3 may still be in
       // flight) and its reads of tile t are done; after the barrier every
       // part has landed and slot S is free
-      if (STEADY || t + 3 < ntiles) wait_vm<2 * LPW>();
-      else if (t + 2 < ntiles) wait_vm<LPW>();
-      else wait_vm<0>();
+      // (paired, odd t: of the pair t + 1, t + 2 only the last copy may be)
+      if constexpr (PAIR && ODD) {
+        if (STEADY || t + 2 < ntiles) wait_vm<1>();
+        else wait_vm<0>();
+      } else {
+        if (STEADY || t + 3 < ntiles) wait_vm<2 * LPW>();
+        else if (t + 2 < ntiles) wait_vm<LPW>();
+        else wait_vm<0>();
+      }
       wait_lds();
       barrier_nofence();
     }
+    if (iss3) dma<S3, 0, 0>(t + 3);
     if (iss) dma<S, 0, 0>(t + 4);
     __builtin_amdgcn_sched_barrier(0);
 #define POETX_DENSE_ROW(I)                                                          \
   mma_row<P, I, FIRST>();                                                           \
+  if (iss3) dma<S3, (I) / 4, (I) % 4>(t + 3);                                       \
   if (iss) dma<S, (I) / 4, (I) % 4>(t + 4);                                         \
   if (more) { read_a<S1, P ^ 1, (I) - 1>(); read_b<S1, P ^ 1, (I) - 1>(); }         \
   __builtin_amdgcn_sched_barrier(0);
@@ -207,6 +234,13 @@ struct Dense {
 
   // copies of the first (up to) four K tiles of the current output tile
   __device__ __forceinline__ void prefetch(int ntiles) {
+    if constexpr (PAIR) {
+      if (ntiles > 1) issue_pair<0>(0);
+      else issue<0>(0);
+      if (ntiles > 3) issue_pair<2>(2);
+      else if (ntiles > 2) issue<2>(2);
+      return;
+    }
     issue<0>(0);
     if (ntiles > 1) issue<1>(1);
     if (ntiles > 2) issue<2>(2);
@@ -216,9 +250,10 @@ struct Dense {
   // every part of K tile 0 landed (this wave's earlier stores too: the
   // count is conservative); its fragments read
   __device__ __forceinline__ void start(int ntiles) {
-    if (ntiles > 3) wait_vm<3 * LPW>();
-    else if (ntiles > 2) wait_vm<2 * LPW>();
-    else if (ntiles > 1) wait_vm<LPW>();
+    // (paired: tile 1 with it)
+    if (ntiles > 3) wait_vm<(PAIR ? 2 : 3) * LPW>();
+    else if (ntiles > 2) wait_vm<(PAIR ? 1 : 2) * LPW>();
+    else if (ntiles > 1) wait_vm<(PAIR ? 0 : 1) * LPW>();
     else wait_vm<0>();
     barrier_nofence();
     read_a<0, 0, 0>(); read_a<0, 0, 1>(); read_a<0, 0, 2>(); read_a<0, 0, 3>();

@@ -21,10 +21,10 @@ namespace {
 template <Activation ACT, bool SAVE_U>
 struct DenseEpilogue {
   // this lane's column of fragment column j
-  static __device__ __forceinline__ int column(const Dense<true>& d, int j, int ln) {
+  static __device__ __forceinline__ int column(const Dense<true, true>& d, int j, int ln) {
     return d.wn * 128 + 16 * j + 4 * (ln >> 4);
   }
-  static __device__ __forceinline__ int row(const Dense<true>& d, int i, int ln) {
+  static __device__ __forceinline__ int row(const Dense<true, true>& d, int i, int ln) {
     return d.wm * 128 + 16 * i + (ln & 15);
   }
   static __device__ __forceinline__ void load_column(const Epilogue& ep, int n, float4& sc,
@@ -38,7 +38,7 @@ struct DenseEpilogue {
     *reinterpret_cast<uint2*>(g_dense_lds + stage_off(m, n)) = v;
   }
 
-  static __device__ __forceinline__ void run(Dense<true>& d, const Epilogue& ep, int m0, int n0) {
+  static __device__ __forceinline__ void run(Dense<true, true>& d, const Epilogue& ep, int m0, int n0) {
     // opaque copies of the lane and thread ids: keeps the compiler from
     // hoisting the epilogue's address arithmetic out of the tile loop
     int ln = d.lane, tid = (int)threadIdx.x;
@@ -104,7 +104,7 @@ dense_epilogue_kernel(const bf16_t* __restrict__ A, const bf16_t* __restrict__ B
   const int num_mt = (M + BM - 1) / BM, num_nt = (N + BN - 1) / BN;
   const int total = num_mt * num_nt;
   const int ntiles = K / BK;
-  Dense<true> d;
+  Dense<true, true> d;
   d.init(lda, ldb, false, b_tiled != 0);
   for (int tile = blockIdx.x; tile < total; tile += (int)gridDim.x) {
     int mt, nt;

@@ -18,6 +18,7 @@
 // launch), so a call needs no device table, no copy and no allocation, and a
 // captured graph holds them by value.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -89,40 +90,37 @@ __device__ __forceinline__ void add_square(double& acc, float v) {
   acc = fma(d, d, acc);
 }
 
+template <typename T> __device__ __forceinline__ void add_squares(double& acc, uint4 w) {
+  float f[16 / sizeof(T)];
+  unpack<T>(w, f);
+#pragma unroll
+  for (int e = 0; e < (int)(16 / sizeof(T)); ++e) add_square(acc, f[e]);
+}
+
+// one thread's share of a chunk that is cut by its run's end or not aligned
 template <typename T>
-__device__ __forceinline__ double chunk_sumsq(const T* p, int64_t n, int64_t at) {
-  constexpr int E = 16 / sizeof(T), PER = kChunkBytes / sizeof(T), Q = PER / E / NT;
+__device__ __forceinline__ double cut_sumsq(const T* p, int64_t n, int64_t at) {
+  constexpr int E = 16 / sizeof(T), PER = kChunkBytes / sizeof(T);
   const int len = (int)min((int64_t)PER, n - at);
   const T* src = p + at;
   double acc = 0.0;
+  int i0 = 0;
   if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    const uint4* v = reinterpret_cast<const uint4*>(src);
-    if (len == PER) {
-      uint4 w[Q];
-#pragma unroll
-      for (int q = 0; q < Q; ++q) w[q] = v[q * NT + threadIdx.x];
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        float f[E];
-        unpack<T>(w[q], f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) add_square(acc, f[e]);
-      }
-      return acc;
-    }
     const int nv = len / E;
-    for (int i = threadIdx.x; i < nv; i += NT) {
-      float f[E];
-      unpack<T>(v[i], f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) add_square(acc, f[e]);
-    }
-    for (int i = nv * E + threadIdx.x; i < len; i += NT)
-      add_square(acc, ElemTraits<T>::to_f32(src[i]));
-  } else {
-    for (int i = threadIdx.x; i < len; i += NT) add_square(acc, ElemTraits<T>::to_f32(src[i]));
+    for (int i = threadIdx.x; i < nv; i += NT)
+      add_squares<T>(acc, reinterpret_cast<const uint4*>(src)[i]);
+    i0 = nv * E;
   }
+  for (int i = i0 + threadIdx.x; i < len; i += NT) add_square(acc, ElemTraits<T>::to_f32(src[i]));
   return acc;
+}
+
+// A store that the caches need not keep: 334 M float32 values, clipped into
+// another buffer, took 742 us with plain stores and 714 with these (what the
+// first pass read last stays in the memory-side cache for the second).
+__device__ __forceinline__ void store_nt(uint4* p, uint4 v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
 }
 
 // (grad and out may be the same memory: each value is read, then written, by
@@ -150,7 +148,7 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int64_t n, int64_t
 #pragma unroll
       for (int q = 0; q < Q; ++q) w[q] = v[q * NT + threadIdx.x];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) d[q * NT + threadIdx.x] = scaled(w[q]);
+      for (int q = 0; q < Q; ++q) store_nt(d + q * NT + threadIdx.x, scaled(w[q]));
       return;
     }
     const int nv = len / E;
@@ -161,16 +159,57 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int64_t n, int64_t
     dst[i] = ElemTraits<T>::from_f32(ElemTraits<T>::to_f32(src[i]) * k);
 }
 
+// a whole chunk's 16-byte vectors of one thread, or null: a cut or unaligned
+// chunk
+__device__ __forceinline__ const uint4* whole_chunk(const Batch& b, int chunk, int* bf16) {
+  const int i = find_run(b, chunk);
+  const int64_t at = (int64_t)(chunk - b.first[i]) * kChunkBytes;
+  const char* p = static_cast<const char*>(b.grad[i]);
+  *bf16 = b.bf16[i];
+  const bool whole = (reinterpret_cast<uintptr_t>(p) & 15) == 0 &&
+                     at + kChunkBytes <= b.n[i] * (b.bf16[i] ? 2 : 4);
+  return whole ? reinterpret_cast<const uint4*>(p + at) + threadIdx.x : nullptr;
+}
+
 __global__ void __launch_bounds__(NT) sumsq_kernel(const Batch b, double* __restrict__ part) {
+  constexpr int Q = kChunkBytes / 16 / NT;
   const int total = b.first[b.count];
   double acc = 0.0;
-  for (int c = blockIdx.x; c < total; c += gridDim.x) {
-    const int i = find_run(b, c);
-    const int64_t k = c - b.first[i];
-    if (b.bf16[i])
-      acc += chunk_sumsq(static_cast<const bf16_t*>(b.grad[i]), b.n[i], k * (kChunkBytes / 2));
-    else
-      acc += chunk_sumsq(static_cast<const float*>(b.grad[i]), b.n[i], k * (kChunkBytes / 4));
+  // a chunk's loads are in flight while the one before it is summed
+  uint4 w[2][Q];
+  int bf16[2] = {};
+  const uint4* src = whole_chunk(b, blockIdx.x, &bf16[0]);
+  if (src)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) w[0][q] = src[q * NT];
+  bool whole = src != nullptr;
+  auto one = [&](auto buf, int c) __attribute__((always_inline)) {
+    constexpr int k = decltype(buf)::value;
+    const int next = c + gridDim.x;
+    const uint4* ns = next < total ? whole_chunk(b, next, &bf16[k ^ 1]) : nullptr;
+    if (ns)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) w[k ^ 1][q] = ns[q * NT];
+    if (whole) {
+      if (bf16[k]) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) add_squares<bf16_t>(acc, w[k][q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) add_squares<float>(acc, w[k][q]);
+      }
+    } else {
+      const int i = find_run(b, c);
+      const int64_t at = c - b.first[i];
+      acc += b.bf16[i] ? cut_sumsq(static_cast<const bf16_t*>(b.grad[i]), b.n[i], at * (kChunkBytes / 2))
+                       : cut_sumsq(static_cast<const float*>(b.grad[i]), b.n[i], at * (kChunkBytes / 4));
+    }
+    whole = ns != nullptr;
+  };
+  for (int c = blockIdx.x; c < total; c += 2 * gridDim.x) {
+    one(std::integral_constant<int, 0>{}, c);
+    if (c + (int)gridDim.x >= total) break;
+    one(std::integral_constant<int, 1>{}, c + gridDim.x);
   }
   const double t = block_sum(acc);
   if (threadIdx.x == 0) part[blockIdx.x] = t;

@@ -522,7 +522,7 @@ constexpr int kCus = 256;
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 constexpr float kLaunch = 3.0f;            // us of a launch and its first loads
 constexpr float kFinish = 2.5f;            // and of the pass that joins the partial tiles
-constexpr float kPartBytesPerUs = 8.0e6f;  // which are written and read near the cores
+constexpr float kPartBytesPerUs = 6.0e6f;  // which are written and read near the cores
 constexpr float kHbmBytesPerUs = 6.2e6f;
 // operands that come from HBM rather than a cache lengthen the steps by about
 // this share of their transfer time

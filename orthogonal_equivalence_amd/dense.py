@@ -15,6 +15,7 @@ streams, and calls captured into different graphs, share no memory.
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -61,33 +62,49 @@ def _desc(name, t, W, activation, w_scale, width):
     _check(name, t, (t.shape[0], W.shape[width]), t.dtype, t.device)
     _check("W", W, (d_out, d_in), torch.int8 if w_scale is not None else t.dtype, t.device)
     _check("w_scale", w_scale, (d_out,), torch.float32, t.device)
-    return P.make_dense_desc(t.shape[0], d_in, d_out, _ACT[t.dtype], ACTIVATIONS[activation],
-                             w_scale)
+    desc, ws = _plan(t.shape[0], d_in, d_out, _ACT[t.dtype], ACTIVATIONS[activation],
+                     w_scale is not None, width == 1)
+    if w_scale is not None:
+        desc = P.make_dense_desc(desc.tokens, d_in, d_out, desc.act, desc.activation, w_scale)
+    return desc, ws
+
+
+@functools.lru_cache(maxsize=4096)
+def _plan(tokens, d_in, d_out, act, activation, int8, forward):
+    """The descriptor of these sizes (its w_scale, with int8, a placeholder)
+    and its workspace bytes: both follow from the sizes alone."""
+    desc = P.make_dense_desc(tokens, d_in, d_out, act, activation, 16 if int8 else None)
+    size = P.poetx_dense_fwd_workspace_size if forward else P.poetx_dense_bwd_workspace_size
+    return desc, size(desc)
 
 
 def _workspace(nbytes, device):
     return torch.empty(nbytes, device=device, dtype=torch.uint8) if nbytes else None
 
 
+def _here(device, stream):
+    """Whether the call runs on the current device's current stream as it is."""
+    return stream is None and device.index == torch.cuda.current_device()
+
+
 def dense_forward(x, W, bias=None, residual=None, activation="none", w_scale=None, save_u=False,
                   stream=None):
     """Returns (y, u): u, the pre-activation that dense_backward takes, with
     save_u, else None."""
-    desc = _desc("x", x, W, activation, w_scale, 1)
+    desc, nbytes = _desc("x", x, W, activation, w_scale, 1)
     out = (x.shape[0], W.shape[0])
     _check("bias", bias, out[1:], torch.float32, x.device)
     _check("residual", residual, out, x.dtype, x.device)
-    if stream is None and x.device.index == torch.cuda.current_device():
-        return _forward(desc, x, W, bias, residual, out, save_u)
+    if _here(x.device, stream):
+        return _forward(desc, x, W, bias, residual, out, save_u, nbytes)
     with _on(x.device, stream):
-        return _forward(desc, x, W, bias, residual, out, save_u)
+        return _forward(desc, x, W, bias, residual, out, save_u, nbytes)
 
 
-def _forward(desc, x, W, bias, residual, out, save_u):
-    y = torch.empty(out, device=x.device, dtype=x.dtype)
-    u = torch.empty_like(y) if save_u else None
-    ws = _workspace(P.poetx_dense_fwd_workspace_size(desc), x.device)
-    P.poetx_dense_fwd(desc, x, W, bias, residual, y, u, ws)
+def _forward(desc, x, W, bias, residual, out, save_u, nbytes):
+    y = x.new_empty(out)
+    u = x.new_empty(out) if save_u else None
+    P.poetx_dense_fwd(desc, x, W, bias, residual, y, u, _workspace(nbytes, x.device))
     return y, u
 
 
@@ -96,7 +113,7 @@ def dense_backward(g_y, W, x=None, u=None, activation="none", w_scale=None, need
     """Returns (g_x, g_W, g_bias), None in the place of one not asked for. x is
     needed for g_W, u (dense_forward's, with save_u) for an activation. The
     gradient of the residual is g_y itself. int8 codes have no g_W."""
-    desc = _desc("g_y", g_y, W, activation, w_scale, 0)
+    desc, nbytes = _desc("g_y", g_y, W, activation, w_scale, 0)
     d_out, d_in = W.shape
     _check("x", x, (g_y.shape[0], d_in), g_y.dtype, g_y.device)
     _check("u", u, tuple(g_y.shape), g_y.dtype, g_y.device)
@@ -108,19 +125,18 @@ def dense_backward(g_y, W, x=None, u=None, activation="none", w_scale=None, need
         raise ValueError("the backward of an activation needs u")
     if not (need_g_x or need_g_W or need_g_bias):
         raise ValueError("no gradient asked for")
-    if stream is None and g_y.device.index == torch.cuda.current_device():
-        return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias)
+    if _here(g_y.device, stream):
+        return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes)
     with _on(g_y.device, stream):
-        return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias)
+        return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes)
 
 
-def _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias):
-    new = dict(device=g_y.device, dtype=g_y.dtype)
-    g_x = torch.empty(g_y.shape[0], W.shape[1], **new) if need_g_x else None
-    g_W = torch.empty(W.shape, **new) if need_g_W else None
-    g_b = torch.empty(W.shape[0], device=g_y.device, dtype=torch.float32) if need_g_bias else None
-    ws = _workspace(P.poetx_dense_bwd_workspace_size(desc), g_y.device)
-    P.poetx_dense_bwd(desc, g_y, x, W, u, g_x, g_W, g_b, ws)
+def _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes):
+    d_out, d_in = W.shape
+    g_x = g_y.new_empty((g_y.shape[0], d_in)) if need_g_x else None
+    g_W = g_y.new_empty((d_out, d_in)) if need_g_W else None
+    g_b = g_y.new_empty(d_out, dtype=torch.float32) if need_g_bias else None
+    P.poetx_dense_bwd(desc, g_y, x, W, u, g_x, g_W, g_b, _workspace(nbytes, g_y.device))
     return g_x, g_W, g_b
 
 

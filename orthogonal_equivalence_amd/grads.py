@@ -11,7 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import poetx as P
-from .dense import _on
+from .dense import _here, _on
 
 
 def _device_of(grads, outs, norm):
@@ -40,10 +40,20 @@ def grad_norm(grads, stream=None):
     scalar tensor on their device."""
     grads, outs, device = _device_of(grads, None, None)
     tensors = P.make_grad_list(grads)
+    if _here(device, stream):
+        return _measure(tensors, len(grads), device, None)
     with _on(device, stream):
-        norm = torch.empty((), device=device, dtype=torch.float32)
-        ws = torch.empty(P.poetx_grad_workspace_size(len(grads)), device=device, dtype=torch.uint8)
+        return _measure(tensors, len(grads), device, None)
+
+
+def _measure(tensors, count, device, max_norm):
+    """The norm of a list of records, which are clipped with a max_norm."""
+    norm = torch.empty((), device=device, dtype=torch.float32)
+    ws = torch.empty(P.poetx_grad_workspace_size(count), device=device, dtype=torch.uint8)
+    if max_norm is None:
         P.poetx_grad_norm(tensors, norm, ws)
+    else:
+        P.poetx_grad_clip(tensors, max_norm, norm, ws)
     return norm
 
 
@@ -58,11 +68,10 @@ def clip_grads(grads, max_norm, outs=None, norm=None, stream=None):
                              norm.device != device):
         raise ValueError(f"norm must be one float32 value on {device}")
     tensors = P.make_grad_list(grads, outs)
+    if norm is None and _here(device, stream):
+        return _measure(tensors, len(grads), device, max_norm)
     with _on(device, stream):
-        if norm is not None:
-            P.poetx_grad_scale(tensors, max_norm, norm)
-            return norm
-        norm = torch.empty((), device=device, dtype=torch.float32)
-        ws = torch.empty(P.poetx_grad_workspace_size(len(grads)), device=device, dtype=torch.uint8)
-        P.poetx_grad_clip(tensors, max_norm, norm, ws)
+        if norm is None:
+            return _measure(tensors, len(grads), device, max_norm)
+        P.poetx_grad_scale(tensors, max_norm, norm)
     return norm

@@ -164,7 +164,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if not torch.cuda.is_available():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream
@@ -322,10 +324,13 @@ def make_grad_list(grads, outs=None) -> array.array:
     half of the last) of contiguous float32 and bfloat16 tensors; outs: where
     the clipped values go (default: in place)."""
     words = []
-    for g, o in zip(grads, grads if outs is None else outs):
-        if not (g.is_contiguous() and o.is_contiguous()):
+    if outs is None:
+        outs = grads
+    for g, o in zip(grads, outs):
+        if not g.is_contiguous() or (o is not g and not o.is_contiguous()):
             raise ValueError("libpoetx takes contiguous tensors")
-        words += (g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_DTYPE[g.dtype])
+        at = g.data_ptr()
+        words += (at, at if o is g else o.data_ptr(), g.numel(), _GRAD_DTYPE[g.dtype])
     return array.array("Q", words)
 
 
