@@ -20,8 +20,10 @@ namespace poetx {
 namespace {
 
 constexpr int NT = 256, kVecs = 32, kLanes = NT / kVecs;
-// rows of one range: four a thread, all of whose loads are in flight at once,
-// and many workgroups; more only where the ranges would pass the grid's limit
+// rows of one range: four a thread, all of whose loads are in flight at once
+// (two a thread and twice the ranges: 4.6 us against 4.8 for g_bias of 1000 x
+// 2048 gelu, with a longer join); more only where the ranges would pass the
+// grid's limit
 constexpr int kRows = 4 * kLanes, kMaxSplits = 32768;
 // so few rows are one range, whose sums are the bias gradient itself: one
 // launch less where launches are what costs
@@ -79,8 +81,8 @@ act_grad_kernel(const T* __restrict__ g_y, const T* __restrict__ u, const float*
       float g[4][E], w[4][E];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        // (rows past the end are read as the last one and left out below)
-        const int64_t at = min(r + q * kLanes, rows - 1) * d + n;
+        // (rows past the range are read as its last one and left out below)
+        const int64_t at = min(r + q * kLanes, r1 - 1) * d + n;
         Vec<T>::load(g_y + at, g[q]);
         if constexpr (ACT != Activation::None) Vec<T>::load(u + at, w[q]);
       }

@@ -15,30 +15,21 @@ from .dense import _here, _on
 
 
 def _device_of(grads, outs, norm):
-    grads = list(grads)
-    outs = grads if outs is None else list(outs)
-    if len(outs) != len(grads):
-        raise ValueError("one output per gradient")
-    tensors = grads if norm is None else [*grads, norm]
+    """The one GPU that all of them are on (the current one if there are none)."""
+    tensors = [*grads, *(outs or ()), *(() if norm is None else (norm,))]
     if not tensors:
-        return grads, outs, torch.device("cuda", torch.cuda.current_device())
-    device = tensors[0].device
-    if device.type != "cuda":
-        raise ValueError("gradients must be on a GPU")
-    for g, o in zip(grads, outs):
-        if g.dtype not in P._GRAD_DTYPE:
-            raise ValueError(f"a gradient is {g.dtype}, expected float32 or bfloat16")
-        if g.device != device:
-            raise ValueError(f"gradients on {device} and {g.device}")
-        if o is not g and (o.shape != g.shape or o.dtype != g.dtype or o.device != device):
-            raise ValueError("an output must have its gradient's shape, type and device")
-    return grads, outs, device
+        return torch.device("cuda", torch.cuda.current_device())
+    found = set(map(torch.Tensor.get_device, tensors))
+    if len(found) != 1 or -1 in found:
+        raise ValueError("gradients, outputs and norm must be on one GPU")
+    return tensors[0].device
 
 
 def grad_norm(grads, stream=None):
     """sqrt of the sum of squares of every value of every tensor: a float32
     scalar tensor on their device."""
-    grads, outs, device = _device_of(grads, None, None)
+    grads = list(grads)
+    device = _device_of(grads, None, None)
     tensors = P.make_grad_list(grads)
     if _here(device, stream):
         return _measure(tensors, len(grads), device, None)
@@ -63,10 +54,14 @@ def clip_grads(grads, max_norm, outs=None, norm=None, stream=None):
     that is not finite leaves the values as they are. norm: a float32 scalar
     tensor to clip by, where the caller has the norm already (joined over the
     ranks of a sharded job, say)."""
-    grads, outs, device = _device_of(grads, outs, norm)
-    if norm is not None and (norm.numel() != 1 or norm.dtype != torch.float32 or
-                             norm.device != device):
-        raise ValueError(f"norm must be one float32 value on {device}")
+    grads = list(grads)
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != len(grads):
+            raise ValueError("one output per gradient")
+    device = _device_of(grads, outs, norm)
+    if norm is not None and (norm.numel() != 1 or norm.dtype != torch.float32):
+        raise ValueError("norm must be one float32 value")
     tensors = P.make_grad_list(grads, outs)
     if norm is None and _here(device, stream):
         return _measure(tensors, len(grads), device, max_norm)

@@ -11,6 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import poetx as P
+from .dense import DenseLinear
 
 _DT = {"f32": (torch.float32, P.POETX_F32), "bf16": (torch.bfloat16, P.POETX_BF16)}
 
@@ -173,6 +174,30 @@ class PoetxLinear:
                            g_x, g_theta_R if g_theta_R.numel() else None,
                            g_theta_P if g_theta_P.numel() else None, ws, stream)
         return g_x, g_theta_R, g_theta_P
+
+
+    # -- after training -----------------------------------------------------
+    def merged_weight(self, rows: int = 1024):
+        """R W0 P [d_out, d_in] in the activation type, from the blocks as they
+        were last built: row i is the backward's g_x for the unit gradient g_y
+        = e_i, formed `rows` rows at a time (in bf16, R W0 is rounded once on
+        the way, the result once)."""
+        W = torch.empty(self.d_out, self.d_in, device=self.device, dtype=self.torch_dtype)
+        for r0 in range(0, self.d_out, rows):
+            n = min(rows, self.d_out - r0)
+            g_y = torch.zeros(n, self.d_out, device=self.device, dtype=self.torch_dtype)
+            g_y.diagonal(r0).fill_(1.0)
+            # the saved tensors enter the generators' gradients only
+            x = torch.zeros(n, self.d_in, device=self.device, dtype=self.torch_dtype)
+            z = None if self.flags & P.POETX_RECOMPUTE_Z else torch.zeros_like(g_y)
+            self.backward(g_y, x, z, g_x=W[r0:r0 + n])
+        return W
+
+    def merge(self, bias=None, activation="none", int8: bool = False) -> DenseLinear:
+        """The trained layer as a DenseLinear on R W0 P: one product a call,
+        with bias, activation and residual in its epilogue."""
+        return DenseLinear(self.merged_weight(), "bf16" if self.act == P.POETX_BF16 else "f32",
+                           bias, activation, self.device, int8)
 
 
 class PoetxLinearSet:

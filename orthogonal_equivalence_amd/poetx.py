@@ -322,16 +322,27 @@ _GRAD_DTYPE = {torch.float32: POETX_F32, torch.bfloat16: POETX_BF16}
 def make_grad_list(grads, outs=None) -> array.array:
     """The GradTensor records (four 64-bit words each: dtype fills the low
     half of the last) of contiguous float32 and bfloat16 tensors; outs: where
-    the clipped values go (default: in place)."""
-    words = []
-    if outs is None:
-        outs = grads
-    for g, o in zip(grads, outs):
-        if not g.is_contiguous() or (o is not g and not o.is_contiguous()):
+    the clipped values go (default: in place). Whole columns at a time: a
+    model has hundreds of gradients."""
+    T = torch.Tensor
+    words = array.array("Q", bytes(32 * len(grads)))
+    dtypes = [_GRAD_DTYPE.get(g.dtype) for g in grads]
+    if None in dtypes:
+        raise ValueError("gradients must be float32 or bfloat16")
+    if not all(map(T.is_contiguous, grads)):
+        raise ValueError("libpoetx takes contiguous tensors")
+    words[0::4] = at = array.array("Q", map(T.data_ptr, grads))
+    words[2::4] = sizes = array.array("Q", map(T.numel, grads))
+    words[3::4] = array.array("Q", dtypes)
+    if outs is not None:
+        if [_GRAD_DTYPE.get(o.dtype) for o in outs] != dtypes or \
+                array.array("Q", map(T.numel, outs)) != sizes:
+            raise ValueError("an output must have its gradient's size and type")
+        if not all(map(T.is_contiguous, outs)):
             raise ValueError("libpoetx takes contiguous tensors")
-        at = g.data_ptr()
-        words += (at, at if o is g else o.data_ptr(), g.numel(), _GRAD_DTYPE[g.dtype])
-    return array.array("Q", words)
+        at = array.array("Q", map(T.data_ptr, outs))
+    words[1::4] = at
+    return words
 
 
 def poetx_grad_workspace_size(count: int) -> int:
