@@ -391,7 +391,7 @@ typedef enum poetx_activation {
 } poetx_activation;
 
 typedef struct poetx_dense_desc {
-  int64_t tokens;     /* rows of x, y, u, residual, g_y, g_x; >= 1 */
+  int64_t tokens;     /* rows of x, y, u, residual, g_y, g_x; 1 .. 2^30 */
   int64_t d_in;       /* columns of W; at most 2^22 */
   int64_t d_out;      /* rows of W; at most 2^22 */
   int32_t act;        /* poetx_dtype of x, W, residual, y, u and their gradients */

@@ -13,13 +13,14 @@
 
 using poetx::Activation;
 using poetx::DType;
+using poetx::TilePairPlan;
 using poetx::TilePlan;
 using poetx::TileProduct;
 using namespace poetx::api;
 
 namespace {
 
-constexpr int64_t kMaxWidth = 1 << 22;
+constexpr int64_t kMaxTokens = 1 << 30, kMaxWidth = 1 << 22;
 
 DType dtype_of(const poetx_dense_desc* d) {
   return d->act == POETX_BF16 ? DType::BF16 : DType::F32;
@@ -30,7 +31,7 @@ int check_desc(const poetx_dense_desc* d) {
   if (!d) return POETX_ERR_NULL;
   if (d->act != POETX_F32 && d->act != POETX_BF16) return POETX_ERR_DTYPE;
   if (d->tokens < 1 || d->d_in < 1 || d->d_out < 1) return POETX_ERR_SHAPE;
-  if (d->tokens > INT32_MAX || d->d_in > kMaxWidth || d->d_out > kMaxWidth) return POETX_ERR_SHAPE;
+  if (d->tokens > kMaxTokens || d->d_in > kMaxWidth || d->d_out > kMaxWidth) return POETX_ERR_SHAPE;
   if (d->activation < POETX_ACT_NONE || d->activation > POETX_ACT_SILU || d->flags != 0 ||
       d->reserved != 0)
     return POETX_ERR_SHAPE;
@@ -101,7 +102,9 @@ FwdPlan plan_fwd(const poetx_dense_desc* d) {
 
 struct BwdPlan {
   TilePlan gx, gw;
-  bool dense;  // g_x on the dense kernel
+  TilePairPlan pair;
+  bool dense;   // g_x on the dense kernel
+  bool paired;  // g_x and g_W, where both are asked for, in one launch
   size_t gu, bias, wq, part, total;
 };
 // whether the products take g_u from the workspace (else g_y is g_u)
@@ -111,10 +114,16 @@ bool forms_gu(const poetx_dense_desc* d) {
 BwdPlan plan_bwd(const poetx_dense_desc* d) {
   BwdPlan p;
   const DType t = dtype_of(d);
-  p.gx = poetx::plan_tile_product(t, d->tokens, d->d_in, d->d_out, false);
-  p.dense = use_dense(t, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in, d->d_in, p.gx);
-  if (p.dense) p.gx.part_floats = 0;
-  p.gw = poetx::plan_tile_product(t, d->d_out, d->d_in, d->tokens, false);
+  const int64_t M = d->tokens, N = d->d_in, K = d->d_out;
+  p.gx = poetx::plan_tile_product(t, M, N, K, false);
+  p.dense = use_dense(t, M, N, K, K, N, N, p.gx);
+  if (p.dense) {
+    p.gx.part_floats = 0;
+    p.gx.cost = dense_cost(M, N, K);
+  }
+  p.gw = poetx::plan_tile_product(t, K, N, M, false);
+  p.pair = poetx::plan_tile_pair(t, M, N, K);
+  p.paired = !int8_weight(d) && p.pair.cost < p.gx.cost + p.gw.cost;
   size_t off = 0;
   p.gu = off;
   if (forms_gu(d)) off += align_up((size_t)d->tokens * d->d_out * act_size(d->act));
@@ -123,7 +132,10 @@ BwdPlan plan_bwd(const poetx_dense_desc* d) {
   p.wq = off;
   off += widened_bytes(d);
   p.part = off;
-  off += align_up(std::max(p.gx.part_floats, int8_weight(d) ? 0 : p.gw.part_floats) * sizeof(float));
+  size_t part = p.gx.part_floats;
+  if (!int8_weight(d)) part = std::max(part, p.gw.part_floats);
+  if (p.paired) part = std::max(part, p.pair.gx.part_floats + p.pair.gw.part_floats);
+  off += align_up(part * sizeof(float));
   p.total = off;
   return p;
 }
@@ -247,7 +259,8 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
   const DType t = dtype_of(d);
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
-  const bool products = g_x || g_W;
+  const bool products = g_x || g_W, pair = plan.paired && g_x && g_W;
+  // (g_u in the dense kernel's fastest layout, which g_W's product cannot read)
   const bool gu_tiled = plan.dense && forms_gu(d) && g_x && !g_W &&
                         d->tokens % poetx::kTileRows == 0;
   const void* gu = g_y;
@@ -262,12 +275,12 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
     a.rows = d->tokens;
     a.d = (int)d->d_out;
     a.act = static_cast<Activation>(d->activation);
-    // (the tiled layout is the dense kernel's fastest; g_W's product does not
-    // read it, nor does K % 32 != 0 reach the dense kernel)
     a.gu_tiled = gu_tiled;
     POETX_TRY(poetx::launch_act_grad(t, a, s));
     if (a.g_u) gu = a.g_u;
   }
+  float* part = reinterpret_cast<float*>(w + plan.part);
+  TileProduct gx, gw;
   if (g_x) {  // g_x = g_u W: B(n, k) = W[k][n]
     const void* B = W;
     if (int8_weight(d)) {
@@ -275,30 +288,31 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
                                           d->d_in, w + plan.wq, false, s));
       B = w + plan.wq;
     }
-    if (plan.dense) {
-      POETX_TRY(poetx::launch_dense(gu, B, g_x, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in,
-                                    d->d_in, false, gu_tiled, false, s));
-    } else {
-      TileProduct p;
-      p.A = gu; p.lda = d->d_out;
-      p.B = B; p.ldb = d->d_in;
-      p.M = (int)d->tokens; p.N = (int)d->d_in; p.K = (int)d->d_out;
-      p.part = reinterpret_cast<float*>(w + plan.part);
-      p.ep.y = g_x;
-      p.ep.ld = d->d_in;
-      POETX_TRY(poetx::launch_tile_product(t, plan.gx, p, true, false, s));
-    }
+    gx.A = gu; gx.lda = d->d_out;
+    gx.B = B; gx.ldb = d->d_in;
+    gx.M = (int)d->tokens; gx.N = (int)d->d_in; gx.K = (int)d->d_out;
+    gx.part = part;
+    gx.ep.y = g_x;
+    gx.ep.ld = d->d_in;
   }
   if (g_W) {  // g_W = g_u^T x: A(m, k) = g_u[k][m], B(n, k) = x[k][n]
-    TileProduct p;
-    p.A = gu; p.lda = d->d_out;
-    p.B = x; p.ldb = d->d_in;
-    p.M = (int)d->d_out; p.N = (int)d->d_in; p.K = (int)d->tokens;
-    p.part = reinterpret_cast<float*>(w + plan.part);
-    p.ep.y = g_W;
-    p.ep.ld = d->d_in;
-    POETX_TRY(poetx::launch_tile_product(t, plan.gw, p, false, false, s));
+    gw.A = gu; gw.lda = d->d_out;
+    gw.B = x; gw.ldb = d->d_in;
+    gw.M = (int)d->d_out; gw.N = (int)d->d_in; gw.K = (int)d->tokens;
+    gw.part = pair ? part + plan.pair.gx.part_floats : part;
+    gw.ep.y = g_W;
+    gw.ep.ld = d->d_in;
   }
+  if (pair) {
+    POETX_TRY(poetx::launch_tile_pair(t, plan.pair, gx, gw, s));
+    return POETX_OK;
+  }
+  if (g_x && plan.dense)
+    POETX_TRY(poetx::launch_dense(gu, gx.B, g_x, d->tokens, d->d_in, d->d_out, d->d_out, d->d_in,
+                                  d->d_in, false, gu_tiled, false, s));
+  else if (g_x)
+    POETX_TRY(poetx::launch_tile_product(t, plan.gx, gx, true, false, s));
+  if (g_W) POETX_TRY(poetx::launch_tile_product(t, plan.gw, gw, false, false, s));
   return POETX_OK;
 }
 

@@ -256,6 +256,15 @@ struct TilePlan {
 TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8);
 hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
                                bool b_kmajor, hipStream_t s);
+// A backward's g_x = g_u W (A K-major) and g_W = g_u^T x (A M-major), both
+// with an N-major B, in one launch; each has its own part.
+struct TilePairPlan {
+  TilePlan gx, gw;
+  float cost;
+};
+TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out);
+hipError_t launch_tile_pair(DType t, const TilePairPlan& plan, TileProduct gx, TileProduct gw,
+                            hipStream_t s);
 
 // The same with A and B K-major bf16 on the dense kernel's 256 x 256 tile
 // loop, where dense_supported(M, N, K, lda, ldb, ep.ld) holds; B tiled as in

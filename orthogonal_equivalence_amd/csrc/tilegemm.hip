@@ -280,8 +280,15 @@ template <int LPW, int NS> __device__ __forceinline__ void wait_steps(int n) {
   }
 }
 
+// bytes of the ring of a BM x BN shape
+template <typename T, typename TB, int BM, int BN, int NW, int NS> constexpr int ring_bytes() {
+  return NS * (Operand<T, BM, true, NW>::BYTES + Operand<TB, BN, true, NW>::BYTES);
+}
+
+// One workgroup's tile (its place `wg` among p's tiles, part `part_k` of a
+// split reduction).
 template <typename T, typename TB, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS>
-__global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct p) {
+__device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part_k, char* ring) {
   constexpr int NW = WM * WN;
   typedef Operand<T, BM, A_KMAJ, NW> OpA;
   typedef Operand<TB, BN, B_KMAJ, NW> OpB;
@@ -290,17 +297,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
   constexpr int FM = TM / 16, FN = TN / 16;
   constexpr int SLOT = OpA::BYTES + OpB::BYTES;
   constexpr int LPW = OpA::PIECES + OpB::PIECES;
-  __shared__ __attribute__((aligned(1024))) char ring[NS * SLOT];
+  static_assert(NS * SLOT == ring_bytes<T, TB, BM, BN, NW, NS>(), "one ring");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
+  const int num_mt = (p.M + BM - 1) / BM, num_nt = (p.N + BN - 1) / BN;
   int mt, nt;
-  xcd_grouped_tile((p.M + BM - 1) / BM, (p.N + BN - 1) / BN, mt, nt);
+  xcd_grouped_tile_at(wg, num_mt * num_nt, num_mt, num_nt, mt, nt);
   const int m0 = __builtin_amdgcn_readfirstlane(mt * BM);
   const int n0 = __builtin_amdgcn_readfirstlane(nt * BN);
-  const int t0 = blockIdx.y * (p.kchunk / BK);
-  const int steps = (min(p.K, (int)(blockIdx.y + 1) * p.kchunk) + BK - 1) / BK - t0;
+  const int t0 = part_k * (p.kchunk / BK);
+  const int steps = (min(p.K, (part_k + 1) * p.kchunk) + BK - 1) / BK - t0;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)ring)));
 
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
 
   // (operand roles swapped: lane l holds row 16 i + l % 16, columns
   // 16 j + 4 (l / 16) .. + 3 of its wave's tile)
-  float* part = p.part ? p.part + (int64_t)blockIdx.y * p.M * p.N : nullptr;
+  float* part = p.part ? p.part + (int64_t)part_k * p.M * p.N : nullptr;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + wm * TM + 16 * i + (lane & 15);
@@ -447,6 +455,33 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
       if (part) Quad<float>::store(part + (int64_t)m * p.N + n, v);
       else epilogue4<T>(p.ep, m, n, v);
     }
+  }
+}
+
+template <typename T, typename TB, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS>
+__global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct p) {
+  __shared__ __attribute__((aligned(1024))) char ring[ring_bytes<T, TB, BM, BN, WM * WN, NS>()];
+  tile_body<T, TB, BM, BN, WM, WN, A_KMAJ, B_KMAJ, NS>(p, blockIdx.x, blockIdx.y, ring);
+}
+
+// The backward's two products, which are independent, in one launch: g_x = g_u
+// W (gx: A K-major, B N-major) and g_W = g_u^T x (gw: both M-, N-major). The
+// product with the longer reduction comes first, so that its tiles do not
+// start last. padded: its workgroups, rounded up to the 8 XCDs (the ones past
+// its tiles return at once).
+template <typename T, int BM, int BN, int WM, int WN, int NS>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+tile_pair_kernel(const TileProduct gx, const TileProduct gw, int gx_tiles, int gw_tiles, int gx_wgs,
+                 int gw_wgs, int padded, int gx_first) {
+  __shared__ __attribute__((aligned(1024))) char ring[ring_bytes<T, T, BM, BN, WM * WN, NS>()];
+  const bool first = (int)blockIdx.x < padded;
+  const int wg = first ? blockIdx.x : blockIdx.x - padded;
+  if (first == (gx_first != 0)) {
+    if (wg >= gx_wgs) return;
+    tile_body<T, T, BM, BN, WM, WN, true, false, NS>(gx, wg % gx_tiles, wg / gx_tiles, ring);
+  } else {
+    if (wg >= gw_wgs) return;
+    tile_body<T, T, BM, BN, WM, WN, false, false, NS>(gw, wg % gw_tiles, wg / gw_tiles, ring);
   }
 }
 
@@ -512,6 +547,22 @@ hipError_t launch_cfg(bool ak, bool bk, const TileProduct& p, int nsplit, hipStr
   return hipGetLastError();
 }
 
+template <typename T, int BM, int BN, int WM, int WN, int NS>
+hipError_t launch_pair_cfg(const TileProduct& gx, int gx_split, const TileProduct& gw, int gw_split,
+                           hipStream_t s) {
+  const int64_t tx = (int64_t)((gx.M + BM - 1) / BM) * ((gx.N + BN - 1) / BN);
+  const int64_t tw = (int64_t)((gw.M + BM - 1) / BM) * ((gw.N + BN - 1) / BN);
+  const bool gx_first = gx.kchunk >= gw.kchunk;
+  const int64_t first = gx_first ? tx * gx_split : tw * gw_split;
+  const int64_t padded = (first + 7) / 8 * 8;
+  const int64_t grid = padded + (gx_first ? tw * gw_split : tx * gx_split);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((tile_pair_kernel<T, BM, BN, WM, WN, NS>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, s, gx, gw, (int)tx, (int)tw, (int)(tx * gx_split),
+                     (int)(tw * gw_split), (int)padded, (int)gx_first);
+  return hipGetLastError();
+}
+
 // The tile shapes: workgroups that fit a CU, and what one step of 128 bytes
 // of k costs there (us) with one of them on it and with all, measured on an
 // MI355X with operands in the caches.
@@ -531,7 +582,7 @@ constexpr Shape kF32Shapes[] = {{64, 64, 2, 0.56f, 0.90f, false}, {32, 64, 3, 0.
 constexpr int kCus = 256;
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 constexpr float kLaunch = 3.0f;            // us of a launch and its first loads
-constexpr float kFinish = 2.5f;            // and of the pass that joins the partial tiles
+constexpr float kFinish = 3.5f;            // and of the pass that joins the partial tiles
 constexpr float kPartBytesPerUs = 6.0e6f;  // which are written and read near the cores
 constexpr float kHbmBytesPerUs = 6.2e6f;
 // operands that come from HBM rather than a cache lengthen the steps by about
@@ -581,11 +632,109 @@ TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8
   return best;
 }
 
-hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
-                               bool b_kmajor, hipStream_t s) {
+// The two products of a backward in one launch: for each shape and pair of
+// splits, the steps of both over the chip, or the longer one's chain if that
+// is more, by the same constants.
+TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out) {
+  const bool bf16 = t == DType::BF16;
+  const Shape* shapes = bf16 ? kBf16Shapes : kF32Shapes;
+  const int nshapes = (int)((bf16 ? sizeof(kBf16Shapes) : sizeof(kF32Shapes)) / sizeof(Shape));
+  const int bk = bf16 ? 64 : 32, es = bf16 ? 2 : 4;
+  const int64_t M[2] = {tokens, d_out}, N = d_in, K[2] = {d_out, tokens};
+  const float hbm = (float)((2 * tokens * d_in + tokens * d_out + 2 * d_in * d_out) * es) /
+                    kHbmBytesPerUs;
+  TilePairPlan best = {};
+  best.cost = 1e30f;
+  for (int i = bf16 ? 1 : 0; i < nshapes; ++i) {  // (256 x 128: large products, which fill the chip)
+    const Shape& h = shapes[i];
+    int64_t tiles[2];
+    int steps[2];
+    for (int q = 0; q < 2; ++q) {
+      tiles[q] = ((M[q] + h.bm - 1) / h.bm) * ((N + h.bn - 1) / h.bn);
+      steps[q] = (int)((K[q] + bk - 1) / bk);
+    }
+    for (int sx : kSplits) {
+      for (int sw : kSplits) {
+        const int want[2] = {sx, sw};
+        int per[2];
+        bool ok = true;
+        float work = 0.0f, extra = 0.0f;
+        for (int q = 0; q < 2; ++q) {
+          per[q] = (steps[q] + want[q] - 1) / want[q];
+          const int split = (steps[q] + per[q] - 1) / per[q];
+          ok = ok && split == want[q] && (split == 1 || per[q] >= 8);
+          work += (float)(tiles[q] * split) * (float)per[q];
+          if (split > 1) extra += kFinish + (float)(2 * split * M[q] * N * 4) / kPartBytesPerUs;
+        }
+        if (!ok) continue;
+        const float slots = (float)(kCus * h.per_cu), longest = (float)std::max(per[0], per[1]);
+        const float shorter = (float)std::min(per[0], per[1]);
+        // (the chip full throughout, and half a short workgroup's time of tail)
+        const float busy = std::max(work / slots * h.full + 0.5f * shorter * h.alone,
+                                    longest * h.alone);
+        const float cost = kLaunch + busy + kCold * hbm + extra;
+        if (cost < best.cost) {
+          best.cost = cost;
+          best.gx = TilePlan{i, sx, per[0] * bk, sx > 1 ? (size_t)sx * M[0] * N : 0, 0.0f};
+          best.gw = TilePlan{i, sw, per[1] * bk, sw > 1 ? (size_t)sw * M[1] * N : 0, 0.0f};
+        }
+      }
+    }
+  }
+  return best;
+}
+
+namespace {
+
+// joins a split product's partial tiles
+hipError_t finish(DType t, const TilePlan& plan, const TileProduct& p, hipStream_t s) {
+  if (plan.nsplit == 1) return hipSuccess;
+  const int64_t groups = (int64_t)p.M * (p.N / 4);
+  const int grid = (int)std::min<int64_t>((groups + NT - 1) / NT, 4096);
+  if (t == DType::BF16)
+    hipLaunchKernelGGL(finish_kernel<bf16_t>, dim3(grid), dim3(NT), 0, s, p.part, plan.nsplit,
+                       (int64_t)p.M, p.N, p.ep);
+  else
+    hipLaunchKernelGGL(finish_kernel<float>, dim3(grid), dim3(NT), 0, s, p.part, plan.nsplit,
+                       (int64_t)p.M, p.N, p.ep);
+  return hipGetLastError();
+}
+
+// p as `plan` has it; false: a split without room for its partial tiles
+bool apply_plan(const TilePlan& plan, TileProduct& p) {
   p.kchunk = plan.kchunk;
   if (plan.nsplit == 1) p.part = nullptr;
-  else if (!p.part) return hipErrorInvalidValue;
+  return plan.nsplit == 1 || p.part;
+}
+
+}  // namespace
+
+hipError_t launch_tile_pair(DType t, const TilePairPlan& plan, TileProduct gx, TileProduct gw,
+                            hipStream_t s) {
+  if (!apply_plan(plan.gx, gx) || !apply_plan(plan.gw, gw) || plan.gx.shape != plan.gw.shape)
+    return hipErrorInvalidValue;
+  const int sx = plan.gx.nsplit, sw = plan.gw.nsplit;
+  hipError_t e = hipErrorInvalidValue;
+  if (t == DType::F32) {
+    switch (plan.gx.shape) {  // kF32Shapes
+      case 0: e = launch_pair_cfg<float, 64, 64, 2, 2, 4>(gx, sx, gw, sw, s); break;
+      case 1: e = launch_pair_cfg<float, 32, 64, 1, 4, 4>(gx, sx, gw, sw, s); break;
+    }
+  } else {
+    switch (plan.gx.shape) {  // kBf16Shapes
+      case 1: e = launch_pair_cfg<bf16_t, 128, 128, 2, 4, 4>(gx, sx, gw, sw, s); break;
+      case 2: e = launch_pair_cfg<bf16_t, 128, 64, 4, 2, 4>(gx, sx, gw, sw, s); break;
+      case 3: e = launch_pair_cfg<bf16_t, 64, 64, 2, 2, 4>(gx, sx, gw, sw, s); break;
+      case 4: e = launch_pair_cfg<bf16_t, 32, 64, 1, 4, 6>(gx, sx, gw, sw, s); break;
+    }
+  }
+  if (e == hipSuccess) e = finish(t, plan.gx, gx, s);
+  return e == hipSuccess ? finish(t, plan.gw, gw, s) : e;
+}
+
+hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
+                               bool b_kmajor, hipStream_t s) {
+  if (!apply_plan(plan, p)) return hipErrorInvalidValue;
   hipError_t e = hipErrorInvalidValue;
   if (t == DType::F32) {
     switch (plan.shape) {  // kF32Shapes
@@ -601,16 +750,7 @@ hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, boo
       case 4: e = launch_cfg<bf16_t, 32, 64, 1, 4, 6, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
     }
   }
-  if (e != hipSuccess || plan.nsplit == 1) return e;
-  const int64_t groups = (int64_t)p.M * (p.N / 4);
-  const int grid = (int)std::min<int64_t>((groups + NT - 1) / NT, 4096);
-  if (t == DType::BF16)
-    hipLaunchKernelGGL(finish_kernel<bf16_t>, dim3(grid), dim3(NT), 0, s, p.part, plan.nsplit,
-                       (int64_t)p.M, p.N, p.ep);
-  else
-    hipLaunchKernelGGL(finish_kernel<float>, dim3(grid), dim3(NT), 0, s, p.part, plan.nsplit,
-                       (int64_t)p.M, p.N, p.ep);
-  return hipGetLastError();
+  return e == hipSuccess ? finish(t, plan, p, s) : e;
 }
 
 }  // namespace poetx
