@@ -31,15 +31,17 @@ constexpr int kMaxRuns = 120;        // 3.5 KB of the 4 KB of kernel arguments
 constexpr int kChunkBytes = 16384;   // four 16-byte loads a thread
 constexpr int kMaxParts = 2048;      // workgroups of a pass: eight per CU
 
-struct Batch {
-  const void* grad[kMaxRuns];
-  void* out[kMaxRuns];
-  int64_t n[kMaxRuns];
-  int32_t first[kMaxRuns + 1];  // chunks before run i
-  int8_t bf16[kMaxRuns];
+constexpr int kFewRuns = 16;         // a short list's arguments: 0.5 KB a launch
+
+template <int N> struct Batch {
+  const void* grad[N];
+  void* out[N];
+  int64_t n[N];
+  int32_t first[N + 1];  // chunks before run i
+  int8_t bf16[N];
   int count;
 };
-static_assert(sizeof(Batch) < 3900, "kernel argument space");
+static_assert(sizeof(Batch<kMaxRuns>) < 3900, "kernel argument space");
 
 int64_t chunks_of(const GradRun& r) {
   const int64_t per = kChunkBytes / (r.dtype == DType::BF16 ? 2 : 4);
@@ -47,7 +49,7 @@ int64_t chunks_of(const GradRun& r) {
 }
 
 // the run that holds `chunk`
-__device__ __forceinline__ int find_run(const Batch& b, int chunk) {
+template <int N> __device__ __forceinline__ int find_run(const Batch<N>& b, int chunk) {
   int lo = 0, hi = b.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -161,7 +163,8 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int64_t n, int64_t
 
 // a whole chunk's 16-byte vectors of one thread, or null: a cut or unaligned
 // chunk
-__device__ __forceinline__ const uint4* whole_chunk(const Batch& b, int chunk, int* bf16) {
+template <int N>
+__device__ __forceinline__ const uint4* whole_chunk(const Batch<N>& b, int chunk, int* bf16) {
   const int i = find_run(b, chunk);
   const int64_t at = (int64_t)(chunk - b.first[i]) * kChunkBytes;
   const char* p = static_cast<const char*>(b.grad[i]);
@@ -171,7 +174,8 @@ __device__ __forceinline__ const uint4* whole_chunk(const Batch& b, int chunk, i
   return whole ? reinterpret_cast<const uint4*>(p + at) + threadIdx.x : nullptr;
 }
 
-__global__ void __launch_bounds__(NT) sumsq_kernel(const Batch b, double* __restrict__ part) {
+template <int N>
+__global__ void __launch_bounds__(NT) sumsq_kernel(const Batch<N> b, double* __restrict__ part) {
   constexpr int Q = kChunkBytes / 16 / NT;
   const int total = b.first[b.count];
   double acc = 0.0;
@@ -227,8 +231,9 @@ norm_kernel(const double* __restrict__ part, int nparts, float* __restrict__ nor
   if (threadIdx.x == 0) *norm = (float)sqrt(t);
 }
 
+template <int N>
 __global__ void __launch_bounds__(NT)
-scale_kernel(const Batch b, const double* part, int nparts, const float* norm_in, float max_norm,
+scale_kernel(const Batch<N> b, const double* part, int nparts, const float* norm_in, float max_norm,
              float* norm_out) {
   const double norm = part ? sqrt(parts_sum(part, nparts)) : (double)*norm_in;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
@@ -253,14 +258,15 @@ int launches_of(int count) { return (count + kMaxRuns - 1) / kMaxRuns; }
 int parts_per_launch(int count) { return std::max(64, kMaxParts / std::max(1, launches_of(count))); }
 
 // The runs in launches of at most kMaxRuns, in order. fn(batch, workgroups).
-template <typename F> hipError_t for_batches(const GradRun* runs, int count, F fn) {
+template <int N, typename F>
+hipError_t for_batches_of(const GradRun* runs, int count, F fn) {
   const int cap = parts_per_launch(count);
-  Batch b;
+  Batch<N> b;
   for (int i = 0; i < count;) {
     b.count = 0;
     int64_t chunks = 0;
     b.first[0] = 0;
-    for (; i < count && b.count < kMaxRuns; ++i, ++b.count) {
+    for (; i < count && b.count < N; ++i, ++b.count) {
       b.grad[b.count] = runs[i].grad;
       b.out[b.count] = runs[i].out;
       b.n[b.count] = runs[i].n;
@@ -274,6 +280,10 @@ template <typename F> hipError_t for_batches(const GradRun* runs, int count, F f
   }
   return hipSuccess;
 }
+template <typename F> hipError_t for_batches(const GradRun* runs, int count, F fn) {
+  return count <= kFewRuns ? for_batches_of<kFewRuns>(runs, count, fn)
+                           : for_batches_of<kMaxRuns>(runs, count, fn);
+}
 
 }  // namespace
 
@@ -284,7 +294,7 @@ int64_t grad_partials_max(int count) {
 hipError_t launch_grad_sumsq(const GradRun* runs, int count, double* part, int* nparts,
                              hipStream_t s) {
   *nparts = 0;
-  return for_batches(runs, count, [&](const Batch& b, int wgs) {
+  return for_batches(runs, count, [&](const auto& b, int wgs) {
     hipLaunchKernelGGL(sumsq_kernel, dim3(wgs), dim3(NT), 0, s, b, part + *nparts);
     *nparts += wgs;
     return hipGetLastError();
@@ -299,7 +309,7 @@ hipError_t launch_grad_norm(const double* part, int nparts, float* norm, hipStre
 hipError_t launch_grad_scale(const GradRun* runs, int count, const double* part, int nparts,
                              const float* norm_in, float max_norm, float* norm_out,
                              hipStream_t s) {
-  return for_batches(runs, count, [&](const Batch& b, int wgs) {
+  return for_batches(runs, count, [&](const auto& b, int wgs) {
     hipLaunchKernelGGL(scale_kernel, dim3(wgs), dim3(NT), 0, s, b, part, nparts, norm_in, max_norm,
                        norm_out);
     norm_out = nullptr;  // the first launch stores it

@@ -645,39 +645,40 @@ TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out
                     kHbmBytesPerUs;
   TilePairPlan best = {};
   best.cost = 1e30f;
+  constexpr int kNumSplits = (int)(sizeof(kSplits) / sizeof(kSplits[0]));
   for (int i = bf16 ? 1 : 0; i < nshapes; ++i) {  // (256 x 128: large products, which fill the chip)
     const Shape& h = shapes[i];
-    int64_t tiles[2];
-    int steps[2];
+    const float slots = (float)(kCus * h.per_cu);
+    struct Option {
+      int split, per;
+      float work, extra;
+    } opt[2][kNumSplits];
+    int nopt[2] = {0, 0};
     for (int q = 0; q < 2; ++q) {
-      tiles[q] = ((M[q] + h.bm - 1) / h.bm) * ((N + h.bn - 1) / h.bn);
-      steps[q] = (int)((K[q] + bk - 1) / bk);
+      const int64_t tiles = ((M[q] + h.bm - 1) / h.bm) * ((N + h.bn - 1) / h.bn);
+      const int steps = (int)((K[q] + bk - 1) / bk);
+      for (int want : kSplits) {
+        const int per = (steps + want - 1) / want, split = (steps + per - 1) / per;
+        if (split != want || (split > 1 && (per < 8 || tiles >= (int64_t)slots))) continue;
+        const float extra =
+            split > 1 ? kFinish + (float)(2 * split * M[q] * N * 4) / kPartBytesPerUs : 0.0f;
+        opt[q][nopt[q]++] = Option{split, per, (float)(tiles * split) * (float)per, extra};
+      }
     }
-    for (int sx : kSplits) {
-      for (int sw : kSplits) {
-        const int want[2] = {sx, sw};
-        int per[2];
-        bool ok = true;
-        float work = 0.0f, extra = 0.0f;
-        for (int q = 0; q < 2; ++q) {
-          per[q] = (steps[q] + want[q] - 1) / want[q];
-          const int split = (steps[q] + per[q] - 1) / per[q];
-          ok = ok && split == want[q] && (split == 1 || per[q] >= 8);
-          work += (float)(tiles[q] * split) * (float)per[q];
-          if (split > 1) extra += kFinish + (float)(2 * split * M[q] * N * 4) / kPartBytesPerUs;
-        }
-        if (!ok) continue;
-        const float slots = (float)(kCus * h.per_cu), longest = (float)std::max(per[0], per[1]);
-        const float shorter = (float)std::min(per[0], per[1]);
+    for (int x = 0; x < nopt[0]; ++x) {
+      for (int w = 0; w < nopt[1]; ++w) {
+        const Option &ox = opt[0][x], &ow = opt[1][w];
         // (the chip full throughout, and half a short workgroup's time of tail)
-        const float busy = std::max(work / slots * h.full + 0.5f * shorter * h.alone,
-                                    longest * h.alone);
-        const float cost = kLaunch + busy + kCold * hbm + extra;
-        if (cost < best.cost) {
-          best.cost = cost;
-          best.gx = TilePlan{i, sx, per[0] * bk, sx > 1 ? (size_t)sx * M[0] * N : 0, 0.0f};
-          best.gw = TilePlan{i, sw, per[1] * bk, sw > 1 ? (size_t)sw * M[1] * N : 0, 0.0f};
-        }
+        const float busy = std::max((ox.work + ow.work) / slots * h.full +
+                                        0.5f * (float)std::min(ox.per, ow.per) * h.alone,
+                                    (float)std::max(ox.per, ow.per) * h.alone);
+        const float cost = kLaunch + busy + kCold * hbm + ox.extra + ow.extra;
+        if (cost >= best.cost) continue;
+        best.cost = cost;
+        best.gx = TilePlan{i, ox.split, ox.per * bk,
+                           ox.split > 1 ? (size_t)ox.split * M[0] * N : 0, 0.0f};
+        best.gw = TilePlan{i, ow.split, ow.per * bk,
+                           ow.split > 1 ? (size_t)ow.split * M[1] * N : 0, 0.0f};
       }
     }
   }

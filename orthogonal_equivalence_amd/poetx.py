@@ -162,11 +162,16 @@ def _ptr(t):
     return t.data_ptr() or None
 
 
+_has_gpu = None  # asked once
+
+
 def _stream(stream):
+    global _has_gpu
     if stream is None:
-        if not torch.cuda.is_available():
-            return None
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _has_gpu is None:
+            _has_gpu = torch.cuda.is_available()
+        # (the stream's address alone: a Stream object costs as much as a launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if _has_gpu else None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream
