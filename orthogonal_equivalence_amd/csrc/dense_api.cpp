@@ -180,7 +180,8 @@ int poetx_dense_fwd(const poetx_dense_desc* d, const void* x, const void* W, con
   if (plan.total && (!ws || ws_bytes < plan.total)) return POETX_ERR_WORKSPACE;
   if (plan.total && !aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t es = act_size(d->act), out = (size_t)d->tokens * d->d_out * es;
-  const Range outs[] = {range_of(y, out), opt_range(u_save, out), opt_range(ws, plan.total)};
+  const Range outs[] = {range_of(y, out), opt_range(u_save, out),
+                        opt_range(plan.total ? ws : nullptr, plan.total)};
   const Range ins[] = {range_of(x, (size_t)d->tokens * d->d_in * es), range_of(W, weight_bytes(d)),
                        opt_range(bias, (size_t)d->d_out * 4), opt_range(residual, out),
                        opt_range(d->w_scale, (size_t)d->d_out * 4)};
@@ -242,6 +243,10 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
   if ((g_x && !W) || (g_W && !x)) return POETX_ERR_NULL;
   if (d->activation != POETX_ACT_NONE && !u_saved) return POETX_ERR_NULL;
   if (g_W && int8_weight(d)) return POETX_ERR_DTYPE;  // codes have no gradient
+  // (what this choice of outputs does not read is not looked at)
+  if (!g_x) W = nullptr;
+  if (!g_W) x = nullptr;
+  if (d->activation == POETX_ACT_NONE) u_saved = nullptr;
   for (const void* p : {g_y, x, W, u_saved, (const void*)g_x, (const void*)g_W,
                         (const void*)g_bias})
     if (p && !aligned16(p)) return POETX_ERR_ALIGN;

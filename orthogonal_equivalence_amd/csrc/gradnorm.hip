@@ -237,8 +237,9 @@ scale_kernel(const Batch<N> b, const double* part, int nparts, const float* norm
              float* norm_out) {
   const double norm = part ? sqrt(parts_sum(part, nparts)) : (double)*norm_in;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  // (a NaN or infinite norm compares false or is refused: factor 1)
-  const bool clip = norm > (double)max_norm && norm < (double)INFINITY;
+  // (factor 1 for a norm that is NaN, infinite or past float32's range, as the
+  // caller reads it)
+  const bool clip = norm > (double)max_norm && (float)norm < INFINITY;
   const float k = clip ? (float)((double)max_norm / norm) : 1.0f;
   const int total = b.first[b.count];
   for (int c = total - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {

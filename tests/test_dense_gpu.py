@@ -166,6 +166,22 @@ def test_backward(i, dtype):
         check_backward(t, dt, act, g_W=not int8)
 
 
+# products large enough for the 256 x 256 tiles, whole (the tiled layouts of
+# INT8 codes and of g_u) and ragged in rows, columns and both reductions
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+@pytest.mark.parametrize("tokens,d_in,d_out", [(4096, 1024, 4096), (4096, 4096, 1024),
+                                               (4200, 1056, 4360), (4333, 4360, 1056),
+                                               (2048, 4096, 14336)])
+def test_large(tokens, d_in, d_out, dtype):
+    int8 = dtype == "int8"
+    t = make(tokens, d_in, d_out, "bf16", seed=41, int8=int8)
+    print(f"  {tokens}x{d_in}x{d_out} {dtype}", flush=True)
+    check_forward(t, "bf16", "silu")
+    check_forward(t, "bf16", "none", bias=False)
+    check_backward(t, "bf16", "gelu", g_W=False)
+    check_backward(t, "bf16", "none", g_W=not int8)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_every_activation(act, dtype):

@@ -130,6 +130,15 @@ def test_a_norm_that_is_not_finite_leaves_the_values(bad):
         assert torch.equal(o.nan_to_num(7.0), r.nan_to_num(7.0))
 
 
+def test_a_norm_past_float32():
+    """Finite values whose norm float32 cannot hold: infinite as it is read,
+    so the values stay."""
+    g = [torch.full((100,), 3e38, device="cuda"), torch.ones(5, device="cuda", dtype=B)]
+    ref = [t.clone() for t in g]
+    assert clip_grads(g, 1.0).item() == math.inf
+    assert all(torch.equal(a, r) for a, r in zip(g, ref))
+
+
 def test_by_a_given_norm():
     g = make([(5000, F), (777, B)], seed=5)
     a, b = [t.clone() for t in g], [t.clone() for t in g]

@@ -112,6 +112,15 @@ def test_aliases():
     assert bwd(d, ws=5 * A) == P.POETX_ERR_ALIAS
 
 
+def test_what_is_not_read_may_be_anything():
+    """An unused u, x or W over an output, or misaligned, is no error: the call
+    gets as far as its workspace."""
+    none = desc(activation=P.POETX_ACT_NONE)
+    for d, over in ((none, dict(u=5 * A)), (none, dict(u=3)), (desc(), dict(g_W=None, x=5 * A)),
+                    (desc(), dict(g_x=None, W=6 * A + 1))):
+        assert bwd(d, ws=None, **over) == P.POETX_ERR_WORKSPACE
+
+
 def test_codes_have_no_gradient():
     assert bwd(desc(w_scale=A * 16)) == P.POETX_ERR_DTYPE
 
