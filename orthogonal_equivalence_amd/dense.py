@@ -31,15 +31,16 @@ def _on(device, stream):
     """The tensors' device, and `stream` (a torch stream, or a hipStream_t
     address) as the current one."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream else
+                  torch.cuda.default_stream(device))
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
 
 
 def _check(name, t, shape, dtype, device):
-    if t is None:
-        return
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
@@ -49,30 +50,35 @@ def _check(name, t, shape, dtype, device):
 
 def _desc(name, t, W, activation, w_scale, width):
     """Checks the weight against the activations t (their columns are W's
-    dimension `width`) and makes the descriptor."""
-    if activation not in ACTIVATIONS:
+    dimension `width`); the descriptor, the workspace bytes and t's device."""
+    code, act = ACTIVATIONS.get(activation), _ACT.get(t.dtype)
+    if code is None:
         raise ValueError(f"unknown activation {activation!r}")
-    if t.dim() != 2 or W.dim() != 2:
-        raise ValueError(f"{name} and W must have two dimensions")
-    if t.dtype not in _ACT:
+    if act is None:
         raise ValueError(f"{name} is {t.dtype}, expected float32 or bfloat16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    d_out, d_in = W.shape
-    _check(name, t, (t.shape[0], W.shape[width]), t.dtype, t.device)
-    _check("W", W, (d_out, d_in), torch.int8 if w_scale is not None else t.dtype, t.device)
-    _check("w_scale", w_scale, (d_out,), torch.float32, t.device)
-    desc, ws = _plan(t.shape[0], d_in, d_out, _ACT[t.dtype], ACTIVATIONS[activation],
-                     w_scale is not None, width == 1)
-    if w_scale is not None:
-        desc = P.make_dense_desc(desc.tokens, d_in, d_out, desc.act, desc.activation, w_scale)
-    return desc, ws
+    shape, w_shape, device = t.shape, W.shape, t.device
+    if len(shape) != 2 or len(w_shape) != 2:
+        raise ValueError(f"{name} and W must have two dimensions")
+    tokens, (d_out, d_in) = shape[0], w_shape
+    if shape[1] != w_shape[width]:
+        raise ValueError(f"{name} has {shape[1]} columns, W is {tuple(w_shape)}")
+    _check("W", W, w_shape, t.dtype if w_scale is None else torch.int8, device)
+    if w_scale is None:
+        desc, ws = _plan(tokens, d_in, d_out, act, code, False, width)
+    else:
+        _check("w_scale", w_scale, (d_out,), torch.float32, device)
+        desc, ws = _plan(tokens, d_in, d_out, act, code, True, width)
+        desc = P.make_dense_desc(tokens, d_in, d_out, act, code, w_scale)
+    return desc, ws, device
 
 
 @functools.lru_cache(maxsize=4096)
 def _plan(tokens, d_in, d_out, act, activation, int8, forward):
     """The descriptor of these sizes (its w_scale, with int8, a placeholder)
-    and its workspace bytes: both follow from the sizes alone."""
+    and its workspace bytes (forward: 1, backward: 0): both follow from the
+    sizes alone."""
     desc = P.make_dense_desc(tokens, d_in, d_out, act, activation, 16 if int8 else None)
     size = P.poetx_dense_fwd_workspace_size if forward else P.poetx_dense_bwd_workspace_size
     return desc, size(desc)
@@ -91,13 +97,15 @@ def dense_forward(x, W, bias=None, residual=None, activation="none", w_scale=Non
                   stream=None):
     """Returns (y, u): u, the pre-activation that dense_backward takes, with
     save_u, else None."""
-    desc, nbytes = _desc("x", x, W, activation, w_scale, 1)
-    out = (x.shape[0], W.shape[0])
-    _check("bias", bias, out[1:], torch.float32, x.device)
-    _check("residual", residual, out, x.dtype, x.device)
-    if _here(x.device, stream):
+    desc, nbytes, device = _desc("x", x, W, activation, w_scale, 1)
+    out = (desc.tokens, desc.d_out)
+    if bias is not None:
+        _check("bias", bias, out[1:], torch.float32, device)
+    if residual is not None:
+        _check("residual", residual, out, x.dtype, device)
+    if _here(device, stream):
         return _forward(desc, x, W, bias, residual, out, save_u, nbytes)
-    with _on(x.device, stream):
+    with _on(device, stream):
         return _forward(desc, x, W, bias, residual, out, save_u, nbytes)
 
 
@@ -113,10 +121,11 @@ def dense_backward(g_y, W, x=None, u=None, activation="none", w_scale=None, need
     """Returns (g_x, g_W, g_bias), None in the place of one not asked for. x is
     needed for g_W, u (dense_forward's, with save_u) for an activation. The
     gradient of the residual is g_y itself. int8 codes have no g_W."""
-    desc, nbytes = _desc("g_y", g_y, W, activation, w_scale, 0)
-    d_out, d_in = W.shape
-    _check("x", x, (g_y.shape[0], d_in), g_y.dtype, g_y.device)
-    _check("u", u, tuple(g_y.shape), g_y.dtype, g_y.device)
+    desc, nbytes, device = _desc("g_y", g_y, W, activation, w_scale, 0)
+    if x is not None:
+        _check("x", x, (desc.tokens, desc.d_in), g_y.dtype, device)
+    if u is not None:
+        _check("u", u, g_y.shape, g_y.dtype, device)
     if need_g_W and x is None:
         raise ValueError("g_W needs x")
     if need_g_W and w_scale is not None:
@@ -125,17 +134,16 @@ def dense_backward(g_y, W, x=None, u=None, activation="none", w_scale=None, need
         raise ValueError("the backward of an activation needs u")
     if not (need_g_x or need_g_W or need_g_bias):
         raise ValueError("no gradient asked for")
-    if _here(g_y.device, stream):
+    if _here(device, stream):
         return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes)
-    with _on(g_y.device, stream):
+    with _on(device, stream):
         return _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes)
 
 
 def _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes):
-    d_out, d_in = W.shape
-    g_x = g_y.new_empty((g_y.shape[0], d_in)) if need_g_x else None
-    g_W = g_y.new_empty((d_out, d_in)) if need_g_W else None
-    g_b = g_y.new_empty(d_out, dtype=torch.float32) if need_g_bias else None
+    g_x = g_y.new_empty((desc.tokens, desc.d_in)) if need_g_x else None
+    g_W = g_y.new_empty((desc.d_out, desc.d_in)) if need_g_W else None
+    g_b = g_y.new_empty(desc.d_out, dtype=torch.float32) if need_g_bias else None
     P.poetx_dense_bwd(desc, g_y, x, W, u, g_x, g_W, g_b, _workspace(nbytes, g_y.device))
     return g_x, g_W, g_b
 

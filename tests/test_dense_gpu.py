@@ -342,6 +342,9 @@ def test_other_stream_and_graph():
     sideb = dense_backward(t["g_y"], t["W"], t["x"], side[1], "silu", need_g_W=True,
                            need_g_bias=True, stream=s)
     handle = dense_forward(t["x"], t["W"], t["bias"], t["residual"], "silu", stream=s.cuda_stream)
+    null = dense_forward(t["x"], t["W"], t["bias"], t["residual"], "silu", stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(null[0], ref[0])
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((*ref, *refb, ref[0]), (*side, *sideb, handle[0])))
 
