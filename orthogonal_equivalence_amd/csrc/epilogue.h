@@ -57,8 +57,6 @@ template <Activation ACT> __device__ __forceinline__ float activate(float u) {
 }
 
 template <Activation ACT> __device__ __forceinline__ float activation_slope(float u) {
-  if constexpr (ACT == Activation::None) return 1.0f;
-  if constexpr (ACT == Activation::Relu) return u > 0.0f ? 1.0f : 0.0f;
   const float v = u > 64.0f ? 64.0f : u < -64.0f ? -64.0f : u;
   if constexpr (ACT == Activation::Silu) {
     const float p = logistic(v);
@@ -72,6 +70,13 @@ template <Activation ACT> __device__ __forceinline__ float activation_slope(floa
   float e;
   const float q = normal_tail(v, &e);
   return fmaf(v * 0.3989422804014327f, e, v < 0.0f ? q : 1.0f - q);
+}
+
+// g times the slope at u; relu's is a choice, not a product, so that an
+// infinite g (a loss scale that overflowed) is dropped where the unit is off
+template <Activation ACT> __device__ __forceinline__ float activation_gradient(float g, float u) {
+  if constexpr (ACT == Activation::Relu) return u <= 0.0f ? 0.0f : g;
+  else return g * activation_slope<ACT>(u);
 }
 
 // the run-time activation of a wave-uniform `act`, four values at a time

@@ -1,0 +1,172 @@
+"""Calls of the dense linear and of clipping at the ends of their ranges: rows
+and weights past 2^32 elements, infinite gradients at units that are off, and
+calls that run at the same time on two streams. Tolerances as in the tests of
+the operators: a float32 sum of n products errs by at most 2 (n + 8) 2^-24
+times its sum of absolute values, an output rounding by half a step."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU too; every test here is gpu-marked
+    pytest.skip("no GPU", allow_module_level=True)
+
+from orthogonal_equivalence_amd.dense import dense_backward, dense_forward  # noqa: E402
+from orthogonal_equivalence_amd.grads import clip_grads  # noqa: E402
+
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def near(name, got, ref, err):
+    """err: of the exact value, before the output's rounding."""
+    half = HALF[got.dtype]
+    tol = err + half * (ref.abs() + err) + 1e-30
+    worst = ((got.double() - ref).abs() / tol).max().item()
+    print(f"    {name}: worst error / tolerance {worst:.3f}", flush=True)
+    assert worst <= 1.0, (name, worst)
+
+
+def rows_of(n):
+    """The first and last rows and those around the middle."""
+    return torch.cat([torch.arange(40), torch.arange(n // 2 - 20, n // 2 + 20),
+                      torch.arange(n - 300, n)]).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 70, 300])
+def test_infinite_gradients_of_units_that_are_off(dtype, tokens):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    u = torch.randn(tokens, 136, generator=g, device="cuda").to(dtype)
+    g_y = torch.randn(tokens, 136, generator=g, device="cuda").to(dtype)
+    x = torch.randn(tokens, 64, generator=g, device="cuda").to(dtype)
+    W = torch.randn(136, 64, generator=g, device="cuda").to(dtype)
+    u[0, :8] = torch.tensor([-1.0, 0.0, -0.0, -3e38, -1e-30, -2.0, -float("inf"), -5.0])
+    want = dense_backward(g_y, W, x, u, "relu", need_g_W=True, need_g_bias=True)
+    g_y[0, :8] = torch.tensor([1.0, -1.0, 1.0, 1.0, 1.0, -1.0, 1.0, float("nan")]) * float("inf")
+    got = dense_backward(g_y, W, x, u, "relu", need_g_W=True, need_g_bias=True)
+    for a, b in zip(got, want):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_rows_past_32_bits(dtype):
+    """y, u, residual, g_y and g_u of more than 2^32 elements each."""
+    tokens, d_in, d_out = 300_031, 64, 14_336
+    assert tokens * d_out > 2 ** 32
+    half = HALF[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(tokens, d_in, generator=gen, device="cuda", dtype=dtype)
+    W = torch.randn(d_out, d_in, generator=gen, device="cuda", dtype=dtype) / 8
+    bias = torch.randn(d_out, generator=gen, device="cuda")
+    r = torch.randn(tokens, d_out, generator=gen, device="cuda", dtype=dtype)
+    y, u = dense_forward(x, W, bias, r, "relu", save_u=True)
+    at = rows_of(tokens)
+    u64 = x[at].double() @ W.double().t() + bias.double()
+    err = 2 * (d_in + 8) * 2.0 ** -24 * (x[at].double().abs() @ W.double().abs().t()
+                                         + bias.double().abs())
+    near("u", u[at], u64, err)
+    y64 = u64.clamp(min=0) + r[at].double()
+    near("y", y[at], y64, err + 2.0 ** -23 * (y64.abs() + r[at].double().abs()))
+    del y
+    g_x, g_W, g_b = dense_backward(r, W, x, u, "relu", need_g_W=True, need_g_bias=True)
+    W64 = W.double()
+    on = (u[at] > 0).double() * r[at].double()
+    near("g_x", g_x[at], on @ W64, 2 * (d_out + 8) * 2.0 ** -24 * (on.abs() @ W64.abs()))
+    ref = torch.zeros(d_out, d_in, device="cuda", dtype=torch.float64)
+    size, sums, sizes = torch.zeros_like(ref), ref.new_zeros(d_out), ref.new_zeros(d_out)
+    for i in range(0, tokens, 10_000):
+        g_u = (u[i:i + 10_000] > 0).double() * r[i:i + 10_000].double()
+        x64 = x[i:i + 10_000].double()
+        ref += g_u.t() @ x64
+        size += g_u.abs().t() @ x64.abs()
+        sums += g_u.sum(0)
+        sizes += g_u.abs().sum(0)
+    # (relu's g_u is exact in the operands' type)
+    near("g_W", g_W, ref, 2 * (tokens + 8) * 2.0 ** -24 * size)
+    # (g_bias: ranges of 32 rows in float32, joined in float64)
+    near("g_bias", g_b, sums, 64 * 2.0 ** -24 * sizes)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 300])
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_weights_past_32_bits(kind, tokens):
+    """W (and g_W, and INT8 codes and their widened copy) of more than 2^32
+    elements."""
+    d_in, d_out = 4096, 1_048_584
+    assert d_in * d_out > 2 ** 32
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(tokens, d_in, generator=gen, device="cuda", dtype=torch.bfloat16)
+    bias = torch.randn(d_out, generator=gen, device="cuda")
+    scale = None
+    if kind == "int8":
+        W = torch.randint(-127, 128, (d_out, d_in), generator=gen, device="cuda", dtype=torch.int8)
+        scale = (0.5 + torch.rand(d_out, generator=gen, device="cuda")) / 4096
+    else:
+        W = torch.randn(d_out, d_in, generator=gen, device="cuda", dtype=torch.bfloat16) / 64
+    y, _ = dense_forward(x, W, bias, w_scale=scale)
+    at = rows_of(d_out)
+    w64 = W[at].double() * (1 if scale is None else scale[at].double()[:, None])
+    y64 = x.double() @ w64.t() + bias[at].double()
+    near("y", y[:, at], y64, 2 * (d_in + 8) * 2.0 ** -24 *
+         (x.double().abs() @ w64.abs().t() + bias[at].double().abs()))
+    g_x, g_W, _ = dense_backward(y, W, x, w_scale=scale, need_g_W=scale is None)
+    ref = torch.zeros(tokens, d_in, device="cuda", dtype=torch.float64)
+    size = torch.zeros_like(ref)
+    for i in range(0, d_out, 65_536):
+        w64 = W[i:i + 65_536].double()
+        if scale is not None:
+            w64 = w64 * scale[i:i + 65_536].double()[:, None]
+        g64 = y[:, i:i + 65_536].double()
+        ref += g64 @ w64
+        size += g64.abs() @ w64.abs()
+    # (with codes, g_u = g_y scale is rounded once as an operand)
+    near("g_x", g_x, ref, (2 * (d_out + 8) * 2.0 ** -24 + (2.0 ** -8 if scale is not None else 0))
+         * size)
+    if g_W is not None:
+        g64, x64 = y[:, at].double(), x.double()
+        near("g_W", g_W[at], g64.t() @ x64,
+             2 * (tokens + 8) * 2.0 ** -24 * (g64.abs().t() @ x64.abs()))
+
+
+def test_clip_of_more_values_than_32_bits_count():
+    n = 2 ** 32 + 4099
+    g = torch.empty(n, device="cuda", dtype=torch.bfloat16)
+    for i in range(0, n, 1 << 28):
+        g[i:i + (1 << 28)] = (i >> 28) % 5 + 1
+    g[-1] = 40.0
+    sq = sum(((i >> 28) % 5 + 1) ** 2 * min(1 << 28, n - i) for i in range(0, n, 1 << 28))
+    sq += 1600 - ((n - 1 >> 28) % 5 + 1) ** 2
+    out = torch.empty_like(g)
+    norm = clip_grads([g], 0.25 * sq ** 0.5, [out])
+    assert abs(norm.item() - sq ** 0.5) <= 2.0 ** -23 * sq ** 0.5
+    # a quarter, within the factor's and the output's roundings: exactly, in
+    # bf16, for values that are small integers
+    for i in range(0, n, 1 << 28):
+        assert torch.equal(out[i:i + (1 << 28)], g[i:i + (1 << 28)] / 4)
+    assert out[-1].item() == 10.0
+
+
+def test_calls_at_the_same_time_on_two_streams():
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(2, 200, 1000, generator=gen, device="cuda", dtype=torch.bfloat16)
+    W = torch.randn(520, 1000, generator=gen, device="cuda", dtype=torch.bfloat16) / 32
+    b = torch.randn(520, generator=gen, device="cuda")
+
+    def step(k):
+        y, u = dense_forward(x[k], W, b, activation="silu", save_u=True)
+        grads = dense_backward(y, W, x[k], u, "silu", need_g_W=True, need_g_bias=True)
+        return y, *grads, clip_grads(grads, 1.0, [torch.empty_like(v) for v in grads])
+
+    want = [step(0), step(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(step(k))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for r in got[k]:
+            assert all(torch.equal(p, q) for p, q in zip(r, want[k]))
