@@ -11,8 +11,8 @@
 //
 // Squares and sums are float64: float32 squares overflow from 1.8e19 and
 // vanish below 1e-23, and the float64 rate is far above what the loads feed.
-// The partials' places and the order of every sum follow from the sizes
-// alone: no atomics, the same bits every time.
+// The partials' places and the order of every sum follow from the sizes and
+// the runs' alignment alone: no atomics, the same bits every time.
 //
 // The runs' addresses and sizes travel in the kernel arguments (kMaxRuns a
 // launch), so a call needs no device table, no copy and no allocation, and a
@@ -255,8 +255,11 @@ scale_kernel(const Batch<N> b, const double* part, int nparts, const float* norm
   }
 }
 
-int launches_of(int count) { return (count + kMaxRuns - 1) / kMaxRuns; }
-int parts_per_launch(int count) { return std::max(64, kMaxParts / std::max(1, launches_of(count))); }
+constexpr int kMinParts = 64;        // of a launch, however many there are
+int64_t launches_of(int64_t count) { return (count + kMaxRuns - 1) / kMaxRuns; }
+int parts_per_launch(int count) {
+  return std::max(kMinParts, kMaxParts / (int)std::max<int64_t>(1, launches_of(count)));
+}
 
 // The runs in launches of at most kMaxRuns, in order. fn(batch, workgroups).
 template <int N, typename F>
@@ -288,8 +291,9 @@ template <typename F> hipError_t for_batches(const GradRun* runs, int count, F f
 
 }  // namespace
 
-int64_t grad_partials_max(int count) {
-  return (int64_t)std::max(1, launches_of(count)) * parts_per_launch(count);
+// (of fewer runs too: neighbours are joined)
+int64_t grad_partials_max(int64_t count) {
+  return std::max<int64_t>(kMaxParts, kMinParts * launches_of(count));
 }
 
 hipError_t launch_grad_sumsq(const GradRun* runs, int count, double* part, int* nparts,

@@ -320,7 +320,7 @@ struct GradRun {
   DType dtype;
 };
 // Most partial sums (float64) that a list of up to `count` runs leaves.
-int64_t grad_partials_max(int count);
+int64_t grad_partials_max(int64_t count);
 // The partial sums of squares, *nparts of them.
 hipError_t launch_grad_sumsq(const GradRun* runs, int count, double* part, int* nparts,
                              hipStream_t s);

@@ -13,7 +13,7 @@ if not torch.cuda.is_available():  # collected on CPU too; every test here is gp
     pytest.skip("no GPU", allow_module_level=True)
 
 from orthogonal_equivalence_amd.dense import dense_backward, dense_forward  # noqa: E402
-from orthogonal_equivalence_amd.grads import clip_grads  # noqa: E402
+from orthogonal_equivalence_amd.grads import clip_grads, grad_norm  # noqa: E402
 
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
@@ -145,6 +145,44 @@ def test_clip_of_more_values_than_32_bits_count():
     for i in range(0, n, 1 << 28):
         assert torch.equal(out[i:i + (1 << 28)], g[i:i + (1 << 28)] / 4)
     assert out[-1].item() == 10.0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("first", range(1, 9))
+@pytest.mark.parametrize("n", [9, 4100, 8200, 70_001])
+def test_clip_of_views_off_the_vector_boundary(dtype, first, n):
+    """Views that start `first` values into a buffer, in a list against memory
+    order: the norm and the values are those of aligned copies, with outputs
+    in place, equally and otherwise placed; what lies between them stays."""
+    gen = torch.Generator(device="cuda").manual_seed(first)
+    flat = torch.randn(4 * n + 200, generator=gen, device="cuda").to(dtype)
+    places = [slice(first + k * (n + 16), first + k * (n + 16) + n) for k in (2, 0, 1)]
+    views = [flat[p] for p in places]
+    copies = [v.clone() for v in views]
+    between = torch.ones_like(flat, dtype=torch.bool)
+    for p in places:
+        between[p] = False
+    norm = grad_norm(copies)
+    got = grad_norm(views)
+    n64 = sum(v.double().square().sum() for v in copies).sqrt().item()
+    assert abs(got.item() - n64) <= 2.0 ** -23 * n64
+    assert abs(norm.item() - n64) <= 2.0 ** -23 * n64
+    want = [v.clone() for v in copies]
+    clip_grads(want, 0.3, norm=norm)
+    for shift in (0, 1, 8):
+        into = torch.full_like(flat, 5.0)
+        outs = [into[p.start + shift:p.stop + shift] for p in places]
+        clip_grads(views, 0.3, outs, norm=norm)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        kept = torch.ones_like(between)
+        for p in places:
+            kept[p.start + shift:p.stop + shift] = False
+        assert (into[kept] == 5.0).all()
+    keep = flat.clone()
+    measured = clip_grads(views, 0.3)
+    assert torch.equal(measured, got) and torch.equal(flat[between], keep[between])
+    for a, b in zip(views, want):  # (the factor from the float64 norm: one rounding less)
+        assert ((a.double() - b.double()).abs() <= 4 * HALF[dtype] * b.double().abs() + 1e-40).all()
 
 
 def test_calls_at_the_same_time_on_two_streams():
