@@ -563,31 +563,51 @@ hipError_t launch_pair_cfg(const TileProduct& gx, int gx_split, const TileProduc
   return hipGetLastError();
 }
 
-// The tile shapes: workgroups that fit a CU, and what one step of 128 bytes
-// of k costs there (us) with one of them on it and with all, measured on an
-// MI355X with operands in the caches.
+// The tile shapes: workgroups that fit a CU, what one step of 128 bytes of k
+// costs there (us) with one of them on it and with all, and what a workgroup
+// costs beside its steps (the first loads, the last products, the epilogue).
+// These and the constants below are fitted to the times of 600 random
+// products on an MI355X under every shape and split (9 .. 4096 tokens, widths
+// 128 .. 14336) and 250 of a model's sizes: the estimates are within 11% (one
+// standard deviation), and the plans chosen by them cost 1.2% (forward) and
+// 2.3% (backward pair) more than the best plan of each product, on average
+// over others like them. Without the fixed costs, which decide the short
+// reductions of g_W at few tokens, 5 and 9%, up to 1.9 times.
 struct Shape {
   int bm, bn, per_cu;
-  float alone, full;
+  float alone, full, fixed;
   bool int8;  // B may be INT8 codes
 };
-constexpr Shape kBf16Shapes[] = {{256, 128, 1, 1.03f, 1.03f, true},
-                                 {128, 128, 1, 0.59f, 0.59f, true},
-                                 {128, 64, 1, 0.41f, 0.41f, false},
-                                 {64, 64, 2, 0.28f, 0.47f, true},
-                                 {32, 64, 2, 0.20f, 0.30f, true}};
+constexpr Shape kBf16Shapes[] = {{256, 128, 1, 0.83f, 0.83f, 6.3f, true},
+                                 {128, 128, 1, 0.50f, 0.50f, 3.5f, true},
+                                 {128, 64, 1, 0.37f, 0.37f, 3.0f, false},
+                                 {64, 64, 2, 0.25f, 0.455f, 2.55f, true},
+                                 {32, 64, 2, 0.19f, 0.37f, 2.0f, true},
+                                 // in a ring of three steps, which leaves
+                                 // room for two: 422 x 2248 x 1440 backward
+                                 // 21.7 -> 16.4 us, 232 x 5216 x 2776 51.8 ->
+                                 // 39.0; 2714 x 128 x 5376 forward 27.2 ->
+                                 // 22.5; but 777 x 2048 x 2048, one on a CU,
+                                 // 19.2 against 15.3 in a ring of four
+                                 {128, 64, 2, 0.42f, 0.70f, 2.1f, false}};
+constexpr int kPairFirst = 1;  // (256 x 128: large products, which fill the chip)
+constexpr int kOneOn = 2;      // 128 x 64, one on a CU: no pair takes it
+constexpr int kTwoOn = 5;      // and two: only where there are two
 // float32 is bound by its matrix rate (a 64 x 64 step is 1024 cycles of it),
 // so small shapes, which fill the chip most evenly, serve all sizes
-constexpr Shape kF32Shapes[] = {{64, 64, 2, 0.56f, 0.90f, false}, {32, 64, 3, 0.26f, 0.76f, false}};
+constexpr Shape kF32Shapes[] = {{64, 64, 2, 0.59f, 0.95f, 2.8f, false},
+                                {32, 64, 3, 0.275f, 0.76f, 1.7f, false}};
 constexpr int kCus = 256;
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
-constexpr float kLaunch = 3.0f;            // us of a launch and its first loads
-constexpr float kFinish = 3.5f;            // and of the pass that joins the partial tiles
-constexpr float kPartBytesPerUs = 6.0e6f;  // which are written and read near the cores
+constexpr int kMinSteps = 4;               // of a split's part
+constexpr float kInt8Step = 1.4f;          // a step with B's codes widened
+constexpr float kLaunch = 2.1f;            // us of a launch
+constexpr float kFinish = 2.75f;           // and of the pass that joins the partial tiles
+constexpr float kPartBytesPerUs = 6.75e6f; // which are written and read near the cores
 constexpr float kHbmBytesPerUs = 6.2e6f;
 // operands that come from HBM rather than a cache lengthen the steps by about
 // this share of their transfer time
-constexpr float kCold = 0.45f;
+constexpr float kCold = 0.38f;
 
 }  // namespace
 
@@ -614,17 +634,20 @@ TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8
     const int64_t slots = (int64_t)kCus * h.per_cu;
     for (int want : kSplits) {
       const int per = (steps + want - 1) / want, split = (steps + per - 1) / per;
-      // (a split leaves at least four steps to each part: 28 x 2560 x 256 in 8
-      // splits of five 6.8 us, in 4 7.9; 11 x 2368 x 1216 7.5 and 8.5. And none
-      // is made of tiles that fill the chip anyway.)
-      if (split != want || (split > 1 && (per < 4 || tiles >= slots))) continue;
+      // (28 x 2560 x 256 in 8 splits of five steps 6.8 us, in 4 7.9; none is
+      // made of tiles that fill the chip anyway)
+      if (split != want || (split > 1 && (per < kMinSteps || tiles >= slots))) continue;
       const int64_t wgs = tiles * split, rest = wgs % slots;
-      float rounds = (float)(wgs / slots) * h.full;
-      if (rest)
-        rounds += h.per_cu == 1 ? h.full
-                                : h.alone + (h.full - h.alone) * (float)((rest - 1) / kCus) /
-                                                (float)(h.per_cu - 1);
-      float cost = kLaunch + std::max(rounds * (float)per + kCold * hbm, hbm);
+      if (bf16 && i == kTwoOn && wgs <= kCus) continue;
+      float rounds = (float)(wgs / slots), step = rounds * h.full;
+      if (rest) {
+        rounds += 1.0f;
+        step += h.per_cu == 1 ? h.full
+                              : h.alone + (h.full - h.alone) * (float)((rest - 1) / kCus) /
+                                              (float)(h.per_cu - 1);
+      }
+      const float busy = step * (float)per * (b_int8 ? kInt8Step : 1.0f) + rounds * h.fixed;
+      float cost = kLaunch + std::max(busy + kCold * hbm, hbm);
       if (split > 1) cost += kFinish + (float)(2 * split * M * N * 4) / kPartBytesPerUs;
       if (cost < best.cost)
         best = TilePlan{i, split, per * bk, split > 1 ? (size_t)split * M * N : 0, cost};
@@ -647,12 +670,13 @@ TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out
   TilePairPlan best = {};
   best.cost = 1e30f;
   constexpr int kNumSplits = (int)(sizeof(kSplits) / sizeof(kSplits[0]));
-  for (int i = bf16 ? 1 : 0; i < nshapes; ++i) {  // (256 x 128: large products, which fill the chip)
+  for (int i = bf16 ? kPairFirst : 0; i < nshapes; ++i) {
+    if (bf16 && i == kOneOn) continue;
     const Shape& h = shapes[i];
     const float slots = (float)(kCus * h.per_cu);
     struct Option {
       int split, per;
-      float work, extra;
+      float work, extra;  // us of the whole chip; of joining the parts
     } opt[2][kNumSplits];
     int nopt[2] = {0, 0};
     for (int q = 0; q < 2; ++q) {
@@ -660,19 +684,20 @@ TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out
       const int steps = (int)((K[q] + bk - 1) / bk);
       for (int want : kSplits) {
         const int per = (steps + want - 1) / want, split = (steps + per - 1) / per;
-        if (split != want || (split > 1 && (per < 8 || tiles >= (int64_t)slots))) continue;
+        if (split != want || (split > 1 && (per < kMinSteps || tiles >= (int64_t)slots))) continue;
         const float extra =
             split > 1 ? kFinish + (float)(2 * split * M[q] * N * 4) / kPartBytesPerUs : 0.0f;
-        opt[q][nopt[q]++] = Option{split, per, (float)(tiles * split) * (float)per, extra};
+        opt[q][nopt[q]++] = Option{
+            split, per, (float)(tiles * split) * ((float)per * h.full + h.fixed) / slots, extra};
       }
     }
     for (int x = 0; x < nopt[0]; ++x) {
       for (int w = 0; w < nopt[1]; ++w) {
         const Option &ox = opt[0][x], &ow = opt[1][w];
         // (the chip full throughout, and half a short workgroup's time of tail)
-        const float busy = std::max((ox.work + ow.work) / slots * h.full +
-                                        0.5f * (float)std::min(ox.per, ow.per) * h.alone,
-                                    (float)std::max(ox.per, ow.per) * h.alone);
+        const float busy =
+            std::max(ox.work + ow.work + 0.44f * (float)std::min(ox.per, ow.per) * h.alone,
+                     (float)std::max(ox.per, ow.per) * h.alone + h.fixed);
         const float cost = kLaunch + busy + kCold * hbm + ox.extra + ow.extra;
         if (cost >= best.cost) continue;
         best.cost = cost;
@@ -725,9 +750,9 @@ hipError_t launch_tile_pair(DType t, const TilePairPlan& plan, TileProduct gx, T
   } else {
     switch (plan.gx.shape) {  // kBf16Shapes
       case 1: e = launch_pair_cfg<bf16_t, 128, 128, 2, 4, 4>(gx, sx, gw, sw, s); break;
-      case 2: e = launch_pair_cfg<bf16_t, 128, 64, 4, 2, 4>(gx, sx, gw, sw, s); break;
       case 3: e = launch_pair_cfg<bf16_t, 64, 64, 2, 2, 4>(gx, sx, gw, sw, s); break;
       case 4: e = launch_pair_cfg<bf16_t, 32, 64, 1, 4, 6>(gx, sx, gw, sw, s); break;
+      case 5: e = launch_pair_cfg<bf16_t, 128, 64, 4, 2, 3>(gx, sx, gw, sw, s); break;
     }
   }
   if (e == hipSuccess) e = finish(t, plan.gx, gx, s);
@@ -750,6 +775,7 @@ hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, boo
       case 2: e = launch_cfg<bf16_t, 128, 64, 4, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
       case 3: e = launch_cfg<bf16_t, 64, 64, 2, 2, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
       case 4: e = launch_cfg<bf16_t, 32, 64, 1, 4, 6, 4>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
+      case 5: e = launch_cfg<bf16_t, 128, 64, 4, 2, 3>(a_kmajor, b_kmajor, p, plan.nsplit, s); break;
     }
   }
   return e == hipSuccess ? finish(t, plan, p, s) : e;
