@@ -451,10 +451,11 @@ int poetx_dense_bwd(const poetx_dense_desc* desc, const void* g_y, const void* x
  *   out  = grad min(1, max_norm / norm)
  * for the gradients of a training step: generator gradients of all layers
  * (float32), bias and weight gradients. Squares and sums are float64, so the
- * norm of any finite gradients is right wherever float32 can hold it; out is
- * rounded once. A norm that is not finite (a NaN or infinity among the
- * gradients) leaves the values as they are: out = grad, and the caller reads
- * it from the norm. Sums are joined in a fixed order: bitwise reproducible. */
+ * norm of any finite gradients is right wherever float32 can hold it; the
+ * factor is not rounded to float32, and out is rounded once (bf16 by way of
+ * float32). A norm that is not finite (a NaN or infinity among the gradients)
+ * leaves the values as they are: out = grad, and the caller reads it from the
+ * norm. Sums are joined in a fixed order: bitwise reproducible. */
 typedef struct poetx_grad_tensor {
   const void* grad; /* n values of `dtype`, contiguous, aligned to one value */
   void* out;        /* the clipped values: grad itself (in place) or memory that
