@@ -92,7 +92,8 @@ act_grad_kernel(const T* __restrict__ g_y, const T* __restrict__ u, const float*
         if (rq >= r1) break;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if constexpr (ACT != Activation::None) g[q][e] = activation_gradient<ACT>(g[q][e], w[q][e]);
+          if constexpr (ACT != Activation::None)
+            g[q][e] = activation_gradient<T, ACT>(g[q][e], w[q][e]);
           sum[e] += g[q][e];
           g[q][e] *= sc[e];
         }

@@ -65,7 +65,7 @@ struct DenseEpilogue {
                       fmaf(d.acc[i][j][2], sc.z, bi.z), fmaf(d.acc[i][j][3], sc.w, bi.w)};
         if constexpr (SAVE_U) stage(row(d, i, ln), n, Quad<bf16_t>::pack(v));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(v[e]);
+        for (int e = 0; e < 4; ++e) v[e] = activate<bf16_t, ACT>(v[e]);
         if (res) {
           const uint2 w = r[j & 1][i];
           v[0] += __uint_as_float(w.x << 16);

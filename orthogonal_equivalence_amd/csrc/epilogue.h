@@ -9,11 +9,18 @@
 //   gelu_tanh(u) = u p,  p = (1 + tanh z) / 2 = 1 / (1 + e^-2z),
 //                  z = C (u + A u^3);                 slope p + u p (1 - p) 2 z'
 //   gelu(u)      = u Phi(u);                          slope Phi(u) + u phi(u)
+//
+// float32 tensors (Precise): the exponential and the complementary error
+// function to float32's last place, true division, and 1 - p as e^-v p where
+// it is small: within about one rounding a step of the formula.
+//
+// bf16 tensors: their last place is 2^16 times float32's, so the cheapest
+// forms that are good to 1.5e-7: the hardware's exponential and reciprocal, and
 // Phi(-|u|) = erfc(|u| / sqrt 2) / 2 by the rational approximation 7.1.26 of
-// Abramowitz and Stegun's handbook (absolute error 1.5e-7, a float32 rounding
-// of the sum 1 + erf it replaces): one exponential, which phi shares, one
-// reciprocal and five products, where a library erf costs several times that
-// in the epilogue of a matrix product.
+// Abramowitz and Stegun's handbook (absolute error 1.5e-7): one exponential,
+// which phi shares, one reciprocal and five products in the epilogue of a
+// matrix product, where erfc costs several times that.
+//
 // A NaN u stays NaN, +inf stays +inf (-inf gives NaN where the formula is
 // -inf times 0); the slopes take |u| > 64 as 64, where they equal their
 // limits 0 and 1 in float32 and u^2 cannot overflow.
@@ -43,12 +50,22 @@ __device__ __forceinline__ float normal_tail(float u, float* gauss) {
   return 0.5f * p * t * e;
 }
 
-template <Activation ACT> __device__ __forceinline__ float activate(float u) {
+// 2 z of gelu_tanh
+__device__ __forceinline__ float tanh_argument(float u) {
+  return 2.0f * kGeluC * fmaf(kGeluA * u * u, u, u);
+}
+
+// whether the activations of T tensors take the forms for float32
+template <typename T> constexpr bool kPrecise = sizeof(T) == 4;
+
+template <typename T, Activation ACT> __device__ __forceinline__ float activate(float u) {
   if constexpr (ACT == Activation::Relu) return u < 0.0f ? 0.0f : u;
-  if constexpr (ACT == Activation::Silu) return u * logistic(u);
+  if constexpr (ACT == Activation::Silu)
+    return kPrecise<T> ? u / (1.0f + expf(-u)) : u * logistic(u);
   if constexpr (ACT == Activation::GeluTanh)
-    return u * logistic(2.0f * kGeluC * fmaf(kGeluA * u * u, u, u));
+    return kPrecise<T> ? u / (1.0f + expf(-tanh_argument(u))) : u * logistic(tanh_argument(u));
   if constexpr (ACT == Activation::Gelu) {
+    if constexpr (kPrecise<T>) return u * (0.5f * erfcf(u * -0.70710678118654752f));
     float e;
     const float q = normal_tail(u, &e);
     return u * (u < 0.0f ? q : 1.0f - q);
@@ -56,17 +73,27 @@ template <Activation ACT> __device__ __forceinline__ float activate(float u) {
   return u;
 }
 
-template <Activation ACT> __device__ __forceinline__ float activation_slope(float u) {
+// the slope of v p(s(v)), p the logistic function and ds the slope of s
+template <typename T>
+__device__ __forceinline__ float logistic_slope(float v, float s, float ds) {
+  if constexpr (kPrecise<T>) {
+    const float e = expf(-s), p = 1.0f / (1.0f + e);
+    return fmaf(v * p * (s > 0.0f ? e * p : 1.0f - p), ds, p);
+  } else {
+    const float p = logistic(s);
+    return fmaf(v * p * (1.0f - p), ds, p);
+  }
+}
+
+template <typename T, Activation ACT> __device__ __forceinline__ float activation_slope(float u) {
   const float v = u > 64.0f ? 64.0f : u < -64.0f ? -64.0f : u;
-  if constexpr (ACT == Activation::Silu) {
-    const float p = logistic(v);
-    return fmaf(v * p, 1.0f - p, p);
-  }
-  if constexpr (ACT == Activation::GeluTanh) {
-    const float w = kGeluA * v * v;
-    const float p = logistic(2.0f * kGeluC * fmaf(w, v, v));
-    return fmaf(v * p * (1.0f - p), 2.0f * kGeluC * fmaf(3.0f, w, 1.0f), p);
-  }
+  if constexpr (ACT == Activation::Silu) return logistic_slope<T>(v, v, 1.0f);
+  if constexpr (ACT == Activation::GeluTanh)
+    return logistic_slope<T>(v, tanh_argument(v),
+                             2.0f * kGeluC * fmaf(3.0f, kGeluA * v * v, 1.0f));
+  if constexpr (kPrecise<T>)
+    return fmaf(v * 0.3989422804014327f, expf(-0.5f * v * v),
+                0.5f * erfcf(v * -0.70710678118654752f));
   float e;
   const float q = normal_tail(v, &e);
   return fmaf(v * 0.3989422804014327f, e, v < 0.0f ? q : 1.0f - q);
@@ -74,16 +101,17 @@ template <Activation ACT> __device__ __forceinline__ float activation_slope(floa
 
 // g times the slope at u; relu's is a choice, not a product, so that an
 // infinite g (a loss scale that overflowed) is dropped where the unit is off
-template <Activation ACT> __device__ __forceinline__ float activation_gradient(float g, float u) {
+template <typename T, Activation ACT>
+__device__ __forceinline__ float activation_gradient(float g, float u) {
   if constexpr (ACT == Activation::Relu) return u <= 0.0f ? 0.0f : g;
-  else return g * activation_slope<ACT>(u);
+  else return g * activation_slope<T, ACT>(u);
 }
 
 // the run-time activation of a wave-uniform `act`, four values at a time
-__device__ __forceinline__ void activate4(int act, float v[4]) {
-#define POETX_ACTIVATE4(A)                                              \
-  case static_cast<int>(Activation::A):                                 \
-    for (int e = 0; e < 4; ++e) v[e] = activate<Activation::A>(v[e]);   \
+template <typename T> __device__ __forceinline__ void activate4(int act, float v[4]) {
+#define POETX_ACTIVATE4(A)                                                \
+  case static_cast<int>(Activation::A):                                   \
+    for (int e = 0; e < 4; ++e) v[e] = activate<T, Activation::A>(v[e]);  \
     break;
   switch (act) {
     POETX_ACTIVATE4(Relu)
@@ -140,7 +168,7 @@ __device__ __forceinline__ void epilogue4(const Epilogue& ep, int64_t m, int n, 
   }
   const int64_t at = m * ep.ld + n;
   if (ep.u) Quad<T>::store(static_cast<T*>(ep.u) + at, v);
-  activate4(ep.act, v);
+  activate4<T>(ep.act, v);
   if (ep.residual) {
     float r[4];
     Quad<T>::load(static_cast<const T*>(ep.residual) + at, r);
