@@ -117,13 +117,6 @@ dense_kernel(const bf16_t* __restrict__ A, const bf16_t* __restrict__ B, bf16_t*
 
 }  // namespace
 
-bool dense_supported(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc) {
-  // the per-lane copy offsets within one 256-row (or 32-row) panel are 32-bit
-  return M >= BM && N >= BN && K >= BK && K % BK == 0 && N % 8 == 0 && lda % 8 == 0 &&
-         ldb % 8 == 0 && ldc % 8 == 0 && M <= INT32_MAX && N <= INT32_MAX && K <= INT32_MAX &&
-         lda <= (1 << 22) && ldb <= (1 << 22);
-}
-
 hipError_t dense_grid(int64_t M, int64_t N, int* grid_out) {
   const int tiles = (int)(((M + BM - 1) / BM) * ((N + BN - 1) / BN));
   // one workgroup per CU (the register and LDS footprints allow no more),

@@ -8,13 +8,12 @@
 #include <cstdint>
 
 #include "api_util.h"
+#include "dense_plan.h"
 #include "kernels.h"
 #include "poetx.h"
 
 using poetx::Activation;
 using poetx::DType;
-using poetx::TilePairPlan;
-using poetx::TilePlan;
 using poetx::TileProduct;
 using namespace poetx::api;
 
@@ -35,13 +34,14 @@ int check_desc(const poetx_dense_desc* d) {
   if (d->activation < POETX_ACT_NONE || d->activation > POETX_ACT_SILU || d->flags != 0 ||
       d->reserved != 0)
     return POETX_ERR_SHAPE;
-  // the grids of the 64 x 64 output tiles
+  // (tile counts are ints)
   if (ceil_div(d->tokens, 64) * ceil_div(std::max(d->d_in, d->d_out), 64) > INT32_MAX)
     return POETX_ERR_SHAPE;
   if (d->w_scale && ((reinterpret_cast<uintptr_t>(d->w_scale) & 15) || d->d_in % 8))
     return POETX_ERR_ALIGN;
   const int v = act_vec(d->act);
   if (d->d_in % v || d->d_out % v) return POETX_ERR_ALIGN;
+  if (!poetx::dense_launchable(dtype_of(d), d->tokens, d->d_in, d->d_out)) return POETX_ERR_SHAPE;
   return POETX_OK;
 }
 
@@ -52,59 +52,20 @@ size_t widened_bytes(const poetx_dense_desc* d) {
   return int8_weight(d) ? align_up((size_t)d->d_out * d->d_in * act_size(d->act)) : 0;
 }
 
-// The dense kernel's time for an M x N x K product, as the tile kernel's plan
-// estimates its own: rounds of 256 x 256 tiles over the CUs (1.38 us a round
-// and 64 of k, 6 us for a round's epilogue, measured at 4096 x 4096 x 4096).
-float dense_cost(int64_t M, int64_t N, int64_t K) {
-  const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), 256);
-  return 3.0f + (float)rounds * (1.38f * (float)K / 64 + 6.0f);
-}
-// Whether an M x N product of K-major A takes that kernel.
-bool use_dense(DType t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
-               const TilePlan& tile) {
-  return t == DType::BF16 && poetx::dense_supported(M, N, K, lda, ldb, ldc) &&
-         dense_cost(M, N, K) < tile.cost;
-}
-constexpr float kWidenLaunch = 3.0f, kWidenBytesPerUs = 4.5e6f;
-
-struct FwdPlan {
-  TilePlan tile;
-  bool stream, dense;
-  bool widen, w_tiled;  // INT8 codes widened into the workspace (in the tiled layout)
+struct FwdPlan : poetx::FwdChoice {
   size_t wq, part, total;
 };
 FwdPlan plan_fwd(const poetx_dense_desc* d) {
   FwdPlan p = {};
-  // few tokens: the weight read once, straight into the products
-  p.stream = d->tokens <= poetx::kStreamRows && !(int8_weight(d) && d->act == POETX_F32);
+  static_cast<poetx::FwdChoice&>(p) =
+      poetx::choose_fwd(dtype_of(d), int8_weight(d), d->tokens, d->d_in, d->d_out);
   if (p.stream) return p;
-  const DType t = dtype_of(d);
-  const int64_t M = d->tokens, N = d->d_out, K = d->d_in;
-  p.tile = poetx::plan_tile_product(t, M, N, K, false);
-  p.dense = use_dense(t, M, N, K, K, K, N, p.tile);
-  p.widen = int8_weight(d);
-  if (int8_weight(d) && t == DType::BF16 && K % 16 == 0) {
-    // the tile kernel can take the codes themselves: worth it while widening
-    // them (a byte read, two written) costs more than the products gain
-    const TilePlan direct = poetx::plan_tile_product(t, M, N, K, true);
-    const float widened = (p.dense ? dense_cost(M, N, K) : p.tile.cost) + kWidenLaunch +
-                          (float)(3 * N * K) / kWidenBytesPerUs;
-    if (direct.cost < widened) {
-      p.tile = direct;
-      p.dense = p.widen = false;
-    }
-  }
-  p.w_tiled = p.dense && p.widen && N % poetx::kTileRows == 0;
   p.part = p.widen ? widened_bytes(d) : 0;
   p.total = p.part + (p.dense ? 0 : align_up(p.tile.part_floats * sizeof(float)));
   return p;
 }
 
-struct BwdPlan {
-  TilePlan gx, gw;
-  TilePairPlan pair;
-  bool dense;   // g_x on the dense kernel
-  bool paired;  // g_x and g_W, where both are asked for, in one launch
+struct BwdPlan : poetx::BwdChoice {
   size_t gu, bias, wq, part, total;
 };
 // whether the products take g_u from the workspace (else g_y is g_u)
@@ -112,18 +73,9 @@ bool forms_gu(const poetx_dense_desc* d) {
   return d->activation != POETX_ACT_NONE || int8_weight(d);
 }
 BwdPlan plan_bwd(const poetx_dense_desc* d) {
-  BwdPlan p;
-  const DType t = dtype_of(d);
-  const int64_t M = d->tokens, N = d->d_in, K = d->d_out;
-  p.gx = poetx::plan_tile_product(t, M, N, K, false);
-  p.dense = use_dense(t, M, N, K, K, N, N, p.gx);
-  if (p.dense) {
-    p.gx.part_floats = 0;
-    p.gx.cost = dense_cost(M, N, K);
-  }
-  p.gw = poetx::plan_tile_product(t, K, N, M, false);
-  p.pair = poetx::plan_tile_pair(t, M, N, K);
-  p.paired = !int8_weight(d) && p.pair.cost < p.gx.cost + p.gw.cost;
+  BwdPlan p = {};
+  static_cast<poetx::BwdChoice&>(p) =
+      poetx::choose_bwd(dtype_of(d), int8_weight(d), d->tokens, d->d_in, d->d_out);
   size_t off = 0;
   p.gu = off;
   if (forms_gu(d)) off += align_up((size_t)d->tokens * d->d_out * act_size(d->act));
@@ -251,6 +203,7 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
                         (const void*)g_bias})
     if (p && !aligned16(p)) return POETX_ERR_ALIGN;
   const BwdPlan plan = plan_bwd(d);
+  if (g_W && plan.gw.nsplit == 0) return POETX_ERR_SHAPE;
   if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
   if (!aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t es = act_size(d->act);

@@ -22,6 +22,7 @@ constexpr int RING = NSLOT * SLOT;         // 128 KB, also the epilogue's stagin
 constexpr int PPW = TILE * 2 / 1024 / NW;  // 1 KB pieces per wave per operand tile
 constexpr int LPW = 2 * PPW;               // copies per wave per K tile
 static_assert(RING == BM * BN, "the epilogue stages the whole output tile in the ring");
+static_assert(BM == 256 && BN == 256 && BK == 32, "dense_supported (kernels.h)");
 static_assert(PPW == 4 && LPW == 8, "one copy after each of the eight rows of products");
 
 // 1 KB alignment: the fragment addressing XORs bits 4..6 of element offsets

@@ -1,0 +1,28 @@
+// The choice of kernels for a dense linear's calls (dense_api.cpp), from the
+// types and sizes alone. Host code, no HIP call.
+#pragma once
+
+#include "kernels.h"
+
+namespace poetx {
+
+struct FwdChoice {
+  bool stream;          // the streaming kernel, and nothing below
+  bool dense;           // the 256 x 256 tiles, else `tile`
+  bool widen, w_tiled;  // INT8 codes widened into the workspace (in the tiled layout)
+  TilePlan tile;
+};
+FwdChoice choose_fwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d_out);
+
+struct BwdChoice {
+  bool dense;       // g_x on the 256 x 256 tiles, else `gx`
+  bool paired;      // g_x and g_W, where both are asked for, in one launch
+  TilePlan gx, gw;  // gw.nsplit 0: no launch takes g_W's tiles
+  TilePairPlan pair;
+};
+BwdChoice choose_bwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d_out);
+
+// Whether launches take the tiles of y and g_x.
+bool dense_launchable(DType t, int64_t tokens, int64_t d_in, int64_t d_out);
+
+}  // namespace poetx

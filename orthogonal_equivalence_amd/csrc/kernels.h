@@ -86,7 +86,14 @@ static_assert(kTileRows == 256 && kTileCols == 32, "tiled_offset's shifts");
 // B[k*ldb + n]; bf16 in and out, float32 accumulation. With a_tiled, A is in
 // the tiled layout (M % 256 == 0 and lda == K, else hipErrorInvalidValue);
 // with b_tiled, a K-major B is (an N x K matrix: N % 256 == 0, ldb == K).
-bool dense_supported(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc);
+// (its 256 x 256 x 32 tiles; the per-lane copy offsets within one 256-row or
+// 32-row panel are 32-bit)
+inline bool dense_supported(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                            int64_t ldc) {
+  return M >= 256 && N >= 256 && K >= 32 && K % 32 == 0 && N % 8 == 0 && lda % 8 == 0 &&
+         ldb % 8 == 0 && ldc % 8 == 0 && M <= INT32_MAX && N <= INT32_MAX && K <= INT32_MAX &&
+         lda <= (1 << 22) && ldb <= (1 << 22);
+}
 // Workgroups of the persistent kernel for an M x N output on this device.
 hipError_t dense_grid(int64_t M, int64_t N, int* grid_out);
 hipError_t launch_dense(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
@@ -247,9 +254,12 @@ struct TileProduct {
   float* part = nullptr;
   Epilogue ep;
 };
+// Work items along one dimension of a launch that HIP takes.
+constexpr int64_t kMaxWorkItems = UINT32_MAX;
 struct TilePlan {
-  int shape;  // of the type's tile shapes
-  int nsplit, kchunk;
+  int shape;   // of the type's tile shapes
+  int nsplit;  // 0: no shape's tiles fit a launch
+  int kchunk;
   size_t part_floats;
   float cost;  // estimate in us, for comparison with another kernel's
 };
