@@ -151,7 +151,8 @@ def _backward(desc, g_y, W, x, u, need_g_x, need_g_W, need_g_bias, nbytes):
 class DenseLinear:
     """y = act(x W^T + bias) + residual with W [d_out, d_in] kept on the device
     in the activation type `act` ("f32", "bf16"), or with int8=True as INT8
-    codes with per-row scales (poetx_quantize_weight)."""
+    codes with per-row scales (poetx_quantize_weight), formed from W as it is
+    given, float32 or the activation type."""
 
     def __init__(self, W: torch.Tensor, act: str, bias=None, activation="none", device="cuda",
                  int8: bool = False):
@@ -160,7 +161,8 @@ class DenseLinear:
         self.torch_dtype = {"f32": torch.float32, "bf16": torch.bfloat16}[act]
         self.device = torch.device(device)
         self.activation = activation
-        self.W = W.to(self.device, self.torch_dtype).contiguous()
+        kept = torch.float32 if int8 and W.dtype != self.torch_dtype else self.torch_dtype
+        self.W = W.to(self.device, kept).contiguous()
         self.d_out, self.d_in = self.W.shape
         self.bias = None
         if bias is not None:
@@ -170,8 +172,7 @@ class DenseLinear:
             with torch.cuda.device(self.W.device):
                 q = torch.empty(self.W.shape, device=self.device, dtype=torch.int8)
                 self.w_scale = torch.empty(self.d_out, device=self.device, dtype=torch.float32)
-                P.poetx_quantize_weight(self.W, self.d_out, self.d_in, _ACT[self.torch_dtype], q,
-                                        self.w_scale)
+                P.poetx_quantize_weight(self.W, self.d_out, self.d_in, _ACT[kept], q, self.w_scale)
             self.W = q
 
     def forward(self, x, residual=None, save_u=False, stream=None):

@@ -11,7 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import poetx as P
-from .dense import DenseLinear
+from .dense import DenseLinear, _on
 
 _DT = {"f32": (torch.float32, P.POETX_F32), "bf16": (torch.bfloat16, P.POETX_BF16)}
 
@@ -175,29 +175,46 @@ class PoetxLinear:
                            g_theta_P if g_theta_P.numel() else None, ws, stream)
         return g_x, g_theta_R, g_theta_P
 
-
     # -- after training -----------------------------------------------------
-    def merged_weight(self, rows: int = 1024):
-        """R W0 P [d_out, d_in] in the activation type, from the blocks as they
-        were last built: row i is the backward's g_x for the unit gradient g_y
-        = e_i, formed `rows` rows at a time (in bf16, R W0 is rounded once on
-        the way, the result once)."""
-        W = torch.empty(self.d_out, self.d_in, device=self.device, dtype=self.torch_dtype)
-        for r0 in range(0, self.d_out, rows):
-            n = min(rows, self.d_out - r0)
-            g_y = torch.zeros(n, self.d_out, device=self.device, dtype=self.torch_dtype)
-            g_y.diagonal(r0).fill_(1.0)
-            # the saved tensors enter the generators' gradients only
-            x = torch.zeros(n, self.d_in, device=self.device, dtype=self.torch_dtype)
-            z = None if self.flags & P.POETX_RECOMPUTE_Z else torch.zeros_like(g_y)
-            self.backward(g_y, x, z, g_x=W[r0:r0 + n])
+    def _merge_into(self, W, rows):
+        """R W0 P into W [d_out, d_in], from the blocks as they were last built
+        (the ones that forward() applies): column j is the forward's y for the
+        unit vector e_j, in float32 whatever the layer's type, so that only W's
+        own type rounds; `rows` vectors a call, nothing kept afterwards."""
+        R, Pb = (t.float() for t in self.blocks_for_act())
+        W0 = self.W0 if self.w_scale is not None else self.W0.float()
+        f32 = dict(device=W.device, dtype=torch.float32)
+        for j0 in range(0, self.d_in, rows):
+            n = min(rows, self.d_in - j0)
+            desc = P.make_desc(n, self.d_in, self.d_out, self.b_in, self.b_out, P.POETX_F32, None,
+                               P.POETX_RECOMPUTE_Z, self.perm_in, self.perm_out, self.w_scale)
+            x = torch.zeros(n, self.d_in, **f32)
+            x.diagonal(j0).fill_(1.0)
+            y = torch.empty(n, self.d_out, **f32)
+            ws = torch.empty(max(P.poetx_fwd_workspace_size(desc), 1), device=W.device,
+                             dtype=torch.uint8)
+            P.poetx_linear_fwd(desc, x, W0, R, Pb, y, None, ws)
+            W[:, j0:j0 + n].copy_(y.t())
         return W
 
-    def merge(self, bias=None, activation="none", int8: bool = False) -> DenseLinear:
+    def merged_weight(self, rows: int = 1024, stream=None):
+        """R W0 P [d_out, d_in] in the activation type, formed in float32 and
+        rounded once, from the blocks as they were last built, `rows` columns
+        at a time."""
+        with _on(self.W0.device, stream):
+            return self._merge_into(torch.empty(self.d_out, self.d_in, device=self.W0.device,
+                                                dtype=self.torch_dtype), rows)
+
+    def merge(self, bias=None, activation="none", int8: bool = False, stream=None) -> DenseLinear:
         """The trained layer as a DenseLinear on R W0 P: one product a call,
-        with bias, activation and residual in its epilogue."""
-        return DenseLinear(self.merged_weight(), "bf16" if self.act == P.POETX_BF16 else "f32",
-                           bias, activation, self.device, int8)
+        with bias, activation and residual in its epilogue. int8 quantises the
+        float32 product."""
+        with _on(self.W0.device, stream):
+            W = torch.empty(self.d_out, self.d_in, device=self.W0.device,
+                            dtype=torch.float32 if int8 else self.torch_dtype)
+            return DenseLinear(self._merge_into(W, 1024),
+                               "bf16" if self.act == P.POETX_BF16 else "f32", bias, activation,
+                               self.device, int8)
 
 
 class PoetxLinearSet:

@@ -1,0 +1,114 @@
+"""PoetxLinear.merge: the merged weight against R W0 P in float64 from the
+layer's own blocks, rounded once, and nothing left behind.
+
+Tolerance of an element, s = (|R| |W0| |P|) there: two float32 sums over a
+block of b products and one over d_in of which b are not zero, each
+intermediate value rounded to float32: (2 (b + 8) + 3) 2^-24 s for each of the
+three products, and half a step of the result's type (bf16 2^-8, float32
+2^-24) of the value."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU too; every test here is gpu-marked
+    pytest.skip("no GPU", allow_module_level=True)
+
+from orthogonal_equivalence_amd.inputs import LayerSpec, make_layer  # noqa: E402
+from orthogonal_equivalence_amd.layer import PoetxLinear  # noqa: E402
+from tests import gpu_util as U  # noqa: E402
+
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def make(d_in, d_out, b, dtype, theta=0.05, **kw):
+    spec = LayerSpec("merge", d_in, d_out, b, 8, dtype, theta, seed=41)
+    L = make_layer(spec)
+    lay = PoetxLinear(U.dev(L.W0, dtype), b, b, dtype, **kw)
+    lay.set_theta(torch.from_numpy(L.theta_R).float(), torch.from_numpy(L.theta_P).float())
+    lay.build()
+    return lay
+
+
+def blocks64(blocks, d):
+    """blockdiag of the blocks, cut to d x d."""
+    return torch.block_diag(*blocks.double().cpu())[:d, :d]
+
+
+def exact(lay):
+    """R W0 P and the product of absolute values, float64 on the CPU."""
+    R, Pb = lay.blocks_for_act()
+    R, Pb = blocks64(R, lay.d_out), blocks64(Pb, lay.d_in)
+    W0 = lay.W0.double().cpu()
+    if lay.w_scale is not None:
+        W0 = W0 * lay.w_scale.double().cpu()[:, None]
+    return R @ W0 @ Pb, R.abs() @ W0.abs() @ Pb.abs()
+
+
+def tolerance(ref, size, b, dtype):
+    e = 3 * (2 * (b + 8) + 3) * 2.0 ** -24 * size
+    return e + HALF[dtype] * (ref.abs() + e)
+
+
+@pytest.mark.parametrize("kw", [{}, {"map": "cnp"}, {"recompute_z": True}, {"saved_y": True},
+                                {"int8": True}], ids=lambda k: next(iter(k), "plain"))
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d_in,d_out,b", [(256, 384, 64), (512, 256, 128), (136, 200, 32)])
+def test_merged_weight_is_rounded_once(d_in, d_out, b, dtype, kw):
+    lay = make(d_in, d_out, b, dtype, **kw)
+    ref, size = exact(lay)
+    for rows in (1024, 100):
+        W = lay.merged_weight(rows=rows)
+        assert W.shape == ref.shape and W.dtype == lay.torch_dtype
+        worst = ((W.double().cpu() - ref).abs() / tolerance(ref, size, b, dtype)).max().item()
+        print(f"    {d_in}x{d_out} b={b} {dtype} {kw} rows={rows}: {worst:.3f}", flush=True)
+        assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_int8_codes_are_those_of_the_float32_product(dtype):
+    """A code is rint(w / s), s the row's largest |w| over 127: at most half a
+    code from the exact product over the kept scale, beside the product's own
+    error and four roundings of float32 values below 128."""
+    lay = make(256, 384, 64, dtype)
+    ref, size = exact(lay)
+    q = lay.merge(int8=True)
+    assert q.W.dtype == torch.int8 and q.torch_dtype == lay.torch_dtype
+    s = q.w_scale.double().cpu()[:, None]
+    e = 3 * (2 * (64 + 8) + 3) * 2.0 ** -24 * size
+    off = (q.W.double().cpu() - ref / s).abs() - e / s
+    print(f"    {dtype}: furthest code {off.max().item():.6f} of a step", flush=True)
+    assert off.max().item() <= 0.5 + 127 * 4 * 2.0 ** -24
+    assert ((s[:, 0] * 127 - ref.abs().amax(1)).abs() <= e.amax(1) + 2.0 ** -22 * ref.abs().amax(1)).all()
+
+
+@pytest.mark.parametrize("kw", [{}, {"recompute_z": True}, {"int8": True}],
+                         ids=lambda k: next(iter(k), "plain"))
+def test_merge_leaves_nothing_behind(kw):
+    """No workspace of its calls stays with the layer, and no memory but the
+    merged weight's."""
+    lay = make(512, 768, 64, "bf16", **kw)
+    x = torch.randn(24, 512, device="cuda", dtype=torch.bfloat16)
+    y, z = lay.forward(x)
+    g = lay.backward(torch.ones_like(y), x, z)
+    before = set(lay._fwd_ws), set(lay._bwd_ws)
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    W = lay.merged_weight(rows=200)
+    torch.cuda.synchronize()
+    assert (set(lay._fwd_ws), set(lay._bwd_ws)) == before
+    assert torch.cuda.memory_allocated() - held <= W.numel() * W.element_size() + 512
+    again = lay.backward(torch.ones_like(y), x, z)
+    assert all(torch.equal(a, b) for a, b in zip(g, again))
+
+
+def test_merge_on_another_stream():
+    lay = make(256, 384, 64, "bf16")
+    want = lay.merged_weight()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    W = lay.merged_weight(stream=s)
+    dense = lay.merge(bias=torch.ones(384), activation="relu", stream=s)
+    s.synchronize()
+    assert torch.equal(W, want) and torch.equal(dense.W, want)
