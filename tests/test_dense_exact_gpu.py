@@ -1,7 +1,7 @@
 """The dense linear on operands of small integers, bit for bit: every product
 and sum is exact in float32 in any order, so an output is the exact value
 rounded once to its type, on every kernel variant that the plans choose
-(dense_cases.py)."""
+(dense_cases.py) and past 2^32 elements, where every element is compared."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -12,7 +12,7 @@ if not torch.cuda.is_available():  # collected on CPU too; every test here is gp
     pytest.skip("no GPU", allow_module_level=True)
 
 from orthogonal_equivalence_amd.dense import dense_backward, dense_forward  # noqa: E402
-from tests.dense_cases import BF16, CASES, DTYPE, integers  # noqa: E402
+from tests.dense_cases import BF16, CASES, DTYPE, F32, integers  # noqa: E402
 
 
 def share(n, other=1.0):
@@ -81,3 +81,79 @@ def test_every_variant(case):
         same(act + " g_x", g_x, ref)
         same(act + " g_W", g_W, ref_W)
         assert torch.equal(g_b, g_u.sum(0).float())
+
+
+def filled(gen, shape, top, part, dtype):
+    """integers() into a large tensor, some rows at a time."""
+    out = torch.empty(shape, device="cuda", dtype=dtype)
+    for i in range(0, shape[0], 65_536):
+        n = min(65_536, shape[0] - i)
+        out[i:i + n] = integers(gen, (n, shape[1]), top, part, "cuda")
+    return out
+
+
+@pytest.mark.parametrize("t", [BF16, F32], ids=["bf16", "f32"])
+def test_rows_past_32_bits(t):
+    """y, u, residual, g_y and g_u of more than 2^32 elements each; every
+    element of every output."""
+    tokens, d_in, d_out = 300_031, 64, 14_336
+    assert tokens * d_out > 2 ** 32
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    dt = DTYPE[t]
+    x = integers(gen, (tokens, d_in), 2, 0.05, "cuda").to(dt)
+    W = integers(gen, (d_out, d_in), 2, 0.2, "cuda").to(dt)
+    bias = integers(gen, (d_out,), 3, 1.0, "cuda").float()
+    r = filled(gen, (tokens, d_out), 3, 0.1, dt)
+    y, u = dense_forward(x, W, bias, r, "relu", save_u=True)
+    W64, b64 = W.double(), bias.double()
+    for i in range(0, tokens, 10_000):
+        u64 = x[i:i + 10_000].double() @ W64.t() + b64
+        same("u", u[i:i + 10_000], u64)
+        same("y", y[i:i + 10_000], u64.clamp_(min=0) + r[i:i + 10_000].double())
+    del y
+    g_x, g_W, g_b = dense_backward(r, W, x, u, "relu", need_g_W=True, need_g_bias=True)
+    ref = torch.zeros(d_out, d_in, device="cuda", dtype=torch.float64)
+    sums = ref.new_zeros(d_out)
+    for i in range(0, tokens, 10_000):
+        g_u = (u[i:i + 10_000] > 0) * r[i:i + 10_000].double()
+        same("g_x", g_x[i:i + 10_000], g_u @ W64)
+        ref += g_u.t() @ x[i:i + 10_000].double()
+        sums += g_u.sum(0)
+    same("g_W", g_W, ref)
+    same("g_bias", g_b, sums)
+    # (the sums show single lost ranges: most of them are of hundreds)
+    assert ref.abs().mean() > 20 and sums.abs().mean() > 100
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 300])
+@pytest.mark.parametrize("int8", [0, 1], ids=["bf16", "int8"])
+def test_weights_past_32_bits(int8, tokens):
+    """W (and g_W, INT8 codes and their widened copy) of more than 2^32
+    elements; every element of every output."""
+    d_in, d_out = 4096, 1_048_584
+    assert d_in * d_out > 2 ** 32
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    x = integers(gen, (tokens, d_in), 2, 0.25, "cuda").bfloat16()
+    bias = integers(gen, (d_out,), 100, 1.0, "cuda").float()
+    scale = None
+    if int8:
+        W = filled(gen, (d_out, d_in), 127, 0.25, torch.int8)
+        scale = torch.exp2(torch.randint(-1, 3, (d_out,), generator=gen, device="cuda").float())
+    else:
+        W = filled(gen, (d_out, d_in), 2, 0.25, torch.bfloat16)
+    g_y = filled(gen, (d_out, tokens), 2, 0.02, torch.bfloat16).t().contiguous()
+    y, _ = dense_forward(x, W, bias, w_scale=scale)
+    g_x, g_W, g_b = dense_backward(g_y, W, x, w_scale=scale, need_g_W=not int8, need_g_bias=True)
+    ref = torch.zeros(tokens, d_in, device="cuda", dtype=torch.float64)
+    for i in range(0, d_out, 65_536):
+        at = slice(i, min(d_out, i + 65_536))
+        w64 = W[at].double()
+        if int8:
+            w64 *= scale[at].double()[:, None]
+        same("y", y[:, at], x.double() @ w64.t() + bias[at].double())
+        ref += g_y[:, at].double() @ w64
+        if not int8:
+            same("g_W", g_W[at], g_y[:, at].double().t() @ x.double())
+    same("g_x", g_x, ref)
+    same("g_bias", g_b, g_y.double().sum(0))
+    assert ref.abs().mean() > 50
