@@ -379,9 +379,9 @@ int poetx_linear_bwd(const poetx_linear_desc* desc, const void* g_y, const void*
  *   backward  g_u = g_y act'(u),  g_x = g_u W,  g_W = g_u^T x,
  *             g_bias = the column sums of g_u;  the residual's gradient is g_y
  * u, act(u) and their sum are formed in float32 and y and the kept u each
- * rounded once. In the backward g_u is rounded to the act type once, as the
- * products' operand (the matrix cores take bf16); g_bias sums the unrounded
- * values. */
+ * rounded once. In the backward g_u (with INT8 codes g_u times the row's
+ * scale) is rounded to the act type once, as the products' operand (the matrix
+ * cores take bf16); g_bias sums the unrounded g_u. */
 typedef enum poetx_activation {
   POETX_ACT_NONE = 0,
   POETX_ACT_RELU = 1,      /* max(u, 0); its slope at 0 is 0 */
@@ -404,7 +404,8 @@ typedef struct poetx_dense_desc {
   /* NULL: W is in the act type. Otherwise W holds int8 codes q [d_out, d_in]
    * and w_scale [d_out] float32 row scales (poetx_quantize_weight; 16-byte
    * aligned), the weight being diag(w_scale) q exactly; d_in must be a
-   * multiple of 8. The scales are applied to the float32 products. */
+   * multiple of 8. The scales are applied to the forward's float32 products,
+   * and to g_u in the backward, whose sums run over the scaled rows. */
   const float* w_scale;
 } poetx_dense_desc;
 

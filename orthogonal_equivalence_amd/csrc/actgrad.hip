@@ -6,10 +6,11 @@
 //
 // A workgroup takes 32 column vectors of 16 bytes (256 bf16 or 128 float32
 // columns) and one range of rows, eight rows at a time; each thread sums its
-// column vector in float32 over an eighth of it, the eight
-// row lanes are joined in LDS, and the ranges' float32 sums are joined by
-// bias_reduce_kernel in float64 in range order: no atomics, the same bits
-// every time. The sums take the unrounded g_u.
+// column vector in float32 over an eighth of it, the eight row lanes are joined
+// in LDS, in float32 too, and the ranges' sums by bias_reduce_kernel in float64,
+// in range order: no atomics, the same bits every time. A range is 32 rows (up
+// to 64 rows are one, whose float32 sum is g_bias; past 2^20 rows ranges grow,
+// to 2^15 rows at 2^30). The sums take the unrounded g_u.
 #include <algorithm>
 
 #include "common.h"
@@ -26,7 +27,10 @@ constexpr int NT = 256, kVecs = 32, kLanes = NT / kVecs;
 // grid's limit
 constexpr int kRows = 4 * kLanes, kMaxSplits = 32768;
 // so few rows are one range, whose sums are the bias gradient itself: one
-// launch less where launches are what costs
+// launch less where launches are what costs (g_bias of d = 2048 silu, in one
+// range against ranges of 32: bf16 48 rows 4.1 us against 5.3, 64 rows 4.5
+// against 5.4, 96 rows 5.7 against 5.5, 128 rows 6.9 against 5.5; float32 64
+// rows 5.3 against 5.7, 96 rows 6.8 against 5.7; d = 256 and 8192 alike)
 constexpr int kOneRange = 64;
 int rows_per_split(int64_t rows) {
   if (rows <= kOneRange) return (int)rows;

@@ -18,8 +18,8 @@ namespace {
 // These and the constants below are fitted to the times of 600 random
 // products on an MI355X under every shape and split (9 .. 4096 tokens, widths
 // 128 .. 14336) and 250 of a model's sizes: the estimates are within 11% (one
-// standard deviation), and the plans chosen by them cost 1.2% (forward) and
-// 2.3% (backward pair) more than the best plan of each product, on average
+// standard deviation), and the plans chosen by them cost 1.0 to 1.2% (forward)
+// and 2.3% (backward pair) more than the best plan of each product, on average
 // over others like them. Without the fixed costs, which decide the short
 // reductions of g_W at few tokens, 5 and 9%, up to 1.9 times.
 struct Shape {
@@ -172,7 +172,10 @@ namespace {
 
 // The dense kernel's time for an M x N x K product, as the tile kernel's plan
 // estimates its own: rounds of 256 x 256 tiles over the CUs (1.38 us a round
-// and 64 of k, 6 us for a round's epilogue, measured at 4096 x 4096 x 4096).
+// and 64 of k, 6 us for a round's epilogue). One estimate for the forward's
+// paired copies and g_x's plain ones; without activation, measured and (estimated):
+// 4096 x 4096 x 4096 forward 104 us, g_x 103 (97); 8192 x 14336 x 4096 674 (663),
+// its g_x 665 (633); 2048 x 8192 x 2048 57 (53); 4096 x 4096 x 1024 36 (31).
 float dense_cost(int64_t M, int64_t N, int64_t K) {
   const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), 256);
   return 3.0f + (float)rounds * (1.38f * (float)K / 64 + 6.0f);

@@ -4,7 +4,8 @@
 // twice:
 //   u(m, n) = scale[n] sum_k x(m, k) W(n, k) + bias[n],  y = act(u) + residual.
 //
-// A workgroup owns 16 rows of W (output columns) for all tokens, up to 16; its
+// A workgroup owns 16 rows of W (output columns) for all tokens (kStreamRows at
+// most, of the 16 that a product has room for); its
 // eight waves take interleaved pieces of k, so that the workgroup reads whole
 // 128-byte lines of each row, kUnroll loads of 16 bytes a lane in flight a
 // wave. The fragments need no LDS: lane l of a 16 x 16 x 32 product holds k =
@@ -14,9 +15,10 @@
 // one thread per four columns ends them with the epilogue: one launch, no
 // workspace.
 //
-// x comes from the caches, once per 16 rows of W: as many bytes as the weight
-// at 16 tokens, which is why more tokens go to the tile kernel, whose
-// workgroups share x among 64 rows and more.
+// x comes from the caches, once per 16 rows of W: half as many bytes as the
+// weight at 8 tokens and as many at 16, which is why more than kStreamRows go to
+// the tile kernel, whose workgroups share x among 64 rows and more (measured at
+// kStreamRows).
 //
 // INT8 codes are widened in registers: code + 128 as an unsigned byte to
 // float32, less 128, to bf16, all exact.

@@ -517,9 +517,13 @@ finish_kernel(const float* __restrict__ part, int nsplit, int64_t rows, int N, E
   }
 }
 
-// NS, NS8: ring depth, and with INT8 codes. (32 x 64 tiles, whose step is
-// short against a load's latency, six deep: 16 x 4096 x 14336 26.6 -> 24.5 us;
-// INT8 there 19.0 us in four, 20.6 in six.)
+// NS, NS8: ring depth, and with INT8 codes. The step of 32 x 64 tiles is short
+// against a load's latency. bf16 six deep against four, 16 tokens of 14336 x
+// 4096 (d_in x d_out) 27.0 us against 29.1, 4096 x 14336 28.2 against 29.5, 4096
+// x 4096 11.6 against 12.3, but 2048 x 2048 7.7 against 7.4 and 1008 x 5000 6.6
+// against 6.2; 9, 30 and 60 tokens alike. INT8 codes, half the bytes a step and
+// more work on them, four deep against six: 20.9 against 22.2, 23.9 against
+// 22.8, 11.7 against 12.2, 7.9 against 7.9, 7.5 against 8.3.
 template <typename T, int BM, int BN, int WM, int WN, int NS, int NS8 = NS>
 hipError_t launch_cfg(bool ak, bool bk, const TileProduct& p, int nsplit, hipStream_t s) {
   const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);

@@ -6,7 +6,8 @@ after training, or a weight that was never reparameterised).
 
 dense_forward and dense_backward take contiguous device tensors x [tokens,
 d_in], W [d_out, d_in], residual and u [tokens, d_out] of one type (float32 or
-bfloat16) and a float32 bias [d_out]; W may be the int8 codes of
+bfloat16) and a float32 bias [d_out], of at least one row, widths that are
+multiples of 16 bytes and 16-byte aligned; W may be the int8 codes of
 poetx_quantize_weight with their float32 row scales w_scale [d_out].
 DenseLinear keeps a weight and its bias. Outputs and workspaces come from
 torch's allocator on the stream that the call runs on, so calls on different
