@@ -10,9 +10,11 @@
 //                  z = C (u + A u^3);                 slope p + u p (1 - p) 2 z'
 //   gelu(u)      = u Phi(u);                          slope Phi(u) + u phi(u)
 //
-// float32 tensors (Precise): the exponential and the complementary error
-// function to float32's last place, true division, and 1 - p as e^-v p where
-// it is small: within about one rounding a step of the formula.
+// float32 tensors (kPrecise): the exponential, the complementary error function
+// and the quotient to float32's last place, and 1 - p as e^-v p where it is
+// small: within about one rounding a step of the formula. 2048 x 2048 g_bias
+// (the slopes alone) gelu 14.7 us, gelu_tanh 12.9, silu 12.7, in the bf16 forms
+// 12.5, 12.0 and 11.8; a forward takes 0 to 3% longer.
 //
 // bf16 tensors: their last place is 2^16 times float32's, so the cheapest
 // forms that are good to 1.5e-7: the hardware's exponential and reciprocal, and
@@ -73,11 +75,25 @@ template <typename T, Activation ACT> __device__ __forceinline__ float activate(
   return u;
 }
 
-// the slope of v p(s(v)), p the logistic function and ds the slope of s
+// e^v for v <= 88 within about one step of float32: what v / ln 2 loses by its
+// rounding, times ln 2, corrects the hardware's 2^x
+__device__ __forceinline__ float exp_below(float v) {
+  constexpr float kHi = 1.44269504f, kLo = 1.92596299e-8f;  // 1 / ln 2
+  const float t = v * kHi, rest = fmaf(v, kLo, fmaf(v, kHi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, rest * 0.69314718f, e);
+}
+
+// the slope of v p(s(v)), p the logistic function and ds the slope of s. In the
+// precise form |s| is cut at 87, where p is 0 or 1 to 2e-38, for exp_below and
+// the reciprocal, a Newton step of the hardware's: 2048 x 2048 silu 12.7 us, with
+// expf and a division 14.2, in the bf16 form 11.8.
 template <typename T>
 __device__ __forceinline__ float logistic_slope(float v, float s, float ds) {
   if constexpr (kPrecise<T>) {
-    const float e = expf(-s), p = 1.0f / (1.0f + e);
+    const float c = s > 87.0f ? 87.0f : s < -87.0f ? -87.0f : s;
+    const float e = exp_below(-c), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+    const float p = fmaf(r, fmaf(-d, r, 1.0f), r);
     return fmaf(v * p * (s > 0.0f ? e * p : 1.0f - p), ds, p);
   } else {
     const float p = logistic(s);
@@ -92,7 +108,7 @@ template <typename T, Activation ACT> __device__ __forceinline__ float activatio
     return logistic_slope<T>(v, tanh_argument(v),
                              2.0f * kGeluC * fmaf(3.0f, kGeluA * v * v, 1.0f));
   if constexpr (kPrecise<T>)
-    return fmaf(v * 0.3989422804014327f, expf(-0.5f * v * v),
+    return fmaf(v * 0.3989422804014327f, exp_below(-0.5f * v * v),
                 0.5f * erfcf(v * -0.70710678118654752f));
   float e;
   const float q = normal_tail(v, &e);
