@@ -112,3 +112,27 @@ def test_merge_on_another_stream():
     dense = lay.merge(bias=torch.ones(384), activation="relu", stream=s)
     s.synchronize()
     assert torch.equal(W, want) and torch.equal(dense.W, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d_in,d_out,b_in,b_out", [(64, 96, 8, 8), (768, 512, 256, 256),
+                                                   (1024, 1536, 512, 512), (520, 264, 64, 32),
+                                                   (256, 640, 32, 128), (96, 104, 24, 8)])
+def test_merged_weight_of_other_block_sizes_and_permutations(d_in, d_out, b_in, b_out, dtype):
+    gen = torch.Generator().manual_seed(d_in)
+    W0 = torch.randn(d_out, d_in, generator=gen) / 16
+    po, pi = torch.randperm(d_out, generator=gen), torch.randperm(d_in, generator=gen)
+    for perms in ({}, {"perm_out": po, "perm_in": pi}):
+        lay = PoetxLinear(W0, b_in, b_out, dtype, **perms)
+        lay.theta_R.normal_(0, 0.02)
+        lay.theta_P.normal_(0, 0.02)
+        lay.build()
+        x = torch.randn(70, d_in, generator=gen).to(lay.torch_dtype).cuda()
+        y, _ = lay.forward(x)
+        W = lay.merged_weight(rows=77)
+        if not perms:
+            ref, size = exact(lay)
+            b = max(b_in, b_out)
+            assert ((W.double().cpu() - ref).abs() <= tolerance(ref, size, b, dtype)).all()
+        # (the layer's own y rounds U, Z and y: the parity tests' tolerance)
+        U.check("merged y", U.host(lay.merge().forward(x)[0]), U.host(y), dtype)
