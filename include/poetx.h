@@ -391,10 +391,10 @@ typedef enum poetx_activation {
 } poetx_activation;
 
 typedef struct poetx_dense_desc {
-  int64_t tokens;     /* rows of x, y, u, residual, g_y, g_x; 1 .. 2^30, and
-                         with float32 fewer than 2^24 tiles of 64 x 64 in y and
-                         in g_x (also in g_W, where it is asked for), the most
-                         that one launch takes: else POETX_ERR_SHAPE */
+  int64_t tokens;     /* rows of x, y, u, residual, g_y, g_x; 1 .. 2^30. An
+                         output asked for of 2^24 or more float32 tiles of 64 x
+                         64 (bf16: 2^23 of 256 x 128) is more than one launch
+                         takes: POETX_ERR_SHAPE */
   int64_t d_in;       /* columns of W; at most 2^22 */
   int64_t d_out;      /* rows of W; at most 2^22 */
   int32_t act;        /* poetx_dtype of x, W, residual, y, u and their gradients */

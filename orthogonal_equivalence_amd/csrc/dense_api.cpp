@@ -41,7 +41,6 @@ int check_desc(const poetx_dense_desc* d) {
     return POETX_ERR_ALIGN;
   const int v = act_vec(d->act);
   if (d->d_in % v || d->d_out % v) return POETX_ERR_ALIGN;
-  if (!poetx::dense_launchable(dtype_of(d), d->tokens, d->d_in, d->d_out)) return POETX_ERR_SHAPE;
   return POETX_OK;
 }
 
@@ -129,6 +128,7 @@ int poetx_dense_fwd(const poetx_dense_desc* d, const void* x, const void* W, con
   for (const void* p : {x, W, (const void*)bias, residual, (const void*)y, (const void*)u_save})
     if (p && !aligned16(p)) return POETX_ERR_ALIGN;
   const FwdPlan plan = plan_fwd(d);
+  if (!plan.launchable()) return POETX_ERR_SHAPE;
   if (plan.total && (!ws || ws_bytes < plan.total)) return POETX_ERR_WORKSPACE;
   if (plan.total && !aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t es = act_size(d->act), out = (size_t)d->tokens * d->d_out * es;
@@ -203,7 +203,7 @@ int poetx_dense_bwd(const poetx_dense_desc* d, const void* g_y, const void* x, c
                         (const void*)g_bias})
     if (p && !aligned16(p)) return POETX_ERR_ALIGN;
   const BwdPlan plan = plan_bwd(d);
-  if (g_W && plan.gw.nsplit == 0) return POETX_ERR_SHAPE;
+  if ((g_x && !plan.gx_launchable()) || (g_W && !plan.gw_launchable())) return POETX_ERR_SHAPE;
   if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
   if (!aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t es = act_size(d->act);

@@ -190,12 +190,6 @@ constexpr float kWidenLaunch = 3.0f, kWidenBytesPerUs = 4.5e6f;
 
 }  // namespace
 
-bool dense_launchable(DType t, int64_t tokens, int64_t d_in, int64_t d_out) {
-  const Shape* shapes = t == DType::BF16 ? kBf16Shapes : kF32Shapes;
-  const Shape& h = shapes[0];  // the fewest work items, where they count
-  return tiles_of(h, tokens, std::max(d_in, d_out)) * h.threads <= kMaxWorkItems;
-}
-
 FwdChoice choose_fwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d_out) {
   FwdChoice p = {};
   // few tokens: the weight read once, straight into the products
@@ -231,7 +225,7 @@ BwdChoice choose_bwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d
   }
   p.gw = plan_tile_product(t, K, N, M, false);
   p.pair = plan_tile_pair(t, M, N, K);
-  p.paired = !int8 && p.pair.cost < p.gx.cost + p.gw.cost;
+  p.paired = !int8 && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
   return p;
 }
 

@@ -11,18 +11,19 @@ struct FwdChoice {
   bool dense;           // the 256 x 256 tiles, else `tile`
   bool widen, w_tiled;  // INT8 codes widened into the workspace (in the tiled layout)
   TilePlan tile;
+  // whether a launch takes the tiles of y
+  bool launchable() const { return stream || dense || tile.nsplit != 0; }
 };
 FwdChoice choose_fwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d_out);
 
 struct BwdChoice {
   bool dense;       // g_x on the 256 x 256 tiles, else `gx`
   bool paired;      // g_x and g_W, where both are asked for, in one launch
-  TilePlan gx, gw;  // gw.nsplit 0: no launch takes g_W's tiles
+  TilePlan gx, gw;
   TilePairPlan pair;
+  bool gx_launchable() const { return dense || gx.nsplit != 0; }
+  bool gw_launchable() const { return gw.nsplit != 0; }
 };
 BwdChoice choose_bwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d_out);
-
-// Whether launches take the tiles of y and g_x.
-bool dense_launchable(DType t, int64_t tokens, int64_t d_in, int64_t d_out);
 
 }  // namespace poetx

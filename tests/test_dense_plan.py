@@ -25,14 +25,14 @@ int main() {
     const DType d = static_cast<DType>(t);
     const FwdChoice f = choose_fwd(d, int8, m, n, k);
     const BwdChoice b = choose_bwd(d, int8, m, n, k);
-    printf("%d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d\n", dense_launchable(d, m, n, k),
-           f.stream, f.dense, f.widen, f.w_tiled, f.tile.shape, f.tile.nsplit, b.dense, b.paired,
+    printf("%d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d\n", f.launchable(),
+           b.gx_launchable(), b.gw_launchable(), f.stream, f.dense, f.widen, f.w_tiled, f.tile.shape, f.tile.nsplit, b.dense, b.paired,
            b.gx.shape, b.gx.nsplit, b.gw.shape, b.gw.nsplit, b.pair.gx.shape, b.pair.gx.nsplit,
            b.pair.gw.shape, b.pair.gw.nsplit);
   }
 }
 """
-FIELDS = ("launchable", "stream", "dense", "widen", "w_tiled", "shape", "split", "b_dense", "paired",
+FIELDS = ("y_fits", "gx_fits", "gw_fits", "stream", "dense", "widen", "w_tiled", "shape", "split", "b_dense", "paired",
           "gx_shape", "gx_split", "gw_shape", "gw_split", "px_shape", "px_split", "pw_shape",
           "pw_split")
 F32, BF16 = 0, 1
@@ -84,53 +84,50 @@ def test_every_chosen_launch_fits():
     for _ in range(4000):
         n, k = (8 * rng.randint(1, 1 << rng.randint(0, 19)) for _ in range(2))
         cases.append((rng.randint(0, 1), 0, rng.randint(9, 1 << rng.randint(4, 30)), n, k))
-    least = {F32: 0, BF16: 0}
+    refused = 0
     for (t, _, m, n, k), p in zip(cases, plans(cases)):
-        if not p["launchable"]:
-            least[t] += 1
-            assert work_items(t, 0, m, max(n, k)) >= 1 << 32
-            continue
-        if not p["dense"]:
-            assert p["split"] >= 1 and work_items(t, p["shape"], m, k) < 1 << 32
-        if not p["b_dense"]:
-            assert p["gx_split"] >= 1 and work_items(t, p["gx_shape"], m, n) < 1 << 32
-        if p["gw_split"]:
-            assert work_items(t, p["gw_shape"], k, n) < 1 << 32
-        else:
-            assert work_items(t, 0, k, n) >= 1 << 32
+        # an output is refused where no shape's tiles fit
+        for fits, dense, shape, split, rows, cols in (
+                (p["y_fits"], p["dense"], p["shape"], p["split"], m, k),
+                (p["gx_fits"], p["b_dense"], p["gx_shape"], p["gx_split"], m, n),
+                (p["gw_fits"], 0, p["gw_shape"], p["gw_split"], k, n)):
+            if dense:
+                assert fits
+            elif fits:
+                assert split >= 1 and work_items(t, shape, rows, cols) < 1 << 32
+            else:
+                refused += 1
+                assert all(work_items(t, i, rows, cols) >= 1 << 32 for i in range(len(SHAPES[t])))
         if p["paired"]:
-            assert p["px_shape"] == p["pw_shape"]
+            assert p["px_shape"] == p["pw_shape"] and p["px_split"] >= 1 and p["pw_split"] >= 1
             assert work_items(t, p["px_shape"], m, n, p["px_split"], 7) + \
                 work_items(t, p["pw_shape"], k, n, p["pw_split"]) < 1 << 32
-    assert least[F32] > 20
+    assert refused > 20
 
 
 def test_products_past_one_launch_are_refused():
-    """Before anything is enqueued, also by the workspace sizes."""
+    """Before anything is enqueued, and only where that output is asked for."""
     P = pytest.importorskip("orthogonal_equivalence_amd.poetx")
     import torch
     if torch.cuda.is_available():
         pytest.skip("host-validation tests use fake device addresses; run them without a GPU")
     A = 1 << 44
 
-    def status(tokens, d_in, d_out, act, g_W=None, activation=P.POETX_ACT_RELU):
-        d = P.make_dense_desc(tokens, d_in, d_out, act, activation)
-        sizes = P.poetx_dense_fwd_workspace_size(d), P.poetx_dense_bwd_workspace_size(d)
-        # (validation ends at the missing workspace, or at the aliased y, where
-        # the sizes are taken: nothing is launched on these addresses)
+    def status(tokens, d_in, d_out, act):
+        """The forward's status, the backward's of g_x, of g_W and of g_bias alone.
+        (Validation ends at the aliased y, or at the missing workspace: nothing is
+        launched on these addresses.)"""
+        d = P.make_dense_desc(tokens, d_in, d_out, act, P.POETX_ACT_RELU)
+        assert P.poetx_dense_bwd_workspace_size(d) > 0
         fwd = P._lib.poetx_dense_fwd(d, A, 2 * A, None, None, A, None, 4 * A, 1 << 43, None)
-        bwd = P._lib.poetx_dense_bwd(d, A, 2 * A, 3 * A, 4 * A, 5 * A, g_W, 6 * A, None, 0, None)
-        return sizes, fwd, bwd
+        return fwd, *(P._lib.poetx_dense_bwd(d, A, 2 * A, 3 * A, 4 * A, *outs, None, 0, None)
+                      for outs in ((5 * A, None, None), (None, 5 * A, None), (None, None, 5 * A)))
 
-    for tokens, d_in, d_out in ((1 << 30, 8, 8), (1 << 29, 72, 8), (1 << 29, 8, 72)):
-        assert status(tokens, d_in, d_out, P.POETX_F32) == ((0, 0), P.POETX_ERR_SHAPE,
-                                                           P.POETX_ERR_SHAPE)
-        (_, size), fwd, bwd = status(tokens, d_in, d_out, P.POETX_BF16)
-        assert size > 0 and (fwd, bwd) == (P.POETX_ERR_ALIAS, P.POETX_ERR_WORKSPACE)
-    for tokens, d_in, d_out in (((1 << 30) - 64, 8, 8), ((1 << 29) - 64, 72, 72)):
-        (_, size), fwd, bwd = status(tokens, d_in, d_out, P.POETX_F32)
-        assert size > 0 and (fwd, bwd) == (P.POETX_ERR_ALIAS, P.POETX_ERR_WORKSPACE)
-    # a weight whose gradient no launch takes: only the gradient is refused
-    (_, size), fwd, bwd = status(9, 1 << 22, 1 << 14, P.POETX_F32)
-    assert size > 0 and (fwd, bwd) == (P.POETX_ERR_ALIAS, P.POETX_ERR_WORKSPACE)
-    assert status(9, 1 << 22, 1 << 14, P.POETX_F32, g_W=7 * A)[2] == P.POETX_ERR_SHAPE
+    # past validation, and refused
+    y, b, no = P.POETX_ERR_ALIAS, P.POETX_ERR_WORKSPACE, P.POETX_ERR_SHAPE
+    for tokens, d_in, d_out, want in (
+            (1 << 30, 8, 8, (no, no, b, b)), ((1 << 30) - 64, 8, 8, (y, b, b, b)),
+            (1 << 29, 8, 72, (no, b, b, b)), (1 << 29, 72, 8, (y, no, b, b)),
+            ((1 << 29) - 64, 72, 72, (y, b, b, b)), (9, 1 << 22, 1 << 14, (y, b, no, b))):
+        assert status(tokens, d_in, d_out, P.POETX_F32) == want, (tokens, d_in, d_out)
+        assert status(tokens, d_in, d_out, P.POETX_BF16) == (y, b, b, b), (tokens, d_in, d_out)
