@@ -83,11 +83,11 @@ def test_every_variant(case):
         assert torch.equal(g_b, g_u.sum(0).float())
 
 
-def filled(gen, shape, top, part, dtype):
+def filled(gen, shape, top, part, dtype, rows=65_536):
     """integers() into a large tensor, some rows at a time."""
     out = torch.empty(shape, device="cuda", dtype=dtype)
-    for i in range(0, shape[0], 65_536):
-        n = min(65_536, shape[0] - i)
+    for i in range(0, shape[0], rows):
+        n = min(rows, shape[0] - i)
         out[i:i + n] = integers(gen, (n, shape[1]), top, part, "cuda")
     return out
 
@@ -157,3 +157,37 @@ def test_weights_past_32_bits(int8, tokens):
     same("g_x", g_x, ref)
     same("g_bias", g_b, g_y.double().sum(0))
     assert ref.abs().mean() > 50
+
+
+@pytest.mark.parametrize("t,tokens,width", [(F32, (1 << 30) - 64, 4), (BF16, 1 << 30, 8)],
+                         ids=["f32", "bf16"])
+def test_most_rows(t, tokens, width):
+    """The most rows that the calls take (float32: 2^24 - 1 tiles): every element
+    of every output. (Sums of 2^30 products of -1, 0 and 1 stay some ten
+    thousand, whole numbers that float32 holds, in any order.)"""
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    dt, part = DTYPE[t], 1 << 23
+    x = filled(gen, (tokens, width), 1, 0.3, dt, part)
+    g_y = filled(gen, (tokens, width), 1, 0.3, dt, part)
+    W = integers(gen, (width, width), 2, 0.8, "cuda").to(dt)
+    bias = integers(gen, (width,), 1, 1.0, "cuda").float()
+    y, u = dense_forward(x, W, bias, g_y, "relu", save_u=True)
+    g_x, g_W, g_b = dense_backward(g_y, W, x, u, "relu", need_g_W=True, need_g_bias=True)
+    W64, b64 = W.double(), bias.double()
+    ref = torch.zeros(width, width, device="cuda", dtype=torch.float64)
+    sums = ref.new_zeros(width)
+    for i in range(0, tokens, part):
+        at = slice(i, min(tokens, i + part))
+        x64, g64 = x[at].double(), g_y[at].double()
+        u64 = x64 @ W64.t() + b64
+        same("u", u[at], u64)
+        same("y", y[at], u64.clamp(min=0) + g64)
+        g64 *= u64 > 0
+        same("g_x", g_x[at], g64 @ W64)
+        # (column by column: a product of so few outputs is slow in the library)
+        ref += torch.stack([(g64 * x64[:, j:j + 1]).sum(0) for j in range(width)], 1)
+        sums += g64.sum(0)
+        if i % (16 * part) == 0:
+            print("    row", i, flush=True)
+    same("g_W", g_W, ref)
+    same("g_bias", g_b, sums)
