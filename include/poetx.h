@@ -449,6 +449,77 @@ int poetx_dense_bwd(const poetx_dense_desc* desc, const void* g_y, const void* x
                     const void* u_saved, void* g_x, void* g_W, float* g_bias, void* ws,
                     size_t ws_bytes, void* stream);
 
+/* ---- Losses over a vocabulary, without the logits ----
+ *
+ * The end of a language model: a projection onto the vocabulary, z = x W^T, and
+ * a loss of each row's logits. The logits live in registers (forward) or, as
+ * their gradient, a piece of the vocabulary at a time in the workspace
+ * (backward, which forms them again); no tensor of tokens x vocab is kept.
+ *
+ *   cross entropy  lse = log sum_j exp(z_j),  loss = lse - z[target]
+ *                  g_z = (g_loss + g_lse) exp(z - lse) - g_loss [j = target]
+ *     A row whose target is negative takes no part: its loss and lse are 0, its
+ *     g_x is 0 and g_W gets nothing of it, whatever its x holds.
+ *   distillation   from the logits t_k that a teacher gave to `top` ids of each
+ *                  row, at the temperature T:
+ *                  p = softmax(t / T) over the row's entries,
+ *                  lse = log sum_j exp(z_j / T),
+ *                  loss = T^2 sum_k p_k (log p_k - z[id_k] / T + lse)
+ *                  g_z = g_loss T (exp(z / T - lse) - sum_k p_k [j = id_k])
+ *     An entry with a negative id or a logit of -infinity takes no part (rows
+ *     with fewer entries than `top`), a row without any neither: its loss,
+ *     lse and gradient are 0. An id listed twice counts twice.
+ *   both           g_x = g_z W,  g_W = g_z^T x
+ *
+ * A target or id past the vocabulary is read nowhere; its row's loss and
+ * gradients are NaN. Logits, sums and losses are float32; g_z is rounded to
+ * the act type once, as the operand of the gradients' products (the matrix
+ * cores take bf16). Sums are joined in a fixed order: bitwise reproducible. */
+typedef struct poetx_vocab_desc {
+  int64_t tokens;      /* rows of x; 1 .. 2^24 */
+  int64_t d;           /* columns of x and W, a multiple of 16 bytes; at most 2^22 */
+  int64_t vocab;       /* rows of W, any number; at most 2^22. x and W hold at
+                          most 2^35 values each (POETX_ERR_SHAPE) */
+  int32_t act;         /* poetx_dtype of x, W, g_x, g_W */
+  int32_t top;         /* 0: cross entropy; 1 .. 1024: distillation */
+  int32_t teacher;     /* distillation: poetx_dtype of the teacher's logits; else 0 */
+  float temperature;   /* distillation: T, 1e-6 .. 1e6; else 1 */
+  int32_t flags;       /* must be 0 */
+  int32_t reserved;    /* must be 0 */
+} poetx_vocab_desc;
+
+/* Workspace bytes (0 if the descriptor is invalid). The backward's covers every
+ * choice of outputs. */
+size_t poetx_vocab_fwd_workspace_size(const poetx_vocab_desc* desc);
+size_t poetx_vocab_bwd_workspace_size(const poetx_vocab_desc* desc);
+
+/*
+ *   x        [tokens, d] act,  W [vocab, d] act
+ *   targets  [tokens] int64 (8-byte aligned);  ids [tokens, top] int64
+ *   teacher  [tokens, top] logits of desc->teacher's type
+ *   loss, lse  out [tokens] float32 (in the backward lse is the forward's)
+ *   z        [tokens, top] float32: the student's logits at the ids, 0 where the
+ *            id is negative; out, and in the backward the forward's
+ *   g_loss   [tokens] float32
+ *   g_lse    [tokens] float32, the gradient to lse (a penalty on it, say), or NULL
+ *   g_x      out [tokens, d] act, or NULL;  g_W out [vocab, d] act, or NULL;
+ *            both NULL is POETX_ERR_NULL
+ */
+int poetx_cross_entropy_fwd(const poetx_vocab_desc* desc, const void* x, const void* W,
+                            const int64_t* targets, float* loss, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+int poetx_cross_entropy_bwd(const poetx_vocab_desc* desc, const float* g_loss, const float* g_lse,
+                            const void* x, const void* W, const int64_t* targets,
+                            const float* lse, void* g_x, void* g_W, void* ws, size_t ws_bytes,
+                            void* stream);
+int poetx_distill_fwd(const poetx_vocab_desc* desc, const void* x, const void* W,
+                      const int64_t* ids, const void* teacher, float* loss, float* lse, float* z,
+                      void* ws, size_t ws_bytes, void* stream);
+int poetx_distill_bwd(const poetx_vocab_desc* desc, const float* g_loss, const void* x,
+                      const void* W, const int64_t* ids, const void* teacher, const float* lse,
+                      const float* z, void* g_x, void* g_W, void* ws, size_t ws_bytes,
+                      void* stream);
+
 /* ---- Gradient norm over many tensors, and clipping ----
  *
  *   norm = sqrt(sum over every value of every tensor of grad^2),

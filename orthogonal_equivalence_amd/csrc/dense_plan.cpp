@@ -70,7 +70,7 @@ constexpr float kCold = 0.38f;
 // 128 x 64, 56 on 256 x 128; 2048 x 4096 x 4096 69 us on 256 x 128, 75 on 128
 // x 128; 16 x 4096 x 14336 26.7 us on 32 x 64, 28.7 on 64 x 64; 16 x 14336 x
 // 4096 25.3 us on 32 x 64 in 8 splits, 27.0 in 4, 32.0 in 3.
-TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8) {
+TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8, int max_split) {
   const bool bf16 = t == DType::BF16;
   const Shape* shapes = bf16 ? kBf16Shapes : kF32Shapes;
   const int nshapes = (int)((bf16 ? sizeof(kBf16Shapes) : sizeof(kF32Shapes)) / sizeof(Shape));
@@ -86,6 +86,7 @@ TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8
     if (tiles * h.threads > kMaxWorkItems) continue;
     const int64_t slots = (int64_t)kCus * h.per_cu;
     for (int want : kSplits) {
+      if (want > max_split) break;
       const int per = (steps + want - 1) / want, split = (steps + per - 1) / per;
       // (28 x 2560 x 256 in 8 splits of five steps 6.8 us, in 4 7.9; none is
       // made of tiles that fill the chip anyway)

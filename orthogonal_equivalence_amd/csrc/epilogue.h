@@ -183,6 +183,16 @@ __device__ __forceinline__ void epilogue4(const Epilogue& ep, int64_t m, int n, 
     v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
   }
   const int64_t at = m * ep.ld + n;
+  if (ep.add) {
+    float a[4];
+    Quad<float>::load(ep.add + at, a);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += a[e];
+  }
+  if (ep.sum) {
+    Quad<float>::store(ep.sum + at, v);
+    return;
+  }
   if (ep.u) Quad<T>::store(static_cast<T*>(ep.u) + at, v);
   activate4<T>(ep.act, v);
   if (ep.residual) {

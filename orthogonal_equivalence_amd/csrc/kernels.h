@@ -229,8 +229,10 @@ hipError_t launch_scale_block_columns(DType t, const void* M, const float* scale
 enum class Activation : int { None = 0, Relu = 1, Gelu = 2, GeluTanh = 3, Silu = 4 };
 
 // What happens to a product's float32 accumulators (epilogue.h):
-//   u = acc scale[n] + bias[n],  y = act(u) + residual;
-// scale, bias, residual and u may be null. residual, u and y are [M][ld].
+//   u = acc scale[n] + bias[n] + add[m][n],  y = act(u) + residual;
+// scale, bias, add, residual and u may be null. residual, u and y are [M][ld].
+// Products that run one after another are summed through add and sum, float32
+// [M][ld]: with sum (which may be add) u goes there and there is no y.
 struct Epilogue {
   const float* scale = nullptr;
   const float* bias = nullptr;
@@ -239,11 +241,14 @@ struct Epilogue {
   void* u = nullptr;
   int64_t ld = 0;
   int act = 0;  // Activation
+  const float* add = nullptr;
+  float* sum = nullptr;
 };
 
 // C(m, n) = sum_k A(m, k) B(n, k) (layouts as GemmParams) through an
-// epilogue, any M >= 1; N, and every extent that is contiguous in memory, a
-// multiple of 16 bytes. part: plan.part_floats floats when the plan splits K.
+// epilogue, any M >= 1; N a multiple of 16 bytes, and every extent that is
+// contiguous in memory too, or its memory padded to one (along K with zeros,
+// where only one operand is K-major). part: plan.part_floats floats when the plan splits K.
 struct TileProduct {
   const void* A = nullptr;
   const void* B = nullptr;
@@ -263,7 +268,9 @@ struct TilePlan {
   size_t part_floats;
   float cost;  // estimate in us, for comparison with another kernel's
 };
-TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8);
+// (max_split 1: for a product whose epilogue needs the whole sum in its kernel)
+TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8,
+                           int max_split = 16);
 hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
                                bool b_kmajor, hipStream_t s);
 // A backward's g_x = g_u W (A K-major) and g_W = g_u^T x (A M-major), both
@@ -320,6 +327,63 @@ struct ActGrad {
 };
 int act_grad_splits(int64_t rows);
 hipError_t launch_act_grad(DType t, const ActGrad& a, hipStream_t s);
+
+// ---- losses over a vocabulary whose logits are not kept ----
+// Logits of a piece of the vocabulary, z = x W^T, x [M][K], W [N][K] (the
+// piece's rows), both contiguous, K a multiple of 16 bytes, any M and N.
+struct VocabProduct {
+  const void* x = nullptr;
+  const void* W = nullptr;
+  int M = 0, N = 0, K = 0;
+  float scale = 0.0f;  // log2(e) / temperature
+};
+// One row's part in the gradient of its logits:
+//   g_z[j] = a 2^(scale z_j - lse2) - (j == target ? b : 0),
+// and 0 where a is 0 and j is not the target, whatever z is.
+struct VocabRow {
+  float a, lse2, b;
+  int target;  // in the whole vocabulary; -1: none
+};
+// Forward: for every row and slot (a group of the piece's columns)
+// part[slot][row] = (max, sum) with sum_j 2^(scale z_j) = sum 2^max over the slot's
+// columns. vocab_tile_slots of them.
+int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N);
+hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
+                                 int64_t part_ld, hipStream_t s);
+// Backward: g_z of the piece, whose first column is `col0` of the vocabulary,
+// in x's type at gz[row][ldg]; columns N up to the next multiple of 8 are zeroed
+// (ldg holds N rounded up to 256).
+hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
+                                  const VocabRow* rows, void* gz, int64_t ldg, int col0,
+                                  hipStream_t s);
+
+// The listed ids of a row: targets (top = 1) or a teacher's [rows][top].
+struct VocabList {
+  const int64_t* ids = nullptr;
+  const void* teacher = nullptr;  // logits [rows][top] of type `type`; null: targets
+  DType type = DType::F32;
+  int top = 1;
+  int64_t vocab = 0;
+  float temperature = 1.0f;
+};
+// z[row][k] = x[row] . W[ids[row][k]]; 0 where the id is negative, NaN where
+// it is past the vocabulary.
+hipError_t launch_listed_logits(DType t, const void* x, const void* W, const VocabList& l,
+                                int64_t rows, int K, float* z, hipStream_t s);
+// lse from the slots, and the loss: of targets with z their logits, else of
+// the teacher's distribution.
+hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots, const VocabList& l,
+                             int64_t rows, const float* z, float* loss, float* lse, hipStream_t s);
+// The rows' parts, and with xs a copy of x [padded][K] in which rows that take
+// no part, and those past `rows`, are zero.
+hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t padded,
+                             const float* g_loss, const float* g_lse, const float* lse,
+                             VocabRow* out, const void* x, int K, void* xs, hipStream_t s);
+// A teacher's ids in the piece [col0, col0 + N): g_z there, from the student's
+// logits z at them.
+hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
+                                    const float* z, void* gz, int64_t ldg, int col0, int N,
+                                    hipStream_t s);
 
 // ---- gradient norm and clipping over many tensors ----
 // One contiguous run of gradient values; out may equal grad.

@@ -1,0 +1,368 @@
+// Everything of the losses over a vocabulary but their matrix products: the
+// logits at listed ids, the join of the forward's partial sums with the loss,
+// the rows' parts in the backward, and a teacher's entries in the gradient of
+// the logits. All are small beside the products (8192 x 131072 logits: 67 MB of
+// partial sums against 8.8 TFLOP).
+//
+//   lse  = ln 2 (M + log2 sum_i s_i 2^(m_i - M)), (m_i, s_i) the slots' parts
+//   loss = lse - z[target], or with p the softmax of the listed teacher
+//          logits over T: T^2 sum_k p_k (log p_k - z_k / T + lse)
+#include <algorithm>
+
+#include "lds_dma.h"
+#include "vocab.h"
+
+namespace poetx {
+namespace {
+
+constexpr int NT = 256, NWAVES = NT / 64;
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
+
+template <typename T> struct Vec;  // one 16-byte vector as float32
+template <> struct Vec<bf16_t> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void load(const bf16_t* p, float v[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Vec<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void load(const float* p, float v[4]) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  }
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+// One wave a row and four entries: x's piece is loaded once for four rows of
+// W. The products are summed in float32 per lane (K / 64 of them), the lanes as a
+// tree.
+constexpr int kEntries = 4;
+template <typename T>
+__global__ void __launch_bounds__(NT)
+listed_logits_kernel(const T* __restrict__ x, const T* __restrict__ W, const VocabList l,
+                     int64_t rows, int K, float* __restrict__ z) {
+  constexpr int E = Vec<T>::E;
+  const int lane = threadIdx.x & 63;
+  const int groups = (l.top + kEntries - 1) / kEntries;
+  const int64_t at = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
+  const int64_t row = at / groups;
+  const int k0 = (int)(at - row * groups) * kEntries;
+  if (row >= rows) return;
+  int64_t id[kEntries];
+  bool any = false;
+#pragma unroll
+  for (int q = 0; q < kEntries; ++q) {
+    id[q] = k0 + q < l.top ? l.ids[row * l.top + k0 + q] : -1;
+    any |= id[q] >= 0 && id[q] < l.vocab;
+  }
+  float acc[kEntries] = {};
+  if (any) {
+    const T* w[kEntries];
+#pragma unroll
+    for (int q = 0; q < kEntries; ++q)
+      w[q] = W + (id[q] >= 0 && id[q] < l.vocab ? id[q] : 0) * (int64_t)K;
+#pragma unroll 2
+    for (int k = lane * E; k < K; k += 64 * E) {
+      float xv[E], wv[kEntries][E];
+      Vec<T>::load(x + row * K + k, xv);
+#pragma unroll
+      for (int q = 0; q < kEntries; ++q) Vec<T>::load(w[q] + k, wv[q]);
+#pragma unroll
+      for (int q = 0; q < kEntries; ++q)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[q] = fmaf(xv[e], wv[q][e], acc[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kEntries; ++q) {
+    const float v = wave_sum(acc[q]);
+    if (lane == 0 && k0 + q < l.top)
+      z[row * l.top + k0 + q] = id[q] < 0 ? 0.0f : id[q] >= l.vocab ? NAN : v;
+  }
+}
+
+// R rows a workgroup, their slots dealt over NT / R threads each (R a power of
+// two, chosen so that a warm row of part is read in whole lines where there
+// are rows enough, and by many threads where there are few); the threads'
+// parts are joined in order. Targets: the loss too.
+template <bool TARGETS>
+__global__ void __launch_bounds__(NT)
+join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int R, const VocabList l,
+            int64_t rows, const float* __restrict__ z, float* __restrict__ loss,
+            float* __restrict__ lse) {
+  const int r = threadIdx.x & (R - 1), g = threadIdx.x / R, groups = NT / R;
+  const int64_t row = (int64_t)blockIdx.x * R + r;
+  float m = -INFINITY, s = 0.0f;
+  auto add = [&](float2 v) {
+    const float top = fmaxf(m, v.x), to = fabsf(top) < INFINITY ? top : 0.0f;
+    // (a part of -inf alone is 0 2^-inf; NaN sums stay)
+    s = s * __builtin_amdgcn_exp2f(m - to) + v.y * __builtin_amdgcn_exp2f(v.x - to);
+    m = top;
+  };
+  if (row < rows) {
+    const float2* p = part + row;
+    int64_t i = g;
+    for (; i + 7 * groups < slots; i += 8 * groups) {  // eight loads in flight
+      float2 v[8];
+      float top = m;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v[q] = p[(i + q * groups) * part_ld];
+        top = fmaxf(top, v[q].x);
+      }
+      const float to = fabsf(top) < INFINITY ? top : 0.0f;
+      s *= __builtin_amdgcn_exp2f(m - to);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += v[q].y * __builtin_amdgcn_exp2f(v[q].x - to);
+      m = top;
+    }
+    for (; i < slots; i += groups) add(p[i * part_ld]);
+  }
+  __shared__ float2 sums[NT];
+  sums[threadIdx.x] = make_float2(m, s);
+  for (int half = groups / 2; half >= 1; half /= 2) {
+    __syncthreads();
+    if (g < half) {
+      add(sums[threadIdx.x + half * R]);
+      sums[threadIdx.x] = make_float2(m, s);
+    }
+  }
+  if (g != 0 || row >= rows) return;
+  const float at = fabsf(m) < INFINITY ? m : 0.0f;
+  float v = (at + log2f(s)) * kLn2;
+  if constexpr (TARGETS) {
+    const bool part_of = l.ids[row] >= 0;
+    v = part_of ? v : 0.0f;
+    loss[row] = part_of ? v - z[row] : 0.0f;
+  }
+  lse[row] = v;
+}
+
+// One row's teacher distribution, by one wave: entry k of lane k % 64. An
+// entry takes part with an id >= 0 and a logit above -inf.
+struct Teacher {
+  float top, total;  // maximum logit, sum of exp((t - top) / T)
+  bool any, bad;     // whether an entry takes part; an id past the vocabulary among them
+};
+__device__ __forceinline__ float teacher_logit(const VocabList& l, int64_t at) {
+  return l.type == DType::BF16 ? bf16_to_f32(static_cast<const bf16_t*>(l.teacher)[at])
+                               : static_cast<const float*>(l.teacher)[at];
+}
+__device__ __forceinline__ bool takes_part(int64_t id, float t) { return id >= 0 && !(t == -INFINITY); }
+__device__ __forceinline__ float teacher_exp(float t, float top, float rt) {
+  return __builtin_amdgcn_exp2f((t - top) * rt);
+}
+__device__ __forceinline__ Teacher read_teacher(const VocabList& l, int64_t row, float rt, int lane) {
+  Teacher w;
+  float top = -INFINITY;
+  bool any = false, bad = false;
+  for (int k = lane; k < l.top; k += 64) {
+    const int64_t id = l.ids[row * l.top + k];
+    const float t = teacher_logit(l, row * l.top + k);
+    if (!takes_part(id, t)) continue;
+    any = true;
+    bad |= id >= l.vocab;
+    top = fmaxf(top, t);
+  }
+  w.top = wave_max(top);
+  w.any = __any(any);
+  w.bad = __any(bad);
+  float e = 0.0f;
+  for (int k = lane; k < l.top; k += 64) {
+    const float t = teacher_logit(l, row * l.top + k);
+    if (takes_part(l.ids[row * l.top + k], t)) e += teacher_exp(t, w.top, rt);
+  }
+  w.total = wave_sum(e);
+  return w;
+}
+
+// log p_k = (t_k - top) / T - log total; an entry whose p is 0 adds nothing
+__global__ void __launch_bounds__(NT)
+distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z,
+                    float* __restrict__ loss, float* __restrict__ lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const float inv = 1.0f / l.temperature, rt = kLog2e / l.temperature;
+  const Teacher w = read_teacher(l, row, rt, lane);
+  const float log_total = logf(w.total), own = lse[row];
+  float sum = 0.0f;
+  for (int k = lane; k < l.top; k += 64) {
+    const float t = teacher_logit(l, row * l.top + k);
+    if (!takes_part(l.ids[row * l.top + k], t)) continue;
+    const float p = teacher_exp(t, w.top, rt) / w.total;
+    if (p == 0.0f) continue;
+    sum += p * (((t - w.top) - z[row * l.top + k]) * inv - log_total + own);
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) {
+    loss[row] = !w.any ? 0.0f : w.bad ? NAN : l.temperature * l.temperature * sum;
+    if (!w.any) lse[row] = 0.0f;
+  }
+}
+
+// Four rows a workgroup, one wave each: the row's part in the gradient, and
+// its copy of x.
+template <typename T>
+__global__ void __launch_bounds__(NT)
+rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __restrict__ g_loss,
+            const float* __restrict__ g_lse, const float* __restrict__ lse,
+            VocabRow* __restrict__ out, const T* __restrict__ x, int K, T* __restrict__ xs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
+  if (row >= padded) return;
+  bool any = false;
+  if (row < rows) {
+    VocabRow r{0.0f, lse[row] * kLog2e, 0.0f, -1};
+    bool bad = false;
+    if (l.teacher) {
+      for (int k = lane; k < l.top; k += 64) {
+        const int64_t id = l.ids[row * l.top + k];
+        if (!takes_part(id, teacher_logit(l, row * l.top + k))) continue;
+        any = true;
+        bad |= id >= l.vocab;
+      }
+      any = __any(any);
+      bad = __any(bad);
+      r.a = any ? g_loss[row] * l.temperature : 0.0f;
+    } else {
+      const int64_t id = l.ids[row];
+      any = id >= 0;
+      bad = id >= l.vocab;
+      r.b = any ? g_loss[row] : 0.0f;
+      r.a = any && g_lse ? r.b + g_lse[row] : r.b;
+      r.target = any && !bad ? (int)id : -1;
+    }
+    if (bad) r.a = NAN;
+    if (lane == 0) out[row] = r;
+  }
+  if (!xs) return;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
+    *reinterpret_cast<uint4*>(xs + row * K + k) =
+        any ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
+}
+
+// One wave a row: where the row's id j lies in the piece,
+//   g_z[j] = a (2^(scale z_j - lse2) - the sum of p over the entries with that id).
+// The entries' p are in LDS, so that each finds its id's other entries (an id
+// listed twice: both write the same value).
+constexpr int kMaxTop = 1024;
+template <typename T>
+__global__ void __launch_bounds__(NT)
+listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__ r,
+                   const float* __restrict__ z, T* __restrict__ gz, int64_t ldg, int col0, int N) {
+  __shared__ int ids[NWAVES][kMaxTop];
+  __shared__ float p[NWAVES][kMaxTop];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * NWAVES + wave;
+  if (row >= rows) return;
+  const VocabRow own = r[row];
+  if (own.a == 0.0f) return;  // (whose gradient is zero)
+  const float rt = kLog2e / l.temperature;
+  const Teacher w = read_teacher(l, row, rt, lane);
+  for (int k = lane; k < l.top; k += 64) {
+    const int64_t id = l.ids[row * l.top + k];
+    const float t = teacher_logit(l, row * l.top + k);
+    const bool in = takes_part(id, t);
+    ids[wave][k] = in && id < l.vocab ? (int)id : -1;
+    p[wave][k] = in ? teacher_exp(t, w.top, rt) / w.total : 0.0f;
+  }
+  // (a wave reads its own row's entries only)
+  asm volatile("" ::: "memory");
+  wait_lds();
+  asm volatile("" ::: "memory");
+  for (int k = lane; k < l.top; k += 64) {
+    const int id = ids[wave][k];
+    if (id < col0 || id >= col0 + N) continue;
+    float sum = 0.0f;
+    for (int q = 0; q < l.top; ++q) sum += ids[wave][q] == id ? p[wave][q] : 0.0f;
+    const float e = __builtin_amdgcn_exp2f(fmaf(z[row * l.top + k], rt, -own.lse2));
+    store_as(gz + row * ldg + (id - col0), own.a * (e - sum));
+  }
+}
+
+bool fits(int64_t blocks) { return blocks * NT <= kMaxWorkItems; }
+
+}  // namespace
+
+hipError_t launch_listed_logits(DType t, const void* x, const void* W, const VocabList& l,
+                                int64_t rows, int K, float* z, hipStream_t s) {
+  const int64_t waves = rows * ((l.top + kEntries - 1) / kEntries);
+  const int64_t blocks = (waves + NWAVES - 1) / NWAVES;
+  if (!fits(blocks)) return hipErrorInvalidValue;
+  if (t == DType::BF16)
+    hipLaunchKernelGGL(listed_logits_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s,
+                       static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(W), l, rows, K, z);
+  else
+    hipLaunchKernelGGL(listed_logits_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s,
+                       static_cast<const float*>(x), static_cast<const float*>(W), l, rows, K, z);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots, const VocabList& l,
+                             int64_t rows, const float* z, float* loss, float* lse, hipStream_t s) {
+  int R = 1;
+  while (R < 32 && R < rows) R *= 2;
+  const int64_t blocks = (rows + R - 1) / R, loss_blocks = (rows + NWAVES - 1) / NWAVES;
+  if (!fits(blocks) || !fits(loss_blocks)) return hipErrorInvalidValue;
+  if (!l.teacher) {
+    hipLaunchKernelGGL(join_kernel<true>, dim3((unsigned)blocks), dim3(NT), 0, s, part, part_ld,
+                       slots, R, l, rows, z, loss, lse);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(join_kernel<false>, dim3((unsigned)blocks), dim3(NT), 0, s, part, part_ld,
+                     slots, R, l, rows, z, loss, lse);
+  hipLaunchKernelGGL(distill_loss_kernel, dim3((unsigned)loss_blocks), dim3(NT), 0, s, l, rows, z,
+                     loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t padded,
+                             const float* g_loss, const float* g_lse, const float* lse,
+                             VocabRow* out, const void* x, int K, void* xs, hipStream_t s) {
+  const int64_t n = xs ? padded : rows, blocks = (n + NWAVES - 1) / NWAVES;
+  if (!fits(blocks)) return hipErrorInvalidValue;
+  if (t == DType::BF16)
+    hipLaunchKernelGGL(rows_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, n,
+                       g_loss, g_lse, lse, out, static_cast<const bf16_t*>(x), K,
+                       static_cast<bf16_t*>(xs));
+  else
+    hipLaunchKernelGGL(rows_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, n,
+                       g_loss, g_lse, lse, out, static_cast<const float*>(x), K,
+                       static_cast<float*>(xs));
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
+                                    const float* z, void* gz, int64_t ldg, int col0, int N,
+                                    hipStream_t s) {
+  const int64_t blocks = (rows + NWAVES - 1) / NWAVES;
+  if (!fits(blocks) || l.top > kMaxTop) return hipErrorInvalidValue;
+  if (t == DType::BF16)
+    hipLaunchKernelGGL(listed_grad_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
+                       r, z, static_cast<bf16_t*>(gz), ldg, col0, N);
+  else
+    hipLaunchKernelGGL(listed_grad_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
+                       r, z, static_cast<float*>(gz), ldg, col0, N);
+  return hipGetLastError();
+}
+
+}  // namespace poetx

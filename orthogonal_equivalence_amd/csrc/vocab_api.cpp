@@ -1,0 +1,315 @@
+// C ABI of the losses over a vocabulary whose logits are not kept
+// (poetx_cross_entropy_fwd / _bwd, poetx_distill_fwd / _bwd): argument
+// validation, workspace planning and the order of kernel launches. Declarations
+// and the contract are in include/poetx.h. Validation touches no HIP API, so
+// every argument error is reported before anything is enqueued.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api_util.h"
+#include "kernels.h"
+#include "poetx.h"
+
+using poetx::DType;
+using poetx::TilePlan;
+using poetx::TileProduct;
+using poetx::VocabList;
+using poetx::VocabProduct;
+using poetx::VocabRow;
+using namespace poetx::api;
+
+namespace {
+
+constexpr int64_t kMaxTokens = 1 << 24, kMaxWidth = 1 << 22, kMaxTop = 1024;
+constexpr int64_t kMaxValues = INT64_C(1) << 35;  // of x or W
+// What the logits' pieces may take in the workspace: the forward's partial
+// sums of a range of rows, the backward's gradient of a range of columns.
+constexpr int64_t kPartBytes = INT64_C(128) << 20, kPieceBytes = INT64_C(256) << 20;
+constexpr int64_t kTile = 256;  // rows and columns of a piece, where there is more than one
+
+DType dtype_of(const poetx_vocab_desc* d) {
+  return d->act == POETX_BF16 ? DType::BF16 : DType::F32;
+}
+
+int check_desc(const poetx_vocab_desc* d) {
+  if (!d) return POETX_ERR_NULL;
+  if (d->act != POETX_F32 && d->act != POETX_BF16) return POETX_ERR_DTYPE;
+  if (d->tokens < 1 || d->d < 1 || d->vocab < 1) return POETX_ERR_SHAPE;
+  if (d->tokens > kMaxTokens || d->d > kMaxWidth || d->vocab > kMaxWidth) return POETX_ERR_SHAPE;
+  if (d->top < 0 || d->top > kMaxTop || d->flags != 0 || d->reserved != 0)
+    return POETX_ERR_SHAPE;
+  if (d->top == 0) {
+    if (d->teacher != 0 || d->temperature != 1.0f) return POETX_ERR_SHAPE;
+  } else {
+    if (d->teacher != POETX_F32 && d->teacher != POETX_BF16) return POETX_ERR_DTYPE;
+    // (so that it, its square and its inverse are ordinary numbers)
+    if (!(d->temperature >= 1e-6f && d->temperature <= 1e6f)) return POETX_ERR_SHAPE;
+  }
+  // (the gradients' tiles fit a launch, their counts an int)
+  if (std::max(d->tokens, d->vocab) * d->d > kMaxValues) return POETX_ERR_SHAPE;
+  if (d->d % act_vec(d->act)) return POETX_ERR_ALIGN;
+  return POETX_OK;
+}
+
+size_t x_bytes(const poetx_vocab_desc* d) { return (size_t)d->tokens * d->d * act_size(d->act); }
+size_t w_bytes(const poetx_vocab_desc* d) { return (size_t)d->vocab * d->d * act_size(d->act); }
+size_t list_entries(const poetx_vocab_desc* d) { return (size_t)d->tokens * std::max(d->top, 1); }
+
+VocabList list_of(const poetx_vocab_desc* d, const int64_t* ids, const void* teacher) {
+  VocabList l;
+  l.ids = ids;
+  l.teacher = teacher;
+  l.type = d->teacher == POETX_BF16 ? DType::BF16 : DType::F32;
+  l.top = std::max(d->top, 1);
+  l.vocab = d->vocab;
+  l.temperature = d->temperature;
+  return l;
+}
+// rows [row, ..) of a list
+VocabList list_at(VocabList l, int64_t row) {
+  l.ids += row * l.top;
+  if (l.teacher)
+    l.teacher = static_cast<const char*>(l.teacher) + row * l.top * (l.type == DType::BF16 ? 2 : 4);
+  return l;
+}
+float scale_of(const poetx_vocab_desc* d) { return 1.44269504088896341f / d->temperature; }
+
+// The forward's partial sums: `rows` rows at a time, so that they stay within
+// kPartBytes.
+struct FwdPlan {
+  TilePlan tile;
+  int64_t rows, slots;
+  size_t z, part, total;
+};
+FwdPlan plan_fwd(const poetx_vocab_desc* d) {
+  FwdPlan p = {};
+  const DType t = dtype_of(d);
+  p.rows = d->tokens;
+  for (;;) {
+    p.tile = plan_tile_product(t, p.rows, d->vocab, d->d, false, 1);
+    p.slots = p.tile.nsplit ? poetx::vocab_tile_slots(t, p.tile, d->vocab) : INT32_MAX;
+    if (p.slots * p.rows * 8 <= kPartBytes || p.rows <= kTile) break;
+    p.rows = (p.rows / 2 + kTile - 1) / kTile * kTile;
+  }
+  p.part = d->top ? 0 : align_up((size_t)d->tokens * 4);  // (the targets' logits)
+  p.total = p.part + align_up((size_t)(p.slots * p.rows * 8));
+  return p;
+}
+
+// The backward: `piece` columns of the vocabulary at a time.
+struct BwdPlan {
+  int64_t padded, piece, pieces, ldg;
+  size_t rows, xs, gz, acc, part, total;
+};
+size_t part_floats(const poetx_vocab_desc* d, const BwdPlan& p, int64_t n) {
+  const DType t = dtype_of(d);
+  return std::max(plan_tile_product(t, d->tokens, d->d, n, false).part_floats,
+                  plan_tile_product(t, n, d->d, p.padded, false).part_floats);
+}
+BwdPlan plan_bwd(const poetx_vocab_desc* d) {
+  BwdPlan p = {};
+  const int64_t es = (int64_t)act_size(d->act);
+  p.padded = ceil_div(d->tokens, 32) * 32;
+  const int64_t most = std::max(kTile, kPieceBytes / (p.padded * es) / kTile * kTile);
+  p.pieces = ceil_div(d->vocab, most);
+  p.piece = p.pieces == 1 ? d->vocab : ceil_div(ceil_div(d->vocab, p.pieces), kTile) * kTile;
+  p.pieces = ceil_div(d->vocab, p.piece);
+  p.ldg = ceil_div(p.piece, kTile) * kTile;
+  size_t off = 0;
+  p.rows = off;
+  off += align_up((size_t)d->tokens * sizeof(VocabRow));
+  p.xs = off;
+  off += align_up((size_t)(p.padded * d->d * es));
+  p.gz = off;
+  off += align_up((size_t)(p.padded * p.ldg * es));
+  p.acc = off;
+  if (p.pieces > 1) off += align_up((size_t)d->tokens * d->d * 4);
+  p.part = off;
+  const size_t last = part_floats(d, p, d->vocab - (p.pieces - 1) * p.piece);
+  off += align_up(std::max(part_floats(d, p, p.piece), last) * 4);
+  p.total = off;
+  return p;
+}
+
+bool any_overlap(const Range* outs, int nout, const Range* ins, int nin) {
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+    for (int j = i + 1; j < nout; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+Range opt_range(const void* p, size_t bytes) { return range_of(p, p ? bytes : 0); }
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+#define POETX_TRY(expr)                            \
+  do {                                             \
+    if ((expr) != hipSuccess) return POETX_ERR_HIP; \
+  } while (0)
+
+// Both forwards: z is the output of a distillation (its targets' logits go to
+// the workspace otherwise).
+int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64_t* ids,
+            const void* teacher, float* loss, float* lse, float* z, void* ws, size_t ws_bytes,
+            void* stream) {
+  if (!x || !W || !ids || !loss || !lse || (d->top && (!teacher || !z))) return POETX_ERR_NULL;
+  if (!aligned16(x) || !aligned16(W) || !aligned_to(ids, 8) || !aligned_to(loss, 4) ||
+      !aligned_to(lse, 4) || !aligned_to(z, 4) || !aligned_to(teacher, act_size(d->teacher)))
+    return POETX_ERR_ALIGN;
+  const FwdPlan plan = plan_fwd(d);
+  if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
+  if (!aligned16(ws)) return POETX_ERR_ALIGN;
+  const size_t rows4 = (size_t)d->tokens * 4, n = list_entries(d);
+  const Range outs[] = {range_of(loss, rows4), range_of(lse, rows4), opt_range(z, n * 4),
+                        range_of(ws, plan.total)};
+  const Range ins[] = {range_of(x, x_bytes(d)), range_of(W, w_bytes(d)), range_of(ids, n * 8),
+                       opt_range(teacher, n * act_size(d->teacher))};
+  if (any_overlap(outs, 4, ins, 4)) return POETX_ERR_ALIAS;
+
+  const DType t = dtype_of(d);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  const VocabList list = list_of(d, ids, teacher);
+  if (!z) z = reinterpret_cast<float*>(w + plan.z);
+  float2* part = reinterpret_cast<float2*>(w + plan.part);
+  POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
+  for (int64_t r = 0; r < d->tokens; r += plan.rows) {
+    const int64_t rows = std::min(plan.rows, d->tokens - r);
+    VocabProduct p;
+    p.x = static_cast<const char*>(x) + r * d->d * act_size(d->act);
+    p.W = W;
+    p.M = (int)rows; p.N = (int)d->vocab; p.K = (int)d->d;
+    p.scale = scale_of(d);
+    POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.tile, p, part, rows, s));
+    POETX_TRY(poetx::launch_vocab_loss(part, rows, plan.slots, list_at(list, r), rows,
+                                       z + r * list.top, loss + r, lse + r, s));
+  }
+  return POETX_OK;
+}
+
+int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse, const void* x,
+             const void* W, const int64_t* ids, const void* teacher, const float* lse,
+             const float* z, void* g_x, void* g_W, void* ws, size_t ws_bytes, void* stream) {
+  if (!g_loss || !x || !W || !ids || !lse || (!g_x && !g_W) || (d->top && (!teacher || !z)))
+    return POETX_ERR_NULL;
+  if (!aligned16(x) || !aligned16(W) || !aligned16(g_x) || !aligned16(g_W) || !aligned_to(ids, 8) ||
+      !aligned_to(g_loss, 4) || !aligned_to(g_lse, 4) || !aligned_to(lse, 4) || !aligned_to(z, 4) ||
+      !aligned_to(teacher, act_size(d->teacher)))
+    return POETX_ERR_ALIGN;
+  const BwdPlan plan = plan_bwd(d);
+  if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
+  if (!aligned16(ws)) return POETX_ERR_ALIGN;
+  const size_t rows4 = (size_t)d->tokens * 4, n = list_entries(d);
+  const Range outs[] = {opt_range(g_x, x_bytes(d)), opt_range(g_W, w_bytes(d)),
+                        range_of(ws, plan.total)};
+  const Range ins[] = {range_of(x, x_bytes(d)), range_of(W, w_bytes(d)), range_of(ids, n * 8),
+                       range_of(g_loss, rows4), opt_range(g_lse, rows4), range_of(lse, rows4),
+                       opt_range(z, n * 4), opt_range(teacher, n * act_size(d->teacher))};
+  if (any_overlap(outs, 3, ins, 8)) return POETX_ERR_ALIAS;
+
+  const DType t = dtype_of(d);
+  const int64_t es = (int64_t)act_size(d->act);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  const VocabList list = list_of(d, ids, teacher);
+  VocabRow* rows = reinterpret_cast<VocabRow*>(w + plan.rows);
+  void* xs = g_W ? w + plan.xs : nullptr;
+  char* gz = w + plan.gz;
+  float* acc = reinterpret_cast<float*>(w + plan.acc);
+  POETX_TRY(poetx::launch_vocab_rows(t, list, d->tokens, plan.padded, g_loss, g_lse, lse, rows, x,
+                                     (int)d->d, xs, s));
+  for (int64_t c = 0; c < d->vocab; c += plan.piece) {
+    const int64_t cols = std::min(plan.piece, d->vocab - c);
+    const char* Wc = static_cast<const char*>(W) + c * d->d * es;
+    VocabProduct p;
+    p.x = x;
+    p.W = Wc;
+    p.M = (int)d->tokens; p.N = (int)cols; p.K = (int)d->d;
+    p.scale = scale_of(d);
+    POETX_TRY(poetx::launch_vocab_grad_tile(
+        t, plan_tile_product(t, d->tokens, cols, d->d, false, 1), p, rows, gz, plan.ldg, (int)c, s));
+    if (teacher)
+      POETX_TRY(poetx::launch_vocab_listed_grad(t, list, d->tokens, rows, z, gz, plan.ldg, (int)c,
+                                                (int)cols, s));
+    TileProduct g;
+    g.A = gz; g.lda = plan.ldg;
+    g.ldb = d->d;
+    g.N = (int)d->d;
+    g.part = reinterpret_cast<float*>(w + plan.part);
+    g.ep.ld = d->d;
+    if (g_x) {  // g_x += g_z W: B(n, k) = W[k][n]
+      TileProduct q = g;
+      q.B = Wc;
+      q.M = (int)d->tokens; q.K = (int)cols;
+      q.ep.y = g_x;
+      q.ep.add = c > 0 ? acc : nullptr;
+      q.ep.sum = c + cols < d->vocab ? acc : nullptr;
+      POETX_TRY(poetx::launch_tile_product(t, plan_tile_product(t, q.M, q.N, q.K, false), q, true,
+                                           false, s));
+    }
+    if (g_W) {  // g_W = g_z^T x: A(m, k) = g_z[k][m], B(n, k) = xs[k][n]
+      TileProduct q = g;
+      q.B = xs;
+      q.M = (int)cols; q.K = (int)d->tokens;
+      q.ep.y = static_cast<char*>(g_W) + c * d->d * es;
+      POETX_TRY(poetx::launch_tile_product(t, plan_tile_product(t, q.M, q.N, q.K, false), q, false,
+                                           false, s));
+    }
+  }
+  return POETX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t poetx_vocab_fwd_workspace_size(const poetx_vocab_desc* d) {
+  return check_desc(d) == POETX_OK ? plan_fwd(d).total : 0;
+}
+
+size_t poetx_vocab_bwd_workspace_size(const poetx_vocab_desc* d) {
+  return check_desc(d) == POETX_OK ? plan_bwd(d).total : 0;
+}
+
+int poetx_cross_entropy_fwd(const poetx_vocab_desc* d, const void* x, const void* W,
+                            const int64_t* targets, float* loss, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  const int st = check_desc(d);
+  if (st != POETX_OK) return st;
+  if (d->top != 0) return POETX_ERR_SHAPE;
+  return forward(d, x, W, targets, nullptr, loss, lse, nullptr, ws, ws_bytes, stream);
+}
+
+int poetx_cross_entropy_bwd(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
+                            const void* x, const void* W, const int64_t* targets, const float* lse,
+                            void* g_x, void* g_W, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_desc(d);
+  if (st != POETX_OK) return st;
+  if (d->top != 0) return POETX_ERR_SHAPE;
+  return backward(d, g_loss, g_lse, x, W, targets, nullptr, lse, nullptr, g_x, g_W, ws, ws_bytes,
+                  stream);
+}
+
+int poetx_distill_fwd(const poetx_vocab_desc* d, const void* x, const void* W, const int64_t* ids,
+                      const void* teacher, float* loss, float* lse, float* z, void* ws,
+                      size_t ws_bytes, void* stream) {
+  const int st = check_desc(d);
+  if (st != POETX_OK) return st;
+  if (d->top == 0) return POETX_ERR_SHAPE;
+  return forward(d, x, W, ids, teacher, loss, lse, z, ws, ws_bytes, stream);
+}
+
+int poetx_distill_bwd(const poetx_vocab_desc* d, const float* g_loss, const void* x, const void* W,
+                      const int64_t* ids, const void* teacher, const float* lse, const float* z,
+                      void* g_x, void* g_W, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_desc(d);
+  if (st != POETX_OK) return st;
+  if (d->top == 0) return POETX_ERR_SHAPE;
+  return backward(d, g_loss, nullptr, x, W, ids, teacher, lse, z, g_x, g_W, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

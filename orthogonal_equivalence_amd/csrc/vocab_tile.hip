@@ -1,0 +1,135 @@
+// The logits of a piece of the vocabulary on the tile products' main loop
+// (tile_core.h), for any number of rows and columns; the logits stay in
+// registers. Two ends:
+//
+//   forward   per row the maximum and the sum of exponentials over the wave's
+//             columns: with c = log2(e) / temperature, m = max c z_j and
+//             s = sum 2^(c z_j - m). 32 lanes' worth of columns of one row lie in four
+//             lanes (16 apart), so a row costs its exponentials and four
+//             exchanges. (m, s) goes to part[slot][row]: nothing is read again
+//             but 8 bytes for every 16 to 64 columns.
+//   backward  g_z = a 2^(c z - lse2), less b at the row's target: rounded once to
+//             x's type, the operand of the two products that follow.
+#include "tile_core.h"
+#include "vocab.h"
+
+namespace poetx {
+namespace {
+
+struct LseEnd {
+  float2* part;
+  int64_t part_ld;
+  float scale;
+  template <typename T, int FM, int FN>
+  __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
+                                      int n_at, int, int wave_col, int lane) const {
+    float2* out = part + (int64_t)wave_col * part_ld;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      float v[4 * FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[4 * j + e] = n_at + 16 * j + 4 * (lane >> 4) + e < p.N ? acc[i][j][e] : -INFINITY;
+      const float2 ms = row_max_sum<4 * FN>(v, scale);
+      const int m = m_at + 16 * i + (lane & 15);
+      if (lane < 16 && m < p.M) out[m] = ms;
+    }
+  }
+};
+
+struct GradEnd {
+  const VocabRow* rows;
+  void* gz;
+  int64_t ldg;
+  int col0;
+  float scale;
+  template <typename T, int FM, int FN>
+  __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
+                                      int n_at, int, int, int lane) const {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = m_at + 16 * i + (lane & 15);
+      if (m >= p.M) continue;
+      const VocabRow r = rows[m];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int n = n_at + 16 * j + 4 * (lane >> 4);
+        if (n >= (p.N + 7) / 8 * 8) continue;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = n + e < p.N ? logit_gradient(r, acc[i][j][e], scale, col0 + n + e) : 0.0f;
+        Quad<T>::store(static_cast<T*>(gz) + (int64_t)m * ldg + n, v);
+      }
+    }
+  }
+};
+
+template <typename T, int BM, int BN, int WM, int WN, int NS, typename End>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+vocab_tile_kernel(const TileProduct p, const End end) {
+  __shared__ __attribute__((aligned(1024))) char ring[ring_bytes<T, T, BM, BN, WM * WN, NS>()];
+  tile_body<T, T, BM, BN, WM, WN, true, true, NS>(p, blockIdx.x, 0, ring, end);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int NS, typename End>
+hipError_t launch_cfg(const TileProduct& p, const End& end, hipStream_t s) {
+  const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+  if (tiles * 64 * WM * WN > kMaxWorkItems) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((vocab_tile_kernel<T, BM, BN, WM, WN, NS, End>), dim3((unsigned)tiles),
+                     dim3(64 * WM * WN), 0, s, p, end);
+  return hipGetLastError();
+}
+
+// the shapes of dense_plan.cpp, with their rings as in tilegemm.hip
+template <typename End>
+hipError_t launch_end(DType t, const TilePlan& plan, const VocabProduct& v, const End& end,
+                      hipStream_t s) {
+  if (plan.nsplit != 1) return hipErrorInvalidValue;
+  TileProduct p;
+  p.A = v.x; p.lda = v.K;
+  p.B = v.W; p.ldb = v.K;
+  p.M = v.M; p.N = v.N; p.K = v.K;
+  p.kchunk = plan.kchunk;
+  if (t == DType::F32) {
+    switch (plan.shape) {
+      case 0: return launch_cfg<float, 64, 64, 2, 2, 4>(p, end, s);
+      case 1: return launch_cfg<float, 32, 64, 1, 4, 4>(p, end, s);
+    }
+  } else {
+    switch (plan.shape) {
+      case 0: return launch_cfg<bf16_t, 256, 128, 4, 2, 3>(p, end, s);
+      case 1: return launch_cfg<bf16_t, 128, 128, 2, 4, 4>(p, end, s);
+      case 2: return launch_cfg<bf16_t, 128, 64, 4, 2, 4>(p, end, s);
+      case 3: return launch_cfg<bf16_t, 64, 64, 2, 2, 4>(p, end, s);
+      case 4: return launch_cfg<bf16_t, 32, 64, 1, 4, 6>(p, end, s);
+      case 5: return launch_cfg<bf16_t, 128, 64, 4, 2, 3>(p, end, s);
+    }
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N) {
+  // wave columns of a tile and its width, by shape (launch_end)
+  static constexpr int kBf16[][2] = {{2, 128}, {4, 128}, {2, 64}, {2, 64}, {4, 64}, {2, 64}};
+  static constexpr int kF32[][2] = {{2, 64}, {4, 64}};
+  const int* h = t == DType::F32 ? kF32[plan.shape] : kBf16[plan.shape];
+  return (N + h[1] - 1) / h[1] * h[0];
+}
+
+hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
+                                 int64_t part_ld, hipStream_t s) {
+  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale}, s);
+}
+
+hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
+                                  const VocabRow* rows, void* gz, int64_t ldg, int col0,
+                                  hipStream_t s) {
+  return launch_end(t, plan, p, GradEnd{rows, gz, ldg, col0, p.scale}, s);
+}
+
+}  // namespace poetx

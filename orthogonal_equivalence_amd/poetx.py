@@ -47,7 +47,9 @@ EXPORTS = (
     "poetx_build_cnp", "poetx_fold_weight", "poetx_quantize_weight", "poetx_fwd_workspace_size",
     "poetx_bwd_workspace_size", "poetx_linear_fwd", "poetx_linear_fwd_noalloc", "poetx_linear_bwd",
     "poetx_dense_fwd_workspace_size", "poetx_dense_bwd_workspace_size", "poetx_dense_fwd",
-    "poetx_dense_bwd", "poetx_grad_workspace_size", "poetx_grad_norm", "poetx_grad_clip",
+    "poetx_dense_bwd", "poetx_vocab_fwd_workspace_size", "poetx_vocab_bwd_workspace_size",
+    "poetx_cross_entropy_fwd", "poetx_cross_entropy_bwd", "poetx_distill_fwd", "poetx_distill_bwd",
+    "poetx_grad_workspace_size", "poetx_grad_norm", "poetx_grad_clip",
     "poetx_grad_scale",
     "poetx_event_create", "poetx_event_destroy", "poetx_event_record",
     "poetx_event_synchronize", "poetx_event_elapsed_ms",
@@ -91,6 +93,20 @@ class DenseDesc(ctypes.Structure):
     ]
 
 
+class VocabDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("act", ctypes.c_int32),
+        ("top", ctypes.c_int32),
+        ("teacher", ctypes.c_int32),
+        ("temperature", ctypes.c_float),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class GradTensor(ctypes.Structure):
     _fields_ = [
         ("grad", ctypes.c_void_p),
@@ -109,7 +125,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     dp = ctypes.POINTER(LinearDesc)
-    dd, f32 = ctypes.POINTER(DenseDesc), ctypes.c_float
+    dd, dv, f32 = ctypes.POINTER(DenseDesc), ctypes.POINTER(VocabDesc), ctypes.c_float
     sig = {
         "poetx_abi_version": (ctypes.c_int, []),
         "poetx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -130,6 +146,12 @@ def _load() -> ctypes.CDLL:
         "poetx_dense_bwd_workspace_size": (sz, [dd]),
         "poetx_dense_fwd": (ctypes.c_int, [dd, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "poetx_dense_bwd": (ctypes.c_int, [dd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "poetx_vocab_fwd_workspace_size": (sz, [dv]),
+        "poetx_vocab_bwd_workspace_size": (sz, [dv]),
+        "poetx_cross_entropy_fwd": (ctypes.c_int, [dv, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "poetx_cross_entropy_bwd": (ctypes.c_int, [dv, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "poetx_distill_fwd": (ctypes.c_int, [dv, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "poetx_distill_bwd": (ctypes.c_int, [dv, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         # (the list of tensors: the address of GradTensor records)
         "poetx_grad_workspace_size": (sz, [i32]),
         "poetx_grad_norm": (ctypes.c_int, [vp, i32, vp, vp, sz, vp]),
@@ -319,6 +341,54 @@ def poetx_dense_bwd(desc, g_y, x, W, u_saved, g_x, g_W, g_bias, ws, stream=None,
     if raw:
         return st
     _check(st, "poetx_dense_bwd")
+
+
+def make_vocab_desc(tokens, d, vocab, act, top=0, teacher=0, temperature=1.0) -> VocabDesc:
+    return VocabDesc(tokens, d, vocab, act, top, teacher, temperature, 0, 0)
+
+
+def poetx_vocab_fwd_workspace_size(desc: VocabDesc) -> int:
+    return _lib.poetx_vocab_fwd_workspace_size(desc)
+
+
+def poetx_vocab_bwd_workspace_size(desc: VocabDesc) -> int:
+    return _lib.poetx_vocab_bwd_workspace_size(desc)
+
+
+def poetx_cross_entropy_fwd(desc, x, W, targets, loss, lse, ws, stream=None, raw=False):
+    st = _lib.poetx_cross_entropy_fwd(desc, _ptr(x), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse),
+                                      _ptr(ws), _nbytes(ws), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_cross_entropy_fwd")
+
+
+def poetx_cross_entropy_bwd(desc, g_loss, g_lse, x, W, targets, lse, g_x, g_W, ws, stream=None,
+                            raw=False):
+    st = _lib.poetx_cross_entropy_bwd(desc, _ptr(g_loss), _ptr(g_lse), _ptr(x), _ptr(W),
+                                      _ptr(targets), _ptr(lse), _ptr(g_x), _ptr(g_W), _ptr(ws),
+                                      _nbytes(ws), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_cross_entropy_bwd")
+
+
+def poetx_distill_fwd(desc, x, W, ids, teacher, loss, lse, z, ws, stream=None, raw=False):
+    st = _lib.poetx_distill_fwd(desc, _ptr(x), _ptr(W), _ptr(ids), _ptr(teacher), _ptr(loss),
+                                _ptr(lse), _ptr(z), _ptr(ws), _nbytes(ws), _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_distill_fwd")
+
+
+def poetx_distill_bwd(desc, g_loss, x, W, ids, teacher, lse, z, g_x, g_W, ws, stream=None,
+                      raw=False):
+    st = _lib.poetx_distill_bwd(desc, _ptr(g_loss), _ptr(x), _ptr(W), _ptr(ids), _ptr(teacher),
+                                _ptr(lse), _ptr(z), _ptr(g_x), _ptr(g_W), _ptr(ws), _nbytes(ws),
+                                _stream(stream))
+    if raw:
+        return st
+    _check(st, "poetx_distill_bwd")
 
 
 _GRAD_DTYPE = {torch.float32: POETX_F32, torch.bfloat16: POETX_BF16}
