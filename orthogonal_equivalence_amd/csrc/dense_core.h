@@ -59,8 +59,18 @@ __device__ __forceinline__ const bf16_t* uniform_ptr(const bf16_t* p) {
 // copies of an even tile and of the odd one behind it are issued together,
 // piece by piece, during every second tile; a line's second half then finds it
 // in the L1.
-template <bool B_KMAJ, bool PAIR = false>
+//
+// MN_TILED (A_KMAJ and B_KMAJ false: C(m, n) = sum_k A[k][m] B[k][n]): both
+// operands are M- or N-major out of the tiled layout (kernels.h), whose rows are k:
+// a K tile is 32 rows of eight blocks, 64 bytes of a row in each, and the next
+// tile lies 32 rows further on in the blocks, the ninth in the next panel.
+// LAST_B: the B rows of K tile last_t come from last_b instead (an N-major B
+// whose rows end inside that tile, of which last_b is a padded copy).
+template <bool B_KMAJ, bool PAIR = false, bool A_KMAJ = true, bool MN_TILED = false,
+          bool LAST_B = false>
 struct Dense {
+  const bf16_t* last_b;
+  int last_t;
   const bf16_t* baseA;  // wave-uniform bases of the current tile's A and B panels
   const bf16_t* baseB;
   int64_t stepA, stepB; // elements between consecutive K tiles of A and of B
@@ -85,7 +95,8 @@ struct Dense {
     stepA = tiled ? (int64_t)BM * BK : BK;
     stepB = B_KMAJ ? (b_tiled ? (int64_t)BN * BK : BK) : (int64_t)BK * ldb;
     const int r = lane & 15;
-    rdA = (wm * 128 + r) * BK + (((lane >> 4) ^ kmaj_swz(r)) << 3);
+    if constexpr (A_KMAJ) rdA = (wm * 128 + r) * BK + (((lane >> 4) ^ kmaj_swz(r)) << 3);
+    else rdA = nmaj_off(8 * (lane >> 4) + (r >> 2), wm * 128 + 4 * (r & 3));
     if (B_KMAJ) {
       rdB = (wn * 128 + r) * BK + (((lane >> 4) ^ kmaj_swz(r)) << 3);
     } else {
@@ -100,6 +111,16 @@ struct Dense {
     // all of its pieces
     const int row = 16 * wave + (lane >> 2);
     const int c = (lane & 3) ^ kmaj_swz(row);
+    if constexpr (MN_TILED) {
+      static_assert(!A_KMAJ && !B_KMAJ, "both operands are read alike");
+      const int k = 2 * wave + (lane >> 5);
+      const int cn = (lane & 31) ^ nmaj_swz(k);
+      offA = offB = (uint32_t)((cn >> 2) * TILE + k * BK + 8 * (cn & 3)) * 2u;
+      strA = strB = 2 * NW * BK * 2;
+      stepA = 256 * lda;  // (between panels)
+      stepB = 256 * ldb;
+      return;
+    }
     // (tiled: the rows of a K tile are 32 elements apart within its block)
     const int64_t rsa = tiled ? BK : lda;
     offA = (uint32_t)(row * rsa + 8 * c) * 2u;
@@ -121,6 +142,11 @@ struct Dense {
                                            int64_t ldb, int m0, int n0) {
     // (tiled: the panel's blocks start at row m0 of the row-major count,
     // since a panel of 256 rows holds 256 lda elements)
+    if constexpr (MN_TILED) {  // (m0, n0 multiples of 32)
+      baseA = uniform_ptr(A + (int64_t)m0 * 256);
+      baseB = uniform_ptr(B + (int64_t)n0 * 256);
+      return;
+    }
     baseA = uniform_ptr(A + (int64_t)m0 * lda);
     baseB = uniform_ptr(B_KMAJ ? B + (int64_t)n0 * ldb : B + n0);
   }
@@ -129,8 +155,18 @@ struct Dense {
   template <int S, int OP, int J>
   __device__ __forceinline__ void dma(int t) {
     const uint32_t m = lds0 + (uint32_t)(S * SLOT * 2 + OP * TILE * 2 + (wave + NW * J) * 1024);
+    if constexpr (MN_TILED) {
+      const int64_t at = (int64_t)(t & 7) * (32 * BK);
+      if (OP == 0)
+        dma16_sb(uniform_ptr(baseA + (t >> 3) * stepA + at), offA + J * strA, m);
+      else
+        dma16_sb(uniform_ptr(baseB + (t >> 3) * stepB + at), offB + J * strB, m);
+      return;
+    }
     if (OP == 0)
       dma16_sb(uniform_ptr(baseA + (int64_t)t * stepA), offA + J * strA, m);
+    else if (LAST_B)
+      dma16_sb(uniform_ptr(t == last_t ? last_b : baseB + (int64_t)t * stepB), offB + J * strB, m);
     else
       dma16_sb(uniform_ptr(baseB + (int64_t)t * stepB), offB + J * strB, m);
   }
@@ -153,7 +189,16 @@ struct Dense {
   // k = 8 (l / 16) .. +7) from ring slot S into set P
   template <int S, int P, int I>
   __device__ __forceinline__ void read_a() {
-    fa[P][I] = *reinterpret_cast<const bf16x8_t*>(g_dense_lds + S * SLOT + rdA + 512 * I);
+    if constexpr (A_KMAJ) {
+      fa[P][I] = *reinterpret_cast<const bf16x8_t*>(g_dense_lds + S * SLOT + rdA + 512 * I);
+    } else {
+      const bf16_t* sa = g_dense_lds + S * SLOT;
+      const int o = rdA ^ (16 * I);
+      union { short4_t h[2]; bf16x8_t v; } u;
+      u.h[0] = ds_read_tr4(sa + o);
+      u.h[1] = ds_read_tr4(sa + o + 4 * BM);
+      fa[P][I] = u.v;
+    }
   }
   // B fragment J (16 of this wave's columns) likewise
   template <int S, int P, int J>
@@ -286,6 +331,22 @@ struct Dense {
     // results in the epilogue (more than any 16x16x32 product needs)
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // The wait states again, tied to the accumulators: without the tie the
+  // compiler, to which the products are no matrix instructions, may copy an
+  // accumulator right behind the last product, ahead of mainloop()'s waits (it
+  // did, at the join of the last tiles' branches, where the code that follows
+  // takes VGPRs).
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      asm volatile("s_nop 7"
+                   : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]),
+                     "+a"(acc[i][4]), "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7])
+                   :
+                   : "memory");
     __builtin_amdgcn_sched_barrier(0);
   }
 

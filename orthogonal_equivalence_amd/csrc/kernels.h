@@ -357,6 +357,35 @@ hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProd
                                   const VocabRow* rows, void* gz, int64_t ldg, int col0,
                                   hipStream_t s);
 
+// Large bf16 pieces on the dense kernel's 256 x 256 tile loop (vocab_dense.hip).
+// A piece that is not whole tiles of the vocabulary (the last one) comes with
+// W_last, a zero-padded copy [256][K] of W's rows from the last whole tile on.
+inline bool vocab_dense_supported(int64_t M, int64_t N, int64_t K) {
+  return M >= 256 && N >= 1 && K >= 256 && K % 32 == 0 && K <= (1 << 22) && M <= INT32_MAX - 256 &&
+         N <= INT32_MAX - 256;
+}
+// 2 ceil(N / 256) slots
+hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
+                                  int64_t part_ld, hipStream_t s);
+// x: the tiled copy of it, M % 256 == 0 rows, as many of `rows`; gz in the tiled
+// layout [M][ldg], ldg % 256 == 0; columns past N of the last tile are zeroed.
+hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, const VocabRow* rows,
+                                   void* gz, int64_t ldg, int col0, hipStream_t s);
+// g_z W of a piece of `cols` columns of a tiled gz (padded to 256 rows): split
+// over `splits` ranges of kchunk of them into slabs [splits][rows][d] float32, added
+// to what they hold with `add`; or with y (one range) g_x itself, bf16.
+hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, const void* W_last,
+                                 int64_t rows, int d, int cols, int splits, int kchunk,
+                                 float* slabs, bool add, void* y, hipStream_t s);
+// g_z^T x from tiled gz and xs, `padded` rows (a multiple of 32) of both: bf16 [cols][d].
+hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
+                                 int cols, void* g_W, hipStream_t s);
+// W_last of W [vocab][K]
+hipError_t launch_vocab_last_rows(const void* W, int64_t vocab, int K, void* W_last, hipStream_t s);
+// out [rows][N] = the sum of nsplit float32 slabs of it, N % 4 == 0.
+hipError_t launch_sum_slabs(DType t, const float* slabs, int nsplit, int64_t rows, int N, void* out,
+                            hipStream_t s);
+
 // The listed ids of a row: targets (top = 1) or a teacher's [rows][top].
 struct VocabList {
   const int64_t* ids = nullptr;
@@ -374,16 +403,18 @@ hipError_t launch_listed_logits(DType t, const void* x, const void* W, const Voc
 // the teacher's distribution.
 hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots, const VocabList& l,
                              int64_t rows, const float* z, float* loss, float* lse, hipStream_t s);
-// The rows' parts, and with xs a copy of x [padded][K] in which rows that take
-// no part, and those past `rows`, are zero.
+// The rows' parts (none for those past `rows`), and with xs a copy of x
+// [padded][K], with `tiled` in the tiled layout, in which rows that take no
+// part, and those past `rows`, are zero.
 hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t padded,
                              const float* g_loss, const float* g_lse, const float* lse,
-                             VocabRow* out, const void* x, int K, void* xs, hipStream_t s);
+                             VocabRow* out, const void* x, int K, void* xs, bool tiled,
+                             hipStream_t s);
 // A teacher's ids in the piece [col0, col0 + N): g_z there, from the student's
 // logits z at them.
 hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
-                                    const float* z, void* gz, int64_t ldg, int col0, int N,
-                                    hipStream_t s);
+                                    const float* z, void* gz, int64_t ldg, bool tiled, int col0,
+                                    int N, hipStream_t s);
 
 // ---- gradient norm and clipping over many tensors ----
 // One contiguous run of gradient values; out may equal grad.

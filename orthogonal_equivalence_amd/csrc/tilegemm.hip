@@ -153,17 +153,20 @@ hipError_t launch_pair_cfg(const TileProduct& gx, int gx_split, const TileProduc
 }
 
 // joins a split product's partial tiles
-hipError_t finish(DType t, const TilePlan& plan, const TileProduct& p, hipStream_t s) {
-  if (plan.nsplit == 1) return hipSuccess;
+hipError_t join(DType t, int nsplit, const TileProduct& p, hipStream_t s) {
   const int64_t groups = (int64_t)p.M * (p.N / 4);
   const int grid = (int)std::min<int64_t>((groups + NT - 1) / NT, 4096);
   if (t == DType::BF16)
-    hipLaunchKernelGGL(finish_kernel<bf16_t>, dim3(grid), dim3(NT), 0, s, p.part, plan.nsplit,
+    hipLaunchKernelGGL(finish_kernel<bf16_t>, dim3(grid), dim3(NT), 0, s, p.part, nsplit,
                        (int64_t)p.M, p.N, p.ep);
   else
-    hipLaunchKernelGGL(finish_kernel<float>, dim3(grid), dim3(NT), 0, s, p.part, plan.nsplit,
+    hipLaunchKernelGGL(finish_kernel<float>, dim3(grid), dim3(NT), 0, s, p.part, nsplit,
                        (int64_t)p.M, p.N, p.ep);
   return hipGetLastError();
+}
+
+hipError_t finish(DType t, const TilePlan& plan, const TileProduct& p, hipStream_t s) {
+  return plan.nsplit == 1 ? hipSuccess : join(t, plan.nsplit, p, s);
 }
 
 // p as `plan` has it; false: a split without room for its partial tiles
@@ -174,6 +177,16 @@ bool apply_plan(const TilePlan& plan, TileProduct& p) {
 }
 
 }  // namespace
+
+hipError_t launch_sum_slabs(DType t, const float* slabs, int nsplit, int64_t rows, int N, void* out,
+                            hipStream_t s) {
+  TileProduct p;
+  p.M = (int)rows; p.N = N;
+  p.part = const_cast<float*>(slabs);
+  p.ep.y = out;
+  p.ep.ld = N;
+  return join(t, nsplit, p, s);
+}
 
 hipError_t launch_tile_pair(DType t, const TilePairPlan& plan, TileProduct gx, TileProduct gw,
                             hipStream_t s) {

@@ -224,13 +224,15 @@ template <typename T>
 __global__ void __launch_bounds__(NT)
 rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __restrict__ g_loss,
             const float* __restrict__ g_lse, const float* __restrict__ lse,
-            VocabRow* __restrict__ out, const T* __restrict__ x, int K, T* __restrict__ xs) {
+            VocabRow* __restrict__ out, const T* __restrict__ x, int K, T* __restrict__ xs,
+            int tiled) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
   if (row >= padded) return;
   bool any = false;
+  VocabRow r{0.0f, 0.0f, 0.0f, -1};
   if (row < rows) {
-    VocabRow r{0.0f, lse[row] * kLog2e, 0.0f, -1};
+    r.lse2 = lse[row] * kLog2e;
     bool bad = false;
     if (l.teacher) {
       for (int k = lane; k < l.top; k += 64) {
@@ -251,12 +253,12 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
       r.target = any && !bad ? (int)id : -1;
     }
     if (bad) r.a = NAN;
-    if (lane == 0) out[row] = r;
   }
+  if (lane == 0) out[row] = r;
   if (!xs) return;
   const uint4 none = make_uint4(0, 0, 0, 0);
   for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
-    *reinterpret_cast<uint4*>(xs + row * K + k) =
+    *reinterpret_cast<uint4*>(xs + (tiled ? tiled_offset(row, k, K) : row * K + k)) =
         any ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
 }
 
@@ -268,7 +270,8 @@ constexpr int kMaxTop = 1024;
 template <typename T>
 __global__ void __launch_bounds__(NT)
 listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__ r,
-                   const float* __restrict__ z, T* __restrict__ gz, int64_t ldg, int col0, int N) {
+                   const float* __restrict__ z, T* __restrict__ gz, int64_t ldg, int tiled,
+                   int col0, int N) {
   __shared__ int ids[NWAVES][kMaxTop];
   __shared__ float p[NWAVES][kMaxTop];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -295,8 +298,17 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
     float sum = 0.0f;
     for (int q = 0; q < l.top; ++q) sum += ids[wave][q] == id ? p[wave][q] : 0.0f;
     const float e = __builtin_amdgcn_exp2f(fmaf(z[row * l.top + k], rt, -own.lse2));
-    store_as(gz + row * ldg + (id - col0), own.a * (e - sum));
+    const int64_t at = tiled ? tiled_offset(row, id - col0, ldg) : row * ldg + (id - col0);
+    store_as(gz + at, own.a * (e - sum));
   }
+}
+
+__global__ void __launch_bounds__(NT)
+last_rows_kernel(const bf16_t* __restrict__ W, int64_t vocab, int K, bf16_t* __restrict__ out) {
+  const int64_t row = vocab / kTileRows * kTileRows + blockIdx.x;
+  for (int k = threadIdx.x * 8; k < K; k += NT * 8)
+    *reinterpret_cast<uint4*>(out + (int64_t)blockIdx.x * K + k) =
+        row < vocab ? *reinterpret_cast<const uint4*>(W + row * K + k) : make_uint4(0, 0, 0, 0);
 }
 
 bool fits(int64_t blocks) { return blocks * NT <= kMaxWorkItems; }
@@ -337,31 +349,38 @@ hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots,
 
 hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t padded,
                              const float* g_loss, const float* g_lse, const float* lse,
-                             VocabRow* out, const void* x, int K, void* xs, hipStream_t s) {
-  const int64_t n = xs ? padded : rows, blocks = (n + NWAVES - 1) / NWAVES;
+                             VocabRow* out, const void* x, int K, void* xs, bool tiled,
+                             hipStream_t s) {
+  const int64_t blocks = (padded + NWAVES - 1) / NWAVES;
   if (!fits(blocks)) return hipErrorInvalidValue;
   if (t == DType::BF16)
-    hipLaunchKernelGGL(rows_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, n,
+    hipLaunchKernelGGL(rows_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, padded,
                        g_loss, g_lse, lse, out, static_cast<const bf16_t*>(x), K,
-                       static_cast<bf16_t*>(xs));
+                       static_cast<bf16_t*>(xs), (int)tiled);
   else
-    hipLaunchKernelGGL(rows_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, n,
+    hipLaunchKernelGGL(rows_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, padded,
                        g_loss, g_lse, lse, out, static_cast<const float*>(x), K,
-                       static_cast<float*>(xs));
+                       static_cast<float*>(xs), (int)tiled);
   return hipGetLastError();
 }
 
 hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
-                                    const float* z, void* gz, int64_t ldg, int col0, int N,
-                                    hipStream_t s) {
+                                    const float* z, void* gz, int64_t ldg, bool tiled, int col0,
+                                    int N, hipStream_t s) {
   const int64_t blocks = (rows + NWAVES - 1) / NWAVES;
   if (!fits(blocks) || l.top > kMaxTop) return hipErrorInvalidValue;
   if (t == DType::BF16)
     hipLaunchKernelGGL(listed_grad_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
-                       r, z, static_cast<bf16_t*>(gz), ldg, col0, N);
+                       r, z, static_cast<bf16_t*>(gz), ldg, (int)tiled, col0, N);
   else
     hipLaunchKernelGGL(listed_grad_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
-                       r, z, static_cast<float*>(gz), ldg, col0, N);
+                       r, z, static_cast<float*>(gz), ldg, (int)tiled, col0, N);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_last_rows(const void* W, int64_t vocab, int K, void* W_last, hipStream_t s) {
+  hipLaunchKernelGGL(last_rows_kernel, dim3(kTileRows), dim3(NT), 0, s,
+                     static_cast<const bf16_t*>(W), vocab, K, static_cast<bf16_t*>(W_last));
   return hipGetLastError();
 }
 

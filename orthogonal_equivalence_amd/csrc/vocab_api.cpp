@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "api_util.h"
+#include "dense_plan.h"
 #include "kernels.h"
 #include "poetx.h"
 
@@ -77,12 +78,18 @@ VocabList list_at(VocabList l, int64_t row) {
 }
 float scale_of(const poetx_vocab_desc* d) { return 1.44269504088896341f / d->temperature; }
 
+bool last_rows(const poetx_vocab_desc* d) { return d->vocab % kTile != 0; }
+size_t last_bytes(const poetx_vocab_desc* d) {
+  return last_rows(d) ? align_up((size_t)kTile * d->d * act_size(d->act)) : 0;
+}
+
 // The forward's partial sums: `rows` rows at a time, so that they stay within
 // kPartBytes.
 struct FwdPlan {
+  bool dense;  // the 256 x 256 tiles, else `tile`
   TilePlan tile;
   int64_t rows, slots;
-  size_t z, part, total;
+  size_t z, last, part, total;
 };
 FwdPlan plan_fwd(const poetx_vocab_desc* d) {
   FwdPlan p = {};
@@ -90,46 +97,98 @@ FwdPlan plan_fwd(const poetx_vocab_desc* d) {
   p.rows = d->tokens;
   for (;;) {
     p.tile = plan_tile_product(t, p.rows, d->vocab, d->d, false, 1);
-    p.slots = p.tile.nsplit ? poetx::vocab_tile_slots(t, p.tile, d->vocab) : INT32_MAX;
+    const int64_t tiles = ceil_div(p.rows, kTile) * ceil_div(d->vocab, kTile);
+    p.dense = t == DType::BF16 && poetx::vocab_dense_supported(p.rows, d->vocab, d->d) &&
+              poetx::dense_rounds_cost(tiles, d->d) < p.tile.cost;
+    p.slots = p.dense         ? 2 * ceil_div(d->vocab, kTile)
+              : p.tile.nsplit ? poetx::vocab_tile_slots(t, p.tile, d->vocab)
+                              : INT32_MAX;
     if (p.slots * p.rows * 8 <= kPartBytes || p.rows <= kTile) break;
     p.rows = (p.rows / 2 + kTile - 1) / kTile * kTile;
   }
-  p.part = d->top ? 0 : align_up((size_t)d->tokens * 4);  // (the targets' logits)
+  p.last = d->top ? 0 : align_up((size_t)d->tokens * 4);  // (the targets' logits)
+  p.part = p.last + (p.dense ? last_bytes(d) : 0);
   p.total = p.part + align_up((size_t)(p.slots * p.rows * 8));
   return p;
 }
 
 // The backward: `piece` columns of the vocabulary at a time.
 struct BwdPlan {
-  int64_t padded, piece, pieces, ldg;
-  size_t rows, xs, gz, acc, part, total;
+  bool dense;
+  int64_t padded;       // rows of xs and gz
+  int64_t piece, pieces, ldg;
+  int splits, kchunk;   // dense: of g_x's reduction over a piece
+  size_t rows, last, xs, gz, acc, part, total;
+  bool summed() const { return pieces > 1 || splits > 1; }
 };
-size_t part_floats(const poetx_vocab_desc* d, const BwdPlan& p, int64_t n) {
+size_t part_floats(const poetx_vocab_desc* d, int64_t n) {
   const DType t = dtype_of(d);
   return std::max(plan_tile_product(t, d->tokens, d->d, n, false).part_floats,
-                  plan_tile_product(t, n, d->d, p.padded, false).part_floats);
+                  plan_tile_product(t, n, d->d, d->tokens, false).part_floats);
 }
-BwdPlan plan_bwd(const poetx_vocab_desc* d) {
-  BwdPlan p = {};
+void set_pieces(const poetx_vocab_desc* d, BwdPlan& p) {
   const int64_t es = (int64_t)act_size(d->act);
-  p.padded = ceil_div(d->tokens, 32) * 32;
   const int64_t most = std::max(kTile, kPieceBytes / (p.padded * es) / kTile * kTile);
   p.pieces = ceil_div(d->vocab, most);
   p.piece = p.pieces == 1 ? d->vocab : ceil_div(ceil_div(d->vocab, p.pieces), kTile) * kTile;
   p.pieces = ceil_div(d->vocab, p.piece);
   p.ldg = ceil_div(p.piece, kTile) * kTile;
+}
+// g_x's tiles are few where tokens and d are: its reduction, the vocabulary, is
+// split so that they fill the CUs
+float split_gx(const poetx_vocab_desc* d, BwdPlan& p) {
+  const int64_t tiles = p.padded / kTile * ceil_div(d->d, kTile);
+  float best = 1e30f;
+  for (int s = 1; s <= 16; ++s) {
+    const int64_t chunk = ceil_div(ceil_div(p.piece, s), kTile) * kTile;
+    const int64_t n = ceil_div(p.piece, chunk);
+    // (a slab is written and read once more)
+    const float cost = poetx::dense_rounds_cost(tiles * n, chunk) +
+                       (n > 1 ? 3.0f + (float)(8 * n * d->tokens * d->d) / 5e6f : 0.0f);
+    if (cost >= best) continue;
+    best = cost;
+    p.splits = (int)n;
+    p.kchunk = (int)chunk;
+  }
+  return best;
+}
+BwdPlan plan_bwd(const poetx_vocab_desc* d) {
+  BwdPlan p = {};
+  const DType t = dtype_of(d);
+  const int64_t es = (int64_t)act_size(d->act);
+  p.splits = 1;
+  if (t == DType::BF16 && poetx::vocab_dense_supported(d->tokens, d->vocab, d->d)) {
+    p.padded = ceil_div(d->tokens, kTile) * kTile;
+    set_pieces(d, p);
+    const int64_t rt = p.padded / kTile, vt = ceil_div(p.piece, kTile), dt = ceil_div(d->d, kTile);
+    const float dense = poetx::dense_rounds_cost(rt * vt, d->d) + split_gx(d, p) +
+                        poetx::dense_rounds_cost(vt * dt, d->tokens);
+    const float tile = plan_tile_product(t, d->tokens, p.piece, d->d, false, 1).cost +
+                       plan_tile_product(t, d->tokens, d->d, p.piece, false).cost +
+                       plan_tile_product(t, p.piece, d->d, d->tokens, false).cost;
+    p.dense = dense < tile;
+  }
+  if (!p.dense) {
+    p.padded = d->tokens;
+    p.splits = 1;
+    set_pieces(d, p);
+  }
   size_t off = 0;
   p.rows = off;
-  off += align_up((size_t)d->tokens * sizeof(VocabRow));
+  off += align_up((size_t)p.padded * sizeof(VocabRow));
+  p.last = off;
+  off += p.dense ? last_bytes(d) : 0;
   p.xs = off;
   off += align_up((size_t)(p.padded * d->d * es));
   p.gz = off;
   off += align_up((size_t)(p.padded * p.ldg * es));
   p.acc = off;
-  if (p.pieces > 1) off += align_up((size_t)d->tokens * d->d * 4);
+  if (p.summed()) off += align_up((size_t)d->tokens * d->d * 4 * p.splits);
   p.part = off;
-  const size_t last = part_floats(d, p, d->vocab - (p.pieces - 1) * p.piece);
-  off += align_up(std::max(part_floats(d, p, p.piece), last) * 4);
+  if (!p.dense) {
+    const size_t rest = part_floats(d, d->vocab - (p.pieces - 1) * p.piece);
+    off += align_up(std::max(part_floats(d, p.piece), rest) * 4);
+  }
   p.total = off;
   return p;
 }
@@ -177,15 +236,23 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   if (!z) z = reinterpret_cast<float*>(w + plan.z);
   float2* part = reinterpret_cast<float2*>(w + plan.part);
   POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
-  for (int64_t r = 0; r < d->tokens; r += plan.rows) {
-    const int64_t rows = std::min(plan.rows, d->tokens - r);
+  const void* last = plan.dense && last_rows(d) ? w + plan.last : nullptr;
+  if (last) POETX_TRY(poetx::launch_vocab_last_rows(W, d->vocab, (int)d->d, w + plan.last, s));
+  for (int64_t at = 0; at < d->tokens; at += plan.rows) {
+    const int64_t rows = std::min(plan.rows, d->tokens - at);
+    // (the dense tiles take 256 rows at least: the last range begins early, and
+    // forms some rows' sums again)
+    const int64_t r = plan.dense ? std::min(at, std::max(d->tokens - kTile, INT64_C(0))) : at;
     VocabProduct p;
     p.x = static_cast<const char*>(x) + r * d->d * act_size(d->act);
     p.W = W;
-    p.M = (int)rows; p.N = (int)d->vocab; p.K = (int)d->d;
+    p.M = (int)(at + rows - r); p.N = (int)d->vocab; p.K = (int)d->d;
     p.scale = scale_of(d);
-    POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.tile, p, part, rows, s));
-    POETX_TRY(poetx::launch_vocab_loss(part, rows, plan.slots, list_at(list, r), rows,
+    if (plan.dense)
+      POETX_TRY(poetx::launch_vocab_lse_dense(p, last, part, p.M, s));
+    else
+      POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.tile, p, part, p.M, s));
+    POETX_TRY(poetx::launch_vocab_loss(part, p.M, plan.slots, list_at(list, r), p.M,
                                        z + r * list.top, loss + r, lse + r, s));
   }
   return POETX_OK;
@@ -217,24 +284,43 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
   char* w = static_cast<char*>(ws);
   const VocabList list = list_of(d, ids, teacher);
   VocabRow* rows = reinterpret_cast<VocabRow*>(w + plan.rows);
-  void* xs = g_W ? w + plan.xs : nullptr;
+  // (the dense products read x out of its tiled copy too)
+  void* xs = g_W || plan.dense ? w + plan.xs : nullptr;
   char* gz = w + plan.gz;
   float* acc = reinterpret_cast<float*>(w + plan.acc);
   POETX_TRY(poetx::launch_vocab_rows(t, list, d->tokens, plan.padded, g_loss, g_lse, lse, rows, x,
-                                     (int)d->d, xs, s));
+                                     (int)d->d, xs, plan.dense, s));
+  const bool ragged = plan.dense && last_rows(d);
+  if (ragged) POETX_TRY(poetx::launch_vocab_last_rows(W, d->vocab, (int)d->d, w + plan.last, s));
   for (int64_t c = 0; c < d->vocab; c += plan.piece) {
     const int64_t cols = std::min(plan.piece, d->vocab - c);
     const char* Wc = static_cast<const char*>(W) + c * d->d * es;
+    const void* last = ragged && c + cols == d->vocab ? w + plan.last : nullptr;
+    char* gWc = g_W ? static_cast<char*>(g_W) + c * d->d * es : nullptr;
     VocabProduct p;
-    p.x = x;
+    p.x = plan.dense ? xs : x;
     p.W = Wc;
-    p.M = (int)d->tokens; p.N = (int)cols; p.K = (int)d->d;
+    p.M = (int)(plan.dense ? plan.padded : d->tokens); p.N = (int)cols; p.K = (int)d->d;
     p.scale = scale_of(d);
-    POETX_TRY(poetx::launch_vocab_grad_tile(
-        t, plan_tile_product(t, d->tokens, cols, d->d, false, 1), p, rows, gz, plan.ldg, (int)c, s));
+    if (plan.dense)
+      POETX_TRY(poetx::launch_vocab_grad_dense(p, last, rows, gz, plan.ldg, (int)c, s));
+    else
+      POETX_TRY(poetx::launch_vocab_grad_tile(t, plan_tile_product(t, p.M, cols, d->d, false, 1), p,
+                                              rows, gz, plan.ldg, (int)c, s));
     if (teacher)
-      POETX_TRY(poetx::launch_vocab_listed_grad(t, list, d->tokens, rows, z, gz, plan.ldg, (int)c,
-                                                (int)cols, s));
+      POETX_TRY(poetx::launch_vocab_listed_grad(t, list, d->tokens, rows, z, gz, plan.ldg,
+                                                plan.dense, (int)c, (int)cols, s));
+    if (plan.dense) {
+      if (g_x)
+        POETX_TRY(poetx::launch_vocab_gx_dense(
+            gz, plan.ldg, Wc, last, d->tokens, (int)d->d, (int)cols,
+            (int)ceil_div(cols, plan.kchunk), plan.kchunk, acc, c > 0,
+            plan.summed() ? nullptr : g_x, s));
+      if (g_W)
+        POETX_TRY(poetx::launch_vocab_gw_dense(gz, plan.ldg, xs, ceil_div(d->tokens, 32) * 32,
+                                               (int)d->d, (int)cols, gWc, s));
+      continue;
+    }
     TileProduct g;
     g.A = gz; g.lda = plan.ldg;
     g.ldb = d->d;
@@ -255,11 +341,13 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
       TileProduct q = g;
       q.B = xs;
       q.M = (int)cols; q.K = (int)d->tokens;
-      q.ep.y = static_cast<char*>(g_W) + c * d->d * es;
+      q.ep.y = gWc;
       POETX_TRY(poetx::launch_tile_product(t, plan_tile_product(t, q.M, q.N, q.K, false), q, false,
                                            false, s));
     }
   }
+  if (plan.dense && g_x && plan.summed())
+    POETX_TRY(poetx::launch_sum_slabs(t, acc, plan.splits, d->tokens, (int)d->d, g_x, s));
   return POETX_OK;
 }
 

@@ -1,0 +1,341 @@
+// The four large bf16 products of the losses over a vocabulary on the 256 x 256
+// tile loop of dense_core.h: the forward's logits ending in partial sums of
+// exponentials, the backward's ending in the gradient g_z of the logits, and
+// g_z's own products with W and x.
+//
+// No end stages its tile in LDS, so the ring is free as soon as the last
+// products have run and the next tile's first four K tiles are copied into it
+// behind the epilogue. g_z leaves as 16-byte stores straight from the
+// registers: a lane holds four consecutive columns of a row of each 16 x 16
+// fragment, and one v_permlane16_swap of a pair of neighbouring fragments makes
+// that eight; in the tiled layout (kernels.h) the wave's 16 rows x 32 columns
+// are then 1 KB of consecutive bytes. Both of g_z's products read whole
+// 128-byte lines of that layout, K-major (g_x = g_z W) and M-major (g_W = g_z^T x).
+#include "dense_core.h"
+#include "epilogue.h"
+#include "vocab.h"
+
+namespace poetx {
+namespace {
+
+// Fragments (i, 2 q) and (i, 2 q + 1), packed, as this lane's 16 bytes: columns
+// pair_column() .. + 7 of the pair's 32 in row 16 i + l % 16.
+__device__ __forceinline__ uint4 swap_pair(uint2 a, uint2 b) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
+}
+// the panel of W's rows n0 .. n0 + 255 less n0 rows: of the vocabulary, or of the
+// zero-padded copy of its last rows
+__device__ __forceinline__ const bf16_t* panel(const bf16_t* W, const bf16_t* W_last, int n0, int N,
+                                               int K) {
+  return n0 + BN <= N ? W : W_last - (int64_t)n0 * K;
+}
+__device__ __forceinline__ int pair_column(int ln) {
+  return 16 * ((ln >> 4) & 1) + 8 * (ln >> 5);
+}
+
+// The persistent loop: products, then the next tile's first copies, then
+// end(m0, n0, q, mt, nt) of this one, for the tiles of nq products side by side (their
+// panels through set(q, m0, n0)).
+template <typename D, typename Set, typename End>
+__device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, int m_last,
+                                          int n_last, const Set& set, const End& end) {
+  const int total = num_mt * num_nt * nq;
+  int tile = blockIdx.x, mt, nt, q, ntiles;
+  if (tile >= total) return;
+  auto go = [&]() __attribute__((always_inline)) {
+    // (wave-uniform; said again where the loop's phis have lost it)
+    d.lds0 = __builtin_amdgcn_readfirstlane(d.lds0);
+    d.wave = __builtin_amdgcn_readfirstlane(d.wave);
+    int ntb;
+    xcd_grouped_tile_at(tile, total, num_mt, num_nt * nq, mt, ntb);
+    q = ntb / num_nt;
+    nt = ntb - q * num_nt;
+    ntiles = set(q, min(mt * BM, m_last), min(nt * BN, n_last));
+    d.prefetch(ntiles);
+  };
+  go();
+  for (;;) {
+    const int mt0 = mt, nt0 = nt, q0 = q;
+    d.start(ntiles);
+    d.mainloop(ntiles);
+    d.settle();
+    wait_lds();
+    barrier_nofence();  // every wave is done with the ring
+    tile += (int)gridDim.x;
+    const bool more = tile < total;
+    if (more) go();
+    end(min(mt0 * BM, m_last), min(nt0 * BN, n_last), q0, nt0);
+    if (!more) break;
+  }
+}
+
+// (opaque: keeps the compiler from hoisting the epilogue's address arithmetic
+// out of the tile loop)
+template <typename D> __device__ __forceinline__ int opaque_lane(const D& d) {
+  int ln = d.lane;
+  asm volatile("" : "+v"(ln));
+  return ln;
+}
+
+__global__ void __launch_bounds__(NT)
+vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
+                 const bf16_t* __restrict__ W_last, int M, int N, int K, float scale, float2* __restrict__ part, int64_t part_ld) {
+  typedef Dense<true, true> D;
+  D d;
+  d.init(K, K, false, false);
+  const int ntiles = K / BK;
+  tile_loop(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M - BM, N,
+            [&](int, int m0, int n0) __attribute__((always_inline)) {
+              d.set_tile(x, panel(W, W_last, n0, N, K), K, K, m0, n0);
+              return ntiles;
+            },
+            [&](int m0, int n0, int, int nt) __attribute__((always_inline)) {
+              const int ln = opaque_lane(d);
+              float2* out = part + (int64_t)(2 * nt + d.wn) * part_ld + m0 + d.wm * 128 + (ln & 15);
+#pragma unroll
+              for (int i = 0; i < FM; ++i) {
+                float v[4 * FN];
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) v[4 * j + e] = d.acc[i][j][e];
+                if (n0 + BN > N) {  // (the last panel, padded)
+                  int left = N - n0 - d.wn * 128 - 4 * (ln >> 4);
+                  asm volatile("" : "+v"(left));
+#pragma unroll
+                  for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (16 * j + e >= left) v[4 * j + e] = -INFINITY;
+                }
+                const float2 ms = row_max_sum<4 * FN>(v, scale);
+                if (ln < 16) out[16 * i] = ms;
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            });
+}
+
+__global__ void __launch_bounds__(NT)
+vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
+                  const bf16_t* __restrict__ W_last, int M, int N, int K, float scale,
+                  const VocabRow* __restrict__ rows, bf16_t* __restrict__ gz, int64_t ldg,
+                  int col0) {
+  typedef Dense<true, true> D;
+  D d;
+  d.init(K, K, true, false);
+  const int ntiles = K / BK;
+  tile_loop(d, M / BM, (N + BN - 1) / BN, 1, M, N,
+            [&](int, int m0, int n0) __attribute__((always_inline)) {
+              d.set_tile(xs, panel(W, W_last, n0, N, K), K, K, m0, n0);
+              return ntiles;
+            },
+            [&](int m0, int n0, int, int) __attribute__((always_inline)) {
+              const int ln = opaque_lane(d);
+              const VocabRow* at = rows + m0 + d.wm * 128 + (ln & 15);
+              // (the wave's first block of 32 columns, this lane's place in it)
+              bf16_t* out = gz + tiled_offset(m0, n0 + d.wn * 128, ldg) +
+                            (d.wm * 128 + (ln & 15)) * kTileCols + pair_column(ln);
+              const int col = col0 + n0 + d.wn * 128 + 4 * (ln >> 4);
+#pragma unroll
+              for (int i = 0; i < FM; ++i) {
+                const VocabRow r = at[16 * i];
+#pragma unroll
+                for (int j = 0; j < FN; j += 2) {
+                  uint2 w[2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      v[e] = logit_gradient(r, d.acc[i][j + h][e], scale, col + 16 * (j + h) + e);
+                    if (n0 + BN > N) {  // (the last panel's padding)
+#pragma unroll
+                      for (int e = 0; e < 4; ++e)
+                        if (n0 + d.wn * 128 + 4 * (ln >> 4) + 16 * (j + h) + e >= N) v[e] = 0.0f;
+                    }
+                    w[h] = Quad<bf16_t>::pack(v);
+                  }
+                  *reinterpret_cast<uint4*>(out + i * 16 * kTileCols + j / 2 * TILE) =
+                      swap_pair(w[0], w[1]);
+                  __builtin_amdgcn_sched_barrier(0);
+                }
+              }
+            });
+}
+
+// g_x: `splits` ranges of the piece's columns (kchunk each) side by side, each
+// into its own float32 slab [rows][N], added to what is there with `add`; or,
+// with y, one range whose result is g_x itself.
+template <bool WHOLE>
+__global__ void __launch_bounds__(NT)
+vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
+                const bf16_t* __restrict__ W_last, int rows, int M, int N, int K, int64_t ldg,
+                int splits, int kchunk, float* __restrict__ slabs, int add, bf16_t* __restrict__ y) {
+  typedef Dense<false, false, true, false, true> D;
+  D d;
+  d.init(ldg, N, true, false);
+  tile_loop(d, M / BM, (N + BN - 1) / BN, splits, M, N - BN,
+            [&](int q, int m0, int n0) __attribute__((always_inline)) {
+              // (the tiled layout's blocks of 32 columns lie one behind another)
+              d.set_tile(gz + (int64_t)q * kchunk * BM, W + (int64_t)q * kchunk * N, ldg, N, m0, n0);
+              const int n = min(K, (q + 1) * kchunk) - q * kchunk;
+              d.last_t = n % BK ? n / BK : -1;
+              d.last_b = W_last + n0;
+              return (n + BK - 1) / BK;
+            },
+            [&](int m0, int n0, int q, int nt) __attribute__((always_inline)) {
+              const int ln = opaque_lane(d);
+              const int m = m0 + d.wm * 128 + (ln & 15);
+              if constexpr (WHOLE) {
+                bf16_t* out = y + (int64_t)m * N + n0 + d.wn * 128 + pair_column(ln);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                  for (int j = 0; j < FN; j += 2) {
+                    uint2 w[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      const float v[4] = {d.acc[i][j + h][0], d.acc[i][j + h][1],
+                                          d.acc[i][j + h][2], d.acc[i][j + h][3]};
+                      w[h] = Quad<bf16_t>::pack(v);
+                    }
+                    const uint4 v = swap_pair(w[0], w[1]);
+                    if (m + 16 * i < rows)
+                      *reinterpret_cast<uint4*>(out + (int64_t)16 * i * N + 16 * j) = v;
+                    __builtin_amdgcn_sched_barrier(0);
+                  }
+                return;
+              }
+              const int n = d.wn * 128 + 4 * (ln >> 4);
+              float* out = slabs + ((int64_t)q * rows + m) * N + n0 + n;
+              // (a tile shifted back repeats columns of its neighbour, which
+              // are added once)
+              const int first = nt * BN - n0;
+#pragma unroll
+              for (int i = 0; i < FM; ++i) {
+                if (m + 16 * i < rows) {
+                  float4 was[FN];
+#pragma unroll
+                  for (int j = 0; j < FN; ++j)
+                    was[j] = add ? *reinterpret_cast<const float4*>(out + 16 * j)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                  for (int j = 0; j < FN; ++j) {
+                    if (n + 16 * j < first) continue;
+                    *reinterpret_cast<float4*>(out + 16 * j) =
+                        make_float4(d.acc[i][j][0] + was[j].x, d.acc[i][j][1] + was[j].y,
+                                    d.acc[i][j][2] + was[j].z, d.acc[i][j][3] + was[j].w);
+                  }
+                }
+                out += (int64_t)16 * N;
+                asm volatile("" : "+v"(out));
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            });
+}
+
+// g_W of the piece: both operands tiled, their rows (tokens) the reduction
+__global__ void __launch_bounds__(NT)
+vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, int M, int N, int K,
+                int64_t ldg, bf16_t* __restrict__ g_W) {
+  typedef Dense<false, false, false, true> D;
+  D d;
+  d.init(ldg, N, true, true);
+  const int ntiles = K / BK;
+  tile_loop(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M, N - BN,
+            [&](int, int m0, int n0) __attribute__((always_inline)) {
+              d.set_tile(gz, xs, ldg, N, m0, n0);
+              return ntiles;
+            },
+            [&](int m0, int n0, int, int) __attribute__((always_inline)) {
+              const int ln = opaque_lane(d);
+              const int m = m0 + d.wm * 128 + (ln & 15);
+              bf16_t* out = g_W + (int64_t)m * N + n0 + d.wn * 128 + pair_column(ln);
+#pragma unroll
+              for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; j += 2) {
+                  uint2 w[2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const float v[4] = {d.acc[i][j + h][0], d.acc[i][j + h][1], d.acc[i][j + h][2],
+                                        d.acc[i][j + h][3]};
+                    w[h] = Quad<bf16_t>::pack(v);
+                  }
+                  const uint4 v = swap_pair(w[0], w[1]);
+                  if (m + 16 * i < M)  // (gz is padded to whole tiles)
+                    *reinterpret_cast<uint4*>(out + (int64_t)16 * i * N + 16 * j) = v;
+                  __builtin_amdgcn_sched_barrier(0);
+                }
+            });
+}
+
+const bf16_t* b16(const void* p) { return static_cast<const bf16_t*>(p); }
+
+}  // namespace
+
+hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
+                                  int64_t part_ld, hipStream_t s) {
+  if (!vocab_dense_supported(p.M, p.N, p.K) || (p.N % BN != 0 && !W_last))
+    return hipErrorInvalidValue;
+  int grid = 0;
+  const hipError_t e = dense_grid(p.M, p.N, &grid);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(vocab_lse_kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last),
+                     p.M, p.N, p.K, p.scale, part, part_ld);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, const VocabRow* rows,
+                                   void* gz, int64_t ldg, int col0, hipStream_t s) {
+  if (!vocab_dense_supported(p.M, p.N, p.K) || (p.N % BN != 0 && !W_last) || p.M % BM != 0 ||
+      ldg % BN != 0 || ldg < p.N)
+    return hipErrorInvalidValue;
+  int grid = 0;
+  const hipError_t e = dense_grid(p.M, p.N, &grid);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(vocab_grad_kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last),
+                     p.M, p.N, p.K, p.scale, rows, static_cast<bf16_t*>(gz), ldg, col0);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, const void* W_last,
+                                 int64_t rows, int d, int cols, int splits, int kchunk,
+                                 float* slabs, bool add, void* y, hipStream_t s) {
+  const int64_t M = (rows + BM - 1) / BM * BM;
+  if (!vocab_dense_supported(M, cols, d) || (cols % BK != 0 && !W_last) || ldg % BN != 0 ||
+      ldg < cols || splits < 1 || kchunk % BK != 0 || kchunk < BK ||
+      (int64_t)(splits - 1) * kchunk >= cols || (int64_t)splits * kchunk < cols ||
+      (y ? splits != 1 || add : !slabs))
+    return hipErrorInvalidValue;
+  int grid = 0;
+  const hipError_t e = dense_grid(M, (int64_t)(d + BN - 1) / BN * BN * splits, &grid);
+  if (e != hipSuccess) return e;
+  // (the rows of W from the last whole K tile on, in their copy)
+  const bf16_t* last = W_last ? b16(W_last) + (int64_t)(cols / BK * BK % BN) * d : nullptr;
+  if (y)
+    hipLaunchKernelGGL(vocab_gx_kernel<true>, dim3(grid), dim3(NT), 0, s, b16(gz), b16(W), last,
+                       (int)rows, (int)M, d, cols, ldg, splits, kchunk, nullptr, 0,
+                       static_cast<bf16_t*>(y));
+  else
+    hipLaunchKernelGGL(vocab_gx_kernel<false>, dim3(grid), dim3(NT), 0, s, b16(gz), b16(W), last,
+                       (int)rows, (int)M, d, cols, ldg, splits, kchunk, slabs, (int)add, nullptr);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
+                                 int cols, void* g_W, hipStream_t s) {
+  if (!vocab_dense_supported(256, cols, d) || ldg % BN != 0 || ldg < cols || padded % BK != 0 ||
+      padded < BK)
+    return hipErrorInvalidValue;
+  int grid = 0;
+  const hipError_t e = dense_grid(cols, d, &grid);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(vocab_gw_kernel, dim3(grid), dim3(NT), 0, s, b16(gz), b16(xs), cols, d,
+                     (int)padded, ldg, static_cast<bf16_t*>(g_W));
+  return hipGetLastError();
+}
+
+}  // namespace poetx
