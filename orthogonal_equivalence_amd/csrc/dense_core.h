@@ -236,8 +236,11 @@ struct Dense {
 
   // K tile t, held in ring slot S, its fragments in set P. STEADY: tiles
   // t+1 .. t+4 all exist, so every step below is taken. FIRST: t == 0.
-  template <int S, int P, bool STEADY, bool FIRST = false>
-  __device__ __forceinline__ void tile(int t, int ntiles) {
+  // LATE (t < 3): with `late`, at least LATE vector memory instructions (the
+  // stores of the output tile before) were issued behind the copies of the first
+  // four K tiles, and need not have completed for those.
+  template <int S, int P, bool STEADY, bool FIRST = false, int LATE = 0>
+  __device__ __forceinline__ void tile(int t, int ntiles, bool late = false) {
     constexpr int S1 = (S + 1) & 3;
     const bool more = STEADY || t + 1 < ntiles;
     // paired: an odd tile issues the copies of tiles t + 3 and t + 4
@@ -252,7 +255,12 @@ struct Dense {
       // flight) and its reads of tile t are done; after the barrier every
       // part has landed and slot S is free
       // (paired, odd t: of the pair t + 1, t + 2 only the last copy may be)
-      if constexpr (PAIR && ODD) {
+      if constexpr (LATE > 0) {
+        static_assert(STEADY && LATE <= 40, "vmcnt range");
+        constexpr int kLeft = PAIR && ODD ? 1 : 2 * LPW;
+        if (late) wait_vm<(kLeft + LATE < 63 ? kLeft + LATE : 63)>();
+        else wait_vm<kLeft>();
+      } else if constexpr (PAIR && ODD) {
         if (STEADY || t + 2 < ntiles) wait_vm<1>();
         else wait_vm<0>();
       } else {
@@ -308,6 +316,44 @@ struct Dense {
     read_b<0, 0, 4>(); read_b<0, 0, 5>(); read_b<0, 0, 6>(); read_b<0, 0, 7>();
   }
 
+  // start() and mainloop() with LATE's waits; ntiles >= 8
+  template <int LATE>
+  __device__ __forceinline__ void start_late(bool late) {
+    constexpr int kLeft = (PAIR ? 2 : 3) * LPW;
+    if (late) wait_vm<(kLeft + LATE < 63 ? kLeft + LATE : 63)>();
+    else wait_vm<kLeft>();
+    barrier_nofence();
+    read_a<0, 0, 0>(); read_a<0, 0, 1>(); read_a<0, 0, 2>(); read_a<0, 0, 3>();
+    read_a<0, 0, 4>(); read_a<0, 0, 5>(); read_a<0, 0, 6>(); read_a<0, 0, 7>();
+    read_b<0, 0, 0>(); read_b<0, 0, 1>(); read_b<0, 0, 2>(); read_b<0, 0, 3>();
+    read_b<0, 0, 4>(); read_b<0, 0, 5>(); read_b<0, 0, 6>(); read_b<0, 0, 7>();
+  }
+  template <int LATE>
+  __device__ __forceinline__ void mainloop_late(int ntiles, bool late) {
+    tile<0, 0, true, true, LATE>(0, ntiles, late);
+    tile<1, 1, true, false, LATE>(1, ntiles, late);
+    tile<2, 0, true, false, LATE>(2, ntiles, late);
+    int t = 3;
+    for (; t + 8 <= ntiles; t += 4) {
+      tile<3, 1, true>(t, ntiles);
+      tile<0, 0, true>(t + 1, ntiles);
+      tile<1, 1, true>(t + 2, ntiles);
+      tile<2, 0, true>(t + 3, ntiles);
+    }
+    // the last 4 .. 7 tiles
+    tile<3, 1, false>(t, ntiles);
+    tile<0, 0, false>(t + 1, ntiles);
+    tile<1, 1, false>(t + 2, ntiles);
+    tile<2, 0, false>(t + 3, ntiles);
+    t += 4;
+    if (t < ntiles) tile<3, 1, false>(t++, ntiles);
+    if (t < ntiles) tile<0, 0, false>(t++, ntiles);
+    if (t < ntiles) tile<1, 1, false>(t++, ntiles);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
   __device__ __forceinline__ void mainloop(int ntiles) {
     // tile 0 writes the accumulators; then slots 1, 2, 3, 0, 1, ...
     if (ntiles > 4) tile<0, 0, true, true>(0, ntiles);
@@ -340,13 +386,22 @@ struct Dense {
   // did, at the join of the last tiles' branches, where the code that follows
   // takes VGPRs).
   __device__ __forceinline__ void settle() {
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+a"(acc[FM - 1][0]), "+a"(acc[FM - 1][1]), "+a"(acc[FM - 1][2]),
+                   "+a"(acc[FM - 1][3]), "+a"(acc[FM - 1][4]), "+a"(acc[FM - 1][5]),
+                   "+a"(acc[FM - 1][6]), "+a"(acc[FM - 1][7])
+                 :
+                 : "memory");
+    in_agprs();
+  }
+  // the accumulators in their AGPRs at this place (an epilogue that reads them
+  // twice would otherwise keep copies, more than the VGPRs hold)
+  __device__ __forceinline__ void in_agprs() {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-      asm volatile("s_nop 7"
+      asm volatile(""
                    : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]),
-                     "+a"(acc[i][4]), "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7])
-                   :
-                   : "memory");
+                     "+a"(acc[i][4]), "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
     __builtin_amdgcn_sched_barrier(0);
   }
 

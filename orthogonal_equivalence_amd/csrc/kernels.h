@@ -346,10 +346,11 @@ struct VocabRow {
 };
 // Forward: for every row and slot (a group of the piece's columns)
 // part[slot][row] = (max, sum) with sum_j 2^(scale z_j) = sum 2^max over the slot's
-// columns. vocab_tile_slots of them.
+// columns. vocab_tile_slots of them. With targets [M], z[row] = the logit of
+// the row's, where the piece has it.
 int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N);
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
-                                 int64_t part_ld, hipStream_t s);
+                                 int64_t part_ld, const int64_t* targets, float* z, hipStream_t s);
 // Backward: g_z of the piece, whose first column is `col0` of the vocabulary,
 // in x's type at gz[row][ldg]; columns N up to the next multiple of 8 are zeroed
 // (ldg holds N rounded up to 256).
@@ -366,7 +367,8 @@ inline bool vocab_dense_supported(int64_t M, int64_t N, int64_t K) {
 }
 // 2 ceil(N / 256) slots
 hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
-                                  int64_t part_ld, hipStream_t s);
+                                  int64_t part_ld, const int64_t* targets, float* z,
+                                  hipStream_t s);
 // x: the tiled copy of it, M % 256 == 0 rows, as many of `rows`; gz in the tiled
 // layout [M][ldg], ldg % 256 == 0; columns past N of the last tile are zeroed.
 hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, const VocabRow* rows,
@@ -399,8 +401,8 @@ struct VocabList {
 // it is past the vocabulary.
 hipError_t launch_listed_logits(DType t, const void* x, const void* W, const VocabList& l,
                                 int64_t rows, int K, float* z, hipStream_t s);
-// lse from the slots, and the loss: of targets with z their logits, else of
-// the teacher's distribution.
+// lse from the slots, and the loss: of targets with z their logits (of those
+// that are in the vocabulary), else of the teacher's distribution.
 hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots, const VocabList& l,
                              int64_t rows, const float* z, float* loss, float* lse, hipStream_t s);
 // The rows' parts (none for those past `rows`), and with xs a copy of x

@@ -8,23 +8,40 @@
 namespace poetx {
 namespace {
 
+// The maximum and the sum over the four lanes that are 16 apart, in all four:
+// two exchanges of rows of 16 lanes, in the vector unit (through LDS, as
+// __shfl_xor goes, each costs its latency).
+__device__ __forceinline__ float quad_max(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// what the exponents of a row's sum are taken from: its maximum, or 0 where
+// that is not finite (the sum is then 0 for -inf alone and +inf with a +inf
+// among the values; a NaN reaches it either way)
+__device__ __forceinline__ float exponent_base(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+
 // The maximum m of c v over a row's values, this lane's NV and those of the
 // lanes 16, 32 and 48 further on, and the sum of 2^(c v - m), in all four
-// lanes. Where m is not finite the sum is that of 2^(c v): 0 for -inf alone,
-// +inf with a +inf among them; a NaN reaches it either way.
+// lanes.
 template <int NV> __device__ __forceinline__ float2 row_max_sum(const float (&v)[NV], float c) {
   float m = v[0];
 #pragma unroll
   for (int q = 1; q < NV; ++q) m = fmaxf(m, v[q]);
-  m = fmaxf(m, __shfl_xor(m, 16));
-  m = fmaxf(m, __shfl_xor(m, 32)) * c;
-  const float at = fabsf(m) < INFINITY ? m : 0.0f;
-  float s = 0.0f;
+  m = quad_max(m) * c;
+  const float at = exponent_base(m);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int q = 0; q < NV; ++q) s += __builtin_amdgcn_exp2f(fmaf(v[q], c, -at));
-  s += __shfl_xor(s, 16);
-  s += __shfl_xor(s, 32);
-  return make_float2(m, s);
+  for (int q = 0; q < NV; ++q) s[q & 3] += __builtin_amdgcn_exp2f(fmaf(v[q], c, -at));
+  return make_float2(m, quad_sum((s[0] + s[1]) + (s[2] + s[3])));
 }
 
 // g_z at a logit z of the vocabulary's column `col` (VocabRow)

@@ -150,7 +150,7 @@ join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int
   if constexpr (TARGETS) {
     const bool part_of = l.ids[row] >= 0;
     v = part_of ? v : 0.0f;
-    loss[row] = part_of ? v - z[row] : 0.0f;
+    loss[row] = !part_of ? 0.0f : l.ids[row] >= l.vocab ? NAN : v - z[row];
   }
   lse[row] = v;
 }

@@ -235,7 +235,8 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   const VocabList list = list_of(d, ids, teacher);
   if (!z) z = reinterpret_cast<float*>(w + plan.z);
   float2* part = reinterpret_cast<float2*>(w + plan.part);
-  POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
+  // (targets' logits come out of the products)
+  if (teacher) POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
   const void* last = plan.dense && last_rows(d) ? w + plan.last : nullptr;
   if (last) POETX_TRY(poetx::launch_vocab_last_rows(W, d->vocab, (int)d->d, w + plan.last, s));
   for (int64_t at = 0; at < d->tokens; at += plan.rows) {
@@ -249,9 +250,11 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
     p.M = (int)(at + rows - r); p.N = (int)d->vocab; p.K = (int)d->d;
     p.scale = scale_of(d);
     if (plan.dense)
-      POETX_TRY(poetx::launch_vocab_lse_dense(p, last, part, p.M, s));
+      POETX_TRY(poetx::launch_vocab_lse_dense(p, last, part, p.M, teacher ? nullptr : ids + r, z + r,
+                                              s));
     else
-      POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.tile, p, part, p.M, s));
+      POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.tile, p, part, p.M,
+                                             teacher ? nullptr : ids + r, z + r, s));
     POETX_TRY(poetx::launch_vocab_loss(part, p.M, plan.slots, list_at(list, r), p.M,
                                        z + r * list.top, loss + r, lse + r, s));
   }

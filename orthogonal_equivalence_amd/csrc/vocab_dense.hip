@@ -36,13 +36,16 @@ __device__ __forceinline__ int pair_column(int ln) {
 }
 
 // The persistent loop: products, then the next tile's first copies, then
-// end(m0, n0, q, mt, nt) of this one, for the tiles of nq products side by side (their
-// panels through set(q, m0, n0)).
-template <typename D, typename Set, typename End>
+// end(m0, n0, q, nt) of this one, for the tiles of nq products side by side (their
+// panels through set(q, m0, n0)). end returns whether it has issued at least
+// LATE vector memory instructions, for which the next products then do not
+// wait before their copies (8192 tokens, 131072 x 4096: see the kernels).
+template <int LATE, typename D, typename Set, typename End>
 __device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, int m_last,
                                           int n_last, const Set& set, const End& end) {
   const int total = num_mt * num_nt * nq;
   int tile = blockIdx.x, mt, nt, q, ntiles;
+  bool late = false;
   if (tile >= total) return;
   auto go = [&]() __attribute__((always_inline)) {
     // (wave-uniform; said again where the loop's phis have lost it)
@@ -58,15 +61,15 @@ __device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, 
   go();
   for (;;) {
     const int mt0 = mt, nt0 = nt, q0 = q;
-    d.start(ntiles);
-    d.mainloop(ntiles);
+    d.template start_late<LATE>(late);
+    d.template mainloop_late<LATE>(ntiles, late);
     d.settle();
     wait_lds();
     barrier_nofence();  // every wave is done with the ring
     tile += (int)gridDim.x;
     const bool more = tile < total;
     if (more) go();
-    end(min(mt0 * BM, m_last), min(nt0 * BN, n_last), q0, nt0);
+    late = end(min(mt0 * BM, m_last), min(nt0 * BN, n_last), q0, nt0);
     if (!more) break;
   }
 }
@@ -79,44 +82,93 @@ template <typename D> __device__ __forceinline__ int opaque_lane(const D& d) {
   return ln;
 }
 
+// The end of the logits' forward: for each of the wave's 128 rows the maximum and
+// the sum of exponentials over its 128 columns, in two passes over the
+// accumulators, so that the eight rows of a lane are exchanged together; and the
+// targets' logits, which few waves hold any of.
 __global__ void __launch_bounds__(NT)
 vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
-                 const bf16_t* __restrict__ W_last, int M, int N, int K, float scale, float2* __restrict__ part, int64_t part_ld) {
+                 const bf16_t* __restrict__ W_last, int M, int N, int K, float scale,
+                 float2* __restrict__ part, int64_t part_ld, const int64_t* __restrict__ targets,
+                 float* __restrict__ z) {
   typedef Dense<true, true> D;
   D d;
   d.init(K, K, false, false);
   const int ntiles = K / BK;
-  tile_loop(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M - BM, N,
-            [&](int, int m0, int n0) __attribute__((always_inline)) {
-              d.set_tile(x, panel(W, W_last, n0, N, K), K, K, m0, n0);
-              return ntiles;
-            },
-            [&](int m0, int n0, int, int nt) __attribute__((always_inline)) {
-              const int ln = opaque_lane(d);
-              float2* out = part + (int64_t)(2 * nt + d.wn) * part_ld + m0 + d.wm * 128 + (ln & 15);
+  tile_loop<FM>(
+      d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M - BM, N,
+      [&](int, int m0, int n0) __attribute__((always_inline)) {
+        d.set_tile(x, panel(W, W_last, n0, N, K), K, K, m0, n0);
+        return ntiles;
+      },
+      [&](int m0, int n0, int, int nt) __attribute__((always_inline)) {
+        const int ln = opaque_lane(d);
+        const int m = m0 + d.wm * 128 + (ln & 15), n = n0 + d.wn * 128;
+        if (n + 128 > N) {  // (the last panel, padded)
+          const int left = N - n - 4 * (ln >> 4);
 #pragma unroll
-              for (int i = 0; i < FM; ++i) {
-                float v[4 * FN];
+          for (int j = 0; j < FN; ++j)
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
+            for (int e = 0; e < 4; ++e) {
+              const bool out = 16 * j + e >= left;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) v[4 * j + e] = d.acc[i][j][e];
-                if (n0 + BN > N) {  // (the last panel, padded)
-                  int left = N - n0 - d.wn * 128 - 4 * (ln >> 4);
-                  asm volatile("" : "+v"(left));
+              for (int i = 0; i < FM; ++i) d.acc[i][j][e] = out ? -INFINITY : d.acc[i][j][e];
+              if (e == 3) d.in_agprs();
+            }
+        }
+        d.in_agprs();
+        float mx[FM], sum[FM];
 #pragma unroll
-                  for (int j = 0; j < FN; ++j)
+        for (int i = 0; i < FM; ++i) {
+          float v = d.acc[i][0][0];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      if (16 * j + e >= left) v[4 * j + e] = -INFINITY;
-                }
-                const float2 ms = row_max_sum<4 * FN>(v, scale);
-                if (ln < 16) out[16 * i] = ms;
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            });
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v = fmaxf(v, d.acc[i][j][e]);
+          mx[i] = v;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) mx[i] = quad_max(mx[i]) * scale;
+        d.in_agprs();
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const float at = exponent_base(mx[i]);
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s[e] += __builtin_amdgcn_exp2f(fmaf(d.acc[i][j][e], scale, -at));
+          sum[i] = (s[0] + s[1]) + (s[2] + s[3]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        float2* out = part + (int64_t)(2 * nt + d.wn) * part_ld + m;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          sum[i] = quad_sum(sum[i]);
+          if (ln < 16) out[16 * i] = make_float2(mx[i], sum[i]);
+        }
+        if (targets) {
+          d.in_agprs();
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            const int64_t at = targets[m + 16 * i] - n;
+            if (!__any(at >= 0 && at < 128)) continue;
+            const int own = at >= 0 && at < 128 ? (int)at - 4 * (ln >> 4) : -1;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (own == 16 * j + e) z[m + 16 * i] = d.acc[i][j][e];
+          }
+        }
+        return true;  // (the eight stores)
+      });
 }
 
+// The end of the logits' backward. A row's target is one column of the
+// vocabulary: few waves hold any, and the others only scale exponentials.
 __global__ void __launch_bounds__(NT)
 vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
                   const bf16_t* __restrict__ W_last, int M, int N, int K, float scale,
@@ -126,43 +178,55 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
   D d;
   d.init(K, K, true, false);
   const int ntiles = K / BK;
-  tile_loop(d, M / BM, (N + BN - 1) / BN, 1, M, N,
-            [&](int, int m0, int n0) __attribute__((always_inline)) {
-              d.set_tile(xs, panel(W, W_last, n0, N, K), K, K, m0, n0);
-              return ntiles;
-            },
-            [&](int m0, int n0, int, int) __attribute__((always_inline)) {
-              const int ln = opaque_lane(d);
-              const VocabRow* at = rows + m0 + d.wm * 128 + (ln & 15);
-              // (the wave's first block of 32 columns, this lane's place in it)
-              bf16_t* out = gz + tiled_offset(m0, n0 + d.wn * 128, ldg) +
-                            (d.wm * 128 + (ln & 15)) * kTileCols + pair_column(ln);
-              const int col = col0 + n0 + d.wn * 128 + 4 * (ln >> 4);
+  tile_loop<FM * FN / 2>(
+      d, M / BM, (N + BN - 1) / BN, 1, M, N,
+      [&](int, int m0, int n0) __attribute__((always_inline)) {
+        d.set_tile(xs, panel(W, W_last, n0, N, K), K, K, m0, n0);
+        return ntiles;
+      },
+      [&](int m0, int n0, int, int) __attribute__((always_inline)) {
+        const int ln = opaque_lane(d);
+        const VocabRow* at = rows + m0 + d.wm * 128 + (ln & 15);
+        // (the wave's first block of 32 columns, this lane's place in it)
+        bf16_t* out = gz + tiled_offset(m0, n0 + d.wn * 128, ldg) +
+                      (d.wm * 128 + (ln & 15)) * kTileCols + pair_column(ln);
+        const int col = col0 + n0 + d.wn * 128;
+        const bool padded = n0 + BN > N;
+        int left = N - n0 - d.wn * 128 - 4 * (ln >> 4);
 #pragma unroll
-              for (int i = 0; i < FM; ++i) {
-                const VocabRow r = at[16 * i];
+        for (int i = 0; i < FM; ++i) {
+          d.in_agprs();
+          const VocabRow r = at[16 * i];
+          const int own = r.target - col - 4 * (ln >> 4);  // (this lane's: 16 j + e)
+          const bool rare = __any((unsigned)(r.target - col) < 128u) || padded;
+          asm volatile("" : "+v"(left));
 #pragma unroll
-                for (int j = 0; j < FN; j += 2) {
-                  uint2 w[2];
+          for (int j = 0; j < FN; j += 2) {
+            uint2 w[2];
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    float v[4];
+            for (int h = 0; h < 2; ++h) {
+              float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      v[e] = logit_gradient(r, d.acc[i][j + h][e], scale, col + 16 * (j + h) + e);
-                    if (n0 + BN > N) {  // (the last panel's padding)
+              for (int e = 0; e < 4; ++e)
+                v[e] = r.a == 0.0f ? 0.0f
+                                   : r.a * __builtin_amdgcn_exp2f(
+                                               fmaf(d.acc[i][j + h][e], scale, -r.lse2));
+              if (rare) {
 #pragma unroll
-                      for (int e = 0; e < 4; ++e)
-                        if (n0 + d.wn * 128 + 4 * (ln >> 4) + 16 * (j + h) + e >= N) v[e] = 0.0f;
-                    }
-                    w[h] = Quad<bf16_t>::pack(v);
-                  }
-                  *reinterpret_cast<uint4*>(out + i * 16 * kTileCols + j / 2 * TILE) =
-                      swap_pair(w[0], w[1]);
-                  __builtin_amdgcn_sched_barrier(0);
+                for (int e = 0; e < 4; ++e) {
+                  if (own == 16 * (j + h) + e) v[e] -= r.b;
+                  if (16 * (j + h) + e >= left) v[e] = 0.0f;
                 }
               }
-            });
+              w[h] = Quad<bf16_t>::pack(v);
+            }
+            *reinterpret_cast<uint4*>(out + i * 16 * kTileCols + j / 2 * TILE) =
+                swap_pair(w[0], w[1]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        return true;
+      });
 }
 
 // g_x: `splits` ranges of the piece's columns (kchunk each) side by side, each
@@ -176,7 +240,7 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
   typedef Dense<false, false, true, false, true> D;
   D d;
   d.init(ldg, N, true, false);
-  tile_loop(d, M / BM, (N + BN - 1) / BN, splits, M, N - BN,
+  tile_loop<FM * FN / 2>(d, M / BM, (N + BN - 1) / BN, splits, M, N - BN,
             [&](int q, int m0, int n0) __attribute__((always_inline)) {
               // (the tiled layout's blocks of 32 columns lie one behind another)
               d.set_tile(gz + (int64_t)q * kchunk * BM, W + (int64_t)q * kchunk * N, ldg, N, m0, n0);
@@ -191,7 +255,8 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
               if constexpr (WHOLE) {
                 bf16_t* out = y + (int64_t)m * N + n0 + d.wn * 128 + pair_column(ln);
 #pragma unroll
-                for (int i = 0; i < FM; ++i)
+                for (int i = 0; i < FM; ++i) {
+                  d.in_agprs();
 #pragma unroll
                   for (int j = 0; j < FN; j += 2) {
                     uint2 w[2];
@@ -204,9 +269,9 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
                     const uint4 v = swap_pair(w[0], w[1]);
                     if (m + 16 * i < rows)
                       *reinterpret_cast<uint4*>(out + (int64_t)16 * i * N + 16 * j) = v;
-                    __builtin_amdgcn_sched_barrier(0);
                   }
-                return;
+                }
+                return m0 + BM <= rows;
               }
               const int n = d.wn * 128 + 4 * (ln >> 4);
               float* out = slabs + ((int64_t)q * rows + m) * N + n0 + n;
@@ -215,6 +280,7 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
               const int first = nt * BN - n0;
 #pragma unroll
               for (int i = 0; i < FM; ++i) {
+                d.in_agprs();
                 if (m + 16 * i < rows) {
                   float4 was[FN];
 #pragma unroll
@@ -233,6 +299,7 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
                 asm volatile("" : "+v"(out));
                 __builtin_amdgcn_sched_barrier(0);
               }
+              return m0 + BM <= rows && first == 0;
             });
 }
 
@@ -244,7 +311,7 @@ vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, in
   D d;
   d.init(ldg, N, true, true);
   const int ntiles = K / BK;
-  tile_loop(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M, N - BN,
+  tile_loop<FM * FN / 2>(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M, N - BN,
             [&](int, int m0, int n0) __attribute__((always_inline)) {
               d.set_tile(gz, xs, ldg, N, m0, n0);
               return ntiles;
@@ -254,7 +321,8 @@ vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, in
               const int m = m0 + d.wm * 128 + (ln & 15);
               bf16_t* out = g_W + (int64_t)m * N + n0 + d.wn * 128 + pair_column(ln);
 #pragma unroll
-              for (int i = 0; i < FM; ++i)
+              for (int i = 0; i < FM; ++i) {
+                d.in_agprs();
 #pragma unroll
                 for (int j = 0; j < FN; j += 2) {
                   uint2 w[2];
@@ -267,8 +335,9 @@ vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, in
                   const uint4 v = swap_pair(w[0], w[1]);
                   if (m + 16 * i < M)  // (gz is padded to whole tiles)
                     *reinterpret_cast<uint4*>(out + (int64_t)16 * i * N + 16 * j) = v;
-                  __builtin_amdgcn_sched_barrier(0);
                 }
+              }
+              return m0 + BM <= M;
             });
 }
 
@@ -277,14 +346,15 @@ const bf16_t* b16(const void* p) { return static_cast<const bf16_t*>(p); }
 }  // namespace
 
 hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
-                                  int64_t part_ld, hipStream_t s) {
+                                  int64_t part_ld, const int64_t* targets, float* z,
+                                  hipStream_t s) {
   if (!vocab_dense_supported(p.M, p.N, p.K) || (p.N % BN != 0 && !W_last))
     return hipErrorInvalidValue;
   int grid = 0;
   const hipError_t e = dense_grid(p.M, p.N, &grid);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(vocab_lse_kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last),
-                     p.M, p.N, p.K, p.scale, part, part_ld);
+                     p.M, p.N, p.K, p.scale, part, part_ld, targets, z);
   return hipGetLastError();
 }
 

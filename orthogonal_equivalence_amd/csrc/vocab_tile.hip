@@ -20,6 +20,8 @@ struct LseEnd {
   float2* part;
   int64_t part_ld;
   float scale;
+  const int64_t* targets;
+  float* z;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int, int wave_col, int lane) const {
@@ -35,6 +37,16 @@ struct LseEnd {
       const float2 ms = row_max_sum<4 * FN>(v, scale);
       const int m = m_at + 16 * i + (lane & 15);
       if (lane < 16 && m < p.M) out[m] = ms;
+      if (!targets) continue;
+      // the row's target, where it is among the wave's columns
+      const int64_t at = m < p.M ? targets[m] - n_at : -1;
+      if (!__any(at >= 0 && at < 16 * FN)) continue;
+      const int own = at >= 0 && at < 16 * FN ? (int)at - 4 * (lane >> 4) : -1;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (own == 16 * j + e) z[m] = acc[i][j][e];
     }
   }
 };
@@ -122,8 +134,8 @@ int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N) {
 }
 
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
-                                 int64_t part_ld, hipStream_t s) {
-  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale}, s);
+                                 int64_t part_ld, const int64_t* targets, float* z, hipStream_t s) {
+  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z}, s);
 }
 
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
