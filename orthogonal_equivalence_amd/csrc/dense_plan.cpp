@@ -169,10 +169,6 @@ TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out
   return best;
 }
 
-float dense_rounds_cost(int64_t tiles, int64_t K) {
-  return 3.0f + (float)ceil_div(tiles, 256) * (1.38f * (float)K / 64 + 6.0f);
-}
-
 namespace {
 
 // The dense kernel's time for an M x N x K product, as the tile kernel's plan
@@ -182,7 +178,8 @@ namespace {
 // 4096 x 4096 x 4096 forward 104 us, g_x 103 (97); 8192 x 14336 x 4096 674 (663),
 // its g_x 665 (633); 2048 x 8192 x 2048 57 (53); 4096 x 4096 x 1024 36 (31).
 float dense_cost(int64_t M, int64_t N, int64_t K) {
-  return dense_rounds_cost(ceil_div(M, 256) * ceil_div(N, 256), K);
+  const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), 256);
+  return 3.0f + (float)rounds * (1.38f * (float)K / 64 + 6.0f);
 }
 // Whether an M x N product of K-major A takes that kernel.
 bool use_dense(DType t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,

@@ -26,7 +26,4 @@ struct BwdChoice {
 };
 BwdChoice choose_bwd(DType t, bool int8, int64_t tokens, int64_t d_in, int64_t d_out);
 
-// Estimated time (us) of `tiles` 256 x 256 tiles of the dense kernel over K.
-float dense_rounds_cost(int64_t tiles, int64_t K);
-
 }  // namespace poetx

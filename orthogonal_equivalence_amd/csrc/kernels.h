@@ -335,6 +335,7 @@ struct VocabProduct {
   const void* x = nullptr;
   const void* W = nullptr;
   int M = 0, N = 0, K = 0;
+  int col0 = 0;        // the piece's first column in the vocabulary
   float scale = 0.0f;  // log2(e) / temperature
 };
 // One row's part in the gradient of its logits:
@@ -351,16 +352,17 @@ struct VocabRow {
 int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N);
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
                                  int64_t part_ld, const int64_t* targets, float* z, hipStream_t s);
-// Backward: g_z of the piece, whose first column is `col0` of the vocabulary,
-// in x's type at gz[row][ldg]; columns N up to the next multiple of 8 are zeroed
-// (ldg holds N rounded up to 256).
+// Backward: g_z of the piece in x's type at gz[row][ldg], or in the tiled layout
+// [..][ldg] of which gz is the piece's first block of columns; columns N up to
+// ldg, and rows M up to the next multiple of 32, are zeroed where tiles reach
+// (as far as the next multiple of 32 columns at least).
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
-                                  const VocabRow* rows, void* gz, int64_t ldg, int col0,
+                                  const VocabRow* rows, void* gz, int64_t ldg, bool tiled,
                                   hipStream_t s);
 
 // Large bf16 pieces on the dense kernel's 256 x 256 tile loop (vocab_dense.hip).
-// A piece that is not whole tiles of the vocabulary (the last one) comes with
-// W_last, a zero-padded copy [256][K] of W's rows from the last whole tile on.
+// A piece that ends inside a tile comes with W_last, a copy [256][K] of W's rows
+// from the last whole tile of the vocabulary on, padded with zeros.
 inline bool vocab_dense_supported(int64_t M, int64_t N, int64_t K) {
   return M >= 256 && N >= 1 && K >= 256 && K % 32 == 0 && K <= (1 << 22) && M <= INT32_MAX - 256 &&
          N <= INT32_MAX - 256;
@@ -369,21 +371,22 @@ inline bool vocab_dense_supported(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
                                   int64_t part_ld, const int64_t* targets, float* z,
                                   hipStream_t s);
-// x: the tiled copy of it, M % 256 == 0 rows, as many of `rows`; gz in the tiled
-// layout [M][ldg], ldg % 256 == 0; columns past N of the last tile are zeroed.
+// x: the tiled copy of it, M % 256 == 0 rows, as many of `rows`; gz in
+// the tiled layout [M][ldg], ldg % 256 == 0; columns past N of the last tile are
+// zeroed.
 hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, const VocabRow* rows,
-                                   void* gz, int64_t ldg, int col0, hipStream_t s);
+                                   void* gz, int64_t ldg, hipStream_t s);
 // g_z W of a piece of `cols` columns of a tiled gz (padded to 256 rows): split
 // over `splits` ranges of kchunk of them into slabs [splits][rows][d] float32, added
 // to what they hold with `add`; or with y (one range) g_x itself, bf16.
+// (W_last: needed where cols is not a multiple of 32.)
 hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, const void* W_last,
                                  int64_t rows, int d, int cols, int splits, int kchunk,
                                  float* slabs, bool add, void* y, hipStream_t s);
-// g_z^T x from tiled gz and xs, `padded` rows (a multiple of 32) of both: bf16 [cols][d].
+// g_z^T x from tiled gz and xs, `padded` rows (a multiple of 32) of both: bf16 [cols][d]
+// (what gz's columns past `cols` hold does not matter).
 hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
                                  int cols, void* g_W, hipStream_t s);
-// W_last of W [vocab][K]
-hipError_t launch_vocab_last_rows(const void* W, int64_t vocab, int K, void* W_last, hipStream_t s);
 // out [rows][N] = the sum of nsplit float32 slabs of it, N % 4 == 0.
 hipError_t launch_sum_slabs(DType t, const float* slabs, int nsplit, int64_t rows, int N, void* out,
                             hipStream_t s);
@@ -407,11 +410,19 @@ hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots,
                              int64_t rows, const float* z, float* loss, float* lse, hipStream_t s);
 // The rows' parts (none for those past `rows`), and with xs a copy of x
 // [padded][K], with `tiled` in the tiled layout, in which rows that take no
-// part, and those past `rows`, are zero.
+// part, and those past `rows`, are zero; with W_last that of W [l.vocab][K].
+struct VocabCopies {
+  const void* x = nullptr;
+  void* xs = nullptr;
+  bool tiled = false;
+  const void* W = nullptr;
+  void* W_last = nullptr;
+};
+hipError_t launch_vocab_last_rows(DType t, int64_t vocab, int K, const VocabCopies& c,
+                                  hipStream_t s);  // W_last alone
 hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t padded,
                              const float* g_loss, const float* g_lse, const float* lse,
-                             VocabRow* out, const void* x, int K, void* xs, bool tiled,
-                             hipStream_t s);
+                             VocabRow* out, int K, const VocabCopies& c, hipStream_t s);
 // A teacher's ids in the piece [col0, col0 + N): g_z there, from the student's
 // logits z at them.
 hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,

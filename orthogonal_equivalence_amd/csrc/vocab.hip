@@ -219,16 +219,28 @@ distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z
 }
 
 // Four rows a workgroup, one wave each: the row's part in the gradient, and
-// its copy of x.
+// its copy of x; then the copy of W's last rows.
+constexpr int kLastRows = kTileRows;
 template <typename T>
 __global__ void __launch_bounds__(NT)
 rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __restrict__ g_loss,
             const float* __restrict__ g_lse, const float* __restrict__ lse,
-            VocabRow* __restrict__ out, const T* __restrict__ x, int K, T* __restrict__ xs,
-            int tiled) {
+            VocabRow* __restrict__ out, int K, const VocabCopies c) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
-  if (row >= padded) return;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  if (row >= padded) {
+    const int64_t last = row - padded, from = l.vocab / kLastRows * kLastRows + last;
+    if (!c.W_last || last >= kLastRows) return;
+    const T* w = static_cast<const T*>(c.W) + from * K;
+    T* out_w = static_cast<T*>(c.W_last) + last * K;
+    for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
+      *reinterpret_cast<uint4*>(out_w + k) =
+          from < l.vocab ? *reinterpret_cast<const uint4*>(w + k) : none;
+    return;
+  }
+  const T* x = static_cast<const T*>(c.x);
+  T* xs = static_cast<T*>(c.xs);
   bool any = false;
   VocabRow r{0.0f, 0.0f, 0.0f, -1};
   if (row < rows) {
@@ -256,9 +268,8 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
   }
   if (lane == 0) out[row] = r;
   if (!xs) return;
-  const uint4 none = make_uint4(0, 0, 0, 0);
   for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
-    *reinterpret_cast<uint4*>(xs + (tiled ? tiled_offset(row, k, K) : row * K + k)) =
+    *reinterpret_cast<uint4*>(xs + (c.tiled ? tiled_offset(row, k, K) : row * K + k)) =
         any ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
 }
 
@@ -303,14 +314,6 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
   }
 }
 
-__global__ void __launch_bounds__(NT)
-last_rows_kernel(const bf16_t* __restrict__ W, int64_t vocab, int K, bf16_t* __restrict__ out) {
-  const int64_t row = vocab / kTileRows * kTileRows + blockIdx.x;
-  for (int k = threadIdx.x * 8; k < K; k += NT * 8)
-    *reinterpret_cast<uint4*>(out + (int64_t)blockIdx.x * K + k) =
-        row < vocab ? *reinterpret_cast<const uint4*>(W + row * K + k) : make_uint4(0, 0, 0, 0);
-}
-
 bool fits(int64_t blocks) { return blocks * NT <= kMaxWorkItems; }
 
 }  // namespace
@@ -349,19 +352,23 @@ hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots,
 
 hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t padded,
                              const float* g_loss, const float* g_lse, const float* lse,
-                             VocabRow* out, const void* x, int K, void* xs, bool tiled,
-                             hipStream_t s) {
-  const int64_t blocks = (padded + NWAVES - 1) / NWAVES;
+                             VocabRow* out, int K, const VocabCopies& c, hipStream_t s) {
+  const int64_t blocks = (padded + (c.W_last ? kLastRows : 0) + NWAVES - 1) / NWAVES;
   if (!fits(blocks)) return hipErrorInvalidValue;
   if (t == DType::BF16)
     hipLaunchKernelGGL(rows_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, padded,
-                       g_loss, g_lse, lse, out, static_cast<const bf16_t*>(x), K,
-                       static_cast<bf16_t*>(xs), (int)tiled);
+                       g_loss, g_lse, lse, out, K, c);
   else
     hipLaunchKernelGGL(rows_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, padded,
-                       g_loss, g_lse, lse, out, static_cast<const float*>(x), K,
-                       static_cast<float*>(xs), (int)tiled);
+                       g_loss, g_lse, lse, out, K, c);
   return hipGetLastError();
+}
+
+hipError_t launch_vocab_last_rows(DType t, int64_t vocab, int K, const VocabCopies& c,
+                                  hipStream_t s) {
+  VocabList l;
+  l.vocab = vocab;
+  return launch_vocab_rows(t, l, 0, 0, nullptr, nullptr, nullptr, nullptr, K, c, s);
 }
 
 hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
@@ -375,12 +382,6 @@ hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, c
   else
     hipLaunchKernelGGL(listed_grad_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
                        r, z, static_cast<float*>(gz), ldg, (int)tiled, col0, N);
-  return hipGetLastError();
-}
-
-hipError_t launch_vocab_last_rows(const void* W, int64_t vocab, int K, void* W_last, hipStream_t s) {
-  hipLaunchKernelGGL(last_rows_kernel, dim3(kTileRows), dim3(NT), 0, s,
-                     static_cast<const bf16_t*>(W), vocab, K, static_cast<bf16_t*>(W_last));
   return hipGetLastError();
 }
 

@@ -27,8 +27,10 @@ namespace {
 constexpr int64_t kMaxTokens = 1 << 24, kMaxWidth = 1 << 22, kMaxTop = 1024;
 constexpr int64_t kMaxValues = INT64_C(1) << 35;  // of x or W
 // What the logits' pieces may take in the workspace: the forward's partial
-// sums of a range of rows, the backward's gradient of a range of columns.
-constexpr int64_t kPartBytes = INT64_C(128) << 20, kPieceBytes = INT64_C(256) << 20;
+// sums of a range of rows, the backward's gradient of a range of columns (every
+// piece adds to g_x's float32 sums; 8192 x 131072 x 4096 in pieces of 128 MB 19300
+// us, 256 19150, 512 18880, 1024 19100).
+constexpr int64_t kPartBytes = INT64_C(128) << 20, kPieceBytes = INT64_C(512) << 20;
 constexpr int64_t kTile = 256;  // rows and columns of a piece, where there is more than one
 
 DType dtype_of(const poetx_vocab_desc* d) {
@@ -78,17 +80,48 @@ VocabList list_at(VocabList l, int64_t row) {
 }
 float scale_of(const poetx_vocab_desc* d) { return 1.44269504088896341f / d->temperature; }
 
-bool last_rows(const poetx_vocab_desc* d) { return d->vocab % kTile != 0; }
-size_t last_bytes(const poetx_vocab_desc* d) {
-  return last_rows(d) ? align_up((size_t)kTile * d->d * act_size(d->act)) : 0;
+// The time (us) of `tiles` 256 x 256 tiles of the products of vocab_dense.hip
+// over K: a round of the 256 CUs is 1.35 us for each 64 of K and 10 for its end
+// (measured: logits 52.7 and 93 a round at K = 2048 and 4096, with their gradient
+// 54.8 and 97.5, g_W 29, 101 and 194 at 1024, 4096 and 8192).
+float dense_cost(int64_t tiles, int64_t K) {
+  return 3.0f + (float)ceil_div(tiles, 256) * (10.0f + 1.35f * (float)K / 64);
+}
+
+// Columns of the logits of `rows` rows on the 256 x 256 tiles; the rest, if any, go
+// to the tile kernel: what a last round of the CUs that would be nearly empty
+// holds (777 x 50001 x 2048 forward 217 -> 174 us), or what is left of the
+// last tile where the copy of W's rows that it would take (`copy` us) costs more.
+struct Columns {
+  int64_t dense;
+  TilePlan tile;
+  float cost;
+};
+Columns split_columns(DType t, int64_t rows, int64_t cols, int64_t K, float copy) {
+  Columns best = {0, plan_tile_product(t, rows, cols, K, false, 1), 0.0f};
+  best.cost = best.tile.nsplit ? best.tile.cost : 1e30f;
+  if (t != DType::BF16 || !poetx::vocab_dense_supported(rows, cols, K)) return best;
+  const int64_t rt = ceil_div(rows, kTile), panels = cols / kTile;
+  const int64_t whole = rt * panels / 256 * 256 / rt;  // (in whole rounds)
+  for (int64_t n : {ceil_div(cols, kTile), panels, whole}) {
+    if (n < 1) continue;
+    Columns c = {std::min(n * kTile, cols), {}, dense_cost(rt * n, K)};
+    if (c.dense % kTile) c.cost += copy;
+    if (c.dense < cols) {
+      c.tile = plan_tile_product(t, rows, cols - c.dense, K, false, 1);
+      c.cost += c.tile.nsplit ? c.tile.cost : 1e30f;
+    }
+    if (c.cost < best.cost) best = c;
+  }
+  return best;
 }
 
 // The forward's partial sums: `rows` rows at a time, so that they stay within
 // kPartBytes.
 struct FwdPlan {
-  bool dense;  // the 256 x 256 tiles, else `tile`
-  TilePlan tile;
+  Columns cols;
   int64_t rows, slots;
+  bool copied;  // W_last
   size_t z, last, part, total;
 };
 FwdPlan plan_fwd(const poetx_vocab_desc* d) {
@@ -96,18 +129,18 @@ FwdPlan plan_fwd(const poetx_vocab_desc* d) {
   const DType t = dtype_of(d);
   p.rows = d->tokens;
   for (;;) {
-    p.tile = plan_tile_product(t, p.rows, d->vocab, d->d, false, 1);
-    const int64_t tiles = ceil_div(p.rows, kTile) * ceil_div(d->vocab, kTile);
-    p.dense = t == DType::BF16 && poetx::vocab_dense_supported(p.rows, d->vocab, d->d) &&
-              poetx::dense_rounds_cost(tiles, d->d) < p.tile.cost;
-    p.slots = p.dense         ? 2 * ceil_div(d->vocab, kTile)
-              : p.tile.nsplit ? poetx::vocab_tile_slots(t, p.tile, d->vocab)
-                              : INT32_MAX;
+    p.cols = split_columns(t, p.rows, d->vocab, d->d, 5.0f);
+    p.slots = 2 * ceil_div(p.cols.dense, kTile);
+    if (p.cols.dense < d->vocab)
+      p.slots += p.cols.tile.nsplit
+                     ? poetx::vocab_tile_slots(t, p.cols.tile, d->vocab - p.cols.dense)
+                     : INT32_MAX;
     if (p.slots * p.rows * 8 <= kPartBytes || p.rows <= kTile) break;
     p.rows = (p.rows / 2 + kTile - 1) / kTile * kTile;
   }
   p.last = d->top ? 0 : align_up((size_t)d->tokens * 4);  // (the targets' logits)
-  p.part = p.last + (p.dense ? last_bytes(d) : 0);
+  p.copied = p.cols.dense % kTile != 0;
+  p.part = p.last + (p.copied ? align_up((size_t)(kTile * d->d) * act_size(d->act)) : 0);
   p.total = p.part + align_up((size_t)(p.slots * p.rows * 8));
   return p;
 }
@@ -143,7 +176,7 @@ float split_gx(const poetx_vocab_desc* d, BwdPlan& p) {
     const int64_t chunk = ceil_div(ceil_div(p.piece, s), kTile) * kTile;
     const int64_t n = ceil_div(p.piece, chunk);
     // (a slab is written and read once more)
-    const float cost = poetx::dense_rounds_cost(tiles * n, chunk) +
+    const float cost = dense_cost(tiles * n, chunk) +
                        (n > 1 ? 3.0f + (float)(8 * n * d->tokens * d->d) / 5e6f : 0.0f);
     if (cost >= best) continue;
     best = cost;
@@ -160,9 +193,8 @@ BwdPlan plan_bwd(const poetx_vocab_desc* d) {
   if (t == DType::BF16 && poetx::vocab_dense_supported(d->tokens, d->vocab, d->d)) {
     p.padded = ceil_div(d->tokens, kTile) * kTile;
     set_pieces(d, p);
-    const int64_t rt = p.padded / kTile, vt = ceil_div(p.piece, kTile), dt = ceil_div(d->d, kTile);
-    const float dense = poetx::dense_rounds_cost(rt * vt, d->d) + split_gx(d, p) +
-                        poetx::dense_rounds_cost(vt * dt, d->tokens);
+    const float dense = split_columns(t, p.padded, p.piece, d->d, 1.0f).cost + split_gx(d, p) +
+                        dense_cost(ceil_div(p.piece, kTile) * ceil_div(d->d, kTile), d->tokens);
     const float tile = plan_tile_product(t, d->tokens, p.piece, d->d, false, 1).cost +
                        plan_tile_product(t, d->tokens, d->d, p.piece, false).cost +
                        plan_tile_product(t, p.piece, d->d, d->tokens, false).cost;
@@ -177,7 +209,7 @@ BwdPlan plan_bwd(const poetx_vocab_desc* d) {
   p.rows = off;
   off += align_up((size_t)p.padded * sizeof(VocabRow));
   p.last = off;
-  off += p.dense ? last_bytes(d) : 0;
+  if (p.dense && d->vocab % kTile) off += align_up((size_t)(kTile * d->d * es));
   p.xs = off;
   off += align_up((size_t)(p.padded * d->d * es));
   p.gz = off;
@@ -237,24 +269,31 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   float2* part = reinterpret_cast<float2*>(w + plan.part);
   // (targets' logits come out of the products)
   if (teacher) POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
-  const void* last = plan.dense && last_rows(d) ? w + plan.last : nullptr;
-  if (last) POETX_TRY(poetx::launch_vocab_last_rows(W, d->vocab, (int)d->d, w + plan.last, s));
+  if (plan.copied) {
+    poetx::VocabCopies c;
+    c.W = W;
+    c.W_last = w + plan.last;
+    POETX_TRY(poetx::launch_vocab_last_rows(t, d->vocab, (int)d->d, c, s));
+  }
   for (int64_t at = 0; at < d->tokens; at += plan.rows) {
     const int64_t rows = std::min(plan.rows, d->tokens - at);
     // (the dense tiles take 256 rows at least: the last range begins early, and
     // forms some rows' sums again)
-    const int64_t r = plan.dense ? std::min(at, std::max(d->tokens - kTile, INT64_C(0))) : at;
+    const int64_t r = plan.cols.dense ? std::min(at, std::max(d->tokens - kTile, INT64_C(0))) : at;
     VocabProduct p;
     p.x = static_cast<const char*>(x) + r * d->d * act_size(d->act);
     p.W = W;
-    p.M = (int)(at + rows - r); p.N = (int)d->vocab; p.K = (int)d->d;
+    p.M = (int)(at + rows - r); p.N = (int)plan.cols.dense; p.K = (int)d->d;
     p.scale = scale_of(d);
-    if (plan.dense)
-      POETX_TRY(poetx::launch_vocab_lse_dense(p, last, part, p.M, teacher ? nullptr : ids + r, z + r,
-                                              s));
-    else
-      POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.tile, p, part, p.M,
-                                             teacher ? nullptr : ids + r, z + r, s));
+    const int64_t* targets = teacher ? nullptr : ids + r;
+    if (p.N) POETX_TRY(poetx::launch_vocab_lse_dense(p, w + plan.last, part, p.M, targets, z + r, s));
+    if (plan.cols.dense < d->vocab) {
+      p.col0 = p.N;
+      p.W = static_cast<const char*>(W) + p.col0 * d->d * act_size(d->act);
+      p.N = (int)(d->vocab - p.col0);
+      POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.cols.tile, p, part + p.col0 / 128 * (int64_t)p.M,
+                                             p.M, targets, z + r, s));
+    }
     POETX_TRY(poetx::launch_vocab_loss(part, p.M, plan.slots, list_at(list, r), p.M,
                                        z + r * list.top, loss + r, lse + r, s));
   }
@@ -291,25 +330,39 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
   void* xs = g_W || plan.dense ? w + plan.xs : nullptr;
   char* gz = w + plan.gz;
   float* acc = reinterpret_cast<float*>(w + plan.acc);
-  POETX_TRY(poetx::launch_vocab_rows(t, list, d->tokens, plan.padded, g_loss, g_lse, lse, rows, x,
-                                     (int)d->d, xs, plan.dense, s));
-  const bool ragged = plan.dense && last_rows(d);
-  if (ragged) POETX_TRY(poetx::launch_vocab_last_rows(W, d->vocab, (int)d->d, w + plan.last, s));
+  const bool ragged = plan.dense && d->vocab % kTile != 0;
+  poetx::VocabCopies copies;
+  copies.x = x;
+  copies.xs = xs;
+  copies.tiled = plan.dense;
+  copies.W = W;
+  copies.W_last = ragged ? w + plan.last : nullptr;
+  POETX_TRY(poetx::launch_vocab_rows(t, list, d->tokens, plan.padded, g_loss, g_lse, lse, rows,
+                                     (int)d->d, copies, s));
   for (int64_t c = 0; c < d->vocab; c += plan.piece) {
     const int64_t cols = std::min(plan.piece, d->vocab - c);
     const char* Wc = static_cast<const char*>(W) + c * d->d * es;
-    const void* last = ragged && c + cols == d->vocab ? w + plan.last : nullptr;
+    const void* last = ragged && c + cols == d->vocab ? copies.W_last : nullptr;
     char* gWc = g_W ? static_cast<char*>(g_W) + c * d->d * es : nullptr;
+    // the gradient of the piece's logits
+    Columns split = {0, {}, 0.0f};
+    if (plan.dense) split = split_columns(t, plan.padded, cols, d->d, 1.0f);
     VocabProduct p;
-    p.x = plan.dense ? xs : x;
+    p.x = xs;
     p.W = Wc;
-    p.M = (int)(plan.dense ? plan.padded : d->tokens); p.N = (int)cols; p.K = (int)d->d;
+    p.M = (int)plan.padded; p.N = (int)split.dense; p.K = (int)d->d;
+    p.col0 = (int)c;
     p.scale = scale_of(d);
-    if (plan.dense)
-      POETX_TRY(poetx::launch_vocab_grad_dense(p, last, rows, gz, plan.ldg, (int)c, s));
-    else
-      POETX_TRY(poetx::launch_vocab_grad_tile(t, plan_tile_product(t, p.M, cols, d->d, false, 1), p,
-                                              rows, gz, plan.ldg, (int)c, s));
+    if (p.N) POETX_TRY(poetx::launch_vocab_grad_dense(p, last, rows, gz, plan.ldg, s));
+    if (split.dense < cols) {
+      p.x = x;
+      p.W = Wc + split.dense * d->d * es;
+      p.M = (int)d->tokens; p.N = (int)(cols - split.dense);
+      p.col0 = (int)(c + split.dense);
+      POETX_TRY(poetx::launch_vocab_grad_tile(
+          t, plan_tile_product(t, p.M, p.N, d->d, false, 1), p, rows,
+          gz + split.dense * kTile * es, plan.ldg, plan.dense, s));
+    }
     if (teacher)
       POETX_TRY(poetx::launch_vocab_listed_grad(t, list, d->tokens, rows, z, gz, plan.ldg,
                                                 plan.dense, (int)c, (int)cols, s));

@@ -22,6 +22,7 @@ struct LseEnd {
   float scale;
   const int64_t* targets;
   float* z;
+  int col0;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int, int wave_col, int lane) const {
@@ -39,7 +40,7 @@ struct LseEnd {
       if (lane < 16 && m < p.M) out[m] = ms;
       if (!targets) continue;
       // the row's target, where it is among the wave's columns
-      const int64_t at = m < p.M ? targets[m] - n_at : -1;
+      const int64_t at = m < p.M ? targets[m] - (col0 + n_at) : -1;
       if (!__any(at >= 0 && at < 16 * FN)) continue;
       const int own = at >= 0 && at < 16 * FN ? (int)at - 4 * (lane >> 4) : -1;
 #pragma unroll
@@ -55,25 +56,27 @@ struct GradEnd {
   const VocabRow* rows;
   void* gz;
   int64_t ldg;
-  int col0;
+  int tiled, col0;
   float scale;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int, int, int lane) const {
+    // (the tiled layout's reductions run over whole K tiles of 32 rows)
+    const int m_end = tiled ? (p.M + 31) / 32 * 32 : p.M, n_end = (p.N + 255) / 256 * 256;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = m_at + 16 * i + (lane & 15);
-      if (m >= p.M) continue;
-      const VocabRow r = rows[m];
+      if (m >= m_end) continue;
+      const VocabRow r = m < p.M ? rows[m] : VocabRow{0.0f, 0.0f, 0.0f, -1};
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int n = n_at + 16 * j + 4 * (lane >> 4);
-        if (n >= (p.N + 7) / 8 * 8) continue;
+        if (n >= n_end) continue;
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           v[e] = n + e < p.N ? logit_gradient(r, acc[i][j][e], scale, col0 + n + e) : 0.0f;
-        Quad<T>::store(static_cast<T*>(gz) + (int64_t)m * ldg + n, v);
+        Quad<T>::store(static_cast<T*>(gz) + (tiled ? tiled_offset(m, n, ldg) : m * ldg + n), v);
       }
     }
   }
@@ -135,13 +138,13 @@ int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N) {
 
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
                                  int64_t part_ld, const int64_t* targets, float* z, hipStream_t s) {
-  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z}, s);
+  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z, p.col0}, s);
 }
 
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
-                                  const VocabRow* rows, void* gz, int64_t ldg, int col0,
+                                  const VocabRow* rows, void* gz, int64_t ldg, bool tiled,
                                   hipStream_t s) {
-  return launch_end(t, plan, p, GradEnd{rows, gz, ldg, col0, p.scale}, s);
+  return launch_end(t, plan, p, GradEnd{rows, gz, ldg, (int)tiled, p.col0, p.scale}, s);
 }
 
 }  // namespace poetx

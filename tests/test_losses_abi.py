@@ -149,7 +149,7 @@ def test_workspaces_stay_bounded():
             k = desc(tokens=tokens, d=d, vocab=vocab, act=act)
             fwd, bwd = P.poetx_vocab_fwd_workspace_size(k), P.poetx_vocab_bwd_workspace_size(k)
             assert 0 < fwd <= (130 << 20) + 4 * tokens + 256 * vocab // 16 * 8
-            piece = max(260 << 20, tokens * 256 * es)
+            piece = max(516 << 20, tokens * 256 * es)
             assert 0 < bwd <= piece + tokens * (d * (es + 4) + 20) + (256 << 20), (tokens, act)
 
 
