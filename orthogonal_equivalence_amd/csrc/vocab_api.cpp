@@ -154,10 +154,25 @@ struct BwdPlan {
   size_t rows, last, xs, gz, acc, part, total;
   bool summed() const { return pieces > 1 || splits > 1; }
 };
-size_t part_floats(const poetx_vocab_desc* d, int64_t n) {
+// g_z's two products of a piece of n columns on the tile kernel, each by itself
+// or (few launches where they are what costs) in one
+struct TileProducts {
+  TilePlan gx, gw;
+  poetx::TilePairPlan pair;
+  bool paired;
+  size_t part_floats() const {
+    const size_t alone = std::max(gx.part_floats, gw.part_floats);
+    return paired ? std::max(alone, pair.gx.part_floats + pair.gw.part_floats) : alone;
+  }
+};
+TileProducts tile_products(const poetx_vocab_desc* d, int64_t n) {
   const DType t = dtype_of(d);
-  return std::max(plan_tile_product(t, d->tokens, d->d, n, false).part_floats,
-                  plan_tile_product(t, n, d->d, d->tokens, false).part_floats);
+  TileProducts p;
+  p.gx = plan_tile_product(t, d->tokens, d->d, n, false);
+  p.gw = plan_tile_product(t, n, d->d, d->tokens, false);
+  p.pair = plan_tile_pair(t, d->tokens, d->d, n);
+  p.paired = p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
+  return p;
 }
 void set_pieces(const poetx_vocab_desc* d, BwdPlan& p) {
   const int64_t es = (int64_t)act_size(d->act);
@@ -218,8 +233,8 @@ BwdPlan plan_bwd(const poetx_vocab_desc* d) {
   if (p.summed()) off += align_up((size_t)d->tokens * d->d * 4 * p.splits);
   p.part = off;
   if (!p.dense) {
-    const size_t rest = part_floats(d, d->vocab - (p.pieces - 1) * p.piece);
-    off += align_up(std::max(part_floats(d, p.piece), rest) * 4);
+    const size_t rest = tile_products(d, d->vocab - (p.pieces - 1) * p.piece).part_floats();
+    off += align_up(std::max(tile_products(d, p.piece).part_floats(), rest) * 4);
   }
   p.total = off;
   return p;
@@ -377,30 +392,31 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
                                                (int)d->d, (int)cols, gWc, s));
       continue;
     }
-    TileProduct g;
-    g.A = gz; g.lda = plan.ldg;
-    g.ldb = d->d;
-    g.N = (int)d->d;
-    g.part = reinterpret_cast<float*>(w + plan.part);
-    g.ep.ld = d->d;
-    if (g_x) {  // g_x += g_z W: B(n, k) = W[k][n]
-      TileProduct q = g;
-      q.B = Wc;
-      q.M = (int)d->tokens; q.K = (int)cols;
-      q.ep.y = g_x;
-      q.ep.add = c > 0 ? acc : nullptr;
-      q.ep.sum = c + cols < d->vocab ? acc : nullptr;
-      POETX_TRY(poetx::launch_tile_product(t, plan_tile_product(t, q.M, q.N, q.K, false), q, true,
-                                           false, s));
+    const TileProducts tiles = tile_products(d, cols);
+    float* part = reinterpret_cast<float*>(w + plan.part);
+    TileProduct qx, qw;
+    // g_x += g_z W: B(n, k) = W[k][n]
+    qx.A = gz; qx.lda = plan.ldg;
+    qx.B = Wc; qx.ldb = d->d;
+    qx.M = (int)d->tokens; qx.N = (int)d->d; qx.K = (int)cols;
+    qx.part = part;
+    qx.ep.y = g_x;
+    qx.ep.add = c > 0 ? acc : nullptr;
+    qx.ep.sum = c + cols < d->vocab ? acc : nullptr;
+    qx.ep.ld = d->d;
+    // g_W = g_z^T x: A(m, k) = g_z[k][m], B(n, k) = xs[k][n]
+    qw.A = gz; qw.lda = plan.ldg;
+    qw.B = xs; qw.ldb = d->d;
+    qw.M = (int)cols; qw.N = (int)d->d; qw.K = (int)d->tokens;
+    qw.part = g_x && tiles.paired ? part + tiles.pair.gx.part_floats : part;
+    qw.ep.y = gWc;
+    qw.ep.ld = d->d;
+    if (g_x && g_W && tiles.paired) {
+      POETX_TRY(poetx::launch_tile_pair(t, tiles.pair, qx, qw, s));
+      continue;
     }
-    if (g_W) {  // g_W = g_z^T x: A(m, k) = g_z[k][m], B(n, k) = xs[k][n]
-      TileProduct q = g;
-      q.B = xs;
-      q.M = (int)cols; q.K = (int)d->tokens;
-      q.ep.y = gWc;
-      POETX_TRY(poetx::launch_tile_product(t, plan_tile_product(t, q.M, q.N, q.K, false), q, false,
-                                           false, s));
-    }
+    if (g_x) POETX_TRY(poetx::launch_tile_product(t, tiles.gx, qx, true, false, s));
+    if (g_W) POETX_TRY(poetx::launch_tile_product(t, tiles.gw, qw, false, false, s));
   }
   if (plan.dense && g_x && plan.summed())
     POETX_TRY(poetx::launch_sum_slabs(t, acc, plan.splits, d->tokens, (int)d->d, g_x, s));

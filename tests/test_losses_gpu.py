@@ -103,11 +103,14 @@ def test_cross_entropy(tokens, d, vocab, dyadic, dtype):
         within("g_x", g_x, ref["g_x"], tol_x)
         within("g_W", g_W, ref["g_W"], tol_W)
         assert bool((g_x[t < 0] == 0).all())
+        # (alone, a product may be cut into other partial sums than beside the other)
         only, none = L.cross_entropy_backward(g, x, W, t, lse, g_lse=g_lse)
-        assert none is None and torch.equal(only, g_x)
+        assert none is None
+        within("g_x alone", only, ref["g_x"], tol_x)
         none, only = L.cross_entropy_backward(g, x, W, t, lse, g_lse=g_lse, need_g_x=False,
                                               need_g_W=True)
-        assert none is None and torch.equal(only, g_W)
+        assert none is None
+        within("g_W alone", only, ref["g_W"], tol_W)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -143,7 +146,8 @@ def test_distill(tokens, d, vocab, top, temperature, dyadic, kind, dtype):
     within("g_W", g_W, ref["g_W"], tol_W)
     assert bool((g_x[~part] == 0).all()) and bool((loss[~part] == 0).all())
     only, none = L.distill_backward(g, x, W, ids, teacher, lse, z, temperature)
-    assert none is None and torch.equal(only, g_x)
+    assert none is None
+    within("g_x alone", only, ref["g_x"], tol_x)
 
 
 def counted(tokens, d, vocab, seed):
