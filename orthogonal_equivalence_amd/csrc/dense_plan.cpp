@@ -50,7 +50,10 @@ int64_t tiles_of(const Shape& h, int64_t M, int64_t N) {
   return ((M + h.bm - 1) / h.bm) * ((N + h.bn - 1) / h.bn);
 }
 constexpr int kCus = 256;
-constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+// (above kFewSplits: only where a caller allows them, for long reductions
+// into small outputs)
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+static_assert(kSplits[7] == kFewSplits, "the default of max_split");
 constexpr int kMinSteps = 4;               // of a split's part
 constexpr float kInt8Step = 1.4f;          // a step with B's codes widened
 constexpr float kLaunch = 2.1f;            // us of a launch
@@ -113,7 +116,7 @@ TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8
 // The two products of a backward in one launch: for each shape and pair of
 // splits, the steps of both over the chip, or the longer one's chain if that
 // is more, by the same constants.
-TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out) {
+TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out, int max_split) {
   const bool bf16 = t == DType::BF16;
   const Shape* shapes = bf16 ? kBf16Shapes : kF32Shapes;
   const int nshapes = (int)((bf16 ? sizeof(kBf16Shapes) : sizeof(kF32Shapes)) / sizeof(Shape));
@@ -137,6 +140,7 @@ TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out
       const int64_t tiles = tiles_of(h, M[q], N);
       const int steps = (int)((K[q] + bk - 1) / bk);
       for (int want : kSplits) {
+        if (want > max_split) break;
         const int per = (steps + want - 1) / want, split = (steps + per - 1) / per;
         if (split != want || (split > 1 && (per < kMinSteps || tiles >= (int64_t)slots))) continue;
         const float extra =

@@ -268,9 +268,11 @@ struct TilePlan {
   size_t part_floats;
   float cost;  // estimate in us, for comparison with another kernel's
 };
-// (max_split 1: for a product whose epilogue needs the whole sum in its kernel)
+// max_split: 1 for a product whose epilogue needs the whole sum in its kernel,
+// more than kFewSplits for a long reduction into a small output.
+constexpr int kFewSplits = 16, kManySplits = 64;
 TilePlan plan_tile_product(DType t, int64_t M, int64_t N, int64_t K, bool b_int8,
-                           int max_split = 16);
+                           int max_split = kFewSplits);
 hipError_t launch_tile_product(DType t, const TilePlan& plan, TileProduct p, bool a_kmajor,
                                bool b_kmajor, hipStream_t s);
 // A backward's g_x = g_u W (A K-major) and g_W = g_u^T x (A M-major), both
@@ -279,7 +281,8 @@ struct TilePairPlan {
   TilePlan gx, gw;
   float cost;
 };
-TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out);
+TilePairPlan plan_tile_pair(DType t, int64_t tokens, int64_t d_in, int64_t d_out,
+                            int max_split = kFewSplits);
 hipError_t launch_tile_pair(DType t, const TilePairPlan& plan, TileProduct gx, TileProduct gw,
                             hipStream_t s);
 

@@ -307,6 +307,7 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
     const int id = ids[wave][k];
     if (id < col0 || id >= col0 + N) continue;
     float sum = 0.0f;
+#pragma unroll 8
     for (int q = 0; q < l.top; ++q) sum += ids[wave][q] == id ? p[wave][q] : 0.0f;
     const float e = __builtin_amdgcn_exp2f(fmaf(z[row * l.top + k], rt, -own.lse2));
     const int64_t at = tiled ? tiled_offset(row, id - col0, ldg) : row * ldg + (id - col0);

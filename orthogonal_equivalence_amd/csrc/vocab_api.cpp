@@ -168,9 +168,9 @@ struct TileProducts {
 TileProducts tile_products(const poetx_vocab_desc* d, int64_t n) {
   const DType t = dtype_of(d);
   TileProducts p;
-  p.gx = plan_tile_product(t, d->tokens, d->d, n, false);
+  p.gx = plan_tile_product(t, d->tokens, d->d, n, false, poetx::kManySplits);
   p.gw = plan_tile_product(t, n, d->d, d->tokens, false);
-  p.pair = plan_tile_pair(t, d->tokens, d->d, n);
+  p.pair = plan_tile_pair(t, d->tokens, d->d, n, poetx::kManySplits);
   p.paired = p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
   return p;
 }
@@ -187,7 +187,7 @@ void set_pieces(const poetx_vocab_desc* d, BwdPlan& p) {
 float split_gx(const poetx_vocab_desc* d, BwdPlan& p) {
   const int64_t tiles = p.padded / kTile * ceil_div(d->d, kTile);
   float best = 1e30f;
-  for (int s = 1; s <= 16; ++s) {
+  for (int s = 1; s <= 128; s += s < 16 ? 1 : 8) {
     const int64_t chunk = ceil_div(ceil_div(p.piece, s), kTile) * kTile;
     const int64_t n = ceil_div(p.piece, chunk);
     // (a slab is written and read once more)
@@ -211,7 +211,7 @@ BwdPlan plan_bwd(const poetx_vocab_desc* d) {
     const float dense = split_columns(t, p.padded, p.piece, d->d, 1.0f).cost + split_gx(d, p) +
                         dense_cost(ceil_div(p.piece, kTile) * ceil_div(d->d, kTile), d->tokens);
     const float tile = plan_tile_product(t, d->tokens, p.piece, d->d, false, 1).cost +
-                       plan_tile_product(t, d->tokens, d->d, p.piece, false).cost +
+                       plan_tile_product(t, d->tokens, d->d, p.piece, false, poetx::kManySplits).cost +
                        plan_tile_product(t, p.piece, d->d, d->tokens, false).cost;
     p.dense = dense < tile;
   }
