@@ -44,6 +44,18 @@ template <int NV> __device__ __forceinline__ float2 row_max_sum(const float (&v)
   return make_float2(m, quad_sum((s[0] + s[1]) + (s[2] + s[3])));
 }
 
+// Two 16 x 16 fragments that are neighbours along the columns (lane l: row l % 16,
+// columns 4 (l / 16) .. + 3 of each), four values packed, as this lane's 16 bytes: columns
+// pair_column() .. + 7 of the pair's 32.
+__device__ __forceinline__ uint4 swap_pair(uint2 a, uint2 b) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
+}
+__device__ __forceinline__ int pair_column(int ln) {
+  return 16 * ((ln >> 4) & 1) + 8 * (ln >> 5);
+}
+
 // g_z at a logit z of the vocabulary's column `col` (VocabRow)
 __device__ __forceinline__ float logit_gradient(const VocabRow& r, float z, float c, int col) {
   const float q = r.a == 0.0f ? 0.0f : r.a * __builtin_amdgcn_exp2f(fmaf(z, c, -r.lse2));

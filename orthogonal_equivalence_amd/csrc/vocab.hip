@@ -218,6 +218,27 @@ distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z
   }
 }
 
+// Whether the row takes part (one wave; *bad: an id past the vocabulary)
+__device__ __forceinline__ bool row_takes_part(const VocabList& l, int64_t row, int lane, bool* bad) {
+  bool any = false, out = false;
+  if (l.teacher) {
+    for (int k = lane; k < l.top; k += 64) {
+      const int64_t id = l.ids[row * l.top + k];
+      if (!takes_part(id, teacher_logit(l, row * l.top + k))) continue;
+      any = true;
+      out |= id >= l.vocab;
+    }
+    any = __any(any);
+    out = __any(out);
+  } else {
+    const int64_t id = l.ids[row];
+    any = id >= 0;
+    out = id >= l.vocab;
+  }
+  *bad = out;
+  return any;
+}
+
 // Four rows a workgroup, one wave each: the row's part in the gradient, and
 // its copy of x; then the copy of W's last rows.
 constexpr int kLastRows = kTileRows;
@@ -239,38 +260,54 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
           from < l.vocab ? *reinterpret_cast<const uint4*>(w + k) : none;
     return;
   }
-  const T* x = static_cast<const T*>(c.x);
-  T* xs = static_cast<T*>(c.xs);
   bool any = false;
   VocabRow r{0.0f, 0.0f, 0.0f, -1};
   if (row < rows) {
+    bool bad;
+    any = row_takes_part(l, row, lane, &bad);
     r.lse2 = lse[row] * kLog2e;
-    bool bad = false;
     if (l.teacher) {
-      for (int k = lane; k < l.top; k += 64) {
-        const int64_t id = l.ids[row * l.top + k];
-        if (!takes_part(id, teacher_logit(l, row * l.top + k))) continue;
-        any = true;
-        bad |= id >= l.vocab;
-      }
-      any = __any(any);
-      bad = __any(bad);
       r.a = any ? g_loss[row] * l.temperature : 0.0f;
     } else {
-      const int64_t id = l.ids[row];
-      any = id >= 0;
-      bad = id >= l.vocab;
       r.b = any ? g_loss[row] : 0.0f;
       r.a = any && g_lse ? r.b + g_lse[row] : r.b;
-      r.target = any && !bad ? (int)id : -1;
+      r.target = any && !bad ? (int)l.ids[row] : -1;
     }
     if (bad) r.a = NAN;
   }
   if (lane == 0) out[row] = r;
+  T* xs = static_cast<T*>(c.xs);
   if (!xs) return;
+  const T* x = static_cast<const T*>(c.x);
   for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
     *reinterpret_cast<uint4*>(xs + (c.tiled ? tiled_offset(row, k, K) : row * K + k)) =
         any ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
+}
+
+// x's copy with the rows innermost, for few rows (after their parts): a workgroup
+// takes 64 columns, reads them row by row into LDS and writes them turned.
+template <typename T>
+__global__ void __launch_bounds__(NT)
+turned_copy_kernel(const VocabRow* __restrict__ parts, int rows, int K, const VocabCopies c) {
+  constexpr int E = Vec<T>::E;
+  __shared__ T tile[kFewTokens][64 + E];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k0 = blockIdx.x * 64;
+  const T* x = static_cast<const T*>(c.x);
+  for (int row = wave; row < c.xt_rows; row += NWAVES) {
+    // (a row whose gradient is zero may as well be left out)
+    const bool any = row < rows && (parts[row].a != 0.0f || parts[row].b != 0.0f);
+    tile[row][lane] = any && k0 + lane < K ? x[(int64_t)row * K + k0 + lane] : T{};
+  }
+  __syncthreads();
+  const int n = min(64, K - k0) * c.xt_rows / E;  // 16-byte pieces
+  T* out = static_cast<T*>(c.xt) + (int64_t)k0 * c.xt_rows;
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const int k = i * E / c.xt_rows, row = i * E % c.xt_rows;
+    union { T e[E]; uint4 v; } u;
+#pragma unroll
+    for (int e = 0; e < E; ++e) u.e[e] = tile[row + e][k];
+    reinterpret_cast<uint4*>(out)[i] = u.v;
+  }
 }
 
 // One wave a row: where the row's id j lies in the piece,
@@ -362,6 +399,18 @@ hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t 
   else
     hipLaunchKernelGGL(rows_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows, padded,
                        g_loss, g_lse, lse, out, K, c);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (c.xt) {
+    if (rows > kFewTokens || c.xt_rows > kFewTokens || c.xt_rows < rows ||
+        c.xt_rows != few_padded(t, (int)rows))
+      return hipErrorInvalidValue;
+    const dim3 grid((unsigned)((K + 63) / 64));
+    if (t == DType::BF16)
+      hipLaunchKernelGGL(turned_copy_kernel<bf16_t>, grid, dim3(NT), 0, s, out, (int)rows, K, c);
+    else
+      hipLaunchKernelGGL(turned_copy_kernel<float>, grid, dim3(NT), 0, s, out, (int)rows, K, c);
+  }
   return hipGetLastError();
 }
 

@@ -160,6 +160,7 @@ struct TileProducts {
   TilePlan gx, gw;
   poetx::TilePairPlan pair;
   bool paired;
+  bool few;  // g_W on its own kernel for few tokens
   size_t part_floats() const {
     const size_t alone = std::max(gx.part_floats, gw.part_floats);
     return paired ? std::max(alone, pair.gx.part_floats + pair.gw.part_floats) : alone;
@@ -171,7 +172,11 @@ TileProducts tile_products(const poetx_vocab_desc* d, int64_t n) {
   p.gx = plan_tile_product(t, d->tokens, d->d, n, false, poetx::kManySplits);
   p.gw = plan_tile_product(t, n, d->d, d->tokens, false);
   p.pair = plan_tile_pair(t, d->tokens, d->d, n, poetx::kManySplits);
-  p.paired = p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
+  // a launch for the turned copy of x and one that stores g_W
+  const float few = 6.0f + (float)(n * d->d * (int64_t)act_size(d->act)) / 4.0e6f;
+  p.few = d->tokens <= poetx::kFewTokens &&
+          few < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
+  p.paired = !p.few && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
   return p;
 }
 void set_pieces(const poetx_vocab_desc* d, BwdPlan& p) {
@@ -226,7 +231,10 @@ BwdPlan plan_bwd(const poetx_vocab_desc* d) {
   p.last = off;
   if (p.dense && d->vocab % kTile) off += align_up((size_t)(kTile * d->d * es));
   p.xs = off;
-  off += align_up((size_t)(p.padded * d->d * es));
+  const int64_t copied = p.dense || d->tokens > poetx::kFewTokens
+                             ? p.padded
+                             : poetx::few_padded(t, (int)d->tokens);
+  off += align_up((size_t)(copied * d->d * es));
   p.gz = off;
   off += align_up((size_t)(p.padded * p.ldg * es));
   p.acc = off;
@@ -352,6 +360,11 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
   copies.tiled = plan.dense;
   copies.W = W;
   copies.W_last = ragged ? w + plan.last : nullptr;
+  if (g_W && !plan.dense && tile_products(d, std::min(plan.piece, d->vocab)).few) {
+    copies.xs = nullptr;
+    copies.xt = w + plan.xs;
+    copies.xt_rows = poetx::few_padded(t, (int)d->tokens);
+  }
   POETX_TRY(poetx::launch_vocab_rows(t, list, d->tokens, plan.padded, g_loss, g_lse, lse, rows,
                                      (int)d->d, copies, s));
   for (int64_t c = 0; c < d->vocab; c += plan.piece) {
@@ -411,12 +424,17 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     qw.part = g_x && tiles.paired ? part + tiles.pair.gx.part_floats : part;
     qw.ep.y = gWc;
     qw.ep.ld = d->d;
-    if (g_x && g_W && tiles.paired) {
+    if (g_x && g_W && tiles.paired && !copies.xt) {
       POETX_TRY(poetx::launch_tile_pair(t, tiles.pair, qx, qw, s));
       continue;
     }
     if (g_x) POETX_TRY(poetx::launch_tile_product(t, tiles.gx, qx, true, false, s));
-    if (g_W) POETX_TRY(poetx::launch_tile_product(t, tiles.gw, qw, false, false, s));
+    // (after g_x, which finds W in the caches)
+    if (g_W && copies.xt)
+      POETX_TRY(poetx::launch_few_gw(t, gz, plan.ldg, copies.xt, (int)d->tokens, (int)cols,
+                                     (int)d->d, gWc, s));
+    else if (g_W)
+      POETX_TRY(poetx::launch_tile_product(t, tiles.gw, qw, false, false, s));
   }
   if (plan.dense && g_x && plan.summed())
     POETX_TRY(poetx::launch_sum_slabs(t, acc, plan.splits, d->tokens, (int)d->d, g_x, s));

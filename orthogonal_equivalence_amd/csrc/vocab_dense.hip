@@ -18,23 +18,12 @@
 namespace poetx {
 namespace {
 
-// Fragments (i, 2 q) and (i, 2 q + 1), packed, as this lane's 16 bytes: columns
-// pair_column() .. + 7 of the pair's 32 in row 16 i + l % 16.
-__device__ __forceinline__ uint4 swap_pair(uint2 a, uint2 b) {
-  const auto lo = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
-  const auto hi = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
-  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
-}
 // the panel of W's rows n0 .. n0 + 255 less n0 rows: of the vocabulary, or of the
 // zero-padded copy of its last rows
 __device__ __forceinline__ const bf16_t* panel(const bf16_t* W, const bf16_t* W_last, int n0, int N,
                                                int K) {
   return n0 + BN <= N ? W : W_last - (int64_t)n0 * K;
 }
-__device__ __forceinline__ int pair_column(int ln) {
-  return 16 * ((ln >> 4) & 1) + 8 * (ln >> 5);
-}
-
 // The persistent loop: products, then the next tile's first copies, then
 // end(m0, n0, q, nt) of this one, for the tiles of nq products side by side (their
 // panels through set(q, m0, n0)). end returns whether it has issued at least

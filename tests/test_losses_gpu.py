@@ -73,7 +73,8 @@ def magnitudes(ref, g_loss, a, temperature, part, ids, p, lse, dyadic, x, W):
 SIZES = [  # tokens, d, vocab
     (1, 8, 1), (1, 64, 7), (1, 2048, 5000), (2, 72, 33), (3, 256, 256), (16, 128, 1000),
     (17, 200, 257), (64, 256, 1000), (100, 264, 513), (255, 64, 2049), (256, 256, 512),
-    (300, 512, 4099), (777, 96, 1031),
+    (300, 512, 4099), (777, 96, 1031), (20, 136, 30011), (40, 256, 20000), (64, 1032, 9000),
+    (7, 40, 100003),
 ]
 
 
@@ -170,7 +171,8 @@ def counted(tokens, d, vocab, seed):
 @pytest.mark.parametrize("tokens,d,vocab", [
     (1, 64, 4096), (31, 128, 30000), (300, 256, 5003), (512, 512, 2048), (777, 256, 50001),
     (1000, 320, 20483), (2048, 64, 131072), (2304, 256, 131072), (4100, 96, 65537),
-    (9000, 64, 131072), (515, 1064, 3001),
+    (9000, 64, 131072), (515, 1064, 3001), (64, 512, 40001), (5, 4096, 9001), (40, 72, 131072),
+    (33, 2056, 20001),
 ])
 def test_counted_operands(tokens, d, vocab):
     """Every element of loss, lse, g_x and g_W of large and ragged sizes (several
