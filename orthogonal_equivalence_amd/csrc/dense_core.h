@@ -405,6 +405,40 @@ struct Dense {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // the accumulator of fragment (f / 8, f % 8), f wave-uniform (reads by name:
+  // the compiler would otherwise copy all accumulators to VGPRs first)
+  __device__ __forceinline__ floatx4 pick(int f) {
+    float a = 0.0f, b = 0.0f, c = 0.0f, e = 0.0f;
+#define POETX_PICK(F)                                                                   \
+  case F:                                                                               \
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(a) : "a"(acc[(F) / 8][(F) % 8][0])); \
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(b) : "a"(acc[(F) / 8][(F) % 8][1])); \
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(c) : "a"(acc[(F) / 8][(F) % 8][2])); \
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(e) : "a"(acc[(F) / 8][(F) % 8][3])); \
+    break;
+    switch (f) {
+      POETX_PICK(0) POETX_PICK(1) POETX_PICK(2) POETX_PICK(3)
+      POETX_PICK(4) POETX_PICK(5) POETX_PICK(6) POETX_PICK(7)
+      POETX_PICK(8) POETX_PICK(9) POETX_PICK(10) POETX_PICK(11)
+      POETX_PICK(12) POETX_PICK(13) POETX_PICK(14) POETX_PICK(15)
+      POETX_PICK(16) POETX_PICK(17) POETX_PICK(18) POETX_PICK(19)
+      POETX_PICK(20) POETX_PICK(21) POETX_PICK(22) POETX_PICK(23)
+      POETX_PICK(24) POETX_PICK(25) POETX_PICK(26) POETX_PICK(27)
+      POETX_PICK(28) POETX_PICK(29) POETX_PICK(30) POETX_PICK(31)
+      POETX_PICK(32) POETX_PICK(33) POETX_PICK(34) POETX_PICK(35)
+      POETX_PICK(36) POETX_PICK(37) POETX_PICK(38) POETX_PICK(39)
+      POETX_PICK(40) POETX_PICK(41) POETX_PICK(42) POETX_PICK(43)
+      POETX_PICK(44) POETX_PICK(45) POETX_PICK(46) POETX_PICK(47)
+      POETX_PICK(48) POETX_PICK(49) POETX_PICK(50) POETX_PICK(51)
+      POETX_PICK(52) POETX_PICK(53) POETX_PICK(54) POETX_PICK(55)
+      POETX_PICK(56) POETX_PICK(57) POETX_PICK(58) POETX_PICK(59)
+      POETX_PICK(60) POETX_PICK(61) POETX_PICK(62) POETX_PICK(63)
+      default: break;
+    }
+#undef POETX_PICK
+    return floatx4{a, b, c, e};
+  }
+
   // accumulators -> bf16 staging tile (the whole ring) -> 16-byte stores of
   // whole 512-byte row segments; the ring is free again on return
   __device__ __forceinline__ void epilogue(bf16_t* __restrict__ C, int64_t ldc, int m0, int n0) {

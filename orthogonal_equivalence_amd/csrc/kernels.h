@@ -332,6 +332,15 @@ int act_grad_splits(int64_t rows);
 hipError_t launch_act_grad(DType t, const ActGrad& a, hipStream_t s);
 
 // ---- losses over a vocabulary whose logits are not kept ----
+// The listed ids of a row: targets (top = 1) or a teacher's [rows][top].
+struct VocabList {
+  const int64_t* ids = nullptr;
+  const void* teacher = nullptr;  // logits [rows][top] of type `type`; null: targets
+  DType type = DType::F32;
+  int top = 1;
+  int64_t vocab = 0;
+  float temperature = 1.0f;
+};
 // Logits of a piece of the vocabulary, z = x W^T, x [M][K], W [N][K] (the
 // piece's rows), both contiguous, K a multiple of 16 bytes, any M and N.
 struct VocabProduct {
@@ -348,13 +357,42 @@ struct VocabRow {
   float a, lse2, b;
   int target;  // in the whole vocabulary; -1: none
 };
+// The entries of listed ids (VocabList) that lie in a piece, by the cells of the
+// logits that one wave holds: entry e of offsets[cell] .. offsets[cell + 1] of a
+// row of cells is row | column << 7 | place in the list << 14 within the cell (its
+// rows and columns at most 128). The forward stores their logits in z[row][top].
+struct VocabCells {
+  const int* offsets = nullptr;  // [row cells][bins + 1]; null: none
+  const uint32_t* entries = nullptr;  // [row cells][per_cell]
+  int bins = 0, per_cell = 0, top = 0;
+  float* z = nullptr;
+};
+// The geometry of a launch's cells.
+struct CellShape {
+  int rows = 0, cols = 0;  // of a cell
+  bool dense = false;      // rows of cells as vocab_lse_kernel's tiles have them
+  int64_t row_cells(int64_t M) const {
+    return dense ? 2 * ((M + 255) / 256) : (M + rows - 1) / rows;
+  }
+  int64_t bins(int64_t N) const { return dense ? 2 * ((N + 255) / 256) : (N + cols - 1) / cols; }
+};
+constexpr int kMaxBins = 16384;  // of a row of cells: their counts are in LDS
+CellShape vocab_tile_cells(DType t, const TilePlan& plan);
+inline CellShape vocab_dense_cells() { return CellShape{128, 128, true}; }
+// Sorts the list's entries with ids in [col0, col0 + N) into the cells of M rows
+// (`own`: and stores z of those that are in no piece, 0 or NaN).
+hipError_t launch_vocab_cells(const VocabList& l, int64_t M, int64_t col0, int64_t N,
+                              const CellShape& shape, int* offsets, uint32_t* entries, float* z,
+                              bool own, hipStream_t s);
+
 // Forward: for every row and slot (a group of the piece's columns)
 // part[slot][row] = (max, sum) with sum_j 2^(scale z_j) = sum 2^max over the slot's
 // columns. vocab_tile_slots of them. With targets [M], z[row] = the logit of
 // the row's, where the piece has it.
 int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N);
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
-                                 int64_t part_ld, const int64_t* targets, float* z, hipStream_t s);
+                                 int64_t part_ld, const int64_t* targets, float* z,
+                                 const VocabCells& cells, hipStream_t s);
 // Backward: g_z of the piece in x's type at gz[row][ldg], or in the tiled layout
 // [..][ldg] of which gz is the piece's first block of columns; columns N up to
 // ldg, and rows M up to the next multiple of 32, are zeroed where tiles reach
@@ -373,7 +411,7 @@ inline bool vocab_dense_supported(int64_t M, int64_t N, int64_t K) {
 // 2 ceil(N / 256) slots
 hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
                                   int64_t part_ld, const int64_t* targets, float* z,
-                                  hipStream_t s);
+                                  const VocabCells& cells, hipStream_t s);
 // x: the tiled copy of it, M % 256 == 0 rows, as many of `rows`; gz in
 // the tiled layout [M][ldg], ldg % 256 == 0; columns past N of the last tile are
 // zeroed.
@@ -400,15 +438,6 @@ hipError_t launch_few_gw(DType t, const void* gz, int64_t ldg, const void* xt, i
 hipError_t launch_sum_slabs(DType t, const float* slabs, int nsplit, int64_t rows, int N, void* out,
                             hipStream_t s);
 
-// The listed ids of a row: targets (top = 1) or a teacher's [rows][top].
-struct VocabList {
-  const int64_t* ids = nullptr;
-  const void* teacher = nullptr;  // logits [rows][top] of type `type`; null: targets
-  DType type = DType::F32;
-  int top = 1;
-  int64_t vocab = 0;
-  float temperature = 1.0f;
-};
 // z[row][k] = x[row] . W[ids[row][k]]; 0 where the id is negative, NaN where
 // it is past the vocabulary.
 hipError_t launch_listed_logits(DType t, const void* x, const void* W, const VocabList& l,

@@ -56,6 +56,47 @@ __device__ __forceinline__ int pair_column(int ln) {
   return 16 * ((ln >> 4) & 1) + 8 * (ln >> 5);
 }
 
+// The entries of one wave's cell: their range and the first 64 of them, read
+// well before their logits are stored (each read waits for the L2, one for the
+// other).
+struct OwnCell {
+  const uint32_t* entries;
+  int begin, end;
+  uint32_t first;  // this lane's of the first 64
+};
+__device__ __forceinline__ OwnCell read_cell(const VocabCells& cells, int64_t row_cell, int bin,
+                                             int lane) {
+  OwnCell c;
+  // (a uniform address: read through the scalar cache)
+  typedef const __attribute__((address_space(4))) int* ConstInts;
+  const ConstInts at = (ConstInts)(cells.offsets + row_cell * (cells.bins + 1) + bin);
+  c.begin = __builtin_amdgcn_readfirstlane(at[0]);
+  c.end = __builtin_amdgcn_readfirstlane(at[1]);
+  c.entries = cells.entries + row_cell * cells.per_cell;
+  c.first = c.begin + lane < c.end ? c.entries[c.begin + lane] : 0;
+  return c;
+}
+// Stores their logits (z's row of the cell's first row: `m`): pick(i, j) is the
+// wave's fragment (i, j), wave-uniform; entries are taken one by one.
+template <typename Pick>
+__device__ __forceinline__ void store_cell(const VocabCells& cells, const OwnCell& c, int64_t m,
+                                           int lane, const Pick& pick) {
+  auto store = [&](uint32_t own, int n) __attribute__((always_inline)) {
+    for (int q = 0; q < n; ++q) {
+      const uint32_t w = __builtin_amdgcn_readlane(own, q);
+      const int row = w & 127, col = (w >> 7) & 127;
+      const floatx4 v = pick(row >> 4, col >> 4);
+      const int k = col & 3;
+      const float z = k < 2 ? (k == 0 ? v[0] : v[1]) : (k == 2 ? v[2] : v[3]);
+      if (lane == (row & 15) + 16 * ((col >> 2) & 3))
+        cells.z[(m + row) * cells.top + (w >> 14)] = z;
+    }
+  };
+  store(c.first, min(64, c.end - c.begin));
+  for (int e = c.begin + 64; e < c.end; e += 64)  // (few cells; these wait for their loads)
+    store(e + lane < c.end ? c.entries[e + lane] : 0, min(64, c.end - e));
+}
+
 // g_z at a logit z of the vocabulary's column `col` (VocabRow)
 __device__ __forceinline__ float logit_gradient(const VocabRow& r, float z, float c, int col) {
   const float q = r.a == 0.0f ? 0.0f : r.a * __builtin_amdgcn_exp2f(fmaf(z, c, -r.lse2));

@@ -16,6 +16,7 @@ namespace poetx {
 namespace {
 
 constexpr int NT = 256, NWAVES = NT / 64;
+constexpr int kMaxTop = 1024;  // entries of a row's list
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 template <typename T> struct Vec;  // one 16-byte vector as float32
@@ -95,6 +96,63 @@ listed_logits_kernel(const T* __restrict__ x, const T* __restrict__ W, const Voc
     const float v = wave_sum(acc[q]);
     if (lane == 0 && k0 + q < l.top)
       z[row * l.top + k0 + q] = id[q] < 0 ? 0.0f : id[q] >= l.vocab ? NAN : v;
+  }
+}
+
+// One workgroup a row of cells: counts of its entries by cell in LDS, their sums,
+// and the entries dealt out. (The order within a cell is the atomics'; each
+// entry's logit is stored at its own place, so results do not depend on it.)
+constexpr int kCellThreads = 1024;
+__global__ void __launch_bounds__(kCellThreads)
+cells_kernel(const VocabList l, int64_t M, int64_t col0, int64_t N, const CellShape shape, int bins,
+             int per_cell, int* __restrict__ offsets, uint32_t* __restrict__ entries,
+             float* __restrict__ z, int own) {
+  extern __shared__ int count[];  // [bins]
+  __shared__ int sums[kCellThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t cell = blockIdx.x;
+  const int64_t m0 = shape.dense ? min(cell / 2 * 256, M - 256) + (cell & 1) * 128
+                                 : cell * shape.rows;
+  const int n = (int)min((int64_t)shape.rows, M - m0) * l.top;
+  const int64_t* ids = l.ids + m0 * l.top;
+  for (int b = tid; b < bins; b += kCellThreads) count[b] = 0;
+  __syncthreads();
+  for (int e = tid; e < n; e += kCellThreads) {
+    const int64_t id = ids[e], at = id - col0;
+    if (at >= 0 && at < N) atomicAdd(&count[(int)at / shape.cols], 1);
+    if (own && (id < 0 || id >= l.vocab)) z[m0 * l.top + e] = id < 0 ? 0.0f : NAN;
+  }
+  __syncthreads();
+  // counts to first places: a run of cells a thread, the runs' sums by waves
+  const int run = (bins + kCellThreads - 1) / kCellThreads;
+  const int b0 = min(bins, tid * run), b1 = min(bins, b0 + run);
+  int own_sum = 0;
+  for (int b = b0; b < b1; ++b) own_sum += count[b];
+  int before = own_sum;
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int v = __shfl_up(before, k);
+    if (lane >= k) before += v;
+  }
+  if (lane == 63) sums[wave] = before;
+  __syncthreads();
+  before -= own_sum;
+  for (int w = 0; w < wave; ++w) before += sums[w];
+  int* out = offsets + cell * (bins + 1);
+  for (int b = b0; b < b1; ++b) {
+    const int c = count[b];
+    count[b] = out[b] = before;
+    before += c;
+  }
+  if (tid == kCellThreads - 1) out[bins] = before;
+  __syncthreads();
+  uint32_t* to = entries + cell * per_cell;
+  for (int e = tid; e < n; e += kCellThreads) {
+    const int64_t at = ids[e] - col0;
+    if (at < 0 || at >= N) continue;
+    const int b = (int)at / shape.cols, row = e / l.top;
+    to[atomicAdd(&count[b], 1)] =
+        (uint32_t)(row | ((int)at - b * shape.cols) << 7 | (e - row * l.top) << 14);
   }
 }
 
@@ -314,7 +372,6 @@ turned_copy_kernel(const VocabRow* __restrict__ parts, int rows, int K, const Vo
 //   g_z[j] = a (2^(scale z_j - lse2) - the sum of p over the entries with that id).
 // The entries' p are in LDS, so that each finds its id's other entries (an id
 // listed twice: both write the same value).
-constexpr int kMaxTop = 1024;
 template <typename T>
 __global__ void __launch_bounds__(NT)
 listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__ r,
@@ -367,6 +424,19 @@ hipError_t launch_listed_logits(DType t, const void* x, const void* W, const Voc
   else
     hipLaunchKernelGGL(listed_logits_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s,
                        static_cast<const float*>(x), static_cast<const float*>(W), l, rows, K, z);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_cells(const VocabList& l, int64_t M, int64_t col0, int64_t N,
+                              const CellShape& shape, int* offsets, uint32_t* entries, float* z,
+                              bool own, hipStream_t s) {
+  const int64_t bins = shape.bins(N), cells = shape.row_cells(M);
+  if (bins < 1 || bins > kMaxBins || shape.rows > 128 || shape.cols > 128 || l.top > kMaxTop ||
+      cells * kCellThreads > kMaxWorkItems || (shape.dense && M < 256))
+    return hipErrorInvalidValue;
+  hipLaunchKernelGGL(cells_kernel, dim3((unsigned)cells), dim3(kCellThreads),
+                     (unsigned)(bins * sizeof(int)), s, l, M, col0, N, shape, (int)bins,
+                     shape.rows * l.top, offsets, entries, z, (int)own);
   return hipGetLastError();
 }
 

@@ -118,12 +118,26 @@ Columns split_columns(DType t, int64_t rows, int64_t cols, int64_t K, float copy
 
 // The forward's partial sums: `rows` rows at a time, so that they stay within
 // kPartBytes.
+// A teacher's ids get their logits out of the products (`cells`, two launches'
+// at most) where reading W's rows for each of them again would take longer than
+// sorting them into the waves' cells and picking them out of the accumulators
+// (4096 x 65536 x 2048, 64 ids a row: 116 us against 11 and about 40).
 struct FwdPlan {
   Columns cols;
   int64_t rows, slots;
   bool copied;  // W_last
-  size_t z, last, part, total;
+  bool cells;
+  size_t z, last, part, offsets[2], entries[2], total;
 };
+struct CellSizes {
+  size_t offsets, entries;  // bytes
+  bool possible;
+};
+CellSizes cell_sizes(const poetx::CellShape& c, int64_t rows, int64_t cols, int top) {
+  const int64_t n = c.row_cells(rows), bins = c.bins(cols);
+  return {align_up((size_t)(n * (bins + 1) * 4)), align_up((size_t)(n * c.rows * top * 4)),
+          bins <= poetx::kMaxBins};
+}
 FwdPlan plan_fwd(const poetx_vocab_desc* d) {
   FwdPlan p = {};
   const DType t = dtype_of(d);
@@ -142,6 +156,20 @@ FwdPlan plan_fwd(const poetx_vocab_desc* d) {
   p.copied = p.cols.dense % kTile != 0;
   p.part = p.last + (p.copied ? align_up((size_t)(kTile * d->d) * act_size(d->act)) : 0);
   p.total = p.part + align_up((size_t)(p.slots * p.rows * 8));
+  const double read = (double)list_entries(d) * d->d * act_size(d->act) / 9.0e6;  // us
+  if (d->top && read > 20.0) {
+    const int64_t rest = d->vocab - p.cols.dense;
+    CellSizes c[2] = {{0, 0, true}, {0, 0, true}};
+    if (p.cols.dense) c[0] = cell_sizes(poetx::vocab_dense_cells(), p.rows, p.cols.dense, d->top);
+    if (rest)
+      c[1] = cell_sizes(poetx::vocab_tile_cells(t, p.cols.tile), p.rows, rest, d->top);
+    p.cells = c[0].possible && c[1].possible;
+    for (int i = 0; p.cells && i < 2; ++i) {
+      p.offsets[i] = p.total;
+      p.entries[i] = p.offsets[i] + c[i].offsets;
+      p.total = p.entries[i] + c[i].entries;
+    }
+  }
   return p;
 }
 
@@ -173,7 +201,7 @@ TileProducts tile_products(const poetx_vocab_desc* d, int64_t n) {
   p.gw = plan_tile_product(t, n, d->d, d->tokens, false);
   p.pair = plan_tile_pair(t, d->tokens, d->d, n, poetx::kManySplits);
   // a launch for the turned copy of x and one that stores g_W
-  const float few = 6.0f + (float)(n * d->d * (int64_t)act_size(d->act)) / 4.0e6f;
+  const float few = 6.0f + (float)(n * d->d * (int64_t)act_size(d->act)) / 3.2e6f;
   p.few = d->tokens <= poetx::kFewTokens &&
           few < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
   p.paired = !p.few && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
@@ -291,7 +319,8 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   if (!z) z = reinterpret_cast<float*>(w + plan.z);
   float2* part = reinterpret_cast<float2*>(w + plan.part);
   // (targets' logits come out of the products)
-  if (teacher) POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
+  if (teacher && !plan.cells)
+    POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
   if (plan.copied) {
     poetx::VocabCopies c;
     c.W = W;
@@ -309,13 +338,32 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
     p.M = (int)(at + rows - r); p.N = (int)plan.cols.dense; p.K = (int)d->d;
     p.scale = scale_of(d);
     const int64_t* targets = teacher ? nullptr : ids + r;
-    if (p.N) POETX_TRY(poetx::launch_vocab_lse_dense(p, w + plan.last, part, p.M, targets, z + r, s));
+    const int64_t dense = plan.cols.dense, rest = d->vocab - dense;
+    poetx::VocabCells cells[2];
+    for (int i = 0; plan.cells && i < 2; ++i) {
+      const int64_t from = i ? dense : 0, n = i ? rest : dense;
+      if (n == 0) continue;
+      const poetx::CellShape shape =
+          i ? poetx::vocab_tile_cells(t, plan.cols.tile) : poetx::vocab_dense_cells();
+      int* offsets = reinterpret_cast<int*>(w + plan.offsets[i]);
+      uint32_t* entries = reinterpret_cast<uint32_t*>(w + plan.entries[i]);
+      POETX_TRY(poetx::launch_vocab_cells(list_at(list, r), p.M, from, n, shape, offsets, entries,
+                                          z + r * list.top, i == 1 || rest == 0, s));
+      cells[i].offsets = offsets;
+      cells[i].entries = entries;
+      cells[i].bins = (int)shape.bins(n);
+      cells[i].per_cell = shape.rows * list.top;
+      cells[i].top = list.top;
+      cells[i].z = z + r * list.top;
+    }
+    if (p.N) POETX_TRY(poetx::launch_vocab_lse_dense(p, w + plan.last, part, p.M, targets, z + r, cells[0],
+                                              s));
     if (plan.cols.dense < d->vocab) {
       p.col0 = p.N;
       p.W = static_cast<const char*>(W) + p.col0 * d->d * act_size(d->act);
       p.N = (int)(d->vocab - p.col0);
       POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.cols.tile, p, part + p.col0 / 128 * (int64_t)p.M,
-                                             p.M, targets, z + r, s));
+                                             p.M, targets, z + r, cells[1], s));
     }
     POETX_TRY(poetx::launch_vocab_loss(part, p.M, plan.slots, list_at(list, r), p.M,
                                        z + r * list.top, loss + r, lse + r, s));

@@ -28,10 +28,15 @@ __device__ __forceinline__ const bf16_t* panel(const bf16_t* W, const bf16_t* W_
 // end(m0, n0, q, nt) of this one, for the tiles of nq products side by side (their
 // panels through set(q, m0, n0)). end returns whether it has issued at least
 // LATE vector memory instructions, for which the next products then do not
-// wait before their copies (8192 tokens, 131072 x 4096: see the kernels).
-template <int LATE, typename D, typename Set, typename End>
+// wait before their copies.
+// What an end reads from memory is loaded by before(m0, n0, nt), ahead of the
+// products, and is there at there(), behind them: a wait for a load after the next
+// tile's copies would be one for the copies too (the counter is in order, and the
+// compiler does not know of them).
+template <int LATE, typename D, typename Set, typename Before, typename There, typename End>
 __device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, int m_last,
-                                          int n_last, const Set& set, const End& end) {
+                                          int n_last, const Set& set, const Before& before,
+                                          const There& there, const End& end) {
   const int total = num_mt * num_nt * nq;
   int tile = blockIdx.x, mt, nt, q, ntiles;
   bool late = false;
@@ -49,16 +54,18 @@ __device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, 
   };
   go();
   for (;;) {
-    const int mt0 = mt, nt0 = nt, q0 = q;
+    const int m0 = min(mt * BM, m_last), n0 = min(nt * BN, n_last), nt0 = nt, q0 = q;
+    before(m0, n0, nt0);
     d.template start_late<LATE>(late);
     d.template mainloop_late<LATE>(ntiles, late);
     d.settle();
+    there();
     wait_lds();
     barrier_nofence();  // every wave is done with the ring
     tile += (int)gridDim.x;
     const bool more = tile < total;
     if (more) go();
-    late = end(min(mt0 * BM, m_last), min(nt0 * BN, n_last), q0, nt0);
+    late = end(m0, n0, q0, nt0);
     if (!more) break;
   }
 }
@@ -75,20 +82,42 @@ template <typename D> __device__ __forceinline__ int opaque_lane(const D& d) {
 // the sum of exponentials over its 128 columns, in two passes over the
 // accumulators, so that the eight rows of a lane are exchanged together; and the
 // targets' logits, which few waves hold any of.
+// LISTED: `cells` in the place of targets.
+template <bool LISTED>
 __global__ void __launch_bounds__(NT)
 vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
                  const bf16_t* __restrict__ W_last, int M, int N, int K, float scale, int col0,
                  float2* __restrict__ part, int64_t part_ld, const int64_t* __restrict__ targets,
-                 float* __restrict__ z) {
+                 float* __restrict__ z, const VocabCells cells) {
   typedef Dense<true, true> D;
   D d;
   d.init(K, K, false, false);
   const int ntiles = K / BK;
+  int64_t target[FM] = {};
+  OwnCell cell = {};
   tile_loop<FM>(
       d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M - BM, N,
       [&](int, int m0, int n0) __attribute__((always_inline)) {
         d.set_tile(x, panel(W, W_last, n0, N, K), K, K, m0, n0);
         return ntiles;
+      },
+      [&](int m0, int n0, int nt) __attribute__((always_inline)) {
+        if constexpr (LISTED) {
+          if (cells.offsets)
+            cell = read_cell(cells, 2 * ((m0 + BM - 1) / BM) + d.wm, 2 * nt + d.wn, d.lane);
+        } else {
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+            target[i] = targets[m0 + d.wm * 128 + 16 * i + (d.lane & 15)];
+        }
+      },
+      [&]() __attribute__((always_inline)) {
+        if constexpr (LISTED) {
+          asm volatile("" : "+v"(cell.first));
+        } else {
+#pragma unroll
+          for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(target[i]));
+        }
       },
       [&](int m0, int n0, int, int nt) __attribute__((always_inline)) {
         const int ln = opaque_lane(d);
@@ -138,11 +167,11 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
           sum[i] = quad_sum(sum[i]);
           if (ln < 16) out[16 * i] = make_float2(mx[i], sum[i]);
         }
-        if (targets) {
+        if constexpr (!LISTED) {
           d.in_agprs();
 #pragma unroll
           for (int i = 0; i < FM; ++i) {
-            const int64_t at = targets[m + 16 * i] - (col0 + n);
+            const int64_t at = target[i] - (col0 + n);
             if (!__any(at >= 0 && at < 128)) continue;
             const int own = at >= 0 && at < 128 ? (int)at - 4 * (ln >> 4) : -1;
 #pragma unroll
@@ -152,6 +181,9 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
                 if (own == 16 * j + e) z[m + 16 * i] = d.acc[i][j][e];
           }
         }
+        if constexpr (LISTED)
+          store_cell(cells, cell, m0 + d.wm * 128, ln,
+                     [&](int i, int j) __attribute__((always_inline)) { return d.pick(8 * i + j); });
         return true;  // (the eight stores)
       });
 }
@@ -166,15 +198,24 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
   D d;
   d.init(K, K, true, false);
   const int ntiles = K / BK;
+  VocabRow row[FM];
   tile_loop<FM * FN / 2>(
       d, M / BM, (N + BN - 1) / BN, 1, M, N,
       [&](int, int m0, int n0) __attribute__((always_inline)) {
         d.set_tile(xs, panel(W, W_last, n0, N, K), K, K, m0, n0);
         return ntiles;
       },
+      [&](int m0, int, int) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) row[i] = rows[m0 + d.wm * 128 + 16 * i + (d.lane & 15)];
+      },
+      [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          asm volatile("" : "+v"(row[i].a), "+v"(row[i].lse2), "+v"(row[i].b), "+v"(row[i].target));
+      },
       [&](int m0, int n0, int, int) __attribute__((always_inline)) {
         const int ln = opaque_lane(d);
-        const VocabRow* at = rows + m0 + d.wm * 128 + (ln & 15);
         // (the wave's first block of 32 columns, this lane's place in it)
         bf16_t* out = gz + tiled_offset(m0, n0 + d.wn * 128, ldg) +
                       (d.wm * 128 + (ln & 15)) * kTileCols + pair_column(ln);
@@ -184,7 +225,7 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
           d.in_agprs();
-          const VocabRow r = at[16 * i];
+          const VocabRow r = row[i];
           const int own = r.target - col - 4 * (ln >> 4);  // (this lane's: 16 j + e)
           const bool rare = __any((unsigned)(r.target - col) < 128u) || padded;
           asm volatile("" : "+v"(left));
@@ -239,6 +280,7 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
               d.last_b = W_last + n0;
               return (n + BK - 1) / BK;
             },
+            [](int, int, int) {}, []() {},
             [&](int m0, int n0, int q, int nt) __attribute__((always_inline)) {
               const int ln = opaque_lane(d);
               const int m = m0 + d.wm * 128 + (ln & 15);
@@ -306,6 +348,7 @@ vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, in
               d.set_tile(gz, xs, ldg, N, m0, n0);
               return ntiles;
             },
+            [](int, int, int) {}, []() {},
             [&](int m0, int n0, int, int) __attribute__((always_inline)) {
               const int ln = opaque_lane(d);
               const int m = m0 + d.wm * 128 + (ln & 15);
@@ -337,14 +380,15 @@ const bf16_t* b16(const void* p) { return static_cast<const bf16_t*>(p); }
 
 hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, float2* part,
                                   int64_t part_ld, const int64_t* targets, float* z,
-                                  hipStream_t s) {
+                                  const VocabCells& cells, hipStream_t s) {
   if (!vocab_dense_supported(p.M, p.N, p.K) || (p.N % BN != 0 && !W_last))
     return hipErrorInvalidValue;
   int grid = 0;
   const hipError_t e = dense_grid(p.M, p.N, &grid);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(vocab_lse_kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last),
-                     p.M, p.N, p.K, p.scale, p.col0, part, part_ld, targets, z);
+  const auto kernel = targets ? vocab_lse_kernel<false> : vocab_lse_kernel<true>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last), p.M, p.N,
+                     p.K, p.scale, p.col0, part, part_ld, targets, z, cells);
   return hipGetLastError();
 }
 

@@ -5,11 +5,11 @@
 //
 // One wave takes 32 rows of g_W (ids): their g_z, at most 64 tokens, are the
 // products' operand and stay in registers; it walks along d with one 16-byte load a
-// lane for 16 columns, out of a copy of x with the tokens innermost
-// (xt [d][tokens padded], from the launch that forms the rows' parts; it stays in
-// the L2), and stores 64-byte pieces of 16 rows (past the caches, with half lines: 3
-// times as long). No LDS, no barrier; many
-// waves a SIMD hide the loads.
+// lane for 16 columns, 32 columns ahead, out of a copy of x with the tokens
+// innermost (xt [d][tokens padded]; it stays in the L2), and stores 64-byte pieces of
+// 16 rows. No LDS, no barrier. 16 tokens, 131072 x 4096: 360 us, 3.0 TB/s of
+// stores alone; 30 tokens, 56370 x 2256: 63 us, on 64 x 64 tiles 113. Stores past
+// the caches (half lines) 194 us there; 16 ids a wave 75; walks of 1024 columns 71.
 #include "epilogue.h"
 #include "vocab.h"
 

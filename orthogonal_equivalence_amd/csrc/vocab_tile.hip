@@ -16,6 +16,25 @@
 namespace poetx {
 namespace {
 
+// fragment (f / FN, f % FN) of the accumulators, f wave-uniform (copied by name:
+// as an index it would put them into memory)
+template <int FM, int FN>
+__device__ __forceinline__ floatx4 pick(const floatx4 (&acc)[FM][FN], int f) {
+  floatx4 v{0.0f, 0.0f, 0.0f, 0.0f};
+  for_each<FM * FN>([&](auto n) POETX_INLINE {
+    constexpr int F = decltype(n)::value;
+    if (f == F) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x;
+        asm volatile("v_mov_b32 %0, %1" : "=v"(x) : "v"(acc[F / FN][F % FN][e]));
+        v[e] = x;
+      }
+    }
+  });
+  return v;
+}
+
 struct LseEnd {
   float2* part;
   int64_t part_ld;
@@ -23,10 +42,15 @@ struct LseEnd {
   const int64_t* targets;
   float* z;
   int col0;
+  VocabCells cells;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int, int wave_col, int lane) const {
     float2* out = part + (int64_t)wave_col * part_ld;
+    // (a wave past the rows or columns has no cell)
+    const bool listed = cells.offsets && m_at < p.M && n_at < p.N;
+    OwnCell cell = {};
+    if (listed) cell = read_cell(cells, m_at / (16 * FM), n_at / (16 * FN), lane);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       float v[4 * FN];
@@ -49,6 +73,9 @@ struct LseEnd {
         for (int e = 0; e < 4; ++e)
           if (own == 16 * j + e) z[m] = acc[i][j][e];
     }
+    if (listed)
+      store_cell(cells, cell, m_at, lane,
+                 [&](int i, int j) POETX_INLINE { return pick(acc, i * FN + j); });
   }
 };
 
@@ -128,17 +155,30 @@ hipError_t launch_end(DType t, const TilePlan& plan, const VocabProduct& v, cons
 
 }  // namespace
 
+namespace {
+// rows, columns, wave rows and wave columns of a tile, by shape (launch_end)
+constexpr int kBf16Tiles[][4] = {{256, 128, 4, 2}, {128, 128, 2, 4}, {128, 64, 4, 2},
+                                 {64, 64, 2, 2},   {32, 64, 1, 4},   {128, 64, 4, 2}};
+constexpr int kF32Tiles[][4] = {{64, 64, 2, 2}, {32, 64, 1, 4}};
+const int* tile_of(DType t, const TilePlan& plan) {
+  return t == DType::F32 ? kF32Tiles[plan.shape] : kBf16Tiles[plan.shape];
+}
+}  // namespace
+
 int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N) {
-  // wave columns of a tile and its width, by shape (launch_end)
-  static constexpr int kBf16[][2] = {{2, 128}, {4, 128}, {2, 64}, {2, 64}, {4, 64}, {2, 64}};
-  static constexpr int kF32[][2] = {{2, 64}, {4, 64}};
-  const int* h = t == DType::F32 ? kF32[plan.shape] : kBf16[plan.shape];
-  return (N + h[1] - 1) / h[1] * h[0];
+  const int* h = tile_of(t, plan);
+  return (N + h[1] - 1) / h[1] * h[3];
+}
+
+CellShape vocab_tile_cells(DType t, const TilePlan& plan) {
+  const int* h = tile_of(t, plan);
+  return CellShape{h[0] / h[2], h[1] / h[3], false};
 }
 
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
-                                 int64_t part_ld, const int64_t* targets, float* z, hipStream_t s) {
-  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z, p.col0}, s);
+                                 int64_t part_ld, const int64_t* targets, float* z,
+                                 const VocabCells& cells, hipStream_t s) {
+  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z, p.col0, cells}, s);
 }
 
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,

@@ -117,6 +117,9 @@ def test_cross_entropy(tokens, d, vocab, dyadic, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("tokens,d,vocab,top,temperature,dyadic", [
+    # (the longer lists get their logits out of the products)
+    (1126, 2832, 501, 59, 1.0, True), (1000, 1024, 8333, 128, 2.0, True),
+    (600, 512, 20000, 400, 1.0, False), (300, 1024, 2000, 600, 1.5, True),
     (1, 8, 1, 1, 1.0, True), (1, 64, 50, 3, 2.0, True), (5, 72, 33, 40, 0.5, True),
     (16, 128, 1000, 8, 1.0, True), (33, 256, 257, 64, 4.0, False), (100, 264, 2049, 65, 1.5, True),
     (300, 512, 4099, 5, 2.0, False), (40, 64, 3000, 1024, 1.0, True), (256, 256, 512, 17, 1.0, True),
@@ -275,6 +278,26 @@ def test_ids_past_the_vocabulary():
         g_x, _ = L.distill_backward(torch.ones(40, device="cuda"), x, W, ids,
                                     torch.zeros(40, 2, device="cuda"), lse, z)
         assert bool(torch.isnan(g_x[7]).all()) and int(torch.isnan(g_x).sum()) == 64
+
+
+@pytest.mark.parametrize("tokens,d,vocab,top", [(700, 512, 9000, 512), (130, 4096, 700, 300)])
+def test_lists_in_one_place(tokens, d, vocab, top):
+    """Every id of every row within a few columns (one wave's cell holds thousands
+    of entries), one of them past the vocabulary: each entry's own logit, exact."""
+    x, W = V.inputs(tokens, d, vocab, "bf16", 1, True)
+    gen = torch.Generator().manual_seed(9)
+    ids = torch.randint(0, 5, (tokens, top), generator=gen).cuda()
+    ids[:, 7] = vocab - 1
+    ids[3, 5] = vocab
+    ids[4, 6] = -7
+    teacher = torch.randn(tokens, top, generator=gen).cuda()
+    loss, lse, z = L.distill_forward(x, W, ids, teacher)
+    want = x.double().mm(W.double().t()).gather(1, ids.clamp(0, vocab - 1))
+    want[4, 6] = 0
+    assert bool(torch.isnan(z[3, 5])) and bool(torch.isnan(loss[3]))
+    want[3, 5] = z[3, 5] = 0
+    assert torch.equal(z.double(), want)
+    assert int(torch.isnan(loss).sum()) == 1
 
 
 def test_large_and_infinite_logits():
