@@ -9,7 +9,8 @@ d_in], W [d_out, d_in], residual and u [tokens, d_out] of one type (float32 or
 bfloat16) and a float32 bias [d_out], of at least one row, widths that are
 multiples of 16 bytes and 16-byte aligned; W may be the int8 codes of
 poetx_quantize_weight with their float32 row scales w_scale [d_out].
-DenseLinear keeps a weight and its bias. Outputs and workspaces come from
+DenseLinear keeps a weight and its bias; as the projection onto a vocabulary it
+also ends in a loss of its logits (losses.py). Outputs and workspaces come from
 torch's allocator on the stream that the call runs on, so calls on different
 streams, and calls captured into different graphs, share no memory.
 """
@@ -187,3 +188,34 @@ class DenseLinear:
             need_g_bias = self.bias is not None
         return dense_backward(g_y, self.W, x, u, self.activation, self.w_scale, need_g_x, need_g_W,
                               need_g_bias, stream)
+
+    def _head(self):
+        """The weight as a projection onto a vocabulary, whose losses take the
+        logits as the product gives them."""
+        if self.bias is not None or self.activation != "none" or self.w_scale is not None:
+            raise ValueError("a loss takes a layer without bias, activation and INT8 codes")
+        return self.W
+
+    def cross_entropy(self, x, targets, stream=None):
+        """(loss, lse) of the logits x W^T, which are not kept (losses.py)."""
+        from .losses import cross_entropy_forward
+        return cross_entropy_forward(x, self._head(), targets, stream)
+
+    def cross_entropy_backward(self, g_loss, x, targets, lse, g_lse=None, need_g_x=True,
+                               need_g_W=False, stream=None):
+        """(g_x, g_W)."""
+        from .losses import cross_entropy_backward
+        return cross_entropy_backward(g_loss, x, self._head(), targets, lse, g_lse, need_g_x,
+                                      need_g_W, stream)
+
+    def distill(self, x, ids, teacher, temperature=1.0, stream=None):
+        """(loss, lse, z) of the logits x W^T against a teacher's at the ids."""
+        from .losses import distill_forward
+        return distill_forward(x, self._head(), ids, teacher, temperature, stream)
+
+    def distill_backward(self, g_loss, x, ids, teacher, lse, z, temperature=1.0, need_g_x=True,
+                         need_g_W=False, stream=None):
+        """(g_x, g_W)."""
+        from .losses import distill_backward
+        return distill_backward(g_loss, x, self._head(), ids, teacher, lse, z, temperature,
+                                need_g_x, need_g_W, stream)

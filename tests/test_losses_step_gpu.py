@@ -1,0 +1,265 @@
+"""The losses as a training step uses them: a POET-X layer, a head whose loss is
+cross entropy with a part from a teacher, their backward, the clip over every
+gradient; eager, in captured graphs, on other streams; and the largest sizes."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU too; every test here is gpu-marked
+    pytest.skip("no GPU", allow_module_level=True)
+
+import oracle.poetx_oracle as O  # noqa: E402
+from orthogonal_equivalence_amd import losses as L  # noqa: E402
+from orthogonal_equivalence_amd import poetx as P  # noqa: E402
+from orthogonal_equivalence_amd.dense import DenseLinear  # noqa: E402
+from orthogonal_equivalence_amd.grads import clip_grads  # noqa: E402
+from orthogonal_equivalence_amd.inputs import LayerSpec, make_layer  # noqa: E402
+from orthogonal_equivalence_amd.layer import PoetxLinear  # noqa: E402
+from tests import gpu_util as U  # noqa: E402
+from tests import vocab_cases as V  # noqa: E402
+
+T = 2.0
+
+
+def _make(dtype, tokens, vocab):
+    spec = LayerSpec("loss_step", 256, 512, 64, tokens, dtype, 0.05, seed=41)
+    layer = make_layer(spec)
+    lay = PoetxLinear(U.dev(layer.W0, dtype), spec.b, spec.b, dtype)
+    lay.set_theta(torch.from_numpy(layer.theta_R).float(), torch.from_numpy(layer.theta_P).float())
+    lay.build()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    head = DenseLinear(torch.randn(vocab, 512, generator=g, device="cuda") * 0.1, dtype)
+    targets = V.draw_targets(tokens, vocab, 6)
+    ids, teacher = V.draw_teacher(tokens, vocab, 12, 7)
+    return layer, spec, lay, head, U.dev(layer.x, dtype), targets, ids, teacher
+
+
+def _step(lay, head, x, targets, ids, teacher, max_norm):
+    """The mean cross entropy over the rows that take part, with 1e-3 lse^2, and
+    half the mean distillation loss; every gradient, clipped."""
+    h, z = lay.forward(x)
+    n = (targets >= 0).sum().clamp(min=1).float()
+    w = torch.ones_like(targets, dtype=torch.float32) / n
+    ce, lse = head.cross_entropy(h, targets)
+    kd, lse_t, z_t = head.distill(h, ids, teacher, T)
+    total = (w * (ce + 1e-3 * lse * lse)).sum() + 0.5 * (w * kd).sum()
+    g_h, g_W = head.cross_entropy_backward(w, h, targets, lse, g_lse=2e-3 * lse * w, need_g_W=True)
+    g_h2, g_W2 = head.distill_backward(0.5 * w, h, ids, teacher, lse_t, z_t, T, need_g_W=True)
+    g_x, gR, gP = lay.backward(g_h + g_h2, x, z)
+    grads = [gR, gP, g_W + g_W2]
+    norm = clip_grads(grads, max_norm)
+    return total, g_x, grads, norm
+
+
+@pytest.mark.parametrize("tokens,vocab", [(150, 777), (600, 4100)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_step_against_float64(dtype, tokens, vocab):
+    layer, spec, lay, head, x, targets, ids, teacher = _make(dtype, tokens, vocab)
+    total, g_x, grads, norm = _step(lay, head, x, targets, ids, teacher, math.inf)
+    # float64, with torch's autograd behind the POET-X layer's oracle output
+    ora = O.LayerOracle(layer.W0, layer.theta_R, layer.theta_P, spec.b, spec.b)
+    h = torch.from_numpy(ora.forward(layer.x)).requires_grad_()
+    W = head.W.detach().double().cpu().requires_grad_()
+    t, i, q = targets.cpu(), ids.cpu(), teacher.double().cpu()
+    logits = h @ W.t()
+    part = t >= 0
+    n = part.sum().double()
+    lse = logits.logsumexp(1)
+    ce = torch.where(part, lse - logits.gather(1, t.clamp(min=0)[:, None])[:, 0] +
+                     1e-3 * lse * lse, 0.0).sum() / n
+    held = (i >= 0) & (q > -math.inf)
+    p = torch.where(held, q / T, -math.inf).softmax(1).nan_to_num(0.0)
+    log_q = (logits / T).log_softmax(1).gather(1, i.clamp(min=0))
+    kd = T * T * torch.where(p > 0, p * (p.clamp(min=1e-300).log() - log_q), 0.0).sum() / n
+    ref = ce + 0.5 * kd
+    ref.backward()
+    # the oracle's tolerance for the whole path: 1e-4 of float32, 2e-2 of bf16
+    tol = {"f32": 1e-4, "bf16": 2e-2}[dtype]
+    assert abs(total.item() - ref.item()) <= tol * abs(ref.item())
+    gx, gR, gP = ora.backward(h.grad.numpy(), layer.x)
+    U.check("g_x", U.host(g_x), gx, dtype)
+    for name, got, want in (("theta_R", grads[0], gR), ("theta_P", grads[1], gP),
+                            ("W", grads[2], W.grad.numpy())):
+        U.check(name, U.host(got), want, dtype)
+    n64 = math.sqrt(sum(g.double().square().sum().item() for g in grads))
+    assert abs(norm.item() - n64) <= 2.0 ** -23 * n64
+
+
+@pytest.mark.parametrize("tokens,vocab", [(130, 777), (40, 30001), (520, 4100)])
+def test_step_in_two_graphs(tokens, vocab):
+    """The step captured twice, the graphs replayed in turn on new inputs between
+    eager steps: the same bits (no graph shares memory with another or with the
+    eager calls)."""
+    made = _make("bf16", tokens, vocab)
+    lay, head, x, targets, ids, teacher = made[2:]
+    _step(lay, head, x, targets, ids, teacher, 0.5)
+    torch.cuda.synchronize()
+    sides = []
+    for _ in range(2):
+        own = [v.clone() for v in (x, targets, ids, teacher)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = _step(lay, head, *own, 0.5)
+        sides.append((own, graph, got))
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for k in range(6):
+        own, graph, got = sides[k % 2]
+        own[0].copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+        own[1].copy_(torch.randint(-1, vocab, targets.shape, generator=gen, device="cuda"))
+        graph.replay()
+        ref = _step(lay, head, *[v.clone() for v in own], 0.5)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        assert all(torch.equal(a, b) for a, b in zip(got[2], ref[2])) and torch.equal(got[3], ref[3])
+
+
+def _both(x, W, t, ids, teacher, stream=None):
+    loss, lse = L.cross_entropy_forward(x, W, t, stream=stream)
+    g = torch.ones_like(loss) if stream is None else None
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            g = torch.ones_like(loss)
+    out = [loss, lse, *L.cross_entropy_backward(g, x, W, t, lse, need_g_W=True, stream=stream)]
+    loss, lse, z = L.distill_forward(x, W, ids, teacher, T, stream=stream)
+    return out + [loss, lse, z, *L.distill_backward(g, x, W, ids, teacher, lse, z, T, need_g_W=True,
+                                                    stream=stream)]
+
+
+@pytest.mark.parametrize("tokens,d,vocab", [(33, 256, 20000), (700, 512, 5000)])
+def test_two_streams_at_once(tokens, d, vocab):
+    sides = []
+    for seed in (1, 2):
+        x, W = V.inputs(tokens, d, vocab, "bf16", seed)
+        args = (x, W, V.draw_targets(tokens, vocab, seed + 10),
+                *V.draw_teacher(tokens, vocab, 20, seed + 20))
+        sides.append((args, _both(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[_both(*args, stream=s) for args, _, s in sides] for _ in range(3)]
+    torch.cuda.synchronize()
+    for row in got:
+        for (_, ref, _), out in zip(sides, row):
+            assert all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
+def test_repeated_calls_give_the_same_bits():
+    x, W = V.inputs(700, 512, 5003, "bf16", 1)
+    t = V.draw_targets(700, 5003, 2)
+    ids, teacher = V.draw_teacher(700, 5003, 256, 3)  # (long enough for the sorted lists)
+    ref = _both(x, W, t, ids, teacher)
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(ref, _both(x, W, t, ids, teacher)))
+
+
+def test_float32_in_pieces():
+    """A float32 gradient of the logits of more than 512 MB: two pieces of the
+    vocabulary, g_x summed over them; against the same call on halves of W
+    (whose gradients are the whole's rows) in float64."""
+    tokens, d, vocab = 1100, 64, 131072
+    x, W = V.inputs(tokens, d, vocab, "f32", 1, True)
+    t = V.draw_targets(tokens, vocab, 2)
+    loss, lse = L.cross_entropy_forward(x, W, t)
+    g = torch.ones(tokens, device="cuda")
+    g_x, g_W = L.cross_entropy_backward(g, x, W, t, lse, need_g_W=True)
+    part = (t >= 0)[:, None]
+    want_x = torch.zeros(tokens, d, device="cuda", dtype=torch.float64)
+    mag_x = torch.zeros_like(want_x)
+    u = 2.0 ** -24
+    for a in range(0, vocab, 16384):
+        w = W[a:a + 16384].double()
+        z = x.double().mm(w.t())
+        p = torch.where(part, torch.exp(z - lse.double()[:, None]), torch.zeros_like(z))
+        g_z = p.clone()
+        here = (t >= a) & (t < a + 16384)
+        g_z[here.nonzero()[:, 0], t[here] - a] -= 1.0
+        # exponents up to ~|z| + lse < 64 lose 4 half steps of it; then sums
+        e_z = 4 * u * 64 * (p + (g_z - p).abs())
+        want_x += g_z.mm(w)
+        mag_x += (e_z + 2 * u * (vocab / 64 + 64) * g_z.abs()).mm(w.abs())
+        want = g_z.t().mm(x.double())
+        tol = (e_z + 2 * u * (tokens + 16) * g_z.abs()).t().mm(x.double().abs()) + \
+            2 * u * want.abs() + 1e-30
+        assert bool(((g_W[a:a + 16384].double() - want).abs() <= tol).all()), a
+    # (the running sums over pieces and splits: as many roundings as terms at most)
+    assert bool(((g_x.double() - want_x).abs() <= mag_x + 2 * u * want_x.abs() + 1e-30).all())
+
+
+def test_weights_past_2_to_the_32_elements():
+    """W and g_W of 4.5e9 values: integer operands, every element."""
+    tokens, d, vocab = 260, 4096, 1100003
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.zeros(vocab, d, device="cuda", dtype=torch.bfloat16)
+    for a in range(0, vocab, 100000):
+        n = min(100000, vocab - a)
+        W[a:a + n, d // 2:] = torch.randint(-1, 2, (n, d // 2), generator=gen, device="cuda",
+                                            dtype=torch.int8).bfloat16()
+    x = torch.zeros(tokens, d, device="cuda", dtype=torch.bfloat16)
+    x[:, :d // 2] = torch.randint(-2, 3, (tokens, d // 2), generator=gen, device="cuda").bfloat16()
+    t = torch.randint(0, vocab, (tokens,), generator=gen, device="cuda")
+    t[0], t[1], t[2] = vocab - 1, -1, 0
+    loss, lse = L.cross_entropy_forward(x, W, t)
+    part = t >= 0
+    want = math.log(vocab)
+    assert bool(((lse[part].double() - want).abs() <= 4 * 2.0 ** -24 * want).all())
+    b = 3.0
+    g_loss = torch.full((tokens,), b, device="cuda")
+    g_lse = torch.full((tokens,), vocab - b, device="cuda")
+    g_x, g_W = L.cross_entropy_backward(g_loss, x, W, t, lse, g_lse=g_lse, need_g_W=True)
+    total = torch.zeros(d, device="cuda", dtype=torch.float64)
+    xs = torch.where(part[:, None], x, torch.zeros_like(x)).double()
+    common = xs.sum(0)
+    for a in range(0, vocab, 100000):
+        n = min(100000, vocab - a)
+        total += W[a:a + n].double().sum(0)
+        rows = common.expand(n, d).clone()
+        here = part & (t >= a) & (t < a + n)
+        rows.index_add_(0, t[here] - a, -b * xs[here])
+        assert torch.equal(g_W[a:a + n], rows.float().bfloat16()), a
+    want_x = torch.where(part[:, None], total - b * W[t.clamp(min=0)].double(), 0.0)
+    assert torch.equal(g_x, want_x.float().bfloat16())
+
+
+def test_refusals():
+    x, W = V.inputs(20, 64, 100, "bf16", 1)
+    t = V.draw_targets(20, 100, 2)
+    ids, teacher = V.draw_teacher(20, 100, 4, 3)
+    f = torch.ones(20, device="cuda")
+    head = DenseLinear(W, "bf16")
+    bad = [
+        lambda: L.cross_entropy_forward(x, W.float(), t),
+        lambda: L.cross_entropy_forward(x[:, :56], W, t),
+        lambda: L.cross_entropy_forward(x, W, t.int()),
+        lambda: L.cross_entropy_forward(x, W, t[:19]),
+        lambda: L.cross_entropy_forward(x, W, t.cpu()),
+        lambda: L.cross_entropy_forward(x[:, ::2], W[:, ::2], t),
+        lambda: L.cross_entropy_forward(x.t().contiguous().t(), W, t),
+        lambda: L.cross_entropy_backward(f.double(), x, W, t, f),
+        lambda: L.cross_entropy_backward(f, x, W, t, f[:19]),
+        lambda: L.cross_entropy_backward(f, x, W, t, f, g_lse=f.bfloat16()),
+        lambda: L.cross_entropy_backward(f, x, W, t, f, need_g_x=False),
+        lambda: L.cross_entropy_backward(f.mean().expand(20), x, W, t, f),
+        lambda: L.distill_forward(x, W, ids, teacher.half()),
+        lambda: L.distill_forward(x, W, ids, teacher[:, :3]),
+        lambda: L.distill_forward(x, W, ids[:, :0], teacher[:, :0]),
+        lambda: L.distill_forward(x, W, t, teacher),
+        lambda: L.distill_backward(f, x, W, ids, teacher, f, teacher[:, :3]),
+        lambda: DenseLinear(W, "bf16", bias=torch.zeros(100)).cross_entropy(x, t),
+        lambda: DenseLinear(W, "bf16", activation="relu").distill(x, ids, teacher),
+        lambda: DenseLinear(W, "bf16", int8=True).cross_entropy(x, t),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+    for temperature in (0.0, -1.0, math.nan, math.inf):
+        with pytest.raises(P.PoetxError):
+            head.distill(x, ids, teacher, temperature)
+    with pytest.raises(P.PoetxError):  # no rows
+        L.cross_entropy_forward(x[:0], W, t[:0])
+    with pytest.raises(P.PoetxError):  # 60 columns of bf16: not whole vectors
+        L.cross_entropy_forward(x[:, :60].contiguous(), W[:, :60].contiguous(), t)
+    with pytest.raises(P.PoetxError):  # a view off the 16-byte boundary
+        flat = torch.zeros(20 * 64 + 1, device="cuda", dtype=torch.bfloat16)
+        L.cross_entropy_forward(flat[1:].view(20, 64), W, t)
