@@ -10,12 +10,11 @@
 #include <cstdint>
 
 #include "api_util.h"
-#include "dense_plan.h"
 #include "kernels.h"
 #include "poetx.h"
+#include "vocab_plan.h"
 
 using poetx::DType;
-using poetx::TilePlan;
 using poetx::TileProduct;
 using poetx::VocabList;
 using poetx::VocabProduct;
@@ -26,13 +25,6 @@ namespace {
 
 constexpr int64_t kMaxTokens = 1 << 24, kMaxWidth = 1 << 22, kMaxTop = 1024;
 constexpr int64_t kMaxValues = INT64_C(1) << 35;  // of x or W
-// What the logits' pieces may take in the workspace: the forward's partial
-// sums of a range of rows, the backward's gradient of a range of columns (every
-// piece adds to g_x's float32 sums; 8192 x 131072 x 4096 in pieces of 128 MB 19300
-// us, 256 19150, 512 18880, 1024 19100).
-constexpr int64_t kPartBytes = INT64_C(128) << 20, kPieceBytes = INT64_C(512) << 20;
-constexpr int64_t kTile = 256;  // rows and columns of a piece, where there is more than one
-
 DType dtype_of(const poetx_vocab_desc* d) {
   return d->act == POETX_BF16 ? DType::BF16 : DType::F32;
 }
@@ -78,203 +70,10 @@ VocabList list_at(VocabList l, int64_t row) {
     l.teacher = static_cast<const char*>(l.teacher) + row * l.top * (l.type == DType::BF16 ? 2 : 4);
   return l;
 }
+poetx::VocabSizes sizes_of(const poetx_vocab_desc* d) {
+  return {dtype_of(d), d->tokens, d->d, d->vocab, d->top};
+}
 float scale_of(const poetx_vocab_desc* d) { return 1.44269504088896341f / d->temperature; }
-
-// The time (us) of `tiles` 256 x 256 tiles of the products of vocab_dense.hip
-// over K: a round of the 256 CUs is 1.35 us for each 64 of K and 10 for its end
-// (measured: logits 52.7 and 93 a round at K = 2048 and 4096, with their gradient
-// 54.8 and 97.5, g_W 29, 101 and 194 at 1024, 4096 and 8192).
-float dense_cost(int64_t tiles, int64_t K) {
-  return 3.0f + (float)ceil_div(tiles, 256) * (10.0f + 1.35f * (float)K / 64);
-}
-
-// Columns of the logits of `rows` rows on the 256 x 256 tiles; the rest, if any, go
-// to the tile kernel: what a last round of the CUs that would be nearly empty
-// holds (777 x 50001 x 2048 forward 217 -> 174 us), or what is left of the
-// last tile where the copy of W's rows that it would take (`copy` us) costs more.
-struct Columns {
-  int64_t dense;
-  TilePlan tile;
-  float cost;
-};
-Columns split_columns(DType t, int64_t rows, int64_t cols, int64_t K, float copy) {
-  Columns best = {0, plan_tile_product(t, rows, cols, K, false, 1), 0.0f};
-  best.cost = best.tile.nsplit ? best.tile.cost : 1e30f;
-  if (t != DType::BF16 || !poetx::vocab_dense_supported(rows, cols, K)) return best;
-  const int64_t rt = ceil_div(rows, kTile), panels = cols / kTile;
-  const int64_t whole = rt * panels / 256 * 256 / rt;  // (in whole rounds)
-  for (int64_t n : {ceil_div(cols, kTile), panels, whole}) {
-    if (n < 1) continue;
-    Columns c = {std::min(n * kTile, cols), {}, dense_cost(rt * n, K)};
-    if (c.dense % kTile) c.cost += copy;
-    if (c.dense < cols) {
-      c.tile = plan_tile_product(t, rows, cols - c.dense, K, false, 1);
-      c.cost += c.tile.nsplit ? c.tile.cost : 1e30f;
-    }
-    if (c.cost < best.cost) best = c;
-  }
-  return best;
-}
-
-// The forward's partial sums: `rows` rows at a time, so that they stay within
-// kPartBytes.
-// A teacher's ids get their logits out of the products (`cells`, two launches'
-// at most) where reading W's rows for each of them again would take longer than
-// sorting them into the waves' cells and picking them out of the accumulators
-// (4096 x 65536 x 2048, 64 ids a row: 116 us against 11 and about 40).
-struct FwdPlan {
-  Columns cols;
-  int64_t rows, slots;
-  bool copied;  // W_last
-  bool cells;
-  size_t z, last, part, offsets[2], entries[2], total;
-};
-struct CellSizes {
-  size_t offsets, entries;  // bytes
-  bool possible;
-};
-CellSizes cell_sizes(const poetx::CellShape& c, int64_t rows, int64_t cols, int top) {
-  const int64_t n = c.row_cells(rows), bins = c.bins(cols);
-  return {align_up((size_t)(n * (bins + 1) * 4)), align_up((size_t)(n * c.rows * top * 4)),
-          bins <= poetx::kMaxBins};
-}
-FwdPlan plan_fwd(const poetx_vocab_desc* d) {
-  FwdPlan p = {};
-  const DType t = dtype_of(d);
-  p.rows = d->tokens;
-  for (;;) {
-    p.cols = split_columns(t, p.rows, d->vocab, d->d, 5.0f);
-    p.slots = 2 * ceil_div(p.cols.dense, kTile);
-    if (p.cols.dense < d->vocab)
-      p.slots += p.cols.tile.nsplit
-                     ? poetx::vocab_tile_slots(t, p.cols.tile, d->vocab - p.cols.dense)
-                     : INT32_MAX;
-    if (p.slots * p.rows * 8 <= kPartBytes || p.rows <= kTile) break;
-    p.rows = (p.rows / 2 + kTile - 1) / kTile * kTile;
-  }
-  p.last = d->top ? 0 : align_up((size_t)d->tokens * 4);  // (the targets' logits)
-  p.copied = p.cols.dense % kTile != 0;
-  p.part = p.last + (p.copied ? align_up((size_t)(kTile * d->d) * act_size(d->act)) : 0);
-  p.total = p.part + align_up((size_t)(p.slots * p.rows * 8));
-  const double read = (double)list_entries(d) * d->d * act_size(d->act) / 9.0e6;  // us
-  if (d->top && read > 20.0) {
-    const int64_t rest = d->vocab - p.cols.dense;
-    CellSizes c[2] = {{0, 0, true}, {0, 0, true}};
-    if (p.cols.dense) c[0] = cell_sizes(poetx::vocab_dense_cells(), p.rows, p.cols.dense, d->top);
-    if (rest)
-      c[1] = cell_sizes(poetx::vocab_tile_cells(t, p.cols.tile), p.rows, rest, d->top);
-    p.cells = c[0].possible && c[1].possible;
-    for (int i = 0; p.cells && i < 2; ++i) {
-      p.offsets[i] = p.total;
-      p.entries[i] = p.offsets[i] + c[i].offsets;
-      p.total = p.entries[i] + c[i].entries;
-    }
-  }
-  return p;
-}
-
-// The backward: `piece` columns of the vocabulary at a time.
-struct BwdPlan {
-  bool dense;
-  int64_t padded;       // rows of xs and gz
-  int64_t piece, pieces, ldg;
-  int splits, kchunk;   // dense: of g_x's reduction over a piece
-  size_t rows, last, xs, gz, acc, part, total;
-  bool summed() const { return pieces > 1 || splits > 1; }
-};
-// g_z's two products of a piece of n columns on the tile kernel, each by itself
-// or (few launches where they are what costs) in one
-struct TileProducts {
-  TilePlan gx, gw;
-  poetx::TilePairPlan pair;
-  bool paired;
-  bool few;  // g_W on its own kernel for few tokens
-  size_t part_floats() const {
-    const size_t alone = std::max(gx.part_floats, gw.part_floats);
-    return paired ? std::max(alone, pair.gx.part_floats + pair.gw.part_floats) : alone;
-  }
-};
-TileProducts tile_products(const poetx_vocab_desc* d, int64_t n) {
-  const DType t = dtype_of(d);
-  TileProducts p;
-  p.gx = plan_tile_product(t, d->tokens, d->d, n, false, poetx::kManySplits);
-  p.gw = plan_tile_product(t, n, d->d, d->tokens, false);
-  p.pair = plan_tile_pair(t, d->tokens, d->d, n, poetx::kManySplits);
-  // a launch for the turned copy of x and one that stores g_W
-  const float few = 6.0f + (float)(n * d->d * (int64_t)act_size(d->act)) / 3.2e6f;
-  p.few = d->tokens <= poetx::kFewTokens &&
-          few < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
-  p.paired = !p.few && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
-  return p;
-}
-void set_pieces(const poetx_vocab_desc* d, BwdPlan& p) {
-  const int64_t es = (int64_t)act_size(d->act);
-  const int64_t most = std::max(kTile, kPieceBytes / (p.padded * es) / kTile * kTile);
-  p.pieces = ceil_div(d->vocab, most);
-  p.piece = p.pieces == 1 ? d->vocab : ceil_div(ceil_div(d->vocab, p.pieces), kTile) * kTile;
-  p.pieces = ceil_div(d->vocab, p.piece);
-  p.ldg = ceil_div(p.piece, kTile) * kTile;
-}
-// g_x's tiles are few where tokens and d are: its reduction, the vocabulary, is
-// split so that they fill the CUs
-float split_gx(const poetx_vocab_desc* d, BwdPlan& p) {
-  const int64_t tiles = p.padded / kTile * ceil_div(d->d, kTile);
-  float best = 1e30f;
-  for (int s = 1; s <= 128; s += s < 16 ? 1 : 8) {
-    const int64_t chunk = ceil_div(ceil_div(p.piece, s), kTile) * kTile;
-    const int64_t n = ceil_div(p.piece, chunk);
-    // (a slab is written and read once more)
-    const float cost = dense_cost(tiles * n, chunk) +
-                       (n > 1 ? 3.0f + (float)(8 * n * d->tokens * d->d) / 5e6f : 0.0f);
-    if (cost >= best) continue;
-    best = cost;
-    p.splits = (int)n;
-    p.kchunk = (int)chunk;
-  }
-  return best;
-}
-BwdPlan plan_bwd(const poetx_vocab_desc* d) {
-  BwdPlan p = {};
-  const DType t = dtype_of(d);
-  const int64_t es = (int64_t)act_size(d->act);
-  p.splits = 1;
-  if (t == DType::BF16 && poetx::vocab_dense_supported(d->tokens, d->vocab, d->d)) {
-    p.padded = ceil_div(d->tokens, kTile) * kTile;
-    set_pieces(d, p);
-    const float dense = split_columns(t, p.padded, p.piece, d->d, 1.0f).cost + split_gx(d, p) +
-                        dense_cost(ceil_div(p.piece, kTile) * ceil_div(d->d, kTile), d->tokens);
-    const float tile = plan_tile_product(t, d->tokens, p.piece, d->d, false, 1).cost +
-                       plan_tile_product(t, d->tokens, d->d, p.piece, false, poetx::kManySplits).cost +
-                       plan_tile_product(t, p.piece, d->d, d->tokens, false).cost;
-    p.dense = dense < tile;
-  }
-  if (!p.dense) {
-    p.padded = d->tokens;
-    p.splits = 1;
-    set_pieces(d, p);
-  }
-  size_t off = 0;
-  p.rows = off;
-  off += align_up((size_t)p.padded * sizeof(VocabRow));
-  p.last = off;
-  if (p.dense && d->vocab % kTile) off += align_up((size_t)(kTile * d->d * es));
-  p.xs = off;
-  const int64_t copied = p.dense || d->tokens > poetx::kFewTokens
-                             ? p.padded
-                             : poetx::few_padded(t, (int)d->tokens);
-  off += align_up((size_t)(copied * d->d * es));
-  p.gz = off;
-  off += align_up((size_t)(p.padded * p.ldg * es));
-  p.acc = off;
-  if (p.summed()) off += align_up((size_t)d->tokens * d->d * 4 * p.splits);
-  p.part = off;
-  if (!p.dense) {
-    const size_t rest = tile_products(d, d->vocab - (p.pieces - 1) * p.piece).part_floats();
-    off += align_up(std::max(tile_products(d, p.piece).part_floats(), rest) * 4);
-  }
-  p.total = off;
-  return p;
-}
 
 bool any_overlap(const Range* outs, int nout, const Range* ins, int nin) {
   for (int i = 0; i < nout; ++i) {
@@ -302,7 +101,7 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   if (!aligned16(x) || !aligned16(W) || !aligned_to(ids, 8) || !aligned_to(loss, 4) ||
       !aligned_to(lse, 4) || !aligned_to(z, 4) || !aligned_to(teacher, act_size(d->teacher)))
     return POETX_ERR_ALIGN;
-  const FwdPlan plan = plan_fwd(d);
+  const poetx::VocabFwdPlan plan = poetx::plan_vocab_fwd(sizes_of(d));
   if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
   if (!aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t rows4 = (size_t)d->tokens * 4, n = list_entries(d);
@@ -331,7 +130,7 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
     const int64_t rows = std::min(plan.rows, d->tokens - at);
     // (the dense tiles take 256 rows at least: the last range begins early, and
     // forms some rows' sums again)
-    const int64_t r = plan.cols.dense ? std::min(at, std::max(d->tokens - kTile, INT64_C(0))) : at;
+    const int64_t r = plan.cols.dense ? std::min(at, std::max(d->tokens - poetx::kTileRows, INT64_C(0))) : at;
     VocabProduct p;
     p.x = static_cast<const char*>(x) + r * d->d * act_size(d->act);
     p.W = W;
@@ -380,7 +179,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
       !aligned_to(g_loss, 4) || !aligned_to(g_lse, 4) || !aligned_to(lse, 4) || !aligned_to(z, 4) ||
       !aligned_to(teacher, act_size(d->teacher)))
     return POETX_ERR_ALIGN;
-  const BwdPlan plan = plan_bwd(d);
+  const poetx::VocabBwdPlan plan = poetx::plan_vocab_bwd(sizes_of(d));
   if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
   if (!aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t rows4 = (size_t)d->tokens * 4, n = list_entries(d);
@@ -401,14 +200,14 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
   void* xs = g_W || plan.dense ? w + plan.xs : nullptr;
   char* gz = w + plan.gz;
   float* acc = reinterpret_cast<float*>(w + plan.acc);
-  const bool ragged = plan.dense && d->vocab % kTile != 0;
+  const bool ragged = plan.dense && d->vocab % poetx::kTileRows != 0;
   poetx::VocabCopies copies;
   copies.x = x;
   copies.xs = xs;
   copies.tiled = plan.dense;
   copies.W = W;
   copies.W_last = ragged ? w + plan.last : nullptr;
-  if (g_W && !plan.dense && tile_products(d, std::min(plan.piece, d->vocab)).few) {
+  if (g_W && !plan.dense && plan.few) {
     copies.xs = nullptr;
     copies.xt = w + plan.xs;
     copies.xt_rows = poetx::few_padded(t, (int)d->tokens);
@@ -421,8 +220,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     const void* last = ragged && c + cols == d->vocab ? copies.W_last : nullptr;
     char* gWc = g_W ? static_cast<char*>(g_W) + c * d->d * es : nullptr;
     // the gradient of the piece's logits
-    Columns split = {0, {}, 0.0f};
-    if (plan.dense) split = split_columns(t, plan.padded, cols, d->d, 1.0f);
+    const poetx::VocabColumns split = poetx::plan_vocab_columns(sizes_of(d), plan, cols);
     VocabProduct p;
     p.x = xs;
     p.W = Wc;
@@ -435,9 +233,9 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
       p.W = Wc + split.dense * d->d * es;
       p.M = (int)d->tokens; p.N = (int)(cols - split.dense);
       p.col0 = (int)(c + split.dense);
-      POETX_TRY(poetx::launch_vocab_grad_tile(
-          t, plan_tile_product(t, p.M, p.N, d->d, false, 1), p, rows,
-          gz + split.dense * kTile * es, plan.ldg, plan.dense, s));
+      POETX_TRY(poetx::launch_vocab_grad_tile(t, split.tile, p, rows,
+                                              gz + split.dense * poetx::kTileRows * es, plan.ldg,
+                                              plan.dense, s));
     }
     if (teacher)
       POETX_TRY(poetx::launch_vocab_listed_grad(t, list, d->tokens, rows, z, gz, plan.ldg,
@@ -453,7 +251,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
                                                (int)d->d, (int)cols, gWc, s));
       continue;
     }
-    const TileProducts tiles = tile_products(d, cols);
+    const poetx::VocabProducts tiles = poetx::plan_vocab_products(sizes_of(d), cols);
     float* part = reinterpret_cast<float*>(w + plan.part);
     TileProduct qx, qw;
     // g_x += g_z W: B(n, k) = W[k][n]
@@ -494,11 +292,11 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
 extern "C" {
 
 size_t poetx_vocab_fwd_workspace_size(const poetx_vocab_desc* d) {
-  return check_desc(d) == POETX_OK ? plan_fwd(d).total : 0;
+  return check_desc(d) == POETX_OK ? poetx::plan_vocab_fwd(sizes_of(d)).total : 0;
 }
 
 size_t poetx_vocab_bwd_workspace_size(const poetx_vocab_desc* d) {
-  return check_desc(d) == POETX_OK ? plan_bwd(d).total : 0;
+  return check_desc(d) == POETX_OK ? poetx::plan_vocab_bwd(sizes_of(d)).total : 0;
 }
 
 int poetx_cross_entropy_fwd(const poetx_vocab_desc* d, const void* x, const void* W,

@@ -11,6 +11,8 @@
 // that eight; in the tiled layout (kernels.h) the wave's 16 rows x 32 columns
 // are then 1 KB of consecutive bytes. Both of g_z's products read whole
 // 128-byte lines of that layout, K-major (g_x = g_z W) and M-major (g_W = g_z^T x).
+#include <algorithm>
+
 #include "dense_core.h"
 #include "epilogue.h"
 #include "vocab.h"
@@ -33,7 +35,9 @@ __device__ __forceinline__ const bf16_t* panel(const bf16_t* W, const bf16_t* W_
 // products, and is there at there(), behind them: a wait for a load after the next
 // tile's copies would be one for the copies too (the counter is in order, and the
 // compiler does not know of them).
-template <int LATE, typename D, typename Set, typename Before, typename There, typename End>
+// SHORT: reductions of fewer than the 8 K tiles that mainloop_late() takes occur.
+template <int LATE, bool SHORT = false, typename D, typename Set, typename Before, typename There,
+          typename End>
 __device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, int m_last,
                                           int n_last, const Set& set, const Before& before,
                                           const There& there, const End& end) {
@@ -56,8 +60,13 @@ __device__ __forceinline__ void tile_loop(D& d, int num_mt, int num_nt, int nq, 
   for (;;) {
     const int m0 = min(mt * BM, m_last), n0 = min(nt * BN, n_last), nt0 = nt, q0 = q;
     before(m0, n0, nt0);
-    d.template start_late<LATE>(late);
-    d.template mainloop_late<LATE>(ntiles, late);
+    if (SHORT && ntiles < 8) {
+      d.start(ntiles);
+      d.mainloop(ntiles);
+    } else {
+      d.template start_late<LATE>(late);
+      d.template mainloop_late<LATE>(ntiles, late);
+    }
     d.settle();
     there();
     wait_lds();
@@ -262,7 +271,8 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
 // into its own float32 slab [rows][N], added to what is there with `add`; or,
 // with y, one range whose result is g_x itself.
 // LAST: the piece ends inside a K tile (a choice of the source at every copy:
-// 8192 x 131072 x 4096 backward 19150 us with it in every piece, 18890 without).
+// 8192 x 131072 x 4096 backward 19150 us with it in every piece, 18890 without),
+// or one of its ranges is shorter than 256.
 template <bool WHOLE, bool LAST>
 __global__ void __launch_bounds__(NT)
 vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
@@ -271,7 +281,7 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
   typedef Dense<false, false, true, false, LAST> D;
   D d;
   d.init(ldg, N, true, false);
-  tile_loop<FM * FN / 2>(d, M / BM, (N + BN - 1) / BN, splits, M, N - BN,
+  tile_loop<FM * FN / 2, LAST>(d, M / BM, (N + BN - 1) / BN, splits, M, N - BN,
             [&](int q, int m0, int n0) __attribute__((always_inline)) {
               // (the tiled layout's blocks of 32 columns lie one behind another)
               d.set_tile(gz + (int64_t)q * kchunk * BM, W + (int64_t)q * kchunk * N, ldg, N, m0, n0);
@@ -374,6 +384,8 @@ vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, in
             });
 }
 
+constexpr int kLongK = 8 * BK;  // of mainloop_late()
+
 const bf16_t* b16(const void* p) { return static_cast<const bf16_t*>(p); }
 
 }  // namespace
@@ -417,9 +429,10 @@ hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, con
   int grid = 0;
   const hipError_t e = dense_grid(M, (int64_t)(d + BN - 1) / BN * BN * splits, &grid);
   if (e != hipSuccess) return e;
-  const bool ragged = cols % BK != 0;
+  const bool cut = cols % BK != 0;
+  const bool ragged = cut || std::min(kchunk, cols - (splits - 1) * kchunk) < kLongK;
   // (its rows from the last whole K tile on)
-  const bf16_t* last = ragged ? b16(W_last) + (int64_t)(cols / BK * BK % BN) * d : nullptr;
+  const bf16_t* last = cut ? b16(W_last) + (int64_t)(cols / BK * BK % BN) * d : nullptr;
 #define POETX_GX(WHOLE, LAST)                                                                  \
   hipLaunchKernelGGL((vocab_gx_kernel<WHOLE, LAST>), dim3(grid), dim3(NT), 0, s, b16(gz),      \
                      b16(W), last, (int)rows, (int)M, d, cols, ldg, splits, kchunk, slabs,     \
@@ -435,7 +448,7 @@ hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, con
 hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
                                  int cols, void* g_W, hipStream_t s) {
   if (!vocab_dense_supported(256, cols, d) || ldg % BN != 0 || ldg < cols || padded % BK != 0 ||
-      padded < BK)
+      padded < kLongK)
     return hipErrorInvalidValue;
   int grid = 0;
   const hipError_t e = dense_grid(cols, d, &grid);

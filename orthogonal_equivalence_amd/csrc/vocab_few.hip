@@ -129,11 +129,6 @@ hipError_t launch_steps(const void* gz, int64_t ldg, const void* xt, int tokens,
 
 }  // namespace
 
-int few_padded(DType t, int tokens) {
-  const int k = t == DType::BF16 ? 32 : 16;
-  return (tokens + k - 1) / k * k;
-}
-
 hipError_t launch_few_gw(DType t, const void* gz, int64_t ldg, const void* xt, int tokens, int cols,
                          int d, void* g_W, hipStream_t s) {
   if (tokens < 1 || tokens > kFewTokens || cols < 1 || d < 1 || d > (1 << 22))

@@ -125,7 +125,8 @@ hipError_t launch_cfg(const TileProduct& p, const End& end, hipStream_t s) {
   return hipGetLastError();
 }
 
-// the shapes of dense_plan.cpp, with their rings as in tilegemm.hip
+// the shapes of dense_plan.cpp, with their rings as in tilegemm.hip (their waves:
+// vocab_plan.cpp's tables too)
 template <typename End>
 hipError_t launch_end(DType t, const TilePlan& plan, const VocabProduct& v, const End& end,
                       hipStream_t s) {
@@ -154,26 +155,6 @@ hipError_t launch_end(DType t, const TilePlan& plan, const VocabProduct& v, cons
 }
 
 }  // namespace
-
-namespace {
-// rows, columns, wave rows and wave columns of a tile, by shape (launch_end)
-constexpr int kBf16Tiles[][4] = {{256, 128, 4, 2}, {128, 128, 2, 4}, {128, 64, 4, 2},
-                                 {64, 64, 2, 2},   {32, 64, 1, 4},   {128, 64, 4, 2}};
-constexpr int kF32Tiles[][4] = {{64, 64, 2, 2}, {32, 64, 1, 4}};
-const int* tile_of(DType t, const TilePlan& plan) {
-  return t == DType::F32 ? kF32Tiles[plan.shape] : kBf16Tiles[plan.shape];
-}
-}  // namespace
-
-int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N) {
-  const int* h = tile_of(t, plan);
-  return (N + h[1] - 1) / h[1] * h[3];
-}
-
-CellShape vocab_tile_cells(DType t, const TilePlan& plan) {
-  const int* h = tile_of(t, plan);
-  return CellShape{h[0] / h[2], h[1] / h[3], false};
-}
 
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
                                  int64_t part_ld, const int64_t* targets, float* z,

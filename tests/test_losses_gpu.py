@@ -154,17 +154,17 @@ def test_distill(tokens, d, vocab, top, temperature, dyadic, kind, dtype):
     within("g_x alone", only, ref["g_x"], tol_x)
 
 
-def counted(tokens, d, vocab, seed):
+def counted(tokens, d, vocab, seed, dtype=torch.bfloat16):
     """Operands whose logits are all 0 (x lives in the first half of the
     columns, W in the second) and whose gradients are integers: with
     g_loss = b and g_lse = vocab - b the logits' gradient is 1, and 1 - b at
     the target (vocab exp(-lse) is within 2^-20 of 1, which bf16 rounds to 1)."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     h = d // 2
-    x = torch.zeros(tokens, d, device="cuda", dtype=torch.bfloat16)
-    W = torch.zeros(vocab, d, device="cuda", dtype=torch.bfloat16)
-    x[:, :h] = torch.randint(-2, 3, (tokens, h), generator=gen, device="cuda").bfloat16()
-    W[:, h:] = torch.randint(-1, 2, (vocab, d - h), generator=gen, device="cuda").bfloat16()
+    x = torch.zeros(tokens, d, device="cuda", dtype=dtype)
+    W = torch.zeros(vocab, d, device="cuda", dtype=dtype)
+    x[:, :h] = torch.randint(-2, 3, (tokens, h), generator=gen, device="cuda").to(dtype)
+    W[:, h:] = torch.randint(-1, 2, (vocab, d - h), generator=gen, device="cuda").to(dtype)
     t = torch.randint(0, vocab, (tokens,), generator=gen, device="cuda")
     t[torch.rand(tokens, generator=gen, device="cuda") < 0.2] = -100
     t[0] = vocab - 1
@@ -176,6 +176,10 @@ def counted(tokens, d, vocab, seed):
     (1000, 320, 20483), (2048, 64, 131072), (2304, 256, 131072), (4100, 96, 65537),
     (9000, 64, 131072), (515, 1064, 3001), (64, 512, 40001), (5, 4096, 9001), (40, 72, 131072),
     (33, 2056, 20001),
+    # (g_x whole in one product, with and without a ragged last K tile; columns
+    # shifted back; several pieces with them)
+    (8192, 2048, 515), (8192, 2048, 1024), (777, 352, 20003), (2304, 288, 131072),
+    (300, 4096, 3001), (256, 256, 256), (257, 2080, 777),
 ])
 def test_counted_operands(tokens, d, vocab):
     """Every element of loss, lse, g_x and g_W of large and ragged sizes (several
@@ -201,6 +205,37 @@ def test_counted_operands(tokens, d, vocab):
     want_W = xd.sum(0).expand(vocab, d).clone()
     want_W.index_add_(0, t.clamp(min=0), -b * xd)
     assert torch.equal(g_W.double(), want_W.float().bfloat16().double())
+
+
+@pytest.mark.parametrize("case", V.CASES, ids=str)
+def test_every_variant(case):
+    """Both directions on operands whose results are whole numbers, every element:
+    as above, with an lse of 0 given to the backward, so that exp(z - lse) is 1
+    to the last bit in both types."""
+    print("variant", case, flush=True)
+    t, tokens, d, vocab = case
+    dtype = torch.bfloat16 if t == V.BF16 else torch.float32
+    x, W, target = counted(tokens, d, vocab, 11, dtype)
+    part = target >= 0
+    loss, lse = L.cross_entropy_forward(x, W, target)
+    want = torch.where(part, math.log(vocab), 0.0).double()
+    assert bool(((lse.double() - want).abs() <= 4 * 2.0 ** -24 * math.log(vocab)).all())
+    assert torch.equal(loss, lse)
+    g_loss = torch.full((tokens,), 3.0, device="cuda")
+    g_x, g_W = L.cross_entropy_backward(g_loss, x, W, target, torch.zeros_like(lse),
+                                        g_lse=g_loss * 0 - 2.0, need_g_W=True)
+    Wd, xd = W.double(), torch.where(part[:, None], x.double(), 0.0)
+    want_x = torch.where(part[:, None], Wd.sum(0) - 3 * Wd[target.clamp(min=0)], 0.0)
+    assert torch.equal(g_x, want_x.float().to(dtype))
+    want_W = xd.sum(0).expand(vocab, d).clone()
+    want_W.index_add_(0, target.clamp(min=0), -3 * xd)
+    assert torch.equal(g_W, want_W.float().to(dtype))
+
+
+@pytest.mark.parametrize("case", V.LISTED, ids=str)
+def test_every_listed_variant(case):
+    t, tokens, d, vocab, top = case
+    test_distill(tokens, d, vocab, top, 1.0, True, "f32", "bf16" if t == V.BF16 else "f32")
 
 
 def test_rows_that_take_no_part():

@@ -109,3 +109,33 @@ def lse_tolerance(ref, temperature, d, x, W, dyadic):
         bound = x.double().abs().mm(W.double().abs().t()).max(1).values
         tol = tol + 2 * u * (d + 8) * bound / temperature
     return tol
+
+
+F32, BF16 = 0, 1
+# Sizes whose plans reach every kernel variant that drawn sizes do (held to it by
+# test_vocab_plan.py). CASES: both directions of cross entropy; LISTED: of
+# distillation, with the entries of a row's list.
+CASES = [  # dtype, tokens, d, vocab
+    (BF16, 65, 8, 11889), (BF16, 44, 8, 24458), (BF16, 1253, 8, 1), (BF16, 4834, 296, 1),
+    (BF16, 471, 3712, 1), (BF16, 168, 336, 6449), (BF16, 16, 72, 96113), (F32, 1, 928, 15857),
+    (BF16, 7398, 392, 279), (BF16, 1422, 8, 5376), (BF16, 5608, 256, 1106), (BF16, 585, 3584, 427),
+    (BF16, 333, 448, 77312), (BF16, 42, 224, 129074), (BF16, 1189, 736, 15165), (F32, 40, 72, 63264),
+    (F32, 20, 152, 74599), (BF16, 759, 768, 22239), (BF16, 5438, 80, 5913), (BF16, 2313, 2752, 1338),
+    (BF16, 1056, 1312, 9504), (F32, 631, 8, 65783), (F32, 39, 400, 40688), (BF16, 672, 2816, 9001),
+    (BF16, 8100, 400, 5148), (BF16, 2560, 256, 14080), (BF16, 298, 256, 115906), (BF16, 650, 256, 69815),
+    (F32, 4623, 8, 60672), (F32, 887, 1152, 1792), (F32, 84, 2048, 11439), (BF16, 1792, 1536, 14592),
+    (BF16, 3137, 2720, 3077), (F32, 7930, 96, 3471), (BF16, 3756, 3840, 2304), (BF16, 1350, 256, 109972),
+    (F32, 4849, 16, 49508), (F32, 1896, 1024, 2972), (BF16, 5600, 3392, 3840), (BF16, 2379, 320, 108458),
+    (BF16, 4096, 2816, 36606),
+]
+# dtype, tokens, d, vocab, top
+LISTED = [
+    (BF16, 1, 8, 1, 6), (F32, 1, 8, 1, 29), (BF16, 4748, 3360, 6, 12),
+    (F32, 2017, 256, 1, 92), (F32, 36, 8, 28221, 54), (BF16, 1792, 1528, 1, 71),
+    (F32, 839, 8, 512, 23), (F32, 7122, 2624, 3, 2), (BF16, 138, 4064, 256, 1),
+    (BF16, 274, 1024, 26351, 3), (BF16, 2, 192, 61450, 11), (BF16, 1263, 288, 14065, 85),
+    (F32, 52, 72, 50853, 1), (BF16, 262, 256, 100366, 5), (BF16, 270, 2432, 10202, 4),
+    (BF16, 953, 768, 17664, 16), (BF16, 6039, 512, 3401, 36), (BF16, 129, 3000, 17764, 10),
+    (F32, 2482, 2336, 256, 1), (BF16, 399, 544, 66539, 10), (BF16, 4698, 8, 65522, 26),
+    (BF16, 3606, 256, 70033, 25),
+]
