@@ -157,9 +157,9 @@ cells_kernel(const VocabList l, int64_t M, int64_t col0, int64_t N, const CellSh
 }
 
 // R rows a workgroup, their slots dealt over NT / R threads each (R a power of
-// two, chosen so that a warm row of part is read in whole lines where there
-// are rows enough, and by many threads where there are few); the threads'
-// parts are joined in order. Targets: the loss too.
+// two: 32 where there are rows enough to read part in whole lines, 1 where there
+// are few: 32 rows of 5408 slots 39.4 us with 32, 5.0 with 1); the threads' parts
+// are joined in order. Targets: the loss too.
 template <bool TARGETS>
 __global__ void __launch_bounds__(NT)
 join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int R, const VocabList l,
@@ -227,26 +227,34 @@ __device__ __forceinline__ bool takes_part(int64_t id, float t) { return id >= 0
 __device__ __forceinline__ float teacher_exp(float t, float top, float rt) {
   return __builtin_amdgcn_exp2f((t - top) * rt);
 }
-__device__ __forceinline__ Teacher read_teacher(const VocabList& l, int64_t row, float rt, int lane) {
+// The row's list is read once, into LDS: ids (-1 where an entry takes no part or is
+// past the vocabulary) and logits (-inf where it takes none), padded to a multiple
+// of 4.
+__device__ __forceinline__ Teacher read_teacher(const VocabList& l, int64_t row, float rt, int lane,
+                                                int* ids, float* t) {
   Teacher w;
   float top = -INFINITY;
   bool any = false, bad = false;
-  for (int k = lane; k < l.top; k += 64) {
-    const int64_t id = l.ids[row * l.top + k];
-    const float t = teacher_logit(l, row * l.top + k);
-    if (!takes_part(id, t)) continue;
-    any = true;
-    bad |= id >= l.vocab;
-    top = fmaxf(top, t);
+  for (int k = lane; k < (l.top + 3) / 4 * 4; k += 64) {
+    int64_t id = -1;
+    float v = -INFINITY;
+    if (k < l.top) {
+      id = l.ids[row * l.top + k];
+      v = teacher_logit(l, row * l.top + k);
+    }
+    const bool in = takes_part(id, v), past = in && id >= l.vocab;
+    any |= in;
+    bad |= past;
+    ids[k] = in && !past ? (int)id : -1;
+    t[k] = in ? v : -INFINITY;
+    if (in) top = fmaxf(top, v);
   }
   w.top = wave_max(top);
   w.any = __any(any);
   w.bad = __any(bad);
   float e = 0.0f;
-  for (int k = lane; k < l.top; k += 64) {
-    const float t = teacher_logit(l, row * l.top + k);
-    if (takes_part(l.ids[row * l.top + k], t)) e += teacher_exp(t, w.top, rt);
-  }
+  for (int k = lane; k < l.top; k += 64)  // (its own entries)
+    if (!(t[k] == -INFINITY)) e += teacher_exp(t[k], w.top, rt);
   w.total = wave_sum(e);
   return w;
 }
@@ -259,15 +267,17 @@ distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z
   const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
   if (row >= rows) return;
   const float inv = 1.0f / l.temperature, rt = kLog2e / l.temperature;
-  const Teacher w = read_teacher(l, row, rt, lane);
+  __shared__ int ids[NWAVES][kMaxTop];
+  __shared__ float ts[NWAVES][kMaxTop];
+  const float* t = ts[threadIdx.x >> 6];
+  const Teacher w = read_teacher(l, row, rt, lane, ids[threadIdx.x >> 6], ts[threadIdx.x >> 6]);
   const float log_total = logf(w.total), own = lse[row];
   float sum = 0.0f;
   for (int k = lane; k < l.top; k += 64) {
-    const float t = teacher_logit(l, row * l.top + k);
-    if (!takes_part(l.ids[row * l.top + k], t)) continue;
-    const float p = teacher_exp(t, w.top, rt) / w.total;
+    if (t[k] == -INFINITY) continue;
+    const float p = teacher_exp(t[k], w.top, rt) / w.total;
     if (p == 0.0f) continue;
-    sum += p * (((t - w.top) - z[row * l.top + k]) * inv - log_total + own);
+    sum += p * (((t[k] - w.top) - z[row * l.top + k]) * inv - log_total + own);
   }
   sum = wave_sum(sum);
   if (lane == 0) {
@@ -377,21 +387,19 @@ __global__ void __launch_bounds__(NT)
 listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__ r,
                    const float* __restrict__ z, T* __restrict__ gz, int64_t ldg, int tiled,
                    int col0, int N) {
-  __shared__ int ids[NWAVES][kMaxTop];
-  __shared__ float p[NWAVES][kMaxTop];
+  __shared__ __attribute__((aligned(16))) int ids[NWAVES][kMaxTop];
+  __shared__ __attribute__((aligned(16))) float p[NWAVES][kMaxTop];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = (int64_t)blockIdx.x * NWAVES + wave;
   if (row >= rows) return;
   const VocabRow own = r[row];
   if (own.a == 0.0f) return;  // (whose gradient is zero)
   const float rt = kLog2e / l.temperature;
-  const Teacher w = read_teacher(l, row, rt, lane);
-  for (int k = lane; k < l.top; k += 64) {
-    const int64_t id = l.ids[row * l.top + k];
-    const float t = teacher_logit(l, row * l.top + k);
-    const bool in = takes_part(id, t);
-    ids[wave][k] = in && id < l.vocab ? (int)id : -1;
-    p[wave][k] = in ? teacher_exp(t, w.top, rt) / w.total : 0.0f;
+  const Teacher w = read_teacher(l, row, rt, lane, ids[wave], p[wave]);
+  const int padded = (l.top + 3) / 4 * 4;
+  for (int k = lane; k < padded; k += 64) {
+    const float t = p[wave][k];
+    p[wave][k] = t == -INFINITY ? 0.0f : teacher_exp(t, w.top, rt) / w.total;
   }
   // (a wave reads its own row's entries only)
   asm volatile("" ::: "memory");
@@ -401,8 +409,14 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
     const int id = ids[wave][k];
     if (id < col0 || id >= col0 + N) continue;
     float sum = 0.0f;
-#pragma unroll 8
-    for (int q = 0; q < l.top; ++q) sum += ids[wave][q] == id ? p[wave][q] : 0.0f;
+    for (int q = 0; q < padded; q += 4) {
+      const int4 i = *reinterpret_cast<const int4*>(&ids[wave][q]);
+      const float4 v = *reinterpret_cast<const float4*>(&p[wave][q]);
+      sum += i.x == id ? v.x : 0.0f;
+      sum += i.y == id ? v.y : 0.0f;
+      sum += i.z == id ? v.z : 0.0f;
+      sum += i.w == id ? v.w : 0.0f;
+    }
     const float e = __builtin_amdgcn_exp2f(fmaf(z[row * l.top + k], rt, -own.lse2));
     const int64_t at = tiled ? tiled_offset(row, id - col0, ldg) : row * ldg + (id - col0);
     store_as(gz + at, own.a * (e - sum));
@@ -443,7 +457,7 @@ hipError_t launch_vocab_cells(const VocabList& l, int64_t M, int64_t col0, int64
 hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots, const VocabList& l,
                              int64_t rows, const float* z, float* loss, float* lse, hipStream_t s) {
   int R = 1;
-  while (R < 32 && R < rows) R *= 2;
+  while (R < 32 && R * 256 <= rows) R *= 2;
   const int64_t blocks = (rows + R - 1) / R, loss_blocks = (rows + NWAVES - 1) / NWAVES;
   if (!fits(blocks) || !fits(loss_blocks)) return hipErrorInvalidValue;
   if (!l.teacher) {
