@@ -388,11 +388,13 @@ hipError_t launch_vocab_cells(const VocabList& l, int64_t M, int64_t col0, int64
 // Forward: for every row and slot (a group of the piece's columns)
 // part[slot][row] = (max, sum) with sum_j 2^(scale z_j) = sum 2^max over the slot's
 // columns. vocab_tile_slots of them. With targets [M], z[row] = the logit of
-// the row's, where the piece has it.
+// the row's, where the piece has it; with list.ids, of a piece that is the whole
+// vocabulary, z[row][top] = the list's, as launch_listed_logits has them (by
+// workgroups beside the tiles').
 int64_t vocab_tile_slots(DType t, const TilePlan& plan, int64_t N);
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
                                  int64_t part_ld, const int64_t* targets, float* z,
-                                 const VocabCells& cells, hipStream_t s);
+                                 const VocabCells& cells, const VocabList& list, hipStream_t s);
 // Backward: g_z of the piece in x's type at gz[row][ldg], or in the tiled layout
 // [..][ldg] of which gz is the piece's first block of columns; columns N up to
 // ldg, and rows M up to the next multiple of 32, are zeroed where tiles reach

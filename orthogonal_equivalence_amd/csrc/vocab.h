@@ -8,6 +8,81 @@
 namespace poetx {
 namespace {
 
+template <typename T> struct Vec;  // one 16-byte vector as float32
+template <> struct Vec<bf16_t> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ void load(const bf16_t* p, float v[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Vec<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ void load(const float* p, float v[4]) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  }
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+// The logits at a row's listed ids, four entries a wave (the `at`-th of
+// listed_waves()): x's piece is loaded once for four rows of W. The products are
+// summed in float32 per lane (K / 64 of them), the lanes as a tree.
+constexpr int kEntries = 4;
+__host__ __device__ inline int64_t listed_waves(int64_t rows, int top) {
+  return rows * ((top + kEntries - 1) / kEntries);
+}
+template <typename T>
+__device__ __forceinline__ void listed_logits(const T* __restrict__ x, const T* __restrict__ W,
+                                              const VocabList& l, int64_t rows, int K,
+                                              float* __restrict__ z, int64_t at, int lane) {
+  constexpr int E = Vec<T>::E;
+  const int groups = (l.top + kEntries - 1) / kEntries;
+  const int64_t row = at / groups;
+  const int k0 = (int)(at - row * groups) * kEntries;
+  if (row >= rows) return;
+  int64_t id[kEntries];
+  bool any = false;
+#pragma unroll
+  for (int q = 0; q < kEntries; ++q) {
+    id[q] = k0 + q < l.top ? l.ids[row * l.top + k0 + q] : -1;
+    any |= id[q] >= 0 && id[q] < l.vocab;
+  }
+  float acc[kEntries] = {};
+  if (any) {
+    const T* w[kEntries];
+#pragma unroll
+    for (int q = 0; q < kEntries; ++q)
+      w[q] = W + (id[q] >= 0 && id[q] < l.vocab ? id[q] : 0) * (int64_t)K;
+#pragma unroll 2
+    for (int k = lane * E; k < K; k += 64 * E) {
+      float xv[E], wv[kEntries][E];
+      Vec<T>::load(x + row * K + k, xv);
+#pragma unroll
+      for (int q = 0; q < kEntries; ++q) Vec<T>::load(w[q] + k, wv[q]);
+#pragma unroll
+      for (int q = 0; q < kEntries; ++q)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[q] = fmaf(xv[e], wv[q][e], acc[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kEntries; ++q) {
+    const float v = wave_sum(acc[q]);
+    if (lane == 0 && k0 + q < l.top)
+      z[row * l.top + k0 + q] = id[q] < 0 ? 0.0f : id[q] >= l.vocab ? NAN : v;
+  }
+}
+
 // The maximum and the sum over the four lanes that are 16 apart, in all four:
 // two exchanges of rows of 16 lanes, in the vector unit (through LDS, as
 // __shfl_xor goes, each costs its latency).

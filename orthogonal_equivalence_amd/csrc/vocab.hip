@@ -19,84 +19,18 @@ constexpr int NT = 256, NWAVES = NT / 64;
 constexpr int kMaxTop = 1024;  // entries of a row's list
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
-template <typename T> struct Vec;  // one 16-byte vector as float32
-template <> struct Vec<bf16_t> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void load(const bf16_t* p, float v[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-    }
-  }
-};
-template <> struct Vec<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void load(const float* p, float v[4]) {
-    const float4 w = *reinterpret_cast<const float4*>(p);
-    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-  }
-};
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
   return v;
 }
 
-// One wave a row and four entries: x's piece is loaded once for four rows of
-// W. The products are summed in float32 per lane (K / 64 of them), the lanes as a
-// tree.
-constexpr int kEntries = 4;
 template <typename T>
 __global__ void __launch_bounds__(NT)
 listed_logits_kernel(const T* __restrict__ x, const T* __restrict__ W, const VocabList l,
                      int64_t rows, int K, float* __restrict__ z) {
-  constexpr int E = Vec<T>::E;
-  const int lane = threadIdx.x & 63;
-  const int groups = (l.top + kEntries - 1) / kEntries;
-  const int64_t at = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
-  const int64_t row = at / groups;
-  const int k0 = (int)(at - row * groups) * kEntries;
-  if (row >= rows) return;
-  int64_t id[kEntries];
-  bool any = false;
-#pragma unroll
-  for (int q = 0; q < kEntries; ++q) {
-    id[q] = k0 + q < l.top ? l.ids[row * l.top + k0 + q] : -1;
-    any |= id[q] >= 0 && id[q] < l.vocab;
-  }
-  float acc[kEntries] = {};
-  if (any) {
-    const T* w[kEntries];
-#pragma unroll
-    for (int q = 0; q < kEntries; ++q)
-      w[q] = W + (id[q] >= 0 && id[q] < l.vocab ? id[q] : 0) * (int64_t)K;
-#pragma unroll 2
-    for (int k = lane * E; k < K; k += 64 * E) {
-      float xv[E], wv[kEntries][E];
-      Vec<T>::load(x + row * K + k, xv);
-#pragma unroll
-      for (int q = 0; q < kEntries; ++q) Vec<T>::load(w[q] + k, wv[q]);
-#pragma unroll
-      for (int q = 0; q < kEntries; ++q)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[q] = fmaf(xv[e], wv[q][e], acc[q]);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < kEntries; ++q) {
-    const float v = wave_sum(acc[q]);
-    if (lane == 0 && k0 + q < l.top)
-      z[row * l.top + k0 + q] = id[q] < 0 ? 0.0f : id[q] >= l.vocab ? NAN : v;
-  }
+  listed_logits(x, W, l, rows, K, z, (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6),
+                threadIdx.x & 63);
 }
 
 // One workgroup a row of cells: counts of its entries by cell in LDS, their sums,
@@ -156,63 +90,6 @@ cells_kernel(const VocabList l, int64_t M, int64_t col0, int64_t N, const CellSh
   }
 }
 
-// R rows a workgroup, their slots dealt over NT / R threads each (R a power of
-// two: 32 where there are rows enough to read part in whole lines, 1 where there
-// are few: 32 rows of 5408 slots 39.4 us with 32, 5.0 with 1); the threads' parts
-// are joined in order. Targets: the loss too.
-template <bool TARGETS>
-__global__ void __launch_bounds__(NT)
-join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int R, const VocabList l,
-            int64_t rows, const float* __restrict__ z, float* __restrict__ loss,
-            float* __restrict__ lse) {
-  const int r = threadIdx.x & (R - 1), g = threadIdx.x / R, groups = NT / R;
-  const int64_t row = (int64_t)blockIdx.x * R + r;
-  float m = -INFINITY, s = 0.0f;
-  auto add = [&](float2 v) {
-    const float top = fmaxf(m, v.x), to = fabsf(top) < INFINITY ? top : 0.0f;
-    // (a part of -inf alone is 0 2^-inf; NaN sums stay)
-    s = s * __builtin_amdgcn_exp2f(m - to) + v.y * __builtin_amdgcn_exp2f(v.x - to);
-    m = top;
-  };
-  if (row < rows) {
-    const float2* p = part + row;
-    int64_t i = g;
-    for (; i + 7 * groups < slots; i += 8 * groups) {  // eight loads in flight
-      float2 v[8];
-      float top = m;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        v[q] = p[(i + q * groups) * part_ld];
-        top = fmaxf(top, v[q].x);
-      }
-      const float to = fabsf(top) < INFINITY ? top : 0.0f;
-      s *= __builtin_amdgcn_exp2f(m - to);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s += v[q].y * __builtin_amdgcn_exp2f(v[q].x - to);
-      m = top;
-    }
-    for (; i < slots; i += groups) add(p[i * part_ld]);
-  }
-  __shared__ float2 sums[NT];
-  sums[threadIdx.x] = make_float2(m, s);
-  for (int half = groups / 2; half >= 1; half /= 2) {
-    __syncthreads();
-    if (g < half) {
-      add(sums[threadIdx.x + half * R]);
-      sums[threadIdx.x] = make_float2(m, s);
-    }
-  }
-  if (g != 0 || row >= rows) return;
-  const float at = fabsf(m) < INFINITY ? m : 0.0f;
-  float v = (at + log2f(s)) * kLn2;
-  if constexpr (TARGETS) {
-    const bool part_of = l.ids[row] >= 0;
-    v = part_of ? v : 0.0f;
-    loss[row] = !part_of ? 0.0f : l.ids[row] >= l.vocab ? NAN : v - z[row];
-  }
-  lse[row] = v;
-}
-
 // One row's teacher distribution, by one wave: entry k of lane k % 64. An
 // entry takes part with an id >= 0 and a logit above -inf.
 struct Teacher {
@@ -259,19 +136,14 @@ __device__ __forceinline__ Teacher read_teacher(const VocabList& l, int64_t row,
   return w;
 }
 
-// log p_k = (t_k - top) / T - log total; an entry whose p is 0 adds nothing
-__global__ void __launch_bounds__(NT)
-distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z,
-                    float* __restrict__ loss, float* __restrict__ lse) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
-  if (row >= rows) return;
+// The loss of one row, by one wave: log p_k = (t_k - top) / T - log total; an entry
+// whose p is 0 adds nothing. Its lse, `own`, is stored with it.
+__device__ __forceinline__ void distill_loss(const VocabList& l, int64_t row, float own,
+                                             const float* __restrict__ z, float* __restrict__ loss,
+                                             float* __restrict__ lse, int lane, int* ids, float* t) {
   const float inv = 1.0f / l.temperature, rt = kLog2e / l.temperature;
-  __shared__ int ids[NWAVES][kMaxTop];
-  __shared__ float ts[NWAVES][kMaxTop];
-  const float* t = ts[threadIdx.x >> 6];
-  const Teacher w = read_teacher(l, row, rt, lane, ids[threadIdx.x >> 6], ts[threadIdx.x >> 6]);
-  const float log_total = logf(w.total), own = lse[row];
+  const Teacher w = read_teacher(l, row, rt, lane, ids, t);
+  const float log_total = logf(w.total);
   float sum = 0.0f;
   for (int k = lane; k < l.top; k += 64) {
     if (t[k] == -INFINITY) continue;
@@ -282,8 +154,88 @@ distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z
   sum = wave_sum(sum);
   if (lane == 0) {
     loss[row] = !w.any ? 0.0f : w.bad ? NAN : l.temperature * l.temperature * sum;
-    if (!w.any) lse[row] = 0.0f;
+    lse[row] = w.any ? own : 0.0f;
   }
+}
+__global__ void __launch_bounds__(NT)
+distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z,
+                    float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ int ids[NWAVES][kMaxTop];
+  __shared__ float ts[NWAVES][kMaxTop];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * NWAVES + wave;
+  if (row >= rows) return;
+  distill_loss(l, row, lse[row], z, loss, lse, lane, ids[wave], ts[wave]);
+}
+
+// R rows a workgroup, their slots dealt over NT / R threads each (R a power of
+// two: 32 where there are rows enough to read part in whole lines, 1 where there
+// are few: 32 rows of 5408 slots 39.4 us with 32, 9.1 with 1); the threads' parts
+// are joined in order. Targets: the loss too; a teacher's where a wave has a row or
+// less (kJoinLoss: a launch less), else it has a kernel of its own.
+enum Join { kTargets, kTeacher, kJoinLoss };
+template <Join JOIN>
+__global__ void __launch_bounds__(NT)
+join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int R, const VocabList l,
+            int64_t rows, const float* __restrict__ z, float* __restrict__ loss,
+            float* __restrict__ lse) {
+  const int r = threadIdx.x & (R - 1), g = threadIdx.x / R, groups = NT / R;
+  const int64_t row = (int64_t)blockIdx.x * R + r;
+  float m = -INFINITY, s = 0.0f;
+  auto add = [&](float2 v) {
+    const float top = fmaxf(m, v.x), to = exponent_base(top);
+    // (a part of -inf alone is 0 2^-inf; NaN sums stay)
+    s = s * __builtin_amdgcn_exp2f(m - to) + v.y * __builtin_amdgcn_exp2f(v.x - to);
+    m = top;
+  };
+  if (row < rows) {
+    const float2* p = part + row;
+    int64_t i = g;
+    for (; i + 7 * groups < slots; i += 8 * groups) {  // eight loads in flight
+      float2 v[8];
+      float top = m;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v[q] = p[(i + q * groups) * part_ld];
+        top = fmaxf(top, v[q].x);
+      }
+      const float to = exponent_base(top);
+      s *= __builtin_amdgcn_exp2f(m - to);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += v[q].y * __builtin_amdgcn_exp2f(v[q].x - to);
+      m = top;
+    }
+    for (; i < slots; i += groups) add(p[i * part_ld]);
+  }
+  __shared__ float2 sums[NT];
+  sums[threadIdx.x] = make_float2(m, s);
+  for (int half = groups / 2; half >= 1; half /= 2) {
+    __syncthreads();
+    if (g < half) {
+      add(sums[threadIdx.x + half * R]);
+      sums[threadIdx.x] = make_float2(m, s);
+    }
+  }
+  if constexpr (JOIN == kJoinLoss) {
+    __shared__ float own[NWAVES];
+    if (g == 0 && r < NWAVES) own[r] = (exponent_base(m) + log2f(s)) * kLn2;
+    __shared__ int ids[NWAVES][kMaxTop];
+    __shared__ float ts[NWAVES][kMaxTop];
+    __syncthreads();
+    const int wave = threadIdx.x >> 6;
+    const int64_t mine = (int64_t)blockIdx.x * R + wave;
+    if (wave < R && mine < rows)
+      distill_loss(l, mine, own[wave], z, loss, lse, threadIdx.x & 63, ids[wave], ts[wave]);
+    return;
+  }
+  if (g != 0 || row >= rows) return;
+  float v = (exponent_base(m) + log2f(s)) * kLn2;
+  if constexpr (JOIN == kTargets) {
+    const bool part_of = l.ids[row] >= 0;
+    v = part_of ? v : 0.0f;
+    loss[row] = !part_of ? 0.0f : l.ids[row] >= l.vocab ? NAN : v - z[row];
+  }
+  lse[row] = v;
 }
 
 // Whether the row takes part (one wave; *bad: an id past the vocabulary)
@@ -429,7 +381,7 @@ bool fits(int64_t blocks) { return blocks * NT <= kMaxWorkItems; }
 
 hipError_t launch_listed_logits(DType t, const void* x, const void* W, const VocabList& l,
                                 int64_t rows, int K, float* z, hipStream_t s) {
-  const int64_t waves = rows * ((l.top + kEntries - 1) / kEntries);
+  const int64_t waves = listed_waves(rows, l.top);
   const int64_t blocks = (waves + NWAVES - 1) / NWAVES;
   if (!fits(blocks)) return hipErrorInvalidValue;
   if (t == DType::BF16)
@@ -460,15 +412,14 @@ hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots,
   while (R < 32 && R * 256 <= rows) R *= 2;
   const int64_t blocks = (rows + R - 1) / R, loss_blocks = (rows + NWAVES - 1) / NWAVES;
   if (!fits(blocks) || !fits(loss_blocks)) return hipErrorInvalidValue;
-  if (!l.teacher) {
-    hipLaunchKernelGGL(join_kernel<true>, dim3((unsigned)blocks), dim3(NT), 0, s, part, part_ld,
-                       slots, R, l, rows, z, loss, lse);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(join_kernel<false>, dim3((unsigned)blocks), dim3(NT), 0, s, part, part_ld,
-                     slots, R, l, rows, z, loss, lse);
-  hipLaunchKernelGGL(distill_loss_kernel, dim3((unsigned)loss_blocks), dim3(NT), 0, s, l, rows, z,
-                     loss, lse);
+  const auto kernel = !l.teacher     ? join_kernel<kTargets>
+                      : R <= NWAVES ? join_kernel<kJoinLoss>
+                                    : join_kernel<kTeacher>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(NT), 0, s, part, part_ld, slots, R, l, rows,
+                     z, loss, lse);
+  if (l.teacher && R > NWAVES)
+    hipLaunchKernelGGL(distill_loss_kernel, dim3((unsigned)loss_blocks), dim3(NT), 0, s, l, rows, z,
+                       loss, lse);
   return hipGetLastError();
 }
 

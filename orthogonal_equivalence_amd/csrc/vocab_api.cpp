@@ -118,7 +118,8 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   if (!z) z = reinterpret_cast<float*>(w + plan.z);
   float2* part = reinterpret_cast<float2*>(w + plan.part);
   // (targets' logits come out of the products)
-  if (teacher && !plan.cells)
+  const bool beside = teacher && !plan.cells && plan.cols.dense == 0;
+  if (teacher && !plan.cells && !beside)
     POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
   if (plan.copied) {
     poetx::VocabCopies c;
@@ -162,7 +163,8 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
       p.W = static_cast<const char*>(W) + p.col0 * d->d * act_size(d->act);
       p.N = (int)(d->vocab - p.col0);
       POETX_TRY(poetx::launch_vocab_lse_tile(t, plan.cols.tile, p, part + p.col0 / 128 * (int64_t)p.M,
-                                             p.M, targets, z + r, cells[1], s));
+                                             p.M, targets, z + r * list.top, cells[1],
+                                             beside ? list_at(list, r) : VocabList(), s));
     }
     POETX_TRY(poetx::launch_vocab_loss(part, p.M, plan.slots, list_at(list, r), p.M,
                                        z + r * list.top, loss + r, lse + r, s));

@@ -36,6 +36,7 @@ __device__ __forceinline__ floatx4 pick(const floatx4 (&acc)[FM][FN], int f) {
 }
 
 struct LseEnd {
+  static constexpr bool kBeside = true;
   float2* part;
   int64_t part_ld;
   float scale;
@@ -43,6 +44,8 @@ struct LseEnd {
   float* z;
   int col0;
   VocabCells cells;
+  VocabList list;  // of workgroups past the tiles (`beside`): its logits, into z
+  int64_t beside;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int, int wave_col, int lane) const {
@@ -80,6 +83,7 @@ struct LseEnd {
 };
 
 struct GradEnd {
+  static constexpr bool kBeside = false;
   const VocabRow* rows;
   void* gz;
   int64_t ldg;
@@ -113,15 +117,31 @@ template <typename T, int BM, int BN, int WM, int WN, int NS, typename End>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 vocab_tile_kernel(const TileProduct p, const End end) {
   __shared__ __attribute__((aligned(1024))) char ring[ring_bytes<T, T, BM, BN, WM * WN, NS>()];
+  if constexpr (End::kBeside) {
+    const int64_t tiles = (int64_t)gridDim.x - end.beside;
+    if ((int64_t)blockIdx.x >= tiles) {
+      listed_logits(static_cast<const T*>(p.A), static_cast<const T*>(p.B), end.list, p.M, p.K, end.z,
+                    ((int64_t)blockIdx.x - tiles) * (WM * WN) + (threadIdx.x >> 6),
+                    threadIdx.x & 63);
+      return;
+    }
+  }
   tile_body<T, T, BM, BN, WM, WN, true, true, NS>(p, blockIdx.x, 0, ring, end);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int NS, typename End>
 hipError_t launch_cfg(const TileProduct& p, const End& end, hipStream_t s) {
   const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  if (tiles * 64 * WM * WN > kMaxWorkItems) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((vocab_tile_kernel<T, BM, BN, WM, WN, NS, End>), dim3((unsigned)tiles),
-                     dim3(64 * WM * WN), 0, s, p, end);
+  End e = end;
+  int64_t grid = tiles;
+  if constexpr (End::kBeside) {
+    if (end.list.ids)
+      e.beside = (listed_waves(p.M, end.list.top) + WM * WN - 1) / (WM * WN);
+    grid += e.beside;
+  }
+  if (grid * 64 * WM * WN > kMaxWorkItems) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((vocab_tile_kernel<T, BM, BN, WM, WN, NS, End>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, s, p, e);
   return hipGetLastError();
 }
 
@@ -158,8 +178,8 @@ hipError_t launch_end(DType t, const TilePlan& plan, const VocabProduct& v, cons
 
 hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProduct& p, float2* part,
                                  int64_t part_ld, const int64_t* targets, float* z,
-                                 const VocabCells& cells, hipStream_t s) {
-  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z, p.col0, cells}, s);
+                                 const VocabCells& cells, const VocabList& list, hipStream_t s) {
+  return launch_end(t, plan, p, LseEnd{part, part_ld, p.scale, targets, z, p.col0, cells, list, 0}, s);
 }
 
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
