@@ -131,6 +131,17 @@ __device__ __forceinline__ int pair_column(int ln) {
   return 16 * ((ln >> 4) & 1) + 8 * (ln >> 5);
 }
 
+// the value of lane l ^ 8
+__device__ __forceinline__ uint32_t ror8(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, false);  // row_ror:8
+}
+__device__ __forceinline__ uint4 ror8(uint4 v) {
+  return make_uint4(ror8(v.x), ror8(v.y), ror8(v.z), ror8(v.w));
+}
+
+__device__ __forceinline__ uint4 choose(bool c, uint4 a, uint4 b) {
+  return make_uint4(c ? a.x : b.x, c ? a.y : b.y, c ? a.z : b.z, c ? a.w : b.w);
+}
 // The entries of one wave's cell: their range and the first 64 of them, read
 // well before their logits are stored (each read waits for the L2, one for the
 // other).

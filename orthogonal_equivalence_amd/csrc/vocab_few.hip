@@ -6,10 +6,11 @@
 // One wave takes 32 rows of g_W (ids): their g_z, at most 64 tokens, are the
 // products' operand and stay in registers; it walks along d with one 16-byte load a
 // lane for 16 columns, 32 columns ahead, out of a copy of x with the tokens
-// innermost (xt [d][tokens padded]; it stays in the L2), and stores 64-byte pieces of
-// 16 rows. No LDS, no barrier. 16 tokens, 131072 x 4096: 360 us, 3.0 TB/s of
-// stores alone; 30 tokens, 56370 x 2256: 63 us, on 64 x 64 tiles 113. Stores past
-// the caches (half lines) 194 us there; 16 ids a wave 75; walks of 1024 columns 71.
+// innermost (xt [d][tokens padded]; it stays in the L2), and stores 8 rows' whole
+// lines at a time. No LDS, no barrier. 16 tokens, 131072 x 4096: 277 us, 3.9 TB/s of
+// stores alone (a fill 6.9); 30 tokens, 56370 x 2256: 60 us, on 64 x 64 tiles 113.
+// Stores of 16 rows' half lines 361 and 63; 16 ids a wave 75; walks of 1024
+// columns 71.
 #include "epilogue.h"
 #include "vocab.h"
 
@@ -20,6 +21,10 @@ constexpr int NT = 256, NWAVES = NT / 64;
 constexpr int VF = 2;            // fragments of 16 ids a wave
 constexpr int kRows = 16 * VF;   // ids a wave
 constexpr int kChunk = 512;      // columns a workgroup walks along
+// a g_W larger than this goes past the caches, where its rows are whole lines (16
+// tokens, 131072 x 4096 361 -> 277 us, and W stays in the cache for the next pass;
+// rows of 4512 bytes 60 -> 160, 131 MB alike)
+constexpr int64_t kCacheBytes = INT64_C(256) << 20;
 
 template <typename T> struct Few;
 template <> struct Few<bf16_t> {
@@ -39,13 +44,44 @@ template <> struct Few<float> {
   }
 };
 
-// STEPS: K tokens each
+template <bool PAST> __device__ __forceinline__ void store16(void* p, uint4 v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 w{v.x, v.y, v.z, v.w};
+  if constexpr (PAST) __builtin_nontemporal_store(w, static_cast<u32x4*>(p));
+  else *static_cast<u32x4*>(p) = w;
+}
+
+// 64 bytes of columns (bf16: two fragments, float32 one): this lane's 16 of them in
+// row l % 16, columns pair_column() or 4 (l / 16) on
 template <typename T, int STEPS>
+__device__ __forceinline__ uint4 half(const typename Few<T>::Frag (*b)[STEPS],
+                                      const typename Few<T>::Frag (&a)[STEPS]) {
+  constexpr int N = sizeof(T) == 2 ? 2 : 1;
+  floatx4 c[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    c[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) c[j] = Few<T>::mma(b[j][s], a[s], c[j]);
+  }
+  if constexpr (sizeof(T) == 2) {
+    const float p[4] = {c[0][0], c[0][1], c[0][2], c[0][3]};
+    const float q[4] = {c[1][0], c[1][1], c[1][2], c[1][3]};
+    return swap_pair(Quad<bf16_t>::pack(p), Quad<bf16_t>::pack(q));
+  } else {
+    return __builtin_bit_cast(uint4, c[0]);
+  }
+}
+
+// STEPS: K tokens each. PAST: stores past the caches.
+template <typename T, int STEPS, bool PAST>
 __global__ void __launch_bounds__(NT)
 few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, int tokens, int cols,
               int d, T* __restrict__ g_W) {
   typedef Few<T> F;
   typedef typename F::Frag Frag;
+  // fragments and columns of one step along d: 128 bytes
+  constexpr int kStep = 128 / sizeof(T), NF = kStep / 16;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int64_t v0 = ((int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6)) * kRows;
   if (v0 >= cols) return;
@@ -67,51 +103,39 @@ few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, i
   }
   constexpr int kPad = STEPS * F::K;
   const int c0 = blockIdx.y * kChunk, c1 = min(d, c0 + kChunk);
-  Frag next[2][STEPS];  // of the 32 columns after the current ones
+  Frag next[NF][STEPS];  // of the kStep columns after the current ones
   auto load = [&](int n0) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NF; ++j)
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
         next[j][s] = *reinterpret_cast<const Frag*>(
             xt + (int64_t)min(n0 + 16 * j + r, d - 1) * kPad + s * F::K + g * F::E);
   };
   load(c0);
-  for (int n0 = c0; n0 < c1; n0 += 32) {
-    Frag b[2][STEPS];
+  const bool upper = r >= 8;
+  // this lane's first column of a step
+  const int at = (upper ? kStep / 2 : 0) + (sizeof(T) == 2 ? pair_column(lane) : 4 * g);
+  for (int n0 = c0; n0 < c1; n0 += kStep) {
+    Frag b[NF][STEPS];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NF; ++j)
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) b[j][s] = next[j][s];
-    load(n0 + 32);
+    load(n0 + kStep);
 #pragma unroll
     for (int f = 0; f < VF; ++f) {
-      floatx4 c[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        c[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) c[j] = F::mma(b[j][s], a[f][s], c[j]);
-      }
-      // (lane l: id l % 16, columns 4 (l / 16) .. + 3 of each fragment)
-      const int64_t v = v0 + 16 * f + r;
-      if constexpr (sizeof(T) == 2) {
-        uint2 w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float q[4] = {c[j][0], c[j][1], c[j][2], c[j][3]};
-          w[j] = Quad<bf16_t>::pack(q);
-        }
-        const uint4 out = swap_pair(w[0], w[1]);
-        const int n = n0 + pair_column(lane);
-        if (v < cols && n < d) *reinterpret_cast<uint4*>(g_W + v * d + n) = out;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = n0 + 16 * j + 4 * g;
-          if (v < cols && n < d)
-            *reinterpret_cast<uint4*>(g_W + v * d + n) = __builtin_bit_cast(uint4, c[j]);
-        }
+      // this lane's 16 bytes of row r, of either half of the columns
+      const uint4 w0 = half<T, STEPS>(&b[0], a[f]), w1 = half<T, STEPS>(&b[NF / 2], a[f]);
+      // rows 8 .. 15 of the first half for rows 0 .. 7 of the second: a store then
+      // covers 8 rows by both halves, whole 128-byte lines
+      const uint4 got = ror8(choose(upper, w0, w1));
+      const uint4 lo = choose(upper, got, w0), hi = choose(upper, w1, got);
+      const int n = n0 + at;
+      const int64_t v = v0 + 16 * f + (r & 7);
+      if (n < d) {
+        if (v < cols) store16<PAST>(g_W + v * d + n, lo);
+        if (v + 8 < cols) store16<PAST>(g_W + (v + 8) * d + n, hi);
       }
     }
   }
@@ -122,7 +146,11 @@ hipError_t launch_steps(const void* gz, int64_t ldg, const void* xt, int tokens,
                         void* g_W, hipStream_t s) {
   const dim3 grid((unsigned)((cols + kRows * NWAVES - 1) / (kRows * NWAVES)),
                   (unsigned)((d + kChunk - 1) / kChunk));
-  hipLaunchKernelGGL((few_gw_kernel<T, STEPS>), grid, dim3(NT), 0, s, static_cast<const T*>(gz), ldg,
+  const int64_t row = d * (int64_t)sizeof(T);
+  const auto kernel = row % 128 == 0 && cols * row > kCacheBytes
+                          ? few_gw_kernel<T, STEPS, true>
+                          : few_gw_kernel<T, STEPS, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(NT), 0, s, static_cast<const T*>(gz), ldg,
                      static_cast<const T*>(xt), tokens, cols, d, static_cast<T*>(g_W));
   return hipGetLastError();
 }

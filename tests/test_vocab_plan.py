@@ -122,7 +122,9 @@ def variants(case, p):
         if p["b_dense"]:
             continue
         if p["few"]:
-            got.add(("few", t, -(-tokens // (32 if t == BF16 else 16))))
+            es = 2 if t == BF16 else 4
+            past = d * es % 128 == 0 and q["cols"] * d * es > 256 << 20
+            got.add(("few", t, -(-tokens // (64 // es)), past))
         if p["few"] or not q["paired"]:
             got.add(("gx tile", t, q["gx_shape"], parts(q["gx_split"])))
             if not p["few"]:

@@ -121,12 +121,13 @@ CASES = [  # dtype, tokens, d, vocab
     (BF16, 7398, 392, 279), (BF16, 1422, 8, 5376), (BF16, 5608, 256, 1106), (BF16, 585, 3584, 427),
     (BF16, 333, 448, 77312), (BF16, 42, 224, 129074), (BF16, 1189, 736, 15165), (F32, 40, 72, 63264),
     (F32, 20, 152, 74599), (BF16, 759, 768, 22239), (BF16, 5438, 80, 5913), (BF16, 2313, 2752, 1338),
-    (BF16, 1056, 1312, 9504), (F32, 631, 8, 65783), (F32, 39, 400, 40688), (BF16, 672, 2816, 9001),
-    (BF16, 8100, 400, 5148), (BF16, 2560, 256, 14080), (BF16, 298, 256, 115906), (BF16, 650, 256, 69815),
-    (F32, 4623, 8, 60672), (F32, 887, 1152, 1792), (F32, 84, 2048, 11439), (BF16, 1792, 1536, 14592),
+    (BF16, 1056, 1312, 9504), (F32, 1, 1728, 45137), (F32, 631, 8, 65783), (F32, 39, 400, 40688),
+    (BF16, 4, 2816, 49035), (BF16, 672, 2816, 9001), (BF16, 8100, 400, 5148), (BF16, 2560, 256, 14080),
+    (BF16, 298, 256, 115906), (BF16, 650, 256, 69815), (BF16, 45, 1792, 88320), (F32, 4623, 8, 60672),
+    (F32, 887, 1152, 1792), (F32, 84, 2048, 11439), (BF16, 1792, 1536, 14592), (F32, 23, 2048, 39497),
     (BF16, 3137, 2720, 3077), (F32, 7930, 96, 3471), (BF16, 3756, 3840, 2304), (BF16, 1350, 256, 109972),
-    (F32, 4849, 16, 49508), (F32, 1896, 1024, 2972), (BF16, 5600, 3392, 3840), (BF16, 2379, 320, 108458),
-    (BF16, 4096, 2816, 36606),
+    (F32, 4849, 16, 49508), (F32, 60, 2752, 30580), (F32, 1896, 1024, 2972), (BF16, 5600, 3392, 3840),
+    (BF16, 2379, 320, 108458), (BF16, 4096, 2816, 36606),
 ]
 # dtype, tokens, d, vocab, top
 LISTED = [
@@ -137,5 +138,5 @@ LISTED = [
     (F32, 52, 72, 50853, 1), (BF16, 262, 256, 100366, 5), (BF16, 270, 2432, 10202, 4),
     (BF16, 953, 768, 17664, 16), (BF16, 6039, 512, 3401, 36), (BF16, 129, 3000, 17764, 10),
     (F32, 2482, 2336, 256, 1), (BF16, 399, 544, 66539, 10), (BF16, 4698, 8, 65522, 26),
-    (BF16, 3606, 256, 70033, 25),
+    (F32, 35, 2816, 41863, 73), (BF16, 3606, 256, 70033, 25),
 ]
