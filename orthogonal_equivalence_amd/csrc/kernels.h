@@ -430,9 +430,9 @@ hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, con
 // (what gz's columns past `cols` hold does not matter).
 hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
                                  int cols, void* g_W, hipStream_t s);
-// g_W of up to kFewTokens rows (vocab_few.hip): row-major gz [tokens][ldg] and xt
+// g_W of up to few_tokens(t) rows (vocab_few.hip): row-major gz [tokens][ldg] and xt
 // [d][few_padded], the copy of x that VocabCopies::xt makes.
-constexpr int kFewTokens = 64;
+constexpr int few_tokens(DType t) { return t == DType::BF16 ? 128 : 64; }
 int few_padded(DType t, int tokens);
 hipError_t launch_few_gw(DType t, const void* gz, int64_t ldg, const void* xt, int tokens, int cols,
                          int d, void* g_W, hipStream_t s);
@@ -457,7 +457,7 @@ struct VocabCopies {
   bool tiled = false;
   const void* W = nullptr;
   void* W_last = nullptr;
-  void* xt = nullptr;  // up to kFewTokens rows: [K][xt_rows], zeros as in xs
+  void* xt = nullptr;  // up to few_tokens(t) rows: [K][xt_rows], zeros as in xs
   int xt_rows = 0;
 };
 hipError_t launch_vocab_last_rows(DType t, int64_t vocab, int K, const VocabCopies& c,

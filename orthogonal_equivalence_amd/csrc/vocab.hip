@@ -310,7 +310,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT)
 turned_copy_kernel(const VocabRow* __restrict__ parts, int rows, int K, const VocabCopies c) {
   constexpr int E = Vec<T>::E;
-  __shared__ T tile[kFewTokens][64 + E];
+  __shared__ T tile[few_tokens(sizeof(T) == 2 ? DType::BF16 : DType::F32)][64 + E];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k0 = blockIdx.x * 64;
   const T* x = static_cast<const T*>(c.x);
   for (int row = wave; row < c.xt_rows; row += NWAVES) {
@@ -437,7 +437,7 @@ hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (c.xt) {
-    if (rows > kFewTokens || c.xt_rows > kFewTokens || c.xt_rows < rows ||
+    if (rows > few_tokens(t) || c.xt_rows > few_tokens(t) || c.xt_rows < rows ||
         c.xt_rows != few_padded(t, (int)rows))
       return hipErrorInvalidValue;
     const dim3 grid((unsigned)((K + 63) / 64));

@@ -1,16 +1,22 @@
-// g_W = g_z^T x for few tokens (up to kFewTokens): each element of g_W is a sum of
-// at most 64 products, so the store of g_W is all there is to it (131072 x 4096
-// bf16 1.07 GB), and tiles that load, wait, multiply once and store spend most of
-// their time on the first two.
+// g_W = g_z^T x for few tokens (up to few_tokens()): each element of g_W is a sum of
+// at most 128 products, so the store of g_W is all there is to it (131072 x 4096
+// bf16 1.07 GB, 180 us at what stores alone reach), and tiles that load, wait, multiply
+// once and store spend most of their time on the first two.
 //
-// One wave takes 32 rows of g_W (ids): their g_z, at most 64 tokens, are the
-// products' operand and stay in registers; it walks along d with one 16-byte load a
-// lane for 16 columns, 32 columns ahead, out of a copy of x with the tokens
+// One wave takes 32 or 64 rows of g_W (ids): their g_z are the products' operand and
+// stay in registers; it walks along d with one 16-byte load a lane for 16 columns
+// and K tokens, 128 bytes of columns ahead, out of a copy of x with the tokens
 // innermost (xt [d][tokens padded]; it stays in the L2), and stores 8 rows' whole
-// lines at a time. No LDS, no barrier. 16 tokens, 131072 x 4096: 277 us, 3.9 TB/s of
-// stores alone (a fill 6.9); 30 tokens, 56370 x 2256: 60 us, on 64 x 64 tiles 113.
-// Stores of 16 rows' half lines 361 and 63; 16 ids a wave 75; walks of 1024
-// columns 71.
+// lines at a time. No LDS, no barrier. Workgroups in the order of g_W's rows, not of its
+// columns: what is stored at one time then lies together (stores alone of 1.07 GB
+// 181 us, the other way 235).
+// us:                      1 token   64   96  128   (on tiles at 65, 96, 128)
+//   131072 x 4096, bf16      211  245  300  385     (575 - 600)
+//   32000 x 4096              61   75                (175)
+// From 33 tokens on 64 ids a wave: 131072 x 4096, 64 tokens 336 -> 245 (32 ids); up to
+// 32 tokens 32 ids (56370 x 2256, 16 tokens: 232 us a backward, 64 ids 239). Stores of
+// 16 rows' half lines: a third more. Walks of 256 columns alike, of 1024 slower. Past
+// 128 tokens the registers are spent.
 #include "epilogue.h"
 #include "vocab.h"
 
@@ -18,13 +24,13 @@ namespace poetx {
 namespace {
 
 constexpr int NT = 256, NWAVES = NT / 64;
-constexpr int VF = 2;            // fragments of 16 ids a wave
-constexpr int kRows = 16 * VF;   // ids a wave
+// fragments of 16 ids a wave: the more, the less often x's copy is read
+template <int STEPS> constexpr int kFrags = STEPS == 1 ? 2 : 4;
 constexpr int kChunk = 512;      // columns a workgroup walks along
-// a g_W larger than this goes past the caches, where its rows are whole lines (16
-// tokens, 131072 x 4096 361 -> 277 us, and W stays in the cache for the next pass;
-// rows of 4512 bytes 60 -> 160, 131 MB alike)
-constexpr int64_t kCacheBytes = INT64_C(256) << 20;
+// a g_W larger than this goes past the caches, where its rows are whole lines, and W
+// stays in them for the next pass (backward of 64 tokens: 32000 x 4096 227 -> 172 us,
+// 131072 x 4096 833 -> 768; 32000 x 1024 float32, 131 MB, alike; rows of 4512 bytes 60 -> 160)
+constexpr int64_t kCacheBytes = INT64_C(128) << 20;
 
 template <typename T> struct Few;
 template <> struct Few<bf16_t> {
@@ -77,13 +83,15 @@ __device__ __forceinline__ uint4 half(const typename Few<T>::Frag (*b)[STEPS],
 template <typename T, int STEPS, bool PAST>
 __global__ void __launch_bounds__(NT)
 few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, int tokens, int cols,
-              int d, T* __restrict__ g_W) {
+              int d, int chunks, T* __restrict__ g_W) {
   typedef Few<T> F;
   typedef typename F::Frag Frag;
   // fragments and columns of one step along d: 128 bytes
   constexpr int kStep = 128 / sizeof(T), NF = kStep / 16;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int64_t v0 = ((int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6)) * kRows;
+  constexpr int VF = kFrags<STEPS>, kRows = 16 * VF;
+  const unsigned group = blockIdx.x / (unsigned)chunks, chunk = blockIdx.x - group * chunks;
+  const int64_t v0 = ((int64_t)group * NWAVES + (threadIdx.x >> 6)) * kRows;
   if (v0 >= cols) return;
   Frag a[VF][STEPS];
 #pragma unroll
@@ -102,7 +110,7 @@ few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, i
     }
   }
   constexpr int kPad = STEPS * F::K;
-  const int c0 = blockIdx.y * kChunk, c1 = min(d, c0 + kChunk);
+  const int c0 = (int)chunk * kChunk, c1 = min(d, c0 + kChunk);
   Frag next[NF][STEPS];  // of the kStep columns after the current ones
   auto load = [&](int n0) {
 #pragma unroll
@@ -144,33 +152,39 @@ few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, i
 template <typename T, int STEPS>
 hipError_t launch_steps(const void* gz, int64_t ldg, const void* xt, int tokens, int cols, int d,
                         void* g_W, hipStream_t s) {
-  const dim3 grid((unsigned)((cols + kRows * NWAVES - 1) / (kRows * NWAVES)),
-                  (unsigned)((d + kChunk - 1) / kChunk));
+  constexpr int kRows = 16 * kFrags<STEPS>;
+  const int chunks = (d + kChunk - 1) / kChunk;
+  const int64_t blocks = ((int64_t)cols + kRows * NWAVES - 1) / (kRows * NWAVES) * chunks;
+  if (blocks >= INT64_C(1) << 24) return hipErrorInvalidValue;  // (2^32 work items)
   const int64_t row = d * (int64_t)sizeof(T);
   const auto kernel = row % 128 == 0 && cols * row > kCacheBytes
                           ? few_gw_kernel<T, STEPS, true>
                           : few_gw_kernel<T, STEPS, false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(NT), 0, s, static_cast<const T*>(gz), ldg,
-                     static_cast<const T*>(xt), tokens, cols, d, static_cast<T*>(g_W));
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(NT), 0, s, static_cast<const T*>(gz), ldg,
+                     static_cast<const T*>(xt), tokens, cols, d, chunks, static_cast<T*>(g_W));
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_type(int steps, const void* gz, int64_t ldg, const void* xt, int tokens, int cols,
+                       int d, void* g_W, hipStream_t s) {
+  switch (steps) {
+    case 1: return launch_steps<T, 1>(gz, ldg, xt, tokens, cols, d, g_W, s);
+    case 2: return launch_steps<T, 2>(gz, ldg, xt, tokens, cols, d, g_W, s);
+    case 3: return launch_steps<T, 3>(gz, ldg, xt, tokens, cols, d, g_W, s);
+    default: return launch_steps<T, 4>(gz, ldg, xt, tokens, cols, d, g_W, s);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_few_gw(DType t, const void* gz, int64_t ldg, const void* xt, int tokens, int cols,
                          int d, void* g_W, hipStream_t s) {
-  if (tokens < 1 || tokens > kFewTokens || cols < 1 || d < 1 || d > (1 << 22))
+  if (tokens < 1 || tokens > few_tokens(t) || cols < 1 || d < 1 || d > (1 << 22))
     return hipErrorInvalidValue;
   const int steps = few_padded(t, tokens) / (t == DType::BF16 ? 32 : 16);
-  if (t == DType::BF16)
-    return steps == 1 ? launch_steps<bf16_t, 1>(gz, ldg, xt, tokens, cols, d, g_W, s)
-                      : launch_steps<bf16_t, 2>(gz, ldg, xt, tokens, cols, d, g_W, s);
-  switch (steps) {
-    case 1: return launch_steps<float, 1>(gz, ldg, xt, tokens, cols, d, g_W, s);
-    case 2: return launch_steps<float, 2>(gz, ldg, xt, tokens, cols, d, g_W, s);
-    case 3: return launch_steps<float, 3>(gz, ldg, xt, tokens, cols, d, g_W, s);
-    default: return launch_steps<float, 4>(gz, ldg, xt, tokens, cols, d, g_W, s);
-  }
+  return t == DType::BF16 ? launch_type<bf16_t>(steps, gz, ldg, xt, tokens, cols, d, g_W, s)
+                          : launch_type<float>(steps, gz, ldg, xt, tokens, cols, d, g_W, s);
 }
 
 }  // namespace poetx

@@ -124,9 +124,12 @@ VocabProducts plan_vocab_products(const VocabSizes& v, int64_t n) {
   p.gx = plan_tile_product(v.t, v.tokens, v.d, n, false, kManySplits);
   p.gw = plan_tile_product(v.t, n, v.d, v.tokens, false);
   p.pair = plan_tile_pair(v.t, v.tokens, v.d, n, kManySplits);
-  // a launch for the turned copy of x and one that stores g_W
-  const float few = 6.0f + (float)(n * v.d * v.es()) / 3.2e6f;
-  p.few = v.tokens <= kFewTokens &&
+  // a launch for the turned copy of x and one that stores g_W (131072 x 4096 1 token
+  // 211 us, 64 245, 96 300, 128 385; rows that are not whole lines take longer)
+  const float mb = (float)n * (float)(v.d * v.es()) / 1e6f;
+  const float few =
+      6.0f + mb * (0.19f + 0.0013f * v.tokens) * (v.d * v.es() % 128 ? 1.2f : 1.0f);
+  p.few = v.tokens <= few_tokens(v.t) &&
           few < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
   p.paired = !p.few && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
   return p;
@@ -188,7 +191,7 @@ VocabBwdPlan plan_vocab_bwd(const VocabSizes& v) {
   p.last = off;
   if (p.dense && v.vocab % kTile) off += align_up((size_t)(kTile * v.d * es));
   p.xs = off;
-  const int64_t copied = p.dense || v.tokens > kFewTokens
+  const int64_t copied = p.dense || v.tokens > few_tokens(v.t)
                              ? p.padded
                              : few_padded(v.t, (int)v.tokens);
   off += align_up((size_t)(copied * v.d * es));

@@ -123,7 +123,7 @@ def variants(case, p):
             continue
         if p["few"]:
             es = 2 if t == BF16 else 4
-            past = d * es % 128 == 0 and q["cols"] * d * es > 256 << 20
+            past = d * es % 128 == 0 and q["cols"] * d * es > 128 << 20
             got.add(("few", t, -(-tokens // (64 // es)), past))
         if p["few"] or not q["paired"]:
             got.add(("gx tile", t, q["gx_shape"], parts(q["gx_split"])))
@@ -199,4 +199,4 @@ def test_plans_hold_together():
                 assert q["gx_split"] >= 1 and q["gw_split"] >= 1, where
                 if q["paired"]:
                     assert q["px_split"] >= 1 and q["pw_split"] >= 1, where
-        assert not p["few"] or tokens <= 64
+        assert not p["few"] or tokens <= (128 if t == BF16 else 64)

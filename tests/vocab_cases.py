@@ -127,7 +127,8 @@ CASES = [  # dtype, tokens, d, vocab
     (F32, 887, 1152, 1792), (F32, 84, 2048, 11439), (BF16, 1792, 1536, 14592), (F32, 23, 2048, 39497),
     (BF16, 3137, 2720, 3077), (F32, 7930, 96, 3471), (BF16, 3756, 3840, 2304), (BF16, 1350, 256, 109972),
     (F32, 4849, 16, 49508), (F32, 60, 2752, 30580), (F32, 1896, 1024, 2972), (BF16, 5600, 3392, 3840),
-    (BF16, 2379, 320, 108458), (BF16, 4096, 2816, 36606),
+    (BF16, 2379, 320, 108458), (BF16, 4096, 2816, 36606), (BF16, 71, 208, 98288), (BF16, 73, 1024, 72448),
+    (BF16, 101, 1792, 47872),
 ]
 # dtype, tokens, d, vocab, top
 LISTED = [
@@ -139,4 +140,6 @@ LISTED = [
     (BF16, 953, 768, 17664, 16), (BF16, 6039, 512, 3401, 36), (BF16, 129, 3000, 17764, 10),
     (F32, 2482, 2336, 256, 1), (BF16, 399, 544, 66539, 10), (BF16, 4698, 8, 65522, 26),
     (F32, 35, 2816, 41863, 73), (BF16, 3606, 256, 70033, 25),
+    (BF16, 68, 8, 118786, 2), (BF16, 97, 1280, 28160, 1), (BF16, 460, 1568, 46189, 2),
+    (BF16, 1792, 256, 78091, 3),
 ]
