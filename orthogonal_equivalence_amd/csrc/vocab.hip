@@ -381,16 +381,27 @@ bool fits(int64_t blocks) { return blocks * NT <= kMaxWorkItems; }
 
 hipError_t launch_listed_logits(DType t, const void* x, const void* W, const VocabList& l,
                                 int64_t rows, int K, float* z, hipStream_t s) {
-  const int64_t waves = listed_waves(rows, l.top);
-  const int64_t blocks = (waves + NWAVES - 1) / NWAVES;
-  if (!fits(blocks)) return hipErrorInvalidValue;
-  if (t == DType::BF16)
-    hipLaunchKernelGGL(listed_logits_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s,
-                       static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(W), l, rows, K, z);
-  else
-    hipLaunchKernelGGL(listed_logits_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s,
-                       static_cast<const float*>(x), static_cast<const float*>(W), l, rows, K, z);
-  return hipGetLastError();
+  // (as many rows a launch as it takes)
+  const int64_t most = (kMaxWorkItems - NT) / 64 / listed_waves(1, l.top);
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = std::min(most, rows - r);
+    const int64_t blocks = (listed_waves(n, l.top) + NWAVES - 1) / NWAVES;
+    if (!fits(blocks)) return hipErrorInvalidValue;
+    VocabList at = l;
+    at.ids += r * l.top;  // (the teacher's logits are not read)
+    float* to = z + r * l.top;
+    if (t == DType::BF16)
+      hipLaunchKernelGGL(listed_logits_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s,
+                         static_cast<const bf16_t*>(x) + r * K, static_cast<const bf16_t*>(W), at, n,
+                         K, to);
+    else
+      hipLaunchKernelGGL(listed_logits_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s,
+                         static_cast<const float*>(x) + r * K, static_cast<const float*>(W), at, n, K,
+                         to);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_vocab_cells(const VocabList& l, int64_t M, int64_t col0, int64_t N,

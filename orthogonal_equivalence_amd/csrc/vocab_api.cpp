@@ -118,7 +118,8 @@ int forward(const poetx_vocab_desc* d, const void* x, const void* W, const int64
   if (!z) z = reinterpret_cast<float*>(w + plan.z);
   float2* part = reinterpret_cast<float2*>(w + plan.part);
   // (targets' logits come out of the products)
-  const bool beside = teacher && !plan.cells && plan.cols.dense == 0;
+  const bool beside = teacher && !plan.cells && plan.cols.dense == 0 &&
+                      list_entries(d) <= (size_t)1 << 24;  // (and few beside a launch's limit)
   if (teacher && !plan.cells && !beside)
     POETX_TRY(poetx::launch_listed_logits(t, x, W, list, d->tokens, (int)d->d, z, s));
   if (plan.copied) {

@@ -222,6 +222,31 @@ def test_weights_past_2_to_the_32_elements():
     assert torch.equal(g_x, want_x.float().bfloat16())
 
 
+def test_more_listed_logits_than_one_launch():
+    """2.7e8 entries of lists over a vocabulary too long to sort them by tiles: each
+    wave of the gathering launch takes four, and no launch takes 2^32 work items.
+    Small integers over 8: every logit is exact."""
+    tokens, d, vocab, top = 262_400, 8, 600_000, 1024
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randint(-1, 2, (tokens, d), generator=gen, device="cuda").bfloat16()
+    W = (torch.randint(-8, 9, (vocab, d), generator=gen, device="cuda") / 8).bfloat16()
+    ids = torch.randint(0, vocab, (tokens, top), generator=gen, device="cuda")
+    teacher = torch.zeros(tokens, top, device="cuda", dtype=torch.bfloat16)
+    loss, lse, z = L.distill_forward(x, W, ids, teacher)
+    wf = W.float()
+    for a in range(0, tokens, 8192):
+        xa = x[a:a + 8192].float()
+        want = torch.zeros(xa.shape[0], top, device="cuda")
+        for k in range(d):
+            want += xa[:, k:k + 1] * wf[:, k][ids[a:a + 8192]]
+        assert torch.equal(z[a:a + 8192], want), a
+    # a uniform teacher: loss = lse - log(top) - the mean of z
+    u = 2.0 ** -24
+    want = lse.double() - math.log(top) - z.double().mean(1)
+    # (terms of at most 20, each a few roundings; the sum of p to within top / 64 + 6)
+    assert bool(((loss.double() - want).abs() <= u * 20 * (top / 64 + 16)).all())
+
+
 def test_refusals():
     x, W = V.inputs(20, 64, 100, "bf16", 1)
     t = V.draw_targets(20, 100, 2)
