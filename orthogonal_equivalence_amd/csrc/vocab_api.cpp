@@ -182,7 +182,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
       !aligned_to(g_loss, 4) || !aligned_to(g_lse, 4) || !aligned_to(lse, 4) || !aligned_to(z, 4) ||
       !aligned_to(teacher, act_size(d->teacher)))
     return POETX_ERR_ALIGN;
-  const poetx::VocabBwdPlan plan = poetx::plan_vocab_bwd(sizes_of(d));
+  const poetx::VocabBwdPlan plan = poetx::plan_vocab_bwd(sizes_of(d), g_W != nullptr);
   if (!ws || ws_bytes < plan.total) return POETX_ERR_WORKSPACE;
   if (!aligned16(ws)) return POETX_ERR_ALIGN;
   const size_t rows4 = (size_t)d->tokens * 4, n = list_entries(d);
@@ -299,7 +299,9 @@ size_t poetx_vocab_fwd_workspace_size(const poetx_vocab_desc* d) {
 }
 
 size_t poetx_vocab_bwd_workspace_size(const poetx_vocab_desc* d) {
-  return check_desc(d) == POETX_OK ? poetx::plan_vocab_bwd(sizes_of(d)).total : 0;
+  if (check_desc(d) != POETX_OK) return 0;
+  return std::max(poetx::plan_vocab_bwd(sizes_of(d), false).total,
+                  poetx::plan_vocab_bwd(sizes_of(d), true).total);
 }
 
 int poetx_cross_entropy_fwd(const poetx_vocab_desc* d, const void* x, const void* W,

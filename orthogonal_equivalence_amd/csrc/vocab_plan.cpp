@@ -119,18 +119,25 @@ VocabFwdPlan plan_vocab_fwd(const VocabSizes& v) {
   return p;
 }
 
+namespace {
+// a launch for the turned copy of x and one that stores g_W (131072 x 4096 1 token
+// 211 us, 64 245, 96 300, 128 385; rows that are not whole lines take longer)
+float few_cost(const VocabSizes& v, int64_t n) {
+  if (v.tokens > few_tokens(v.t)) return 1e30f;
+  const float mb = (float)n * (float)(v.d * v.es()) / 1e6f;
+  return 6.0f + mb * (0.19f + 0.0013f * v.tokens) * (v.d * v.es() % 128 ? 1.2f : 1.0f);
+}
+float gw_cost(const VocabSizes& v, int64_t n) {
+  return std::min(few_cost(v, n), plan_tile_product(v.t, n, v.d, v.tokens, false).cost);
+}
+}  // namespace
+
 VocabProducts plan_vocab_products(const VocabSizes& v, int64_t n) {
   VocabProducts p;
   p.gx = plan_tile_product(v.t, v.tokens, v.d, n, false, kManySplits);
   p.gw = plan_tile_product(v.t, n, v.d, v.tokens, false);
   p.pair = plan_tile_pair(v.t, v.tokens, v.d, n, kManySplits);
-  // a launch for the turned copy of x and one that stores g_W (131072 x 4096 1 token
-  // 211 us, 64 245, 96 300, 128 385; rows that are not whole lines take longer)
-  const float mb = (float)n * (float)(v.d * v.es()) / 1e6f;
-  const float few =
-      6.0f + mb * (0.19f + 0.0013f * v.tokens) * (v.d * v.es() % 128 ? 1.2f : 1.0f);
-  p.few = v.tokens <= few_tokens(v.t) &&
-          few < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
+  p.few = few_cost(v, n) < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
   p.paired = !p.few && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
   return p;
 }
@@ -166,18 +173,26 @@ float split_gx(const VocabSizes& v, VocabBwdPlan& p) {
 
 }  // namespace
 
-VocabBwdPlan plan_vocab_bwd(const VocabSizes& v) {
+VocabBwdPlan plan_vocab_bwd(const VocabSizes& v, bool weight) {
   VocabBwdPlan p = {};
   const int64_t es = v.es();
   p.splits = 1;
-  if (v.t == DType::BF16 && vocab_dense_supported(v.tokens, v.vocab, v.d)) {
-    p.padded = ceil_div(v.tokens, kTile) * kTile;
+  // Fewer rows than a tile's 256 are padded, from where g_W has its kernel for few
+  // tokens on. (160 tokens, on tiles and padded, us: 131072 x 4096 1214, 885, 50257 x 2048
+  // 271, 234, 32000 x 4096 323, 262; W frozen 577, 501, 121, 121, 134, 145, where the tiles'
+  // estimate is a tenth too high.)
+  p.padded = ceil_div(v.tokens, kTile) * kTile;
+  if (v.t == DType::BF16 && v.tokens > few_tokens(v.t) &&
+      vocab_dense_supported(p.padded, v.vocab, v.d)) {
     set_pieces(v, p);
-    const float dense = split_columns(v.t, p.padded, p.piece, v.d, 1.0f).cost + split_gx(v, p) +
-                        dense_cost(ceil_div(p.piece, kTile) * ceil_div(v.d, kTile), v.tokens);
-    const float tile = plan_tile_product(v.t, v.tokens, p.piece, v.d, false, 1).cost +
-                       plan_tile_product(v.t, v.tokens, v.d, p.piece, false, kManySplits).cost +
-                       plan_tile_product(v.t, p.piece, v.d, v.tokens, false).cost;
+    float dense = split_columns(v.t, p.padded, p.piece, v.d, 1.0f).cost + split_gx(v, p);
+    float tile = plan_tile_product(v.t, v.tokens, p.piece, v.d, false, 1).cost +
+                 plan_tile_product(v.t, v.tokens, v.d, p.piece, false, kManySplits).cost;
+    if (weight) {
+      dense += dense_cost(ceil_div(p.piece, kTile) * ceil_div(v.d, kTile), v.tokens);
+      tile += gw_cost(v, p.piece);
+    }
+    if (!weight && v.tokens < kTile) tile *= 0.9f;
     p.dense = dense < tile;
   }
   if (!p.dense) {

@@ -39,7 +39,8 @@ struct VocabFwdPlan {
 };
 VocabFwdPlan plan_vocab_fwd(const VocabSizes& v);
 
-// The backward: `piece` columns of the vocabulary at a time.
+// The backward: `piece` columns of the vocabulary at a time. weight: g_W too (the
+// workspace is that of the larger of the two).
 struct VocabBwdPlan {
   bool dense;
   int64_t padded;       // rows of xs and gz
@@ -49,7 +50,7 @@ struct VocabBwdPlan {
   size_t rows, last, xs, gz, acc, part, total;
   bool summed() const { return pieces > 1 || splits > 1; }
 };
-VocabBwdPlan plan_vocab_bwd(const VocabSizes& v);
+VocabBwdPlan plan_vocab_bwd(const VocabSizes& v, bool weight);
 // of a piece's logits
 VocabColumns plan_vocab_columns(const VocabSizes& v, const VocabBwdPlan& p, int64_t cols);
 

@@ -16,20 +16,20 @@ from tests.vocab_cases import CASES, LISTED
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "orthogonal_equivalence_amd", "csrc")
 
-# reads lines "dtype tokens d vocab top" and prints the forward's choices and
-# the backward's, piece by piece
+# reads lines "dtype tokens d vocab top weight" and prints the forward's choices and
+# the backward's (weight: of both gradients), piece by piece
 PROGRAM = r"""
 #include <cstdio>
 #include <algorithm>
 #include "vocab_plan.h"
 using namespace poetx;
 int main() {
-  int t, top;
+  int t, top, weight;
   long long m, d, n;
-  while (scanf("%d %lld %lld %lld %d", &t, &m, &d, &n, &top) == 5) {
+  while (scanf("%d %lld %lld %lld %d %d", &t, &m, &d, &n, &top, &weight) == 6) {
     const VocabSizes v{static_cast<DType>(t), m, d, n, top};
     const VocabFwdPlan f = plan_vocab_fwd(v);
-    const VocabBwdPlan b = plan_vocab_bwd(v);
+    const VocabBwdPlan b = plan_vocab_bwd(v, weight != 0);
     printf("%lld %d %d %lld %d %d %zu %d %lld %lld %lld %d %d %d %zu", (long long)f.cols.dense, f.cols.tile.shape,
            f.cols.tile.nsplit, (long long)f.rows, f.copied, f.cells, f.total, b.dense,
            (long long)b.padded, (long long)b.piece, (long long)b.ldg, b.few, b.splits, b.kchunk, b.total);
@@ -68,10 +68,10 @@ def _program():
     return exe
 
 
-def plans(cases):
+def plans(cases, weight=1):
     """The choices for each (dtype, tokens, d, vocab, top), as dicts with a list
     of the backward's pieces."""
-    text = "".join("%d %d %d %d %d\n" % c for c in cases)
+    text = "".join("%d %d %d %d %d %d\n" % (*c, weight) for c in cases)
     out = subprocess.run([_program()], input=text, capture_output=True, text=True, check=True).stdout
     rows = []
     for line in out.splitlines():
@@ -111,7 +111,8 @@ def variants(case, p):
             last = q["cols"] - (-(-q["cols"] // p["kchunk"]) - 1) * p["kchunk"]
             got.add(("gx", whole, q["cols"] % 32 != 0, min(last, p["kchunk"]) < 256))
             got.add(("gx steps", -(-last // 32) % 4 if last >= 256 else -(-last // 32)))
-            got.add(("gw steps", -(-tokens // 32) % 4))
+            steps = -(-tokens // 32)
+            got.add(("gw steps", steps % 4 if steps >= 8 else steps))
             got.add(("grad steps", d // 32 % 4))
             got.add(("gx added", i > 0, d % 256 != 0, tokens % 256 != 0))
             got.add(("gw", d % 256 != 0, q["cols"] % 256 != 0, tokens % 32 != 0))
@@ -176,7 +177,8 @@ def test_plans_hold_together():
                       rng.choice((0, 1, rng.randint(1, 1024)))))
     cases += [(t, 1 << 24, 8, 1, 0) for t in (F32, BF16)] + [(t, 1, 8, 1 << 22, 1024) for t in (F32, BF16)]
     cases += [(t, 1 << 24, 1 << 11, 1 << 22, 1024) for t in (F32, BF16)]
-    for (t, tokens, d, vocab, top), p in zip(cases, plans(cases)):
+    both = list(zip(cases, plans(cases))) + list(zip(cases, plans(cases, 0)))
+    for (t, tokens, d, vocab, top), p in both:
         where = (t, tokens, d, vocab, top)
         assert 0 < p["total"] < 1 << 62 and 0 < p["b_total"] < 1 << 62, where
         assert p["dense"] == vocab or p["split"] == 1, where
@@ -191,7 +193,7 @@ def test_plans_hold_together():
         for q in p["pieces"]:
             assert q["dense"] == q["cols"] or q["split"] == 1, where
             if p["b_dense"]:
-                assert p["padded"] % 256 == 0 and p["padded"] >= tokens
+                assert p["padded"] % 256 == 0 and p["padded"] >= tokens > 128
                 assert p["kchunk"] % 32 == 0
                 n = -(-q["cols"] // p["kchunk"])
                 assert 1 <= n <= p["splits"], where

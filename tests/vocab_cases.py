@@ -128,7 +128,7 @@ CASES = [  # dtype, tokens, d, vocab
     (BF16, 3137, 2720, 3077), (F32, 7930, 96, 3471), (BF16, 3756, 3840, 2304), (BF16, 1350, 256, 109972),
     (F32, 4849, 16, 49508), (F32, 60, 2752, 30580), (F32, 1896, 1024, 2972), (BF16, 5600, 3392, 3840),
     (BF16, 2379, 320, 108458), (BF16, 4096, 2816, 36606), (BF16, 71, 208, 98288), (BF16, 73, 1024, 72448),
-    (BF16, 101, 1792, 47872),
+    (BF16, 101, 1792, 47872), (BF16, 153, 256, 110689),
 ]
 # dtype, tokens, d, vocab, top
 LISTED = [
@@ -141,5 +141,5 @@ LISTED = [
     (F32, 2482, 2336, 256, 1), (BF16, 399, 544, 66539, 10), (BF16, 4698, 8, 65522, 26),
     (F32, 35, 2816, 41863, 73), (BF16, 3606, 256, 70033, 25),
     (BF16, 68, 8, 118786, 2), (BF16, 97, 1280, 28160, 1), (BF16, 460, 1568, 46189, 2),
-    (BF16, 1792, 256, 78091, 3),
+    (BF16, 1792, 256, 78091, 3), (BF16, 166, 768, 41256, 14), (BF16, 215, 256, 110749, 3),
 ]
