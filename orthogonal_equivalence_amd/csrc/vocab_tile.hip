@@ -11,8 +11,8 @@
 //   backward  g_z = a 2^(c z - lse2), less b at the row's target: rounded once to
 //             x's type, the operand of the two products that follow.
 //
-// Few rows are bound by W's bytes: 1 token, 131072 x 4096 bf16 167 us (6.4 TB/s), 64 tokens
-// 180. float32: 100 x 5003 x 1024 26 us, one round of workgroups; 6508 x 80128 x 168 2.4 ms (73
+// Few rows are bound by W's bytes: 1 token, 131072 x 4096 bf16 167 us (6.4 TB/s).
+// float32: 100 x 5003 x 1024 26 us, one round of workgroups; 6508 x 80128 x 168 2.4 ms (73
 // TFLOP/s), where a tile's six steps are followed by its exponentials.
 #include "tile_core.h"
 #include "vocab.h"
