@@ -386,8 +386,8 @@ hipError_t launch_vocab_cells(const VocabList& l, int64_t M, int64_t col0, int64
                               bool own, hipStream_t s);
 
 // Forward: for every row and slot (a group of the piece's columns)
-// part[slot][row] = (max, sum) with sum_j 2^(scale z_j) = sum 2^max over the slot's
-// columns. vocab_tile_slots of them. With targets [M], z[row] = the logit of
+// part[slot][row] = (max, sum) of the slot's columns, max = max_j z_j and
+// sum = sum_j 2^(scale (z_j - max)). vocab_tile_slots of them. With targets [M], z[row] = the logit of
 // the row's, where the piece has it; with list.ids, of a piece that is the whole
 // vocabulary, z[row][top] = the list's, as launch_listed_logits has them (by
 // workgroups beside the tiles').

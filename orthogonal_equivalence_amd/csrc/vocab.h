@@ -104,18 +104,21 @@ __device__ __forceinline__ float quad_sum(float v) {
 // among the values; a NaN reaches it either way)
 __device__ __forceinline__ float exponent_base(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
 
-// The maximum m of c v over a row's values, this lane's NV and those of the
-// lanes 16, 32 and 48 further on, and the sum of 2^(c v - m), in all four
-// lanes.
+// The maximum m of a row's values, this lane's NV and those of the lanes 16, 32
+// and 48 further on, and the sum of 2^(c (v - m)), in all four lanes. (The
+// difference before the product: the maximum's own term is then exactly 1 and
+// what a term loses goes by its distance from the maximum. As 2^(c v - c m), one
+// instruction less, it went by |m|, and one to two steps of lse were lost; 8192 x
+// 131072 x 4096 5940 us that way, 5965 this.)
 template <int NV> __device__ __forceinline__ float2 row_max_sum(const float (&v)[NV], float c) {
   float m = v[0];
 #pragma unroll
   for (int q = 1; q < NV; ++q) m = fmaxf(m, v[q]);
-  m = quad_max(m) * c;
+  m = quad_max(m);
   const float at = exponent_base(m);
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int q = 0; q < NV; ++q) s[q & 3] += __builtin_amdgcn_exp2f(fmaf(v[q], c, -at));
+  for (int q = 0; q < NV; ++q) s[q & 3] += __builtin_amdgcn_exp2f((v[q] - at) * c);
   return make_float2(m, quad_sum((s[0] + s[1]) + (s[2] + s[3])));
 }
 

@@ -4,9 +4,13 @@
 // the logits. All are small beside the products (8192 x 131072 logits: 67 MB of
 // partial sums against 8.8 TFLOP).
 //
-//   lse  = ln 2 (M + log2 sum_i s_i 2^(m_i - M)), (m_i, s_i) the slots' parts
-//   loss = lse - z[target], or with p the softmax of the listed teacher
-//          logits over T: T^2 sum_k p_k (log p_k - z_k / T + lse)
+//   L    = log sum_i s_i 2^((m_i - M) log2(e) / T), (m_i, s_i) the slots' parts
+//          and M the largest of the m_i;  lse = M / T + L
+//   loss = L + (M - z[target]), or with p the softmax of the listed teacher
+//          logits over T: T^2 sum_k p_k (log p_k + (M - z_k) / T + L)
+// The sum holds M's own term, 1, so L >= 0, and M - z is a difference of two
+// logits: a loss is off by roundings of its own size, however large the logits
+// are, and not below 0. (lse - z loses a step of lse.)
 #include <algorithm>
 
 #include "lds_dma.h"
@@ -17,7 +21,7 @@ namespace {
 
 constexpr int NT = 256, NWAVES = NT / 64;
 constexpr int kMaxTop = 1024;  // entries of a row's list
-constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
+constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -137,11 +141,12 @@ __device__ __forceinline__ Teacher read_teacher(const VocabList& l, int64_t row,
   return w;
 }
 
-// The loss of one row, by one wave: log p_k = (t_k - top) / T - log total; an entry
-// whose p is 0 adds nothing. Its lse, `own`, is stored with it.
-__device__ __forceinline__ void distill_loss(const VocabList& l, int64_t row, float own,
-                                             const float* __restrict__ z, float* __restrict__ loss,
-                                             float* __restrict__ lse, int lane, int* ids, float* t) {
+// The loss of one row, by one wave, from M = base and L = log_sum: log p_k =
+// (t_k - top) / T - log total; an entry whose p is 0 adds nothing. Its lse is stored
+// with it.
+__device__ __forceinline__ void distill_loss(const VocabList& l, int64_t row, float base,
+                                             float log_sum, const float* __restrict__ z, float* loss,
+                                             float* lse, int lane, int* ids, float* t) {
   const float inv = 1.0f / l.temperature, rt = kLog2e / l.temperature;
   const Teacher w = read_teacher(l, row, rt, lane, ids, t);
   const float log_total = logf(w.total);
@@ -150,23 +155,24 @@ __device__ __forceinline__ void distill_loss(const VocabList& l, int64_t row, fl
     if (t[k] == -INFINITY) continue;
     const float p = teacher_exp(t[k], w.top, rt) / w.total;
     if (p == 0.0f) continue;
-    sum += p * (((t[k] - w.top) - z[row * l.top + k]) * inv - log_total + own);
+    sum += p * (((t[k] - w.top) + (base - z[row * l.top + k])) * inv - log_total + log_sum);
   }
   sum = wave_sum(sum);
   if (lane == 0) {
     loss[row] = !w.any ? 0.0f : w.bad ? NAN : l.temperature * l.temperature * sum;
-    lse[row] = w.any ? own : 0.0f;
+    lse[row] = w.any ? base * inv + log_sum : 0.0f;
   }
 }
+// (join_kernel left M in loss and L in lse)
 __global__ void __launch_bounds__(NT)
-distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z,
-                    float* __restrict__ loss, float* __restrict__ lse) {
+distill_loss_kernel(const VocabList l, int64_t rows, const float* __restrict__ z, float* loss,
+                    float* lse) {
   __shared__ int ids[NWAVES][kMaxTop];
   __shared__ float ts[NWAVES][kMaxTop];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = (int64_t)blockIdx.x * NWAVES + wave;
   if (row >= rows) return;
-  distill_loss(l, row, lse[row], z, loss, lse, lane, ids[wave], ts[wave]);
+  distill_loss(l, row, loss[row], lse[row], z, loss, lse, lane, ids[wave], ts[wave]);
 }
 
 // R rows a workgroup, their slots dealt over NT / R threads each (R a power of
@@ -182,11 +188,13 @@ join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int
             float* __restrict__ lse) {
   const int r = threadIdx.x & (R - 1), g = threadIdx.x / R, groups = NT / R;
   const int64_t row = (int64_t)blockIdx.x * R + r;
+  const float scale = kLog2e / l.temperature;
   float m = -INFINITY, s = 0.0f;
+  auto scaled = [&](float2 v, float to) { return v.y * __builtin_amdgcn_exp2f((v.x - to) * scale); };
   auto add = [&](float2 v) {
     const float top = fmaxf(m, v.x), to = exponent_base(top);
     // (a part of -inf alone is 0 2^-inf; NaN sums stay)
-    s = s * __builtin_amdgcn_exp2f(m - to) + v.y * __builtin_amdgcn_exp2f(v.x - to);
+    s = scaled(make_float2(m, s), to) + scaled(v, to);
     m = top;
   };
   if (row < rows) {
@@ -201,9 +209,9 @@ join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int
         top = fmaxf(top, v[q].x);
       }
       const float to = exponent_base(top);
-      s *= __builtin_amdgcn_exp2f(m - to);
+      s = scaled(make_float2(m, s), to);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s += v[q].y * __builtin_amdgcn_exp2f(v[q].x - to);
+      for (int q = 0; q < 8; ++q) s += scaled(v[q], to);
       m = top;
     }
     for (; i < slots; i += groups) add(p[i * part_ld]);
@@ -218,25 +226,28 @@ join_kernel(const float2* __restrict__ part, int64_t part_ld, int64_t slots, int
     }
   }
   if constexpr (JOIN == kJoinLoss) {
-    __shared__ float own[NWAVES];
-    if (g == 0 && r < NWAVES) own[r] = (exponent_base(m) + log2f(s)) * kLn2;
+    __shared__ float2 own[NWAVES];
+    if (g == 0 && r < NWAVES) own[r] = make_float2(exponent_base(m), logf(s));
     __shared__ int ids[NWAVES][kMaxTop];
     __shared__ float ts[NWAVES][kMaxTop];
     __syncthreads();
     const int wave = threadIdx.x >> 6;
     const int64_t mine = (int64_t)blockIdx.x * R + wave;
     if (wave < R && mine < rows)
-      distill_loss(l, mine, own[wave], z, loss, lse, threadIdx.x & 63, ids[wave], ts[wave]);
+      distill_loss(l, mine, own[wave].x, own[wave].y, z, loss, lse, threadIdx.x & 63, ids[wave],
+                   ts[wave]);
     return;
   }
   if (g != 0 || row >= rows) return;
-  float v = (exponent_base(m) + log2f(s)) * kLn2;
+  const float base = exponent_base(m), log_sum = logf(s);
   if constexpr (JOIN == kTargets) {
     const bool part_of = l.ids[row] >= 0;
-    v = part_of ? v : 0.0f;
-    loss[row] = !part_of ? 0.0f : l.ids[row] >= l.vocab ? NAN : v - z[row];
+    lse[row] = part_of ? base + log_sum : 0.0f;
+    loss[row] = !part_of ? 0.0f : l.ids[row] >= l.vocab ? NAN : log_sum + (base - z[row]);
+  } else {
+    loss[row] = base;
+    lse[row] = log_sum;
   }
-  lse[row] = v;
 }
 
 // Whether the row takes part (one wave; *bad: an id past the vocabulary)

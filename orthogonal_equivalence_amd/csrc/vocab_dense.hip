@@ -159,7 +159,7 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < FM; ++i) mx[i] = quad_max(mx[i]) * scale;
+        for (int i = 0; i < FM; ++i) mx[i] = quad_max(mx[i]);
         d.in_agprs();
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -169,7 +169,7 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
           for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[e] += __builtin_amdgcn_exp2f(fmaf(d.acc[i][j][e], scale, -at));
+              s[e] += __builtin_amdgcn_exp2f((d.acc[i][j][e] - at) * scale);
           sum[i] = (s[0] + s[1]) + (s[2] + s[3]);
           __builtin_amdgcn_sched_barrier(0);
         }

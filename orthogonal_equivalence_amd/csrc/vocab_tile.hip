@@ -3,8 +3,8 @@
 // registers. Two ends:
 //
 //   forward   per row the maximum and the sum of exponentials over the wave's
-//             columns: with c = log2(e) / temperature, m = max c z_j and
-//             s = sum 2^(c z_j - m). 32 lanes' worth of columns of one row lie in four
+//             columns: with c = log2(e) / temperature, m = max z_j and
+//             s = sum 2^(c (z_j - m)). 32 lanes' worth of columns of one row lie in four
 //             lanes (16 apart), so a row costs its exponentials and four
 //             exchanges. (m, s) goes to part[slot][row]: nothing is read again
 //             but 8 bytes for every 16 to 64 columns.
