@@ -348,13 +348,13 @@ struct VocabProduct {
   const void* W = nullptr;
   int M = 0, N = 0, K = 0;
   int col0 = 0;        // the piece's first column in the vocabulary
-  float scale = 0.0f;  // log2(e) / temperature
+  float scale = 0.0f;  // log2(e) / temperature (forward), 1 / temperature (backward)
 };
 // One row's part in the gradient of its logits:
-//   g_z[j] = a 2^(scale z_j - lse2) - (j == target ? b : 0),
+//   g_z[j] = a exp(scale z_j - lse) - (j == target ? b : 0),
 // and 0 where a is 0 and j is not the target, whatever z is.
 struct VocabRow {
-  float a, lse2, b;
+  float a, lse, b;
   int target;  // in the whole vocabulary; -1: none
 };
 // The entries of listed ids (VocabList) that lie in a piece, by the cells of the

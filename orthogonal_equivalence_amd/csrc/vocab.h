@@ -186,9 +186,14 @@ __device__ __forceinline__ void store_cell(const VocabCells& cells, const OwnCel
     store(e + lane < c.end ? c.entries[e + lane] : 0, min(64, c.end - e));
 }
 
+// exp(z / T - lse), inv = 1 / T. (In base 2 from the start, 2^(c z - log2(e) lse), it
+// lost a rounding of lse; this loses one of the difference, where 1 / T is exact.)
+__device__ __forceinline__ float softmax_at(float z, float inv, float lse) {
+  return __builtin_amdgcn_exp2f(fmaf(z, inv, -lse) * 1.44269504088896341f);
+}
 // g_z at a logit z of the vocabulary's column `col` (VocabRow)
-__device__ __forceinline__ float logit_gradient(const VocabRow& r, float z, float c, int col) {
-  const float q = r.a == 0.0f ? 0.0f : r.a * __builtin_amdgcn_exp2f(fmaf(z, c, -r.lse2));
+__device__ __forceinline__ float logit_gradient(const VocabRow& r, float z, float inv, int col) {
+  const float q = r.a == 0.0f ? 0.0f : r.a * softmax_at(z, inv, r.lse);
   return col == r.target ? q - r.b : q;
 }
 

@@ -297,7 +297,7 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
   if (row < rows) {
     bool bad;
     any = row_takes_part(l, row, lane, &bad);
-    r.lse2 = lse[row] * kLog2e;
+    r.lse = lse[row];
     if (l.teacher) {
       r.a = any ? g_loss[row] * l.temperature : 0.0f;
     } else {
@@ -343,7 +343,7 @@ turned_copy_kernel(const VocabRow* __restrict__ parts, int rows, int K, const Vo
 }
 
 // One wave a row: where the row's id j lies in the piece,
-//   g_z[j] = a (2^(scale z_j - lse2) - the sum of p over the entries with that id).
+//   g_z[j] = a (exp(z_j / T - lse) - the sum of p over the entries with that id).
 // The entries' p are in LDS, so that each finds its id's other entries (an id
 // listed twice: both write the same value). 4096 rows of 64 entries 12 us.
 template <typename T>
@@ -358,7 +358,7 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
   if (row >= rows) return;
   const VocabRow own = r[row];
   if (own.a == 0.0f) return;  // (whose gradient is zero)
-  const float rt = kLog2e / l.temperature;
+  const float inv = 1.0f / l.temperature, rt = kLog2e / l.temperature;
   const Teacher w = read_teacher(l, row, rt, lane, ids[wave], p[wave]);
   const int padded = (l.top + 3) / 4 * 4;
   for (int k = lane; k < padded; k += 64) {
@@ -381,7 +381,7 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
       sum += i.z == id ? v.z : 0.0f;
       sum += i.w == id ? v.w : 0.0f;
     }
-    const float e = __builtin_amdgcn_exp2f(fmaf(z[row * l.top + k], rt, -own.lse2));
+    const float e = softmax_at(z[row * l.top + k], inv, own.lse);
     const int64_t at = tiled ? tiled_offset(row, id - col0, ldg) : row * ldg + (id - col0);
     store_as(gz + at, own.a * (e - sum));
   }

@@ -229,7 +229,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     p.W = Wc;
     p.M = (int)plan.padded; p.N = (int)split.dense; p.K = (int)d->d;
     p.col0 = (int)c;
-    p.scale = scale_of(d);
+    p.scale = 1.0f / d->temperature;
     if (p.N) POETX_TRY(poetx::launch_vocab_grad_dense(p, last, rows, gz, plan.ldg, s));
     if (split.dense < cols) {
       p.x = x;

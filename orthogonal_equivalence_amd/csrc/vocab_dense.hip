@@ -225,7 +225,7 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
       [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
-          asm volatile("" : "+v"(row[i].a), "+v"(row[i].lse2), "+v"(row[i].b), "+v"(row[i].target));
+          asm volatile("" : "+v"(row[i].a), "+v"(row[i].lse), "+v"(row[i].b), "+v"(row[i].target));
       },
       [&](int m0, int n0, int, int) __attribute__((always_inline)) {
         const int ln = opaque_lane(d);
@@ -250,9 +250,7 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
               float v[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                v[e] = r.a == 0.0f ? 0.0f
-                                   : r.a * __builtin_amdgcn_exp2f(
-                                               fmaf(d.acc[i][j + h][e], scale, -r.lse2));
+                v[e] = r.a == 0.0f ? 0.0f : r.a * softmax_at(d.acc[i][j + h][e], scale, r.lse);
               if (rare) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

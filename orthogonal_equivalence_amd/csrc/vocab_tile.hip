@@ -8,8 +8,8 @@
 //             lanes (16 apart), so a row costs its exponentials and four
 //             exchanges. (m, s) goes to part[slot][row]: nothing is read again
 //             but 8 bytes for every 16 to 64 columns.
-//   backward  g_z = a 2^(c z - lse2), less b at the row's target: rounded once to
-//             x's type, the operand of the two products that follow.
+//   backward  g_z = a exp(z / temperature - lse), less b at the row's target: rounded
+//             once to x's type, the operand of the two products that follow.
 //
 // Few rows are bound by W's bytes: 1 token, 131072 x 4096 bf16 167 us (6.4 TB/s).
 // float32: 100 x 5003 x 1024 26 us, one round of workgroups; 6508 x 80128 x 168 2.4 ms (73

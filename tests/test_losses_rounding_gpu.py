@@ -125,3 +125,33 @@ def test_losses_are_not_negative(name, scale):
     clear = (two[:, 0] - two[:, 1]).double() > 4 * bound
     assert int(clear.sum()) > tokens // 2
     assert bool((loss[clear] >= 0).all()), loss[clear].min().item()
+
+
+@pytest.mark.parametrize("name", ROUTES)
+def test_gradients_do_not_depend_on_an_offset(name):
+    """The same constant in every logit and in lse (both exact): the differences that
+    the gradients are made of are the same, and so is every bit of g_x and g_W, but
+    for the column of W that holds the constant."""
+    print("gradients, offset", name, flush=True)
+    case = ROUTES[name]
+    _, tokens, d, vocab = case
+    targets = V.draw_targets(tokens, vocab, 6)
+    ids, teacher = V.draw_teacher(tokens, vocab, 5, 7)
+    g = (torch.rand(tokens, generator=torch.Generator().manual_seed(3)) + 0.5).cuda()
+    x, W = _inputs(case, 0.0)
+    # (of the size of the rows' lse, in sixteenths; at T = 2 z / T is exact too)
+    _, lse = L.cross_entropy_forward(x, W, targets)
+    lse = torch.where(targets >= 0, torch.round(lse * 16) / 16, lse)
+    _, kd_lse, _ = L.distill_forward(x, W, ids, teacher, 2.0)
+    kd_lse = torch.round(kd_lse * 16) / 16
+    got = []
+    for offset in (0.0, 1024.0, -1024.0):
+        x, W = _inputs(case, offset)
+        _, _, z = L.distill_forward(x, W, ids, teacher, 2.0)
+        got.append((
+            *L.cross_entropy_backward(g, x, W, targets, lse + offset, g_lse=0.25 * g, need_g_W=True),
+            *L.distill_backward(g, x, W, ids, teacher, kd_lse + offset / 2, z, 2.0, need_g_W=True)))
+    for other in got[1:]:
+        for k, (a, b) in enumerate(zip(got[0], other)):
+            assert torch.equal(a[:, 1:], b[:, 1:]), (k, (a - b)[:, 1:].abs().max().item())
+            assert k % 2 == 0 or torch.equal(a, b)
