@@ -471,6 +471,8 @@ int poetx_dense_bwd(const poetx_dense_desc* desc, const void* g_y, const void* x
  *     lse and gradient are 0. An id listed twice counts twice.
  *   both           g_x = g_z W,  g_W = g_z^T x
  *
+ * A row whose gradients to loss and lse are 0 adds nothing to g_W either, and has
+ * a g_x of 0, whatever its x holds.
  * A target or id past the vocabulary is read nowhere; its row's loss and
  * gradients are NaN. Logits, sums and losses are float32; g_z is rounded to
  * the act type once, as the operand of the gradients' products (the matrix

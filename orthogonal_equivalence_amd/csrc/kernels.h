@@ -450,7 +450,8 @@ hipError_t launch_vocab_loss(const float2* part, int64_t part_ld, int64_t slots,
                              int64_t rows, const float* z, float* loss, float* lse, hipStream_t s);
 // The rows' parts (none for those past `rows`), and with xs a copy of x
 // [padded][K], with `tiled` in the tiled layout, in which rows that take no
-// part, and those past `rows`, are zero; with W_last that of W [l.vocab][K].
+// part or have no gradient, and those past `rows`, are zero; with W_last that of W
+// [l.vocab][K].
 struct VocabCopies {
   const void* x = nullptr;
   void* xs = nullptr;

@@ -271,6 +271,11 @@ __device__ __forceinline__ bool row_takes_part(const VocabList& l, int64_t row, 
   return any;
 }
 
+// Whether a row is in the copies of x: a row that takes no part, or whose gradients
+// to loss and lse are zero, has g_z = 0 whatever its x holds, and 0 times an
+// infinity there must not reach g_W.
+__device__ __forceinline__ bool has_gradient(float a, float b) { return a != 0.0f || b != 0.0f; }
+
 // Four rows a workgroup, one wave each: the row's part in the gradient, and
 // its copy of x; then the copy of W's last rows. (8192 rows of 4096: 29 us, 4.6 TB/s.)
 constexpr int kLastRows = kTileRows;
@@ -292,28 +297,28 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
           from < l.vocab ? *reinterpret_cast<const uint4*>(w + k) : none;
     return;
   }
-  bool any = false;
-  VocabRow r{0.0f, 0.0f, 0.0f, -1};
+  float a = 0.0f, b = 0.0f, own = 0.0f;
+  int target = -1;
   if (row < rows) {
     bool bad;
-    any = row_takes_part(l, row, lane, &bad);
-    r.lse = lse[row];
+    const bool any = row_takes_part(l, row, lane, &bad);
+    own = lse[row];
     if (l.teacher) {
-      r.a = any ? g_loss[row] * l.temperature : 0.0f;
+      a = any ? g_loss[row] * l.temperature : 0.0f;
     } else {
-      r.b = any ? g_loss[row] : 0.0f;
-      r.a = any && g_lse ? r.b + g_lse[row] : r.b;
-      r.target = any && !bad ? (int)l.ids[row] : -1;
+      b = any ? g_loss[row] : 0.0f;
+      a = any && g_lse ? b + g_lse[row] : b;
+      target = any && !bad ? (int)l.ids[row] : -1;
     }
-    if (bad) r.a = NAN;
+    if (bad) a = NAN;
   }
-  if (lane == 0) out[row] = r;
+  if (lane == 0) out[row] = VocabRow{a, own, b, target};
   T* xs = static_cast<T*>(c.xs);
   if (!xs) return;
   const T* x = static_cast<const T*>(c.x);
   for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
     *reinterpret_cast<uint4*>(xs + (c.tiled ? tiled_offset(row, k, K) : row * K + k)) =
-        any ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
+        has_gradient(a, b) ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
 }
 
 // x's copy with the rows innermost, for few rows (after their parts): a workgroup
@@ -326,8 +331,7 @@ turned_copy_kernel(const VocabRow* __restrict__ parts, int rows, int K, const Vo
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k0 = blockIdx.x * 64;
   const T* x = static_cast<const T*>(c.x);
   for (int row = wave; row < c.xt_rows; row += NWAVES) {
-    // (a row whose gradient is zero may as well be left out)
-    const bool any = row < rows && (parts[row].a != 0.0f || parts[row].b != 0.0f);
+    const bool any = row < rows && has_gradient(parts[row].a, parts[row].b);
     tile[row][lane] = any && k0 + lane < K ? x[(int64_t)row * K + k0 + lane] : T{};
   }
   __syncthreads();

@@ -20,8 +20,9 @@ other reduction is the caller's (a mean over n rows: g_loss = 1 / n).
 A row whose target is negative takes no part: its loss and lse are 0, and it
 adds nothing to a gradient, whatever its x holds. Likewise an entry of a
 teacher's list with a negative id or a logit of -inf, and a row without any
-other. A target or id past the vocabulary makes its row's loss, and the
-gradients, NaN.
+other. A row whose g_loss (and g_lse) is 0 adds nothing to a gradient, either.
+A target or id past the vocabulary makes its row's loss, and the gradients,
+NaN.
 
 Outputs and workspaces come from torch's allocator on the stream that the call
 runs on, so calls on different streams, and calls captured into different
