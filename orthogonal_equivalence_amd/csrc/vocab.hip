@@ -276,6 +276,14 @@ __device__ __forceinline__ bool row_takes_part(const VocabList& l, int64_t row, 
 // infinity there must not reach g_W.
 __device__ __forceinline__ bool has_gradient(float a, float b) { return a != 0.0f || b != 0.0f; }
 
+// 16 bytes at p, or zeros (as a choice of two values the compiler loads through an
+// address that may be the zeros' in scratch memory)
+__device__ __forceinline__ uint4 load16_if(bool c, const void* p) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (c) v = *static_cast<const uint4*>(p);
+  return v;
+}
+
 // Four rows a workgroup, one wave each: the row's part in the gradient, and
 // its copy of x; then the copy of W's last rows. (8192 rows of 4096: 29 us, 4.6 TB/s.)
 constexpr int kLastRows = kTileRows;
@@ -286,15 +294,13 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
             VocabRow* __restrict__ out, int K, const VocabCopies c) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * NWAVES + (threadIdx.x >> 6);
-  const uint4 none = make_uint4(0, 0, 0, 0);
   if (row >= padded) {
     const int64_t last = row - padded, from = l.vocab / kLastRows * kLastRows + last;
     if (!c.W_last || last >= kLastRows) return;
     const T* w = static_cast<const T*>(c.W) + from * K;
     T* out_w = static_cast<T*>(c.W_last) + last * K;
     for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
-      *reinterpret_cast<uint4*>(out_w + k) =
-          from < l.vocab ? *reinterpret_cast<const uint4*>(w + k) : none;
+      *reinterpret_cast<uint4*>(out_w + k) = load16_if(from < l.vocab, w + k);
     return;
   }
   float a = 0.0f, b = 0.0f, own = 0.0f;
@@ -318,7 +324,7 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
   const T* x = static_cast<const T*>(c.x);
   for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
     *reinterpret_cast<uint4*>(xs + (c.tiled ? tiled_offset(row, k, K) : row * K + k)) =
-        has_gradient(a, b) ? *reinterpret_cast<const uint4*>(x + row * K + k) : none;
+        load16_if(has_gradient(a, b), x + row * K + k);
 }
 
 // x's copy with the rows innermost, for few rows (after their parts): a workgroup
