@@ -2,7 +2,7 @@
 import pytest
 
 from tests.test_vocab_plan import plans
-from tests.vocab_routes import ROUTES
+from tests.vocab_routes import RANGES, ROUTES, SORTED
 
 # of the forward and of the backward of both gradients: columns on 256 x 256
 # tiles, whether the backward runs on them, g_W on the kernel for few tokens, pieces
@@ -26,3 +26,19 @@ def test_route(name):
     if p["b_dense"]:  # (g_x's reduction in ranges, summed from slabs)
         assert p["splits"] > 1 and p["padded"] % 256 == 0
         assert p["pieces"][0]["dense"] == min(p["dense"] or case[3], p["piece"])
+
+
+@pytest.mark.parametrize("name", SORTED)
+def test_sorted_route(name):
+    p, = plans([SORTED[name]])
+    dense = {"sorted, 256 x 256 tiles": 20000, "sorted, both": 49152}.get(name, 0)
+    assert p["cells"] and p["dense"] == dense
+
+
+@pytest.mark.parametrize("name", RANGES)
+def test_ranges(name):
+    _, tokens, _, vocab, top = RANGES[name]
+    p, = plans([RANGES[name]])
+    assert p["cells"] == (top > 0) and 0 < tokens % p["rows"] < 256 and p["rows"] < tokens
+    # (16384 cells a row of cells, the most that are sorted)
+    assert p["dense"] == (vocab if top else (vocab // 256) * 256)
