@@ -55,3 +55,70 @@ def test_rows_without_gradient(name):
     assert _same(*out)
     for g_x in out[1][::2]:
         assert bool((g_x[off] == 0).all())
+
+
+@pytest.mark.parametrize("name", ROUTES)
+def test_rows_that_take_no_part(name):
+    """Padding may hold anything: NaN and infinities in the x of a row without a target or
+    entries reach no other row's results and no gradient."""
+    print("no part", name, flush=True)
+    t, tokens, d, vocab = ROUTES[name]
+    x, W = V.inputs(tokens, d, vocab, DTYPE[t], 1, True)
+    targets = V.draw_targets(tokens, vocab, 2, ignored=0.4)
+    ids, teacher = V.draw_teacher(tokens, vocab, 6, 3)
+    ids = torch.where((targets < 0)[:, None], -1, ids)
+    g = torch.rand(tokens, generator=torch.Generator().manual_seed(5)).cuda() + 0.5
+    rows = targets < 0
+    held = (ids >= 0) & (teacher > -math.inf)
+    kd_rows = ~held.any(1)
+    out = []
+    for v, kd in zip(_dirty(x, rows), _dirty(x, kd_rows)):
+        loss, lse = L.cross_entropy_forward(v, W, targets)
+        got = [loss, lse, *L.cross_entropy_backward(g, v, W, targets, lse, g_lse=g, need_g_W=True),
+               *L.cross_entropy_backward(g, v, W, targets, lse)[:1]]
+        assert all(bool((r[rows] == 0).all()) for r in (got[0], got[1], got[2], got[4]))
+        loss, lse, z = L.distill_forward(kd, W, ids, teacher, 2.0)
+        got += [loss, lse, *L.distill_backward(g, kd, W, ids, teacher, lse, z, 2.0, need_g_W=True)]
+        assert all(bool((r[kd_rows] == 0).all()) for r in got[5:8])
+        # (masked by the teacher's logits alone: entries with ids)
+        own = torch.where(ids < 0, 7, ids)
+        masked = torch.where(ids < 0, -math.inf, teacher)
+        loss, lse, z = L.distill_forward(kd, W, own, masked, 2.0)
+        got += [loss, lse, *L.distill_backward(g, kd, W, own, masked, lse, z, 2.0, need_g_W=True)]
+        out.append(got)
+        assert all(bool(torch.isfinite(r).all()) for r in got)
+    assert _same(*out)
+
+
+@pytest.mark.parametrize("name", ROUTES)
+def test_ids_past_the_vocabulary(name):
+    """Read nowhere: the row's loss and g_x are NaN and g_W is; the other rows keep their
+    bits."""
+    print("past the vocabulary", name, flush=True)
+    t, tokens, d, vocab = ROUTES[name]
+    x, W = V.inputs(tokens, d, vocab, DTYPE[t], 1, True)
+    targets = V.draw_targets(tokens, vocab, 2)
+    ids, teacher = V.draw_teacher(tokens, vocab, 6, 3)
+    g = torch.ones(tokens, device="cuda")
+    row = tokens - 2
+    targets[row] = ids[row, 0] = 5
+    teacher[row, 0] = 0.5
+
+    def both(targets, ids):
+        loss, lse = L.cross_entropy_forward(x, W, targets)
+        first = [loss, lse, *L.cross_entropy_backward(g, x, W, targets, lse, need_g_W=True)]
+        loss, lse, z = L.distill_forward(x, W, ids, teacher, 2.0)
+        return first + [loss, lse, *L.distill_backward(g, x, W, ids, teacher, lse, z, 2.0,
+                                                       need_g_W=True)]
+
+    ref = both(targets, ids)
+    keep = torch.arange(tokens, device="cuda") != row
+    for bad in (vocab, vocab + 255, 2 ** 31 + 5, 2 ** 40):
+        targets[row] = ids[row, 0] = bad
+        got = both(targets, ids)
+        for k in (0, 2, 4, 6):
+            assert torch.equal(got[k][keep], ref[k][keep]) and bool(torch.isnan(got[k][row]).all())
+        for k in (3, 7):
+            assert bool(torch.isnan(got[k]).all())
+        for k in (1, 5):
+            assert torch.equal(got[k], ref[k])
