@@ -188,12 +188,19 @@ __device__ __forceinline__ void store_cell(const VocabCells& cells, const OwnCel
 
 // exp(z / T - lse), inv = 1 / T. (In base 2 from the start, 2^(c z - log2(e) lse), it
 // lost a rounding of lse; this loses one of the difference, where 1 / T is exact.)
-__device__ __forceinline__ float softmax_at(float z, float inv, float lse) {
-  return __builtin_amdgcn_exp2f(fmaf(z, inv, -lse) * 1.44269504088896341f);
+// float32 also takes back what the product with log2(e) lost, x 2^-24 of the value
+// (bf16's rounding is far above it).
+template <typename T> __device__ __forceinline__ float softmax_at(float z, float inv, float lse) {
+  constexpr float kHigh = 1.44269502162933349609375f, kLow = 1.92596299112661768e-8f;  // log2(e)
+  const float x = fmaf(z, inv, -lse), t = x * kHigh, e = __builtin_amdgcn_exp2f(t);
+  if constexpr (sizeof(T) == 2) return e;
+  const float left = fmaf(x, kLow, fmaf(x, kHigh, -t)) * 0.693147180559945309f;
+  return fabsf(t) < 126.0f ? fmaf(e, left, e) : e;
 }
 // g_z at a logit z of the vocabulary's column `col` (VocabRow)
+template <typename T>
 __device__ __forceinline__ float logit_gradient(const VocabRow& r, float z, float inv, int col) {
-  const float q = r.a == 0.0f ? 0.0f : r.a * softmax_at(z, inv, r.lse);
+  const float q = r.a == 0.0f ? 0.0f : r.a * softmax_at<T>(z, inv, r.lse);
   return col == r.target ? q - r.b : q;
 }
 

@@ -391,7 +391,7 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
       sum += i.z == id ? v.z : 0.0f;
       sum += i.w == id ? v.w : 0.0f;
     }
-    const float e = softmax_at(z[row * l.top + k], inv, own.lse);
+    const float e = softmax_at<T>(z[row * l.top + k], inv, own.lse);
     const int64_t at = tiled ? tiled_offset(row, id - col0, ldg) : row * ldg + (id - col0);
     store_as(gz + at, own.a * (e - sum));
   }

@@ -250,7 +250,7 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
               float v[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                v[e] = r.a == 0.0f ? 0.0f : r.a * softmax_at(d.acc[i][j + h][e], scale, r.lse);
+                v[e] = r.a == 0.0f ? 0.0f : r.a * softmax_at<bf16_t>(d.acc[i][j + h][e], scale, r.lse);
               if (rare) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

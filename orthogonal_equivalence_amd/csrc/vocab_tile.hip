@@ -110,7 +110,7 @@ struct GradEnd {
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          v[e] = n + e < p.N ? logit_gradient(r, acc[i][j][e], scale, col0 + n + e) : 0.0f;
+          v[e] = n + e < p.N ? logit_gradient<T>(r, acc[i][j][e], scale, col0 + n + e) : 0.0f;
         Quad<T>::store(static_cast<T*>(gz) + (tiled ? tiled_offset(m, n, ldg) : m * ldg + n), v);
       }
     }

@@ -155,3 +155,34 @@ def test_gradients_do_not_depend_on_an_offset(name):
         for k, (a, b) in enumerate(zip(got[0], other)):
             assert torch.equal(a[:, 1:], b[:, 1:]), (k, (a - b)[:, 1:].abs().max().item())
             assert k % 2 == 0 or torch.equal(a, b)
+
+
+def test_exponentials_of_float32():
+    """g_W of one token whose x is 1 in one column: g_loss exp(z - lse) itself, of logits
+    that are exact, from e^-64 to e^64. Within half steps: 2 of the hardware's
+    exponential, 1 each of its correction, of the product with g_loss and of the matrix
+    product, and 1 of what a correction of second order leaves."""
+    vocab = 8193
+    z = (torch.arange(vocab, device="cuda") - 4096).double() / 64
+    x, W = torch.zeros(1, 8, device="cuda"), torch.zeros(vocab, 8, device="cuda")
+    x[0, 0] = 1
+    W[:, 0] = z.float()
+    target = torch.tensor([0], device="cuda")
+    g = torch.full((1,), 0.75, device="cuda")
+    for lse in (0.0, 3.0, -5.0):
+        _, g_W = L.cross_entropy_backward(g, x, W, target, torch.full((1,), lse, device="cuda"),
+                                          need_g_x=False, need_g_W=True)
+        want = 0.75 * torch.exp(z - lse)
+        err = ((g_W[:, 0].double() - want).abs() / want)[1:]
+        print(f"    worst {err.max().item() / U32:.2f} half steps", flush=True)
+        assert bool((err <= 6 * U32).all())
+    # z / T with an exact 1 / T, and entries of a list among them
+    ids = torch.tensor([[5, 4096, 8000]], device="cuda")
+    teacher = torch.zeros(1, 3, device="cuda")
+    z32 = W[ids[0], 0][None].contiguous()
+    _, g_W = L.distill_backward(g, x, W, ids, teacher, torch.full((1,), 2.0, device="cuda"), z32, 4.0,
+                                need_g_x=False, need_g_W=True)
+    want = 3.0 * torch.exp(z / 4 - 2)
+    keep = torch.ones(vocab, dtype=torch.bool, device="cuda")
+    keep[ids[0]] = False
+    assert bool((((g_W[:, 0].double() - want).abs() / want)[keep] <= 6 * U32).all())
