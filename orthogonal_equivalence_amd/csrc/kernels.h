@@ -258,6 +258,7 @@ struct TileProduct {
   bool b_int8 = false;  // B: INT8 codes of a bf16 product, both K-major, K % 16 == 0
   float* part = nullptr;
   Epilogue ep;
+  bool blocked = false;  // float32: sums of 16 k apart (tile_core.h), an N-major B
 };
 // Work items along one dimension of a launch that HIP takes.
 constexpr int64_t kMaxWorkItems = UINT32_MAX;

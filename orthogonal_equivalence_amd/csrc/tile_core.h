@@ -244,6 +244,10 @@ template <int J> __device__ __forceinline__ void mma(const bf16x8_t& a, const bf
 template <int J> __device__ __forceinline__ void mma(const floatx4& a, const floatx4& b, floatx4& c) {
   asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+v"(c) : "v"(a[J]), "v"(b[J]));
 }
+// float32 product J alone: c = a b
+template <int J> __device__ __forceinline__ void mma_alone(const floatx4& a, const floatx4& b, floatx4& c) {
+  asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, 0" : "=&v"(c) : "v"(a[J]), "v"(b[J]));
+}
 // wait states between VALU writes (of operands, accumulators or EXEC) and the
 // products that read them, and between products and VALU reads of their
 // results: more than any 16 x 16 product needs
@@ -284,6 +288,13 @@ template <typename T, typename TB, int BM, int BN, int NW, int NS> constexpr int
   return NS * (Operand<T, BM, true, NW>::BYTES + Operand<TB, BN, true, NW>::BYTES);
 }
 
+// One accumulator, or (an end with kBlocked, float32) sums of blocks of k that are
+// added to it: what a long sum loses goes by the number of additions to the whole.
+// A block is a half of each of NS steps (the last steps: of one), whose sums are
+// added while the next one's products run. (g_W of 8 tokens, 2440 x 3247, 3.2e-6 off in
+// one chain, 0.6e-6 in blocks, 0.4e-6 by a library's products; 2048 tokens, 2048 x
+// 32000, forward 1900 us, 1955 in blocks, both gradients 5870, 6070.)
+//
 // One workgroup's tile (its place `wg` among p's tiles, part `part_k` of a
 // split reduction), whose accumulators go to end.run(): lane l holds row
 // m + 16 i + l % 16, columns n + 16 j + 4 (l / 16) .. + 3 of its wave's part of
@@ -327,6 +338,25 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  constexpr bool kBlocks = End::kBlocked && sizeof(T) == 4;
+  floatx4 blk[2][kBlocks ? FM : 1][kBlocks ? FN : 1];  // of the two halves of a step
+  for (auto& h : blk)
+    for (auto& row : h)
+      for (auto& c : row) c = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  // acc += a block's sums, at least a half step after its products
+  auto add_block = [&](int h) POETX_INLINE {
+    if constexpr (kBlocks) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += blk[h][i][j][e];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
   // zeros past the reduction's end where step t is not full
   auto clear_tail = [&](int slot, int t) POETX_INLINE {
     const int kleft = p.K - (t0 + t) * BK;
@@ -364,8 +394,10 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
   // the products of one half step, after(r) behind fragment row r (float32:
   // product by product over all pairs, so that no two in a row take the same
   // accumulator)
-  auto products = [&](auto half, auto after) POETX_INLINE {
+  // ALONE: they begin a block.
+  auto products = [&](auto half, auto alone, auto after) POETX_INLINE {
     constexpr int H = decltype(half)::value;
+    constexpr bool ALONE = decltype(alone)::value;
     typename Elem<T>::Frag b[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -375,13 +407,18 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
     settle_before();
     for_each<FM>([&](auto r) POETX_INLINE {
       constexpr int i = decltype(r)::value;
-      for_each<FN>([&](auto j) POETX_INLINE { mma<0>(b[j], fa[H][i], acc[i][j]); });
+      for_each<FN>([&](auto j) POETX_INLINE {
+        if constexpr (kBlocks && ALONE) mma_alone<0>(b[j], fa[H][i], blk[H][i][j]);
+        else if constexpr (kBlocks) mma<0>(b[j], fa[H][i], blk[H][i][j]);
+        else mma<0>(b[j], fa[H][i], acc[i][j]);
+      });
       after(r);
     });
     if constexpr (sizeof(T) == 4)
       for_each<3 * FM * FN>([&](auto q) POETX_INLINE {
         constexpr int e = decltype(q)::value / (FM * FN), ij = decltype(q)::value % (FM * FN);
-        mma<1 + e>(b[ij % FN], fa[H][ij / FN], acc[ij / FN][ij % FN]);
+        if constexpr (kBlocks) mma<1 + e>(b[ij % FN], fa[H][ij / FN], blk[H][ij / FN][ij % FN]);
+        else mma<1 + e>(b[ij % FN], fa[H][ij / FN], acc[ij / FN][ij % FN]);
       });
   };
   constexpr std::integral_constant<int, 0> kFirst{};
@@ -394,8 +431,9 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
   // address unit takes 16 cycles a copy, for four waves at once). Half way
   // the second half's fragments are in registers too; once this wave's copies
   // of step t + 1 have landed, the barrier makes that hold for every wave.
-  // Steady: steps t + 1 .. t + NS - 1 exist and are full; nothing is tested.
-  auto step = [&](int slot, int t, auto steady) POETX_INLINE {
+  // Steady: steps t + 1 .. t + NS - 1 exist and are full; nothing is tested. first,
+  // last: of a block.
+  auto step = [&](int slot, int t, auto steady, auto first, auto last) POETX_INLINE {
     constexpr bool kSteady = decltype(steady)::value;
     const int prev = slot == 0 ? NS - 1 : slot - 1;
     const int next = slot + 1 == NS ? 0 : slot + 1;
@@ -414,8 +452,9 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
     read(slot, kSecond);
     if (!kSteady && t + NS - 1 < steps) issue_all(prev, t + NS - 1);
     __builtin_amdgcn_sched_barrier(0);
-    products(kFirst, behind(kFirst));
+    products(kFirst, first, behind(kFirst));
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(first)::value) add_block(1);  // (of the block before)
     if (kSteady || t + 1 < steps) {
       if constexpr (kSteady) wait_vm<(NS - 3) * LPW + FIRST_HALF>();
       else wait_steps<LPW, NS>(min(NS - 2, steps - 2 - t));
@@ -425,7 +464,8 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
       read(next, kFirst);
     }
     __builtin_amdgcn_sched_barrier(0);
-    products(kSecond, behind(kSecond));
+    products(kSecond, first, behind(kSecond));
+    if constexpr (decltype(last)::value) add_block(0);
   };
 
   for_each<NS - 1>([&](auto t) POETX_INLINE {
@@ -437,12 +477,17 @@ __device__ __forceinline__ void tile_body(const TileProduct& p, int wg, int part
   read(0, kFirst);
   int t = 0;
   for (; t + 2 * NS - 1 < steps; t += NS)
-    for_each<NS>([&](auto q) POETX_INLINE { step(decltype(q)::value, t + decltype(q)::value, std::true_type{}); });
+    for_each<NS>([&](auto q) POETX_INLINE {
+      constexpr int Q = decltype(q)::value;
+      step(Q, t + Q, std::true_type{}, std::bool_constant<Q == 0>{},
+           std::bool_constant<Q == NS - 1>{});
+    });
   for (int slot = 0; t < steps; ++t, slot = slot + 1 == NS ? 0 : slot + 1)
-    step(slot, t, std::false_type{});
+    step(slot, t, std::false_type{}, std::true_type{}, std::true_type{});
   __builtin_amdgcn_sched_barrier(0);
   settle_after();
   __builtin_amdgcn_sched_barrier(0);
+  add_block(1);
 
   end.template run<T, FM, FN>(p, acc, m0 + wm * TM, n0 + wn * TN, part_k, nt * WN + wn, lane);
 }

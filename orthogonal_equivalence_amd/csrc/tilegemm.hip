@@ -18,7 +18,8 @@ namespace {
 constexpr int NT = 256;
 
 // the plain end: the epilogue, or a split's partial tile
-struct StoreEnd {
+template <bool BLOCKED> struct StoreEnd {
+  static constexpr bool kBlocked = BLOCKED;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int part_k, int, int lane) const {
@@ -39,11 +40,12 @@ struct StoreEnd {
   }
 };
 
-template <typename T, typename TB, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS>
+template <typename T, typename TB, int BM, int BN, int WM, int WN, bool A_KMAJ, bool B_KMAJ, int NS,
+          bool BLOCKED = false>
 __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct p) {
   __shared__ __attribute__((aligned(1024))) char ring[ring_bytes<T, TB, BM, BN, WM * WN, NS>()];
   tile_body<T, TB, BM, BN, WM, WN, A_KMAJ, B_KMAJ, NS>(p, blockIdx.x, blockIdx.y, ring,
-                                                      StoreEnd{});
+                                                      StoreEnd<BLOCKED>{});
 }
 
 // The backward's two products, which are independent, in one launch: g_x = g_u
@@ -51,7 +53,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) tile_kernel(const TileProduct
 // product with the longer reduction comes first, so that its tiles do not
 // start last. padded: its workgroups, rounded up to the 8 XCDs (the ones past
 // its tiles return at once).
-template <typename T, int BM, int BN, int WM, int WN, int NS>
+template <typename T, int BM, int BN, int WM, int WN, int NS, bool BLOCKED>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 tile_pair_kernel(const TileProduct gx, const TileProduct gw, int gx_tiles, int gw_tiles, int gx_wgs,
                  int gw_wgs, int padded, int gx_first) {
@@ -61,11 +63,11 @@ tile_pair_kernel(const TileProduct gx, const TileProduct gw, int gx_tiles, int g
   if (first == (gx_first != 0)) {
     if (wg >= gx_wgs) return;
     tile_body<T, T, BM, BN, WM, WN, true, false, NS>(gx, wg % gx_tiles, wg / gx_tiles, ring,
-                                                     StoreEnd{});
+                                                     StoreEnd<BLOCKED>{});
   } else {
     if (wg >= gw_wgs) return;
     tile_body<T, T, BM, BN, WM, WN, false, false, NS>(gw, wg % gw_tiles, wg / gw_tiles, ring,
-                                                      StoreEnd{});
+                                                      StoreEnd<BLOCKED>{});
   }
 }
 
@@ -124,6 +126,15 @@ hipError_t launch_cfg(bool ak, bool bk, const TileProduct& p, int nsplit, hipStr
     }
     return hipErrorInvalidValue;
   }
+  if constexpr (sizeof(T) == 4) {
+    if (p.blocked) {
+      if (bk) return hipErrorInvalidValue;  // (no caller)
+      const auto kernel = ak ? tile_kernel<T, T, BM, BN, WM, WN, true, false, NS, true>
+                             : tile_kernel<T, T, BM, BN, WM, WN, false, false, NS, true>;
+      hipLaunchKernelGGL(kernel, grid, block, 0, s, p);
+      return hipGetLastError();
+    }
+  }
   if (ak && bk)
     hipLaunchKernelGGL((tile_kernel<T, T, BM, BN, WM, WN, true, true, NS>), grid, block, 0, s, p);
   else if (ak)
@@ -146,9 +157,11 @@ hipError_t launch_pair_cfg(const TileProduct& gx, int gx_split, const TileProduc
   const int64_t grid = padded + (gx_first ? tw * gw_split : tx * gx_split);
   if (gx_split < 1 || gw_split < 1 || grid * 64 * WM * WN > kMaxWorkItems)
     return hipErrorInvalidValue;
-  hipLaunchKernelGGL((tile_pair_kernel<T, BM, BN, WM, WN, NS>), dim3((unsigned)grid),
-                     dim3(64 * WM * WN), 0, s, gx, gw, (int)tx, (int)tw, (int)(tx * gx_split),
-                     (int)(tw * gw_split), (int)padded, (int)gx_first);
+  const auto kernel = sizeof(T) == 4 && gx.blocked
+                          ? tile_pair_kernel<T, BM, BN, WM, WN, NS, sizeof(T) == 4>
+                          : tile_pair_kernel<T, BM, BN, WM, WN, NS, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, gx, gw, (int)tx, (int)tw,
+                     (int)(tx * gx_split), (int)(tw * gw_split), (int)padded, (int)gx_first);
   return hipGetLastError();
 }
 

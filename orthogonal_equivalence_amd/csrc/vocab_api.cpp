@@ -257,6 +257,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     const poetx::VocabProducts tiles = poetx::plan_vocab_products(sizes_of(d), cols);
     float* part = reinterpret_cast<float*>(w + plan.part);
     TileProduct qx, qw;
+    qx.blocked = qw.blocked = true;
     // g_x += g_z W: B(n, k) = W[k][n]
     qx.A = gz; qx.lda = plan.ldg;
     qx.B = Wc; qx.ldb = d->d;

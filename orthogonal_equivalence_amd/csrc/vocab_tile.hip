@@ -40,7 +40,7 @@ __device__ __forceinline__ floatx4 pick(const floatx4 (&acc)[FM][FN], int f) {
 }
 
 struct LseEnd {
-  static constexpr bool kBeside = true;
+  static constexpr bool kBeside = true, kBlocked = true;
   float2* part;
   int64_t part_ld;
   float scale;
@@ -87,7 +87,7 @@ struct LseEnd {
 };
 
 struct GradEnd {
-  static constexpr bool kBeside = false;
+  static constexpr bool kBeside = false, kBlocked = true;
   const VocabRow* rows;
   void* gz;
   int64_t ldg;

@@ -186,3 +186,47 @@ def test_exponentials_of_float32():
     keep = torch.ones(vocab, dtype=torch.bool, device="cuda")
     keep[ids[0]] = False
     assert bool((((g_W[:, 0].double() - want).abs() / want)[keep] <= 6 * U32).all())
+
+
+SMALL = 0.75 * 2.0 ** -12  # lost wherever it is added to 4096 (a half step of which is 2^-12)
+
+
+def test_long_sums_of_float32():
+    """One large term and thousands that are below half a step of it: added to it one by
+    one they would all be lost. They are summed in blocks of at most 64 before: half a
+    step of 4096 for each of the first block's and for each block."""
+    def bound(terms):
+        return (64 + terms / 64 + 8) * 2.0 ** -12  # (the last blocks are smaller)
+
+    # a logit over d columns, against one that is 4096 exactly
+    for tokens in (3, 300):
+        d, vocab = 4096, 2
+        x = torch.ones(tokens, d, device="cuda")
+        W = torch.zeros(vocab, d, device="cuda")
+        W[:, 0] = 4096
+        W[0, 1:] = SMALL
+        more = (d - 1) * SMALL
+        targets = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+        loss, lse = L.cross_entropy_forward(x, W, targets)
+        want = math.log1p(math.exp(-more))
+        # (the loss's slope in the logit's difference is below 1)
+        assert bool(((loss.double() - want).abs() <= bound(d) + 1e-6).all())
+        assert abs(want - math.log(2.0)) > 0.2 > bound(d)
+    # g_x over the vocabulary and g_W over the tokens: logits of 0, lse of 0, so that g_z is
+    # g_loss but at the targets, whose column of W and row of x are 0
+    tokens, d, vocab = 2049, 2048, 8193
+    x = torch.zeros(tokens, d, device="cuda")
+    W = torch.zeros(vocab, d, device="cuda")
+    x[:, :d // 2] = SMALL
+    x[0, :d // 2] = 4096
+    W[:, d // 2:] = SMALL
+    W[0, d // 2:] = 4096
+    W[vocab - 1] = 0
+    targets = torch.full((tokens,), vocab - 1, device="cuda")
+    one, zero = torch.ones(tokens, device="cuda"), torch.zeros(tokens, device="cuda")
+    g_x, g_W = L.cross_entropy_backward(one, x, W, targets, zero, need_g_W=True)
+    want_x, want_W = 4096 + (vocab - 2) * SMALL, 4096 + (tokens - 1) * SMALL
+    assert (vocab - 2) * SMALL > 1.4 and bound(vocab) < 0.2
+    assert bool(((g_x[:, d // 2:].double() - want_x).abs() <= bound(vocab)).all())
+    assert bool(((g_W[:vocab - 1, :d // 2].double() - want_W).abs() <= bound(tokens)).all())
+    assert bool((g_x[:, :d // 2] == 0).all()) and bool((g_W[:, d // 2:] == 0).all())
