@@ -474,9 +474,10 @@ int poetx_dense_bwd(const poetx_dense_desc* desc, const void* g_y, const void* x
  * A row whose gradients to loss and lse are 0 adds nothing to g_W either, and has
  * a g_x of 0, whatever its x holds.
  * A target or id past the vocabulary is read nowhere; its row's loss and
- * gradients are NaN. Logits, sums and losses are float32; g_z is rounded to
- * the act type once, as the operand of the gradients' products (the matrix
- * cores take bf16). Sums are joined in a fixed order: bitwise reproducible. */
+ * gradients are NaN. Logits, sums and losses are float32. The gradients'
+ * products take g_z in the act type: bf16 from 256 tokens on rounded once (it
+ * adds a rounding of the size of the result's own, averaged over a row's entries
+ * and the tokens), of fewer tokens in two parts, to 16 bits. Sums are joined in a fixed order: bitwise reproducible. */
 typedef struct poetx_vocab_desc {
   int64_t tokens;      /* rows of x; 1 .. 2^24 */
   int64_t d;           /* columns of x and W, a multiple of 16 bytes; at most 2^22 */

@@ -80,6 +80,11 @@ __host__ __device__ inline int64_t tiled_offset(int64_t r, int64_t k, int64_t K)
   return (((r >> 8) * (K >> 5) + (k >> 5)) << 13) + ((r & 255) << 5) + (k & 31);
 }
 static_assert(kTileRows == 256 && kTileCols == 32, "tiled_offset's shifts");
+// Where rows have a second part each, in the tiled layout: 16 rows, then their second
+// parts, kPairLow elements further on.
+__host__ __device__ inline int64_t pair_row(int64_t r) { return r + (r & ~(int64_t)15); }
+constexpr int kPairLow = 16 * kTileCols;
+inline int64_t pair_rows(int64_t rows) { return (rows + 15) / 16 * 32; }
 
 // ---- dense bf16 GEMM with direct-to-LDS loads (the W0 products) ----
 // C[M][N] = A[M][K] B(n, k), B(n, k) = B[n*ldb + k] (b_kmajor) or
@@ -258,6 +263,9 @@ struct TileProduct {
   bool b_int8 = false;  // B: INT8 codes of a bf16 product, both K-major, K % 16 == 0
   float* part = nullptr;
   Epilogue ep;
+  // 2: A's rows are two parts of M / 2 rows each, whose products are summed (an output of M / 2
+  // rows, through `part` always)
+  int halves = 1;
   bool blocked = false;  // float32: sums of 16 k apart (tile_core.h), an N-major B
 };
 // Work items along one dimension of a launch that HIP takes.
@@ -399,10 +407,12 @@ hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProdu
 // Backward: g_z of the piece in x's type at gz[row][ldg], or in the tiled layout
 // [..][ldg] of which gz is the piece's first block of columns; columns N up to
 // ldg, and rows M up to the next multiple of 32, are zeroed where tiles reach
-// (as far as the next multiple of 32 columns at least).
+// (as far as the next multiple of 32 columns at least). low: what bf16 takes off g_z
+// goes that many elements further on (0: nowhere; tiled gz: kPairLow, rows by pair_row(),
+// zeroed up to the next multiple of 16 rows).
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
                                   const VocabRow* rows, void* gz, int64_t ldg, bool tiled,
-                                  hipStream_t s);
+                                  int64_t low, hipStream_t s);
 
 // Large bf16 pieces on the dense kernel's 256 x 256 tile loop (vocab_dense.hip).
 // A piece that ends inside a tile comes with W_last, a copy [256][K] of W's rows
@@ -417,9 +427,9 @@ hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, flo
                                   const VocabCells& cells, hipStream_t s);
 // x: the tiled copy of it, M % 256 == 0 rows, as many of `rows`; gz in
 // the tiled layout [M][ldg], ldg % 256 == 0; columns past N of the last tile are
-// zeroed.
+// zeroed. pairs: gz [2 M][ldg] by pair_row().
 hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, const VocabRow* rows,
-                                   void* gz, int64_t ldg, hipStream_t s);
+                                   void* gz, int64_t ldg, bool pairs, hipStream_t s);
 // g_z W of a piece of `cols` columns of a tiled gz (padded to 256 rows): split
 // over `splits` ranges of kchunk of them into slabs [splits][rows][d] float32, added
 // to what they hold with `add`; or with y (one range) g_x itself, bf16.
@@ -431,15 +441,17 @@ hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, con
 // (what gz's columns past `cols` hold does not matter).
 hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
                                  int cols, void* g_W, hipStream_t s);
-// g_W of up to few_tokens(t) rows (vocab_few.hip): row-major gz [tokens][ldg] and xt
-// [d][few_padded], the copy of x that VocabCopies::xt makes.
+// g_W of up to few_tokens(t) rows (vocab_few.hip): row-major gz [tokens][ldg], bf16 its
+// second part [tokens][ldg] behind it, and xt [d][few_padded], the copy of x that
+// VocabCopies::xt makes.
 constexpr int few_tokens(DType t) { return t == DType::BF16 ? 128 : 64; }
 int few_padded(DType t, int tokens);
 hipError_t launch_few_gw(DType t, const void* gz, int64_t ldg, const void* xt, int tokens, int cols,
                          int d, void* g_W, hipStream_t s);
-// out [rows][N] = the sum of nsplit float32 slabs of it, N % 4 == 0.
+// out [rows][N] = the sum of nsplit float32 slabs of it, N % 4 == 0; pairs: of slabs of
+// pair_rows(rows) rows, by pair_row().
 hipError_t launch_sum_slabs(DType t, const float* slabs, int nsplit, int64_t rows, int N, void* out,
-                            hipStream_t s);
+                            bool pairs, hipStream_t s);
 
 // z[row][k] = x[row] . W[ids[row][k]]; 0 where the id is negative, NaN where
 // it is past the vocabulary.
@@ -457,6 +469,8 @@ struct VocabCopies {
   const void* x = nullptr;
   void* xs = nullptr;
   bool tiled = false;
+  bool twice = false;  // (row-major xs) the copy once more behind it
+  void* pairs = nullptr;  // (tiled xs) [2 padded][K], each row as both of pair_row()'s
   const void* W = nullptr;
   void* W_last = nullptr;
   void* xt = nullptr;  // up to few_tokens(t) rows: [K][xt_rows], zeros as in xs
@@ -470,8 +484,8 @@ hipError_t launch_vocab_rows(DType t, const VocabList& l, int64_t rows, int64_t 
 // A teacher's ids in the piece [col0, col0 + N): g_z there, from the student's
 // logits z at them.
 hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
-                                    const float* z, void* gz, int64_t ldg, bool tiled, int col0,
-                                    int N, hipStream_t s);
+                                    const float* z, void* gz, int64_t ldg, bool tiled, int64_t low,
+                                    int col0, int N, hipStream_t s);
 
 // ---- gradient norm and clipping over many tensors ----
 // One contiguous run of gradient values; out may equal grad.

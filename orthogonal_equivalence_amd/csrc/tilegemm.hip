@@ -72,18 +72,29 @@ tile_pair_kernel(const TileProduct gx, const TileProduct gw, int gx_tiles, int g
 }
 
 // sum of the partial tiles in split order, then the epilogue; four columns a
-// thread
-template <typename T>
+// thread. PAIRS: the tiles' rows are pair_row()'s.
+template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(NT)
-finish_kernel(const float* __restrict__ part, int nsplit, int64_t rows, int N, Epilogue ep) {
+finish_kernel(const float* __restrict__ part, int nsplit, int64_t rows, int64_t stride, int N,
+              Epilogue ep) {
   const int quads = N / 4;
-  const int64_t total = rows * quads, stride = rows * N;
+  const int64_t total = rows * quads;
   for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < total; i += (int64_t)gridDim.x * NT) {
     const int64_t m = i / quads;
     const int n = (int)(i - m * quads) * 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float* p = part + m * N + n;
+    const float* p = part + (PAIRS ? pair_row(m) : m) * N + n;
     int s = 0;
+    if constexpr (PAIRS) {
+      for (; s < nsplit; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float w[4];
+          Quad<float>::load(p + s * stride + (int64_t)16 * h * N, w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += w[e];
+        }
+    }
     for (; s + 4 <= nsplit; s += 4) {  // four loads in flight
       float w[4][4];
 #pragma unroll
@@ -166,39 +177,44 @@ hipError_t launch_pair_cfg(const TileProduct& gx, int gx_split, const TileProduc
 }
 
 // joins a split product's partial tiles
-hipError_t join(DType t, int nsplit, const TileProduct& p, hipStream_t s) {
+hipError_t join(DType t, int nsplit, const TileProduct& p, bool pairs, hipStream_t s) {
   const int64_t groups = (int64_t)p.M * (p.N / 4);
   const int grid = (int)std::min<int64_t>((groups + NT - 1) / NT, 4096);
-  if (t == DType::BF16)
-    hipLaunchKernelGGL(finish_kernel<bf16_t>, dim3(grid), dim3(NT), 0, s, p.part, nsplit,
-                       (int64_t)p.M, p.N, p.ep);
-  else
-    hipLaunchKernelGGL(finish_kernel<float>, dim3(grid), dim3(NT), 0, s, p.part, nsplit,
-                       (int64_t)p.M, p.N, p.ep);
+  const int64_t stride = (pairs ? pair_rows(p.M) : (int64_t)p.M) * p.N;
+  const auto kernel = t == DType::F32 ? finish_kernel<float, false>
+                      : pairs         ? finish_kernel<bf16_t, true>
+                                      : finish_kernel<bf16_t, false>;
+  if (pairs && t == DType::F32) return hipErrorInvalidValue;  // (no caller)
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, s, p.part, nsplit, (int64_t)p.M, stride, p.N,
+                     p.ep);
   return hipGetLastError();
 }
 
-hipError_t finish(DType t, const TilePlan& plan, const TileProduct& p, hipStream_t s) {
-  return plan.nsplit == 1 ? hipSuccess : join(t, plan.nsplit, p, s);
+hipError_t finish(DType t, const TilePlan& plan, TileProduct p, hipStream_t s) {
+  // (a partial tile of two halves is two partial tiles of the output)
+  p.M /= p.halves;
+  const int parts = plan.nsplit * p.halves;
+  return parts == 1 ? hipSuccess : join(t, parts, p, false, s);
 }
 
 // p as `plan` has it; false: a split without room for its partial tiles
 bool apply_plan(const TilePlan& plan, TileProduct& p) {
   p.kchunk = plan.kchunk;
-  if (plan.nsplit == 1) p.part = nullptr;
-  return plan.nsplit == 1 || p.part;
+  const bool whole = plan.nsplit == 1 && p.halves == 1;
+  if (whole) p.part = nullptr;
+  return (whole || p.part) && p.M % p.halves == 0;
 }
 
 }  // namespace
 
 hipError_t launch_sum_slabs(DType t, const float* slabs, int nsplit, int64_t rows, int N, void* out,
-                            hipStream_t s) {
+                            bool pairs, hipStream_t s) {
   TileProduct p;
   p.M = (int)rows; p.N = N;
   p.part = const_cast<float*>(slabs);
   p.ep.y = out;
   p.ep.ld = N;
-  return join(t, nsplit, p, s);
+  return join(t, nsplit, p, pairs, s);
 }
 
 hipError_t launch_tile_pair(DType t, const TilePairPlan& plan, TileProduct gx, TileProduct gw,

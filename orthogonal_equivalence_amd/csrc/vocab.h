@@ -145,6 +145,13 @@ __device__ __forceinline__ uint4 ror8(uint4 v) {
 __device__ __forceinline__ uint4 choose(bool c, uint4 a, uint4 b) {
   return make_uint4(c ? a.x : b.x, c ? a.y : b.y, c ? a.z : b.z, c ? a.w : b.w);
 }
+// what is left of v where bf16 keeps `high` of it (less than 2^-16 of it is nothing
+// beside the result's rounding, and left out: a g_z that is a bf16 value but for the
+// rounding of lse stays one)
+__device__ __forceinline__ float low_part(float v, float high) {
+  const float low = v - high;
+  return fabsf(low) > 0x1p-16f * fabsf(high) && fabsf(high) < INFINITY ? low : 0.0f;
+}
 // The entries of one wave's cell: their range and the first 64 of them, read
 // well before their logits are stored (each read waits for the L2, one for the
 // other).

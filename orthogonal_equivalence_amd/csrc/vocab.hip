@@ -322,9 +322,16 @@ rows_kernel(const VocabList l, int64_t rows, int64_t padded, const float* __rest
   T* xs = static_cast<T*>(c.xs);
   if (!xs) return;
   const T* x = static_cast<const T*>(c.x);
-  for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E)
-    *reinterpret_cast<uint4*>(xs + (c.tiled ? tiled_offset(row, k, K) : row * K + k)) =
-        load16_if(has_gradient(a, b), x + row * K + k);
+  for (int k = lane * Vec<T>::E; k < K; k += 64 * Vec<T>::E) {
+    const uint4 v = load16_if(has_gradient(a, b), x + row * K + k);
+    *reinterpret_cast<uint4*>(xs + (c.tiled ? tiled_offset(row, k, K) : row * K + k)) = v;
+    if (c.twice) *reinterpret_cast<uint4*>(xs + (padded + row) * K + k) = v;
+    if (c.pairs) {
+      T* two = static_cast<T*>(c.pairs) + tiled_offset(pair_row(row), k, K);
+      *reinterpret_cast<uint4*>(two) = v;
+      *reinterpret_cast<uint4*>(two + kPairLow) = v;
+    }
+  }
 }
 
 // x's copy with the rows innermost, for few rows (after their parts): a workgroup
@@ -360,7 +367,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT)
 listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__ r,
                    const float* __restrict__ z, T* __restrict__ gz, int64_t ldg, int tiled,
-                   int col0, int N) {
+                   int64_t low, int col0, int N) {
   __shared__ __attribute__((aligned(16))) int ids[NWAVES][kMaxTop];
   __shared__ __attribute__((aligned(16))) float p[NWAVES][kMaxTop];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -392,8 +399,13 @@ listed_grad_kernel(const VocabList l, int64_t rows, const VocabRow* __restrict__
       sum += i.w == id ? v.w : 0.0f;
     }
     const float e = softmax_at<T>(z[row * l.top + k], inv, own.lse);
-    const int64_t at = tiled ? tiled_offset(row, id - col0, ldg) : row * ldg + (id - col0);
-    store_as(gz + at, own.a * (e - sum));
+    const int64_t at = tiled ? tiled_offset(low ? pair_row(row) : row, id - col0, ldg)
+                             : row * ldg + (id - col0);
+    const float v = own.a * (e - sum);
+    store_as(gz + at, v);
+    if constexpr (sizeof(T) == 2) {
+      if (low) store_as(gz + at + low, low_part(v, bf16_to_f32(f32_to_bf16(v))));
+    }
   }
 }
 
@@ -490,16 +502,16 @@ hipError_t launch_vocab_last_rows(DType t, int64_t vocab, int K, const VocabCopi
 }
 
 hipError_t launch_vocab_listed_grad(DType t, const VocabList& l, int64_t rows, const VocabRow* r,
-                                    const float* z, void* gz, int64_t ldg, bool tiled, int col0,
-                                    int N, hipStream_t s) {
+                                    const float* z, void* gz, int64_t ldg, bool tiled, int64_t low,
+                                    int col0, int N, hipStream_t s) {
   const int64_t blocks = (rows + NWAVES - 1) / NWAVES;
-  if (!fits(blocks) || l.top > kMaxTop) return hipErrorInvalidValue;
+  if (!fits(blocks) || l.top > kMaxTop || (tiled && low && low != kPairLow)) return hipErrorInvalidValue;
   if (t == DType::BF16)
     hipLaunchKernelGGL(listed_grad_kernel<bf16_t>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
-                       r, z, static_cast<bf16_t*>(gz), ldg, (int)tiled, col0, N);
+                       r, z, static_cast<bf16_t*>(gz), ldg, (int)tiled, low, col0, N);
   else
     hipLaunchKernelGGL(listed_grad_kernel<float>, dim3((unsigned)blocks), dim3(NT), 0, s, l, rows,
-                       r, z, static_cast<float*>(gz), ldg, (int)tiled, col0, N);
+                       r, z, static_cast<float*>(gz), ldg, (int)tiled, low, col0, N);
   return hipGetLastError();
 }
 

@@ -203,11 +203,16 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
   void* xs = g_W || plan.dense ? w + plan.xs : nullptr;
   char* gz = w + plan.gz;
   float* acc = reinterpret_cast<float*>(w + plan.acc);
+  const int parts = plan.two ? 2 : 1;
+  const int64_t low = !plan.two ? 0 : plan.dense ? poetx::kPairLow : d->tokens * plan.ldg;
+  const int64_t dense_rows = sizes_of(d).dense_rows();
   const bool ragged = plan.dense && d->vocab % poetx::kTileRows != 0;
   poetx::VocabCopies copies;
   copies.x = x;
   copies.xs = xs;
   copies.tiled = plan.dense;
+  copies.twice = plan.two && !plan.dense;
+  if (plan.two && plan.dense && g_W) copies.pairs = w + plan.pairs;
   copies.W = W;
   copies.W_last = ragged ? w + plan.last : nullptr;
   if (g_W && !plan.dense && plan.few) {
@@ -230,7 +235,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     p.M = (int)plan.padded; p.N = (int)split.dense; p.K = (int)d->d;
     p.col0 = (int)c;
     p.scale = 1.0f / d->temperature;
-    if (p.N) POETX_TRY(poetx::launch_vocab_grad_dense(p, last, rows, gz, plan.ldg, s));
+    if (p.N) POETX_TRY(poetx::launch_vocab_grad_dense(p, last, rows, gz, plan.ldg, plan.two, s));
     if (split.dense < cols) {
       p.x = x;
       p.W = Wc + split.dense * d->d * es;
@@ -238,20 +243,21 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
       p.col0 = (int)(c + split.dense);
       POETX_TRY(poetx::launch_vocab_grad_tile(t, split.tile, p, rows,
                                               gz + split.dense * poetx::kTileRows * es, plan.ldg,
-                                              plan.dense, s));
+                                              plan.dense, low, s));
     }
     if (teacher)
       POETX_TRY(poetx::launch_vocab_listed_grad(t, list, d->tokens, rows, z, gz, plan.ldg,
-                                                plan.dense, (int)c, (int)cols, s));
+                                                plan.dense, low, (int)c, (int)cols, s));
     if (plan.dense) {
       if (g_x)
         POETX_TRY(poetx::launch_vocab_gx_dense(
-            gz, plan.ldg, Wc, last, d->tokens, (int)d->d, (int)cols,
+            gz, plan.ldg, Wc, last, dense_rows, (int)d->d, (int)cols,
             (int)ceil_div(cols, plan.kchunk), plan.kchunk, acc, c > 0,
             plan.summed() ? nullptr : g_x, s));
       if (g_W)
-        POETX_TRY(poetx::launch_vocab_gw_dense(gz, plan.ldg, xs, ceil_div(d->tokens, 32) * 32,
-                                               (int)d->d, (int)cols, gWc, s));
+        POETX_TRY(poetx::launch_vocab_gw_dense(gz, plan.ldg, plan.two ? copies.pairs : xs,
+                                               ceil_div(dense_rows, 32) * 32, (int)d->d, (int)cols,
+                                               gWc, s));
       continue;
     }
     const poetx::VocabProducts tiles = poetx::plan_vocab_products(sizes_of(d), cols);
@@ -261,8 +267,9 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     // g_x += g_z W: B(n, k) = W[k][n]
     qx.A = gz; qx.lda = plan.ldg;
     qx.B = Wc; qx.ldb = d->d;
-    qx.M = (int)d->tokens; qx.N = (int)d->d; qx.K = (int)cols;
+    qx.M = (int)d->tokens * parts; qx.N = (int)d->d; qx.K = (int)cols;
     qx.part = part;
+    qx.halves = parts;
     qx.ep.y = g_x;
     qx.ep.add = c > 0 ? acc : nullptr;
     qx.ep.sum = c + cols < d->vocab ? acc : nullptr;
@@ -270,7 +277,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
     // g_W = g_z^T x: A(m, k) = g_z[k][m], B(n, k) = xs[k][n]
     qw.A = gz; qw.lda = plan.ldg;
     qw.B = xs; qw.ldb = d->d;
-    qw.M = (int)cols; qw.N = (int)d->d; qw.K = (int)d->tokens;
+    qw.M = (int)cols; qw.N = (int)d->d; qw.K = (int)d->tokens * parts;
     qw.part = g_x && tiles.paired ? part + tiles.pair.gx.part_floats : part;
     qw.ep.y = gWc;
     qw.ep.ld = d->d;
@@ -287,7 +294,7 @@ int backward(const poetx_vocab_desc* d, const float* g_loss, const float* g_lse,
       POETX_TRY(poetx::launch_tile_product(t, tiles.gw, qw, false, false, s));
   }
   if (plan.dense && g_x && plan.summed())
-    POETX_TRY(poetx::launch_sum_slabs(t, acc, plan.splits, d->tokens, (int)d->d, g_x, s));
+    POETX_TRY(poetx::launch_sum_slabs(t, acc, plan.splits, d->tokens, (int)d->d, g_x, plan.two, s));
   return POETX_OK;
 }
 

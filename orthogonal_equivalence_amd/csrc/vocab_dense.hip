@@ -203,6 +203,10 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
 // The end of the logits' backward. A row's target is one column of the
 // vocabulary: few waves hold any, and the others only scale exponentials.
 // 8192 x 32768 x 4096 1.59 ms (1.39 PFLOP/s), matrix units busy 71% at 1.87 GHz.
+// g_z is rounded to bf16, the products' operand (gradients 0.0024 off, 2-norm, where the
+// result's rounding alone gives 0.0017; a second part from 256 tokens on would add
+// two products to three). PAIRS: what the rounding takes off g_z too, rows by pair_row().
+template <bool PAIRS>
 __global__ void __launch_bounds__(NT)
 vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
                   const bf16_t* __restrict__ W_last, int M, int N, int K, float scale, int col0,
@@ -230,8 +234,9 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
       [&](int m0, int n0, int, int) __attribute__((always_inline)) {
         const int ln = opaque_lane(d);
         // (the wave's first block of 32 columns, this lane's place in it)
-        bf16_t* out = gz + tiled_offset(m0, n0 + d.wn * 128, ldg) +
-                      (d.wm * 128 + (ln & 15)) * kTileCols + pair_column(ln);
+        constexpr int kRows = PAIRS ? 2 : 1;  // of gz a row
+        bf16_t* out = gz + tiled_offset(kRows * (m0 + d.wm * 128), n0 + d.wn * 128, ldg) +
+                      (ln & 15) * kTileCols + pair_column(ln);
         const int col = col0 + n0 + d.wn * 128;
         const bool padded = n0 + BN > N;
         int left = N - n0 - d.wn * 128 - 4 * (ln >> 4);
@@ -244,7 +249,7 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
           asm volatile("" : "+v"(left));
 #pragma unroll
           for (int j = 0; j < FN; j += 2) {
-            uint2 w[2];
+            uint2 w[2], low[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v[4];
@@ -259,9 +264,16 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
                 }
               }
               w[h] = Quad<bf16_t>::pack(v);
+              if constexpr (PAIRS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  v[e] = low_part(v[e], bf16_to_f32(f32_to_bf16(v[e])));
+                low[h] = Quad<bf16_t>::pack(v);
+              }
             }
-            *reinterpret_cast<uint4*>(out + i * 16 * kTileCols + j / 2 * TILE) =
-                swap_pair(w[0], w[1]);
+            bf16_t* at = out + i * kRows * 16 * kTileCols + j / 2 * TILE;
+            *reinterpret_cast<uint4*>(at) = swap_pair(w[0], w[1]);
+            if constexpr (PAIRS) *reinterpret_cast<uint4*>(at + kPairLow) = swap_pair(low[0], low[1]);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -413,14 +425,15 @@ hipError_t launch_vocab_lse_dense(const VocabProduct& p, const void* W_last, flo
 }
 
 hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, const VocabRow* rows,
-                                   void* gz, int64_t ldg, hipStream_t s) {
+                                   void* gz, int64_t ldg, bool pairs, hipStream_t s) {
   if (!vocab_dense_supported(p.M, p.N, p.K) || (p.N % BN != 0 && !W_last) || p.M % BM != 0 ||
       ldg % BN != 0 || ldg < p.N)
     return hipErrorInvalidValue;
   int grid = 0;
   const hipError_t e = dense_grid(p.M, p.N, &grid);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(vocab_grad_kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last),
+  const auto kernel = pairs ? vocab_grad_kernel<true> : vocab_grad_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, s, b16(p.x), b16(p.W), b16(W_last),
                      p.M, p.N, p.K, p.scale, p.col0, rows, static_cast<bf16_t*>(gz), ldg);
   return hipGetLastError();
 }

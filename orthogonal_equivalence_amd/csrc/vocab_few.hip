@@ -3,6 +3,9 @@
 // bf16 1.07 GB, 180 us at what stores alone reach), and tiles that load, wait, multiply
 // once and store spend most of their time on the first two.
 //
+// bf16: g_z in two parts, the second what rounding took off the first, both times the
+// same x.
+//
 // One wave takes 32 or 64 rows of g_W (ids): their g_z are the products' operand and
 // stay in registers; it walks along d with one 16-byte load a lane for 16 columns
 // and K tokens, 128 bytes of columns ahead, out of a copy of x with the tokens
@@ -10,13 +13,12 @@
 // lines at a time. No LDS, no barrier. Workgroups in the order of g_W's rows, not of its
 // columns: what is stored at one time then lies together (stores alone of 1.07 GB
 // 181 us, the other way 235).
-// us:                      1 token   64   96  128   (on tiles at 65, 96, 128)
-//   131072 x 4096, bf16      211  245  300  385     (575 - 600)
-//   32000 x 4096              61   75                (175)
-// From 33 tokens on 64 ids a wave: 131072 x 4096, 64 tokens 336 -> 245 (32 ids); up to
-// 32 tokens 32 ids (56370 x 2256, 16 tokens: 232 us a backward, 64 ids 239). Stores of
-// 16 rows' half lines: a third more. Walks of 256 columns alike, of 1024 slower. Past
-// 128 tokens the registers are spent.
+// us:                      1 token   64   96  128
+//   131072 x 4096, bf16      211  275  323  454     (with one part of g_z 211, 245, 300, 385)
+//   32000 x 4096              55   64
+// From 33 tokens on 64 ids a wave (32 ids: a third more at 64 tokens, a tenth at 128); up
+// to 32 tokens 32 ids (56370 x 2256, 16 tokens: 232 us a backward, 64 ids 239). Stores of
+// 16 rows' half lines: a third more. Past 128 tokens the registers are spent.
 #include "epilogue.h"
 #include "vocab.h"
 
@@ -26,7 +28,12 @@ namespace {
 constexpr int NT = 256, NWAVES = NT / 64;
 // fragments of 16 ids a wave: the more, the less often x's copy is read
 template <int STEPS> constexpr int kFrags = STEPS == 1 ? 2 : 4;
-constexpr int kChunk = 512;      // columns a workgroup walks along
+// Columns a workgroup walks along: as many as pay for its g_z, while there are
+// workgroups enough (131072 x 4096, both gradients, us: 64 tokens 743 with 512, 706 with
+// 1024, 782 with 2048; 96 tokens 890, 854, 872; 128 tokens 1244, 1075, 1017).
+template <typename T, int STEPS>
+constexpr int kChunk = sizeof(T) == 4 || STEPS == 1 ? 512 : STEPS == 4 ? 2048 : 1024;
+constexpr int kGroups = 128;
 // a g_W larger than this goes past the caches, where its rows are whole lines, and W
 // stays in them for the next pass (backward of 64 tokens: 32000 x 4096 227 -> 172 us,
 // 131072 x 4096 833 -> 768; 32000 x 1024 float32, 131 MB, alike; rows of 4512 bytes 60 -> 160)
@@ -36,6 +43,7 @@ template <typename T> struct Few;
 template <> struct Few<bf16_t> {
   typedef bf16x8_t Frag;
   static constexpr int K = 32, E = 8;  // tokens a product and a fragment's lane takes
+  static constexpr int kParts = 2;     // of g_z
   static __device__ __forceinline__ floatx4 mma(const Frag& a, const Frag& b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -43,6 +51,7 @@ template <> struct Few<bf16_t> {
 template <> struct Few<float> {
   typedef floatx4 Frag;
   static constexpr int K = 16, E = 4;  // (four products of 4 tokens)
+  static constexpr int kParts = 1;
   static __device__ __forceinline__ floatx4 mma(const Frag& a, const Frag& b, floatx4 c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
@@ -61,14 +70,16 @@ template <bool PAST> __device__ __forceinline__ void store16(void* p, uint4 v) {
 // row l % 16, columns pair_column() or 4 (l / 16) on
 template <typename T, int STEPS>
 __device__ __forceinline__ uint4 half(const typename Few<T>::Frag (*b)[STEPS],
-                                      const typename Few<T>::Frag (&a)[STEPS]) {
+                                      const typename Few<T>::Frag (&a)[STEPS][Few<T>::kParts]) {
   constexpr int N = sizeof(T) == 2 ? 2 : 1;
   floatx4 c[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     c[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) c[j] = Few<T>::mma(b[j][s], a[s], c[j]);
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int h = 0; h < Few<T>::kParts; ++h) c[j] = Few<T>::mma(b[j][s], a[s][h], c[j]);
   }
   if constexpr (sizeof(T) == 2) {
     const float p[4] = {c[0][0], c[0][1], c[0][2], c[0][3]};
@@ -83,7 +94,7 @@ __device__ __forceinline__ uint4 half(const typename Few<T>::Frag (*b)[STEPS],
 template <typename T, int STEPS, bool PAST>
 __global__ void __launch_bounds__(NT)
 few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, int tokens, int cols,
-              int d, int chunks, T* __restrict__ g_W) {
+              int d, int chunks, int walk, T* __restrict__ g_W) {
   typedef Few<T> F;
   typedef typename F::Frag Frag;
   // fragments and columns of one step along d: 128 bytes
@@ -93,24 +104,26 @@ few_gw_kernel(const T* __restrict__ gz, int64_t ldg, const T* __restrict__ xt, i
   const unsigned group = blockIdx.x / (unsigned)chunks, chunk = blockIdx.x - group * chunks;
   const int64_t v0 = ((int64_t)group * NWAVES + (threadIdx.x >> 6)) * kRows;
   if (v0 >= cols) return;
-  Frag a[VF][STEPS];
+  Frag a[VF][STEPS][F::kParts];
 #pragma unroll
   for (int f = 0; f < VF; ++f) {
     const int64_t v = min(v0 + 16 * f + r, (int64_t)cols - 1);
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      union { T e[F::E]; Frag v; } u;
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-      for (int e = 0; e < F::E; ++e) {
-        const int t = s * F::K + g * F::E + e;
-        const T z = gz[min(t, tokens - 1) * ldg + v];
-        u.e[e] = t < tokens ? z : T{};
+      for (int h = 0; h < F::kParts; ++h) {
+        union { T e[F::E]; Frag v; } u;
+#pragma unroll
+        for (int e = 0; e < F::E; ++e) {
+          const int t = s * F::K + g * F::E + e;
+          const T z = gz[(h * tokens + min(t, tokens - 1)) * ldg + v];
+          u.e[e] = t < tokens ? z : T{};
+        }
+        a[f][s][h] = u.v;
       }
-      a[f][s] = u.v;
-    }
   }
   constexpr int kPad = STEPS * F::K;
-  const int c0 = (int)chunk * kChunk, c1 = min(d, c0 + kChunk);
+  const int c0 = (int)chunk * walk, c1 = min(d, c0 + walk);
   Frag next[NF][STEPS];  // of the kStep columns after the current ones
   auto load = [&](int n0) {
 #pragma unroll
@@ -153,15 +166,18 @@ template <typename T, int STEPS>
 hipError_t launch_steps(const void* gz, int64_t ldg, const void* xt, int tokens, int cols, int d,
                         void* g_W, hipStream_t s) {
   constexpr int kRows = 16 * kFrags<STEPS>;
-  const int chunks = (d + kChunk - 1) / kChunk;
-  const int64_t blocks = ((int64_t)cols + kRows * NWAVES - 1) / (kRows * NWAVES) * chunks;
+  const int64_t groups = ((int64_t)cols + kRows * NWAVES - 1) / (kRows * NWAVES);
+  int walk = kChunk<T, STEPS>;
+  while (walk > 512 && groups * ((d + walk - 1) / walk) < kGroups) walk /= 2;
+  const int chunks = (d + walk - 1) / walk;
+  const int64_t blocks = groups * chunks;
   if (blocks >= INT64_C(1) << 24) return hipErrorInvalidValue;  // (2^32 work items)
   const int64_t row = d * (int64_t)sizeof(T);
   const auto kernel = row % 128 == 0 && cols * row > kCacheBytes
                           ? few_gw_kernel<T, STEPS, true>
                           : few_gw_kernel<T, STEPS, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(NT), 0, s, static_cast<const T*>(gz), ldg,
-                     static_cast<const T*>(xt), tokens, cols, d, chunks, static_cast<T*>(g_W));
+                     static_cast<const T*>(xt), tokens, cols, d, chunks, walk, static_cast<T*>(g_W));
   return hipGetLastError();
 }
 

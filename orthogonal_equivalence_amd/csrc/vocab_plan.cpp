@@ -120,23 +120,31 @@ VocabFwdPlan plan_vocab_fwd(const VocabSizes& v) {
 }
 
 namespace {
-// a launch for the turned copy of x and one that stores g_W (131072 x 4096 1 token
-// 211 us, 64 245, 96 300, 128 385; rows that are not whole lines take longer)
+// a launch for the turned copy of x and one that stores g_W, by its products' steps (us a
+// MB, from 131072 x 4096 bf16: 1 token 211 us, 64 275, 96 323, 128 454; rows that are not
+// whole lines take longer)
 float few_cost(const VocabSizes& v, int64_t n) {
   if (v.tokens > few_tokens(v.t)) return 1e30f;
+  constexpr float kStep[4] = {0.191f, 0.251f, 0.295f, 0.417f};
+  const int step = few_padded(v.t, (int)v.tokens) / few_padded(v.t, 1) - 1;
   const float mb = (float)n * (float)(v.d * v.es()) / 1e6f;
-  return 6.0f + mb * (0.19f + 0.0013f * v.tokens) * (v.d * v.es() % 128 ? 1.2f : 1.0f);
+  const float rate = v.parts() == 2 ? kStep[step] : 0.19f + 0.0013f * v.tokens;
+  return 6.0f + mb * rate * (v.d * v.es() % 128 ? 1.2f : 1.0f);
 }
 float gw_cost(const VocabSizes& v, int64_t n) {
-  return std::min(few_cost(v, n), plan_tile_product(v.t, n, v.d, v.tokens, false).cost);
+  return std::min(few_cost(v, n), plan_tile_product(v.t, n, v.d, v.tokens * v.parts(), false).cost);
 }
 }  // namespace
 
 VocabProducts plan_vocab_products(const VocabSizes& v, int64_t n) {
   VocabProducts p;
-  p.gx = plan_tile_product(v.t, v.tokens, v.d, n, false, kManySplits);
-  p.gw = plan_tile_product(v.t, n, v.d, v.tokens, false);
-  p.pair = plan_tile_pair(v.t, v.tokens, v.d, n, kManySplits);
+  const int64_t rows = v.tokens * v.parts();
+  p.gx = plan_tile_product(v.t, rows, v.d, n, false, kManySplits);
+  p.gw = plan_tile_product(v.t, n, v.d, rows, false);
+  p.pair = plan_tile_pair(v.t, rows, v.d, n, kManySplits);
+  if (v.parts() == 2)  // (summed by the join even where the reduction is whole)
+    for (TilePlan* gx : {&p.gx, &p.pair.gx})
+      if (gx->nsplit == 1) gx->part_floats = (size_t)(rows * v.d);
   p.few = few_cost(v, n) < std::min(p.gw.cost, std::max(p.pair.cost - p.gx.cost, 0.0f));
   p.paired = !p.few && p.pair.gx.nsplit != 0 && p.pair.cost < p.gx.cost + p.gw.cost;
   return p;
@@ -146,7 +154,7 @@ namespace {
 
 void set_pieces(const VocabSizes& v, VocabBwdPlan& p) {
   const int64_t es = v.es();
-  const int64_t most = std::max(kTile, kPieceBytes / (p.padded * es) / kTile * kTile);
+  const int64_t most = std::max(kTile, kPieceBytes / (p.padded * v.parts() * es) / kTile * kTile);
   p.pieces = ceil_div(v.vocab, most);
   p.piece = p.pieces == 1 ? v.vocab : ceil_div(ceil_div(v.vocab, p.pieces), kTile) * kTile;
   p.pieces = ceil_div(v.vocab, p.piece);
@@ -155,14 +163,16 @@ void set_pieces(const VocabSizes& v, VocabBwdPlan& p) {
 // g_x's tiles are few where tokens and d are: its reduction, the vocabulary, is
 // split so that they fill the CUs
 float split_gx(const VocabSizes& v, VocabBwdPlan& p) {
-  const int64_t tiles = p.padded / kTile * ceil_div(v.d, kTile);
+  const int64_t tiles = p.padded * v.parts() / kTile * ceil_div(v.d, kTile);
   float best = 1e30f;
   for (int s = 1; s <= 128; s += s < 16 ? 1 : 8) {
     const int64_t chunk = ceil_div(ceil_div(p.piece, s), kTile) * kTile;
     const int64_t n = ceil_div(p.piece, chunk);
     // (a slab is written and read once more)
     const float cost = dense_cost(tiles * n, chunk) +
-                       (n > 1 ? 3.0f + (float)(8 * n * v.tokens * v.d) / 5e6f : 0.0f);
+                       (n > 1 || v.parts() == 2
+                            ? 3.0f + (float)(8 * n * v.dense_rows() * v.d) / 5e6f
+                            : 0.0f);
     if (cost >= best) continue;
     best = cost;
     p.splits = (int)n;
@@ -178,18 +188,19 @@ VocabBwdPlan plan_vocab_bwd(const VocabSizes& v, bool weight) {
   const int64_t es = v.es();
   p.splits = 1;
   // Fewer rows than a tile's 256 are padded, from where g_W has its kernel for few
-  // tokens on. (160 tokens, on tiles and padded, us: 131072 x 4096 1214, 885, 50257 x 2048
-  // 271, 234, 32000 x 4096 323, 262; W frozen 577, 501, 121, 121, 134, 145, where the tiles'
-  // estimate is a tenth too high.)
+  // tokens on. (160 tokens, on tiles and padded, us: 131072 x 4096 1484, 1162, 50257 x 2048
+  // 324, 305, 32000 x 4096 397, 329; W frozen 764, 678, 154, 166, 185, 190, 32000 x 1024 70, 77:
+  // there the tiles' estimate is a tenth too high.)
   p.padded = ceil_div(v.tokens, kTile) * kTile;
+  p.two = v.parts() == 2;
   if (v.t == DType::BF16 && v.tokens > few_tokens(v.t) &&
       vocab_dense_supported(p.padded, v.vocab, v.d)) {
     set_pieces(v, p);
     float dense = split_columns(v.t, p.padded, p.piece, v.d, 1.0f).cost + split_gx(v, p);
     float tile = plan_tile_product(v.t, v.tokens, p.piece, v.d, false, 1).cost +
-                 plan_tile_product(v.t, v.tokens, v.d, p.piece, false, kManySplits).cost;
+                 plan_vocab_products(v, p.piece).gx.cost;
     if (weight) {
-      dense += dense_cost(ceil_div(p.piece, kTile) * ceil_div(v.d, kTile), v.tokens);
+      dense += dense_cost(ceil_div(p.piece, kTile) * ceil_div(v.d, kTile), v.dense_rows());
       tile += gw_cost(v, p.piece);
     }
     if (!weight && v.tokens < kTile) tile *= 0.9f;
@@ -206,14 +217,16 @@ VocabBwdPlan plan_vocab_bwd(const VocabSizes& v, bool weight) {
   p.last = off;
   if (p.dense && v.vocab % kTile) off += align_up((size_t)(kTile * v.d * es));
   p.xs = off;
-  const int64_t copied = p.dense || v.tokens > few_tokens(v.t)
-                             ? p.padded
-                             : few_padded(v.t, (int)v.tokens);
+  int64_t copied = p.dense ? p.padded : p.padded * v.parts();
+  if (v.tokens <= few_tokens(v.t)) copied = std::max<int64_t>(copied, few_padded(v.t, (int)v.tokens));
   off += align_up((size_t)(copied * v.d * es));
+  p.pairs = off;
+  if (p.dense && p.two && weight) off += align_up((size_t)(2 * p.padded * v.d * es));
   p.gz = off;
-  off += align_up((size_t)(p.padded * p.ldg * es));
+  off += align_up((size_t)(p.padded * v.parts() * p.ldg * es));
   p.acc = off;
-  if (p.summed()) off += align_up((size_t)v.tokens * v.d * 4 * p.splits);
+  if (p.summed())
+    off += align_up((size_t)(p.dense ? v.dense_rows() : v.tokens) * v.d * 4 * p.splits);
   p.part = off;
   if (!p.dense) {
     const size_t rest = plan_vocab_products(v, v.vocab - (p.pieces - 1) * p.piece).part_floats();

@@ -13,6 +13,14 @@ struct VocabSizes {
   int64_t tokens, d, vocab;
   int top;  // 0: cross entropy
   int64_t es() const { return t == DType::BF16 ? 2 : 4; }
+  // The rows of g_z a token. One entry often makes most of a row (the target's), and its
+  // rounding to bf16 shifts the whole row of g_x, and of g_W, by up to half a step; over
+  // hundreds of tokens that averages to a rounding beside the result's own, over few it
+  // may be 2.5 times that. There g_z has a second row, of what rounding took off the
+  // first (and the products' bytes, which bound them, stay as they are).
+  int parts() const { return t == DType::BF16 && tokens < kTileRows ? 2 : 1; }
+  // rows of the dense products' tiled g_z
+  int64_t dense_rows() const { return parts() == 2 ? pair_rows(tokens) : tokens; }
 };
 
 // Columns of the logits of `rows` rows on the 256 x 256 tiles; the rest, if any, go
@@ -43,12 +51,13 @@ VocabFwdPlan plan_vocab_fwd(const VocabSizes& v);
 // workspace is that of the larger of the two).
 struct VocabBwdPlan {
   bool dense;
-  int64_t padded;       // rows of xs and gz
+  int64_t padded;       // rows of xs and gz (row-major: of each part)
   int64_t piece, pieces, ldg;
   bool few;             // g_W on the kernel for few tokens
   int splits, kchunk;   // dense: of g_x's reduction over a piece
-  size_t rows, last, xs, gz, acc, part, total;
-  bool summed() const { return pieces > 1 || splits > 1; }
+  size_t rows, last, xs, pairs, gz, acc, part, total;
+  bool two;  // rows of g_z a token
+  bool summed() const { return pieces > 1 || splits > 1 || (dense && two); }
 };
 VocabBwdPlan plan_vocab_bwd(const VocabSizes& v, bool weight);
 // of a piece's logits

@@ -8,8 +8,9 @@
 //             lanes (16 apart), so a row costs its exponentials and four
 //             exchanges. (m, s) goes to part[slot][row]: nothing is read again
 //             but 8 bytes for every 16 to 64 columns.
-//   backward  g_z = a exp(z / temperature - lse), less b at the row's target: rounded
-//             once to x's type, the operand of the two products that follow.
+//   backward  g_z = a exp(z / temperature - lse), less b at the row's target: in x's
+//             type, the operand of the two products that follow (bf16 of few tokens in
+//             two parts, VocabSizes::parts()).
 //
 // Few rows are bound by W's bytes: 1 token, 131072 x 4096 bf16 167 us (6.4 TB/s).
 // float32: 100 x 5003 x 1024 26 us, one round of workgroups; 6508 x 80128 x 168 2.4 ms (73
@@ -93,11 +94,13 @@ struct GradEnd {
   int64_t ldg;
   int tiled, col0;
   float scale;
+  int64_t low;
   template <typename T, int FM, int FN>
   __device__ __forceinline__ void run(const TileProduct& p, const floatx4 (&acc)[FM][FN], int m_at,
                                       int n_at, int, int, int lane) const {
-    // (the tiled layout's reductions run over whole K tiles of 32 rows)
-    const int m_end = tiled ? (p.M + 31) / 32 * 32 : p.M, n_end = (p.N + 255) / 256 * 256;
+    // (the tiled layout's reductions run over whole K tiles of 32 rows, 16 of pairs)
+    const int whole = low ? 15 : 31;
+    const int m_end = tiled ? (p.M + whole) & ~whole : p.M, n_end = (p.N + 255) / 256 * 256;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = m_at + 16 * i + (lane & 15);
@@ -111,7 +114,15 @@ struct GradEnd {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           v[e] = n + e < p.N ? logit_gradient<T>(r, acc[i][j][e], scale, col0 + n + e) : 0.0f;
-        Quad<T>::store(static_cast<T*>(gz) + (tiled ? tiled_offset(m, n, ldg) : m * ldg + n), v);
+        T* out = static_cast<T*>(gz) +
+                 (tiled ? tiled_offset(low ? pair_row(m) : m, n, ldg) : m * ldg + n);
+        Quad<T>::store(out, v);
+        if constexpr (sizeof(T) == 2) {
+          if (!low) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = low_part(v[e], bf16_to_f32(f32_to_bf16(v[e])));
+          Quad<T>::store(out + low, v);
+        }
       }
     }
   }
@@ -188,8 +199,8 @@ hipError_t launch_vocab_lse_tile(DType t, const TilePlan& plan, const VocabProdu
 
 hipError_t launch_vocab_grad_tile(DType t, const TilePlan& plan, const VocabProduct& p,
                                   const VocabRow* rows, void* gz, int64_t ldg, bool tiled,
-                                  hipStream_t s) {
-  return launch_end(t, plan, p, GradEnd{rows, gz, ldg, (int)tiled, p.col0, p.scale}, s);
+                                  int64_t low, hipStream_t s) {
+  return launch_end(t, plan, p, GradEnd{rows, gz, ldg, (int)tiled, p.col0, p.scale, low}, s);
 }
 
 }  // namespace poetx

@@ -128,7 +128,8 @@ CASES = [  # dtype, tokens, d, vocab
     (BF16, 3137, 2720, 3077), (F32, 7930, 96, 3471), (BF16, 3756, 3840, 2304), (BF16, 1350, 256, 109972),
     (F32, 4849, 16, 49508), (F32, 60, 2752, 30580), (F32, 1896, 1024, 2972), (BF16, 5600, 3392, 3840),
     (BF16, 2379, 320, 108458), (BF16, 4096, 2816, 36606), (BF16, 71, 208, 98288), (BF16, 73, 1024, 72448),
-    (BF16, 101, 1792, 47872), (BF16, 153, 256, 110689),
+    (BF16, 101, 1792, 47872), (BF16, 153, 256, 110689), (BF16, 19, 3512, 115968),
+    (BF16, 53, 1312, 119532),
 ]
 # dtype, tokens, d, vocab, top
 LISTED = [
