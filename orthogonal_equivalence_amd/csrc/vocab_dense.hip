@@ -92,9 +92,9 @@ template <typename D> __device__ __forceinline__ int opaque_lane(const D& d) {
 // accumulators, so that the eight rows of a lane are exchanged together; and the
 // targets' logits, which few waves hold any of.
 // LISTED: `cells` in the place of targets.
-// Bound by the matrix units at the clock that the chip's power leaves: 8192 x 131072 x
-// 4096 5.8 - 6.07 ms (1.45 - 1.5 PFLOP/s), units busy 75% at 1.65 GHz; 4096 x 65536 x 2048
-// with 64 listed logits a row 0.94 ms (64%), 0.90 without them.
+// Bound by the matrix units at the clock that the chip's power leaves (a launch under the
+// profiler): 8192 x 131072 x 4096 6.0 ms (1.46 PFLOP/s), units busy 74% at 1.73 GHz; 4096 x
+// 65536 x 2048 with 64 listed logits a row 0.92 ms (64%), 0.88 without them.
 template <bool LISTED>
 __global__ void __launch_bounds__(NT)
 vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
@@ -202,7 +202,7 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
 
 // The end of the logits' backward. A row's target is one column of the
 // vocabulary: few waves hold any, and the others only scale exponentials.
-// 8192 x 32768 x 4096 1.59 ms (1.39 PFLOP/s), matrix units busy 71% at 1.87 GHz.
+// 8192 x 32768 x 4096 1.60 ms (1.38 PFLOP/s), matrix units busy 70% at 1.88 GHz.
 // g_z is rounded to bf16, the products' operand (gradients 0.0024 off, 2-norm, where the
 // result's rounding alone gives 0.0017; a second part from 256 tokens on would add
 // two products to three). PAIRS: what the rounding takes off g_z too, rows by pair_row().
@@ -362,8 +362,8 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
 }
 
 // g_W of the piece: both operands tiled, their rows (tokens) the reduction. SHORT: fewer
-// than 225 of them. 32768 x 4096 x 8192 1.63 ms (1.35 PFLOP/s), busy 71%, bank
-// conflicts in 18% of the cycles; 50001 x 2048 x 1000 0.208 ms: seven rounds for 6.1 of
+// than 225 of them. 32768 x 4096 x 8192 1.62 ms (1.36 PFLOP/s), busy 72%, bank
+// conflicts in 18% of the cycles; 50001 x 2048 x 1000 0.209 ms: seven rounds for 6.1 of
 // tiles, of 23 us and 6 for what is not products.
 template <bool SHORT>
 __global__ void __launch_bounds__(NT)
