@@ -437,7 +437,7 @@ hipError_t launch_vocab_grad_dense(const VocabProduct& p, const void* W_last, co
 hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, const void* W_last,
                                  int64_t rows, int d, int cols, int splits, int kchunk,
                                  float* slabs, bool add, void* y, hipStream_t s);
-// g_z^T x from tiled gz and xs, `padded` rows (a multiple of 32) of both: bf16 [cols][d]
+// g_z^T x from tiled gz and xs, `padded` rows (a multiple of 32, 256 at least) of both: bf16 [cols][d]
 // (what gz's columns past `cols` hold does not matter).
 hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
                                  int cols, void* g_W, hipStream_t s);

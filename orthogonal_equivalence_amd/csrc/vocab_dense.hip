@@ -93,8 +93,8 @@ template <typename D> __device__ __forceinline__ int opaque_lane(const D& d) {
 // targets' logits, which few waves hold any of.
 // LISTED: `cells` in the place of targets.
 // Bound by the matrix units at the clock that the chip's power leaves (a launch under the
-// profiler): 8192 x 131072 x 4096 6.0 ms (1.46 PFLOP/s), units busy 74% at 1.73 GHz; 4096 x
-// 65536 x 2048 with 64 listed logits a row 0.92 ms (64%), 0.88 without them.
+// profiler): 8192 x 131072 x 4096 5.86 ms (1.5 PFLOP/s), units busy 74% at 1.76 GHz; 4096 x
+// 65536 x 2048 with 64 listed logits a row 0.90 ms (64%), 0.86 without them.
 template <bool LISTED>
 __global__ void __launch_bounds__(NT)
 vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
@@ -202,7 +202,7 @@ vocab_lse_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W,
 
 // The end of the logits' backward. A row's target is one column of the
 // vocabulary: few waves hold any, and the others only scale exponentials.
-// 8192 x 32768 x 4096 1.60 ms (1.38 PFLOP/s), matrix units busy 70% at 1.88 GHz.
+// 8192 x 32768 x 4096 1.55 ms (1.42 PFLOP/s), matrix units busy 70% at 1.89 GHz.
 // g_z is rounded to bf16, the products' operand (gradients 0.0024 off, 2-norm, where the
 // result's rounding alone gives 0.0017; a second part from 256 tokens on would add
 // two products to three). PAIRS: what the rounding takes off g_z too, rows by pair_row().
@@ -287,7 +287,7 @@ vocab_grad_kernel(const bf16_t* __restrict__ xs, const bf16_t* __restrict__ W,
 // LAST: the piece ends inside a K tile (a choice of the source at every copy:
 // 8192 x 131072 x 4096 backward 19150 us with it in every piece, 18890 without),
 // or one of its ranges is shorter than 256.
-// 8192 x 4096 x 32768 1.53 ms (1.43 PFLOP/s), busy 76%; LDS bank conflicts (W's rows
+// 8192 x 4096 x 32768 1.50 ms (1.47 PFLOP/s), busy 76%; LDS bank conflicts (W's rows
 // read across) in 10% of the cycles.
 template <bool WHOLE, bool LAST>
 __global__ void __launch_bounds__(NT)
@@ -361,11 +361,10 @@ vocab_gx_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ W,
             });
 }
 
-// g_W of the piece: both operands tiled, their rows (tokens) the reduction. SHORT: fewer
-// than 225 of them. 32768 x 4096 x 8192 1.62 ms (1.36 PFLOP/s), busy 72%, bank
-// conflicts in 18% of the cycles; 50001 x 2048 x 1000 0.209 ms: seven rounds for 6.1 of
+// g_W of the piece: both operands tiled, their rows (tokens) the reduction (256 of
+// them at least). 32768 x 4096 x 8192 1.58 ms (1.39 PFLOP/s), busy 71%, bank
+// conflicts in 18% of the cycles; 50001 x 2048 x 1000 0.205 ms: seven rounds for 6.1 of
 // tiles, of 23 us and 6 for what is not products.
-template <bool SHORT>
 __global__ void __launch_bounds__(NT)
 vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, int M, int N, int K,
                 int64_t ldg, bf16_t* __restrict__ g_W) {
@@ -373,7 +372,7 @@ vocab_gw_kernel(const bf16_t* __restrict__ gz, const bf16_t* __restrict__ xs, in
   D d;
   d.init(ldg, N, true, true);
   const int ntiles = K / BK;
-  tile_loop<FM * FN / 2, SHORT>(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M, N - BN,
+  tile_loop<FM * FN / 2>(d, (M + BM - 1) / BM, (N + BN - 1) / BN, 1, M, N - BN,
             [&](int, int m0, int n0) __attribute__((always_inline)) {
               d.set_tile(gz, xs, ldg, N, m0, n0);
               return ntiles;
@@ -469,13 +468,12 @@ hipError_t launch_vocab_gx_dense(const void* gz, int64_t ldg, const void* W, con
 hipError_t launch_vocab_gw_dense(const void* gz, int64_t ldg, const void* xs, int64_t padded, int d,
                                  int cols, void* g_W, hipStream_t s) {
   if (!vocab_dense_supported(256, cols, d) || ldg % BN != 0 || ldg < cols || padded % BK != 0 ||
-      padded < BK)
+      padded < kLongK)
     return hipErrorInvalidValue;
   int grid = 0;
   const hipError_t e = dense_grid(cols, d, &grid);
   if (e != hipSuccess) return e;
-  const auto kernel = padded < kLongK ? vocab_gw_kernel<true> : vocab_gw_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, s, b16(gz), b16(xs), cols, d,
+  hipLaunchKernelGGL(vocab_gw_kernel, dim3(grid), dim3(NT), 0, s, b16(gz), b16(xs), cols, d,
                      (int)padded, ldg, static_cast<bf16_t*>(g_W));
   return hipGetLastError();
 }

@@ -16,8 +16,8 @@
 // us:                      1 token   64   96  128
 //   131072 x 4096, bf16      211  275  323  454     (with one part of g_z 211, 245, 300, 385)
 //   32000 x 4096              55   64
-// From 33 tokens on 64 ids a wave (32 ids: a third more at 64 tokens, a tenth at 128); up
-// to 32 tokens 32 ids (56370 x 2256, 16 tokens: 232 us a backward, 64 ids 239). Stores of
+// From 33 tokens on 64 ids a wave (32 ids: a third more at 64 tokens, a sixth at 96, alike at
+// 128); up to 32 tokens 32 ids (56370 x 2256, 16 tokens: 232 us a backward, 64 ids 239). Stores of
 // 16 rows' half lines: a third more. Past 128 tokens the registers are spent.
 #include "epilogue.h"
 #include "vocab.h"

@@ -12,7 +12,7 @@
 //             type, the operand of the two products that follow (bf16 of few tokens in
 //             two parts, VocabSizes::parts()).
 //
-// Few rows are bound by W's bytes: 1 token, 131072 x 4096 bf16 169 us (6.4 TB/s).
+// Few rows are bound by W's bytes: 1 token, 131072 x 4096 bf16 167 us (6.4 TB/s).
 // float32: 100 x 5003 x 1024 27 us, one round of workgroups; 2048 x 32000 x 2048 1.94 ms
 // (138 TFLOP/s); 6508 x 80128 x 168 2.5 ms (70), where a tile's six steps are followed by
 // its exponentials.
